@@ -72,7 +72,8 @@ typedef enum {
     GPTQ_CALL_PREPARE = 1,
     GPTQ_CALL_ASYM_CORRECTION = 2,
     GPTQ_CALL_QUANTIZE_LAYER = 3,
-    GPTQ_CALL_ACT_ORDER = 4
+    GPTQ_CALL_ACT_ORDER = 4,
+    GPTQ_CALL_ROUTE = 5
 } gptq_call_t;
 
 /* Flags of gptq_quantize_layer. */
@@ -85,7 +86,7 @@ typedef enum {
  * gptq_workspace_bytes - bytes of `workspace` a call needs for the given sizes.
  *   call: which entry point; K, N, M: sizes as in that call (unused ones are ignored; for
  *   GPTQ_CALL_QUANTIZE_LAYER, M is the number of output-channel groups of gptq_quantize_layer_groups, 0 or 1 for
- *   gptq_quantize_layer); flags: for
+ *   gptq_quantize_layer; for GPTQ_CALL_ROUTE, K is the number of experts and M the tokens); flags: for
  *   gptq_accumulate_hessian 1 if X_float will be given | 2 if row_scale will be given; for
  *   gptq_quantize_layer its flags (GPTQ_FLAG_CAE matters) | 2 if P1 will be given; else 0.
  * Returns 0 for an unknown call.  Never fails otherwise.
@@ -374,6 +375,108 @@ int64_t gptq_packed_words(int64_t K, int bits);
 gptq_status_t gptq_unpack_codes(const uint32_t* packed, int64_t ldp, int64_t K, int64_t N, int bits,
                                 const float* scales, uint8_t* codes, int64_t c_rs, int64_t c_cs,
                                 void* W_hat, gptq_dtype_t w_dtype, int64_t w_rs, int64_t w_cs, void* stream);
+
+/*
+ * Serving the packed layers: the products that read the words of gptq_pack_codes directly, a router's choice of experts
+ * and the join of their results.  All four calls are asynchronous, allocate nothing, may be captured into a HIP graph
+ * and give the same bits for the same inputs.  The integer lists that steer them (offsets, rows, positions, requests,
+ * adapter) live on the device, so that no call waits for the host; an entry outside its range selects nothing, as
+ * stated at each, and never reads or writes out of bounds.
+ *
+ * The layer W[k][n] = s (c - z), z = 2^(bits-1): codes and scales as gptq_quantize_layer and gptq_pack_codes leave them.
+ * A layer quantised in act-order with scales re-estimated in the loop has its groups in processing order: pack
+ * codes[perm] and give X[:, perm].  Codes enter the matrix cores exactly, scales multiply fp32 partial sums (of at most
+ * 128 products), so nothing but the output is rounded.  fp32 activations are split into three bf16 parts (exact).
+ * A NaN or infinity in a row of X makes that row of Y NaN or infinite and touches no other row.
+ */
+
+/* Flags of the serving calls. */
+#define GPTQ_FLAG_RENORM 1u   /* gptq_route: weights divided by their sum over the chosen experts */
+#define GPTQ_FLAG_SWIGLU 1u   /* gptq_expert_matmul: silu(first half of the channels) * second half */
+
+/*
+ * gptq_route - the topk experts of every token and the rows of every expert.
+ *   p_t = softmax(logits_t); token t chooses the topk experts with the largest logits, largest first, ties by the lower
+ *   index; weight p (with GPTQ_FLAG_RENORM p / sum of the chosen p).  An expert with logit -infinity is never chosen
+ *   (its p is 0); where fewer than topk are left, the last choices are experts = positions = -1 with weight 0.
+ *   The choices are then sorted by expert, stably (an expert's rows are in the order of the tokens).
+ *
+ *   logits     device, T x E, dtype, leading dimension ld >= E.   T >= 0.   E 1..1024.   topk 1..32 (may exceed E).
+ *   weights    device fp32[T * topk].        experts   device int32[T * topk].
+ *   offsets    device int32[E + 1]: expert e has rows [offsets[e], offsets[e + 1]).
+ *   rows       device int32[T * topk]: the token of every row; -1 from offsets[E] on.
+ *   positions  device int32[T * topk]: the row of choice j of token t at [t * topk + j], -1 where there is none.
+ *   flags      GPTQ_FLAG_RENORM or 0.
+ *   workspace  device scratch of gptq_workspace_bytes(GPTQ_CALL_ROUTE, E, 0, T, 0).
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.  A NaN or +infinity logit latches GPTQ_ERR_NONFINITE in the
+ * workspace status word (gptq_device_status); its token then chooses nothing, the others are as they should be.
+ */
+gptq_status_t gptq_route(const void* logits, gptq_dtype_t dtype, int64_t T, int64_t E, int64_t ld, int topk,
+                         unsigned flags, float* weights, int32_t* experts, int32_t* offsets, int32_t* rows,
+                         int32_t* positions, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of gptq_expert_matmul (rank 0) and of gptq_adapter_matmul (experts 1; rank 0 without adapters) for M >= 1
+ * rows; 0 for sizes that those calls refuse. */
+size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank);
+
+/*
+ * gptq_expert_matmul - matrix products grouped by expert, of any (ragged) sizes:
+ *   Y[r] = X[rows[r]] W_e  for r in [offsets[e], offsets[e + 1]); with GPTQ_FLAG_SWIGLU
+ *   Y[r][n] = silu(y_n) y_{n + N/2}, n < N/2, silu(g) = g / (1 + e^-g), in fp32 before the one rounding.
+ *
+ *   X          device, x_rows x K, dtype, leading dimension ldx >= K.
+ *   rows       NULL (row r of X; x_rows >= M), or device int32[M]; a value outside [0, x_rows) gives a zero row.
+ *   M          rows of Y, 0 .. 2^30.
+ *   offsets    device int32[E + 1], non-decreasing; clamped to [0, M].  Rows before offsets[0] and from offsets[E] on
+ *              are written as zeros.
+ *   E          1 .. 16384 experts.
+ *   packed     device uint32, word w of channel n of expert e at packed[e * p_stride + w * ldp + n]; ldp >= N,
+ *              p_stride >= gptq_packed_words(K, bits) * ldp (E > 1).
+ *   K          1 .. 2^22.   N: 4 .. 2^22 channels (even with GPTQ_FLAG_SWIGLU).   bits 2..6.
+ *   scales     device fp32, contiguous N per expert (groups: ceil(K / groupsize) x N), expert e at e * s_stride.
+ *   groupsize  0, 32, 64 or 128 consecutive k that share a scale.
+ *   Y          device, M x N (N / 2 with GPTQ_FLAG_SWIGLU), dtype, leading dimension ldy; not X.
+ *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, E, 0).
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_rows, int64_t ldx, const int32_t* rows,
+                                 int64_t M, const int32_t* offsets, int64_t E, const uint32_t* packed, int64_t ldp,
+                                 int64_t p_stride, int64_t K, int64_t N, int bits, const float* scales,
+                                 int64_t s_stride, int64_t groupsize, unsigned flags, void* Y, int64_t ldy,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gptq_adapter_matmul - a packed projection with low-rank adapters of many requests beside it:
+ *   Y[r] = X[r] W + alpha_a B_a (A_a X[r]),  a = adapter[q] for the request q with requests[q] <= r < requests[q + 1].
+ * Without adapters (n_adapters or n_requests 0) it is the plain product.
+ *
+ *   X, K, N, bits, scales, groupsize, Y: as for gptq_expert_matmul with one expert; X is M x K.
+ *   A          device bf16, rank x K per adapter (the layout of an nn.Linear weight), row i of adapter a at
+ *              A + a * a_stride + i * lda; lda >= K.
+ *   B          device bf16, N x rank per adapter, row n of adapter a at B + a * b_stride + n * ldb; ldb >= rank.
+ *   alpha      device fp32[n_adapters].      rank 1..128 (smaller ones: zero rows of A).
+ *   requests   device int32[n_requests + 1], non-decreasing, clamped to [0, M]; rows outside have no adapter.
+ *   adapter    device int32[n_requests]; -1 (or any value outside [0, n_adapters)): no adapter.
+ *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, 1, rank).
+ * A x is summed and kept in fp32 (it enters the second product in bf16 parts: two for bf16 rows, with an error 2^-17 of
+ * the adapter's term, exactly three for fp32 rows).  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, int64_t ldx, const uint32_t* packed,
+                                  int64_t ldp, int64_t K, int64_t N, int bits, const float* scales, int64_t groupsize,
+                                  const void* A, int64_t lda, int64_t a_stride, const void* B, int64_t ldb,
+                                  int64_t b_stride, const float* alpha, int64_t n_adapters, int64_t rank,
+                                  const int32_t* requests, const int32_t* adapter, int64_t n_requests, void* Y,
+                                  int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gptq_combine - a token's experts joined: out[t] = sum_j weights[t * topk + j] Y[positions[t * topk + j]], in the order
+ * of j, in fp32.  A position outside [0, M) is left out; a token with none gets zeros.
+ *   Y          device, M x N, dtype, leading dimension ldy >= N.   out: device, T x N, dtype, ldo >= N; not Y.
+ *   positions  device int32[T * topk] and weights fp32[T * topk], as gptq_route writes them.   topk 1..32.
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_combine(const void* Y, gptq_dtype_t dtype, int64_t M, int64_t ldy, const int32_t* positions,
+                           const float* weights, int64_t T, int topk, int64_t N, void* out, int64_t ldo, void* stream);
 
 /*
  * gptq_device_status - the error latched on the device by the latest gptq_prepare, gptq_prepare_groups,

@@ -16,11 +16,13 @@ LIB_PATH = os.path.join(_PKG_DIR, "libgptq_hip.so")
 
 GPTQ_OK, GPTQ_ERR_ARG, GPTQ_ERR_NONFINITE, GPTQ_ERR_NOT_PD, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP = range(6)
 GPTQ_DTYPE_F32, GPTQ_DTYPE_BF16 = 0, 1
-GPTQ_CALL_ACCUMULATE_HESSIAN, GPTQ_CALL_PREPARE, GPTQ_CALL_ASYM_CORRECTION, GPTQ_CALL_QUANTIZE_LAYER, GPTQ_CALL_ACT_ORDER = range(5)
+GPTQ_CALL_ACCUMULATE_HESSIAN, GPTQ_CALL_PREPARE, GPTQ_CALL_ASYM_CORRECTION, GPTQ_CALL_QUANTIZE_LAYER, GPTQ_CALL_ACT_ORDER, GPTQ_CALL_ROUTE = range(6)
 GPTQ_FLAG_SCALES_GIVEN = 1
 GPTQ_FLAG_CAE = 4
 GPTQ_FLAG_STATIC_GROUPS = 8
 GPTQ_FLAG_MSE = 16
+GPTQ_FLAG_RENORM = 1
+GPTQ_FLAG_SWIGLU = 1
 
 _i64, _f32, _u32, _ptr, _size = ctypes.c_int64, ctypes.c_float, ctypes.c_uint, ctypes.c_void_p, ctypes.c_size_t
 
@@ -52,6 +54,16 @@ _SIGNATURES = {
                                                    ctypes.c_int, ctypes.c_int, _u32, _ptr, _i64, _i64, _ptr, _ptr, _ptr,
                                                    _ptr, _ptr, _i64, _ptr, _ptr]),
     "gptq_gram_plan": (ctypes.c_int, [_i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_i64)]),
+    "gptq_matmul_workspace_bytes": (_size, [ctypes.c_int, _i64, _i64, _i64, _i64, _i64]),
+    "gptq_route": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _u32, _ptr, _ptr, _ptr, _ptr, _ptr,
+                                  _ptr, _size, _ptr]),
+    "gptq_expert_matmul": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _i64, _i64,
+                                          _i64, ctypes.c_int, _ptr, _i64, _i64, _u32, _ptr, _i64, _ptr, _size, _ptr]),
+    "gptq_adapter_matmul": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _ptr, _i64, _i64, _i64, ctypes.c_int, _ptr,
+                                           _i64, _ptr, _i64, _i64, _ptr, _i64, _i64, _ptr, _i64, _i64, _ptr, _ptr, _i64,
+                                           _ptr, _i64, _ptr, _size, _ptr]),
+    "gptq_combine": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _ptr, _ptr, _i64, ctypes.c_int, _i64, _ptr, _i64,
+                                    _ptr]),
     "gptq_timer_enable": (ctypes.c_int, [ctypes.c_int]),
     "gptq_timer_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
 }
@@ -445,3 +457,203 @@ def gptq_act_order(H: torch.Tensor, A: Optional[torch.Tensor] = None, perm: Opti
     st = load().gptq_act_order(_dptr(H), _dptr(A), K, _dptr(perm), wp, wb, _stream(H.device, stream))
     _check(st, "gptq_act_order")
     return perm
+
+
+# --- serving the packed layers -------------------------------------------------------------------------------------
+# These calls are short (a few microseconds on the GPU for single tokens), so their marshalling is kept to plain
+# integers: addresses and the stream handle go to ctypes as they are.
+
+_DTYPES = {torch.float32: GPTQ_DTYPE_F32, torch.bfloat16: GPTQ_DTYPE_BF16}
+
+
+def _device_tensor(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) -> int:
+    """The address of a contiguous tensor of this dtype on this device."""
+    if t.dtype != dtype or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _rows_of(t: torch.Tensor, name: str, device=None) -> int:
+    """The leading dimension of a 2-D tensor of rows with unit column stride, on the GPU."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on the GPU of the other tensors")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _handle(device, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _scratch(need: int, device, workspace: Optional[torch.Tensor]):
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError("workspace must be on the GPU of the other tensors")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gptq_matmul_workspace_bytes(dtype: torch.dtype, M: int, K: int, N: int, experts: int = 1, rank: int = 0) -> int:
+    """Bytes of workspace of gptq_expert_matmul and gptq_adapter_matmul; 0 for sizes that they refuse."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return int(load().gptq_matmul_workspace_bytes(_DTYPES[dtype], int(M), int(K), int(N), int(experts), int(rank)))
+
+
+def gptq_route(logits: torch.Tensor, topk: int, renorm: bool = False, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> dict:
+    """The topk experts of every token (logits T x E, fp32 or bf16) and the rows of every expert.
+
+    Returns dict(weights fp32[T, topk], experts int32[T, topk], offsets int32[E + 1], rows int32[T * topk], positions
+    int32[T, topk]).  Stream-ordered: a NaN or +infinity logit is latched in `workspace` (gptq_device_status).
+    """
+    ld = _rows_of(logits, "logits")
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {logits.dtype}")
+    T, E = logits.shape
+    dev, topk = logits.device, int(topk)
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
+    lib = load()
+    n = T * topk
+    ints = torch.empty(3 * n + E + 1, dtype=torch.int32, device=dev)      # experts, positions, rows, offsets
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    need = 0 if workspace is not None else gptq_workspace_bytes(GPTQ_CALL_ROUTE, E, 0, T)
+    workspace, wp, wb = _scratch(need, dev, workspace)
+    at = ints.data_ptr()
+    _check(lib.gptq_route(logits.data_ptr(), dt, T, E, ld, topk, GPTQ_FLAG_RENORM if renorm else 0, weights.data_ptr(),
+                          at, at + 12 * n, at + 8 * n, at + 4 * n, wp, wb, _handle(dev, stream)), "gptq_route")
+    return {"weights": weights, "experts": ints[:n].view(T, topk), "offsets": ints[3 * n:], "rows": ints[2 * n:3 * n],
+            "positions": ints[n:2 * n].view(T, topk)}
+
+
+def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor, bits: int,
+                       rows: Optional[torch.Tensor] = None, groupsize: int = 0, swiglu: bool = False,
+                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """out[r] = X[rows[r]] W_e for the rows r of expert e, [offsets[e], offsets[e + 1]); W_e from packed codes.
+
+    X: rows x K (fp32 or bf16).  packed: int32 E x words x N (gptq_pack_codes per expert).  scales: fp32 E x N, or
+    E x groups x N with groupsize.  rows: int32[M], None for M = len(X) rows as they are.  swiglu: out is M x N / 2,
+    silu(first half) * second half.
+    """
+    dt = _DTYPES.get(X.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {X.dtype}")
+    ldx = _rows_of(X, "X")
+    dev, (x_rows, K) = X.device, X.shape
+    if packed.dim() != 3 or packed.dtype != torch.int32 or packed.stride(2) != 1 or packed.device != dev:
+        raise ValueError("packed must be int32 E x words x N on the GPU of X, with unit channel stride")
+    E, nw, N = packed.shape
+    if nw != (K * int(bits) + 31) // 32:
+        raise ValueError(f"packed has {nw} words per channel, not those of {K} codes of {bits} bits")
+    groups = -(-K // groupsize) if groupsize > 0 else 1
+    if scales.numel() != E * groups * N or scales.shape[0] != E or scales.shape[-1] != N:
+        raise ValueError("scales must be E x N, or E x groups x N with groupsize")
+    sp = _device_tensor(scales, "scales", torch.float32, dev)
+    op = _device_tensor(offsets, "offsets", torch.int32, dev)
+    if offsets.numel() != E + 1:
+        raise ValueError("offsets must hold E + 1 entries")
+    rp, M = None, x_rows
+    if rows is not None:
+        rp, M = _device_tensor(rows, "rows", torch.int32, dev), rows.numel()
+    width = N // 2 if swiglu else N
+    if out is None:
+        out = torch.empty(M, width, dtype=X.dtype, device=dev)
+    elif out.shape != (M, width) or out.dtype != X.dtype:
+        raise ValueError(f"out must be {M} x {width} of X's dtype")
+    ldy = _rows_of(out, "out", dev)
+    lib = load()
+    need = 0 if workspace is not None else lib.gptq_matmul_workspace_bytes(dt, M, K, N, E, 0)
+    workspace, wp, wb = _scratch(need, dev, workspace)
+    _check(lib.gptq_expert_matmul(X.data_ptr(), dt, x_rows, ldx, rp, M, op, E, packed.data_ptr(), packed.stride(1),
+                                  packed.stride(0), K, N, bits, sp, groups * N, groupsize,
+                                  GPTQ_FLAG_SWIGLU if swiglu else 0, out.data_ptr(), ldy, wp, wb,
+                                  _handle(dev, stream)), "gptq_expert_matmul")
+    return out
+
+
+def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, bits: int, groupsize: int = 0,
+                        A: Optional[torch.Tensor] = None, B: Optional[torch.Tensor] = None,
+                        alpha: Optional[torch.Tensor] = None, requests: Optional[torch.Tensor] = None,
+                        adapter: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out = X W, plus alpha_a B_a (A_a x) for the rows of the requests with adapter a; W from packed codes.
+
+    X: M x K (fp32 or bf16).  packed: int32 words x N.  scales: fp32 N, or groups x N with groupsize.  A: bf16
+    adapters x rank x K, B: bf16 adapters x N x rank, alpha: fp32[adapters].  requests: int32[R + 1] row offsets,
+    adapter: int32[R] (-1: none).  Without A the plain product.
+    """
+    dt = _DTYPES.get(X.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {X.dtype}")
+    ldx = _rows_of(X, "X")
+    dev, (M, K) = X.device, X.shape
+    if packed.dim() != 2 or packed.dtype != torch.int32 or packed.stride(1) != 1 or packed.device != dev:
+        raise ValueError("packed must be int32 words x N on the GPU of X, with unit channel stride")
+    nw, N = packed.shape
+    if nw != (K * int(bits) + 31) // 32:
+        raise ValueError(f"packed has {nw} words per channel, not those of {K} codes of {bits} bits")
+    groups = -(-K // groupsize) if groupsize > 0 else 1
+    if scales.numel() != groups * N or scales.shape[-1] != N:
+        raise ValueError("scales must be N, or groups x N with groupsize")
+    sp = _device_tensor(scales, "scales", torch.float32, dev)
+    n_adapters = n_requests = rank = lda = a_stride = ldb = b_stride = 0
+    ap = bp = lp = qp = ip = None
+    if A is not None:
+        if B is None or alpha is None or requests is None or adapter is None:
+            raise ValueError("adapters need A, B, alpha, requests and adapter")
+        n_adapters, rank = A.shape[0], A.shape[1]
+        if A.dim() != 3 or A.shape[2] != K or A.dtype != torch.bfloat16 or A.stride(2) != 1 or A.device != dev:
+            raise ValueError("A must be bf16 adapters x rank x K with unit stride along K")
+        if B.shape != (n_adapters, N, rank) or B.dtype != torch.bfloat16 or B.device != dev or \
+                (rank > 1 and B.stride(2) != 1):
+            raise ValueError("B must be bf16 adapters x N x rank with unit stride along the rank")
+        ap, lda, a_stride = A.data_ptr(), max(A.stride(1), K), A.stride(0)
+        bp, ldb, b_stride = B.data_ptr(), max(B.stride(1), rank), B.stride(0)
+        lp = _device_tensor(alpha, "alpha", torch.float32, dev)
+        qp = _device_tensor(requests, "requests", torch.int32, dev)
+        ip = _device_tensor(adapter, "adapter", torch.int32, dev)
+        n_requests = adapter.numel()
+        if alpha.numel() != n_adapters or requests.numel() != n_requests + 1:
+            raise ValueError("alpha must hold one entry per adapter, requests one more than adapter")
+        if n_adapters == 0 or n_requests == 0:
+            rank = 0
+    if out is None:
+        out = torch.empty(M, N, dtype=X.dtype, device=dev)
+    elif out.shape != (M, N) or out.dtype != X.dtype:
+        raise ValueError(f"out must be {M} x {N} of X's dtype")
+    ldy = _rows_of(out, "out", dev)
+    lib = load()
+    need = 0 if workspace is not None else lib.gptq_matmul_workspace_bytes(dt, M, K, N, 1, rank)
+    workspace, wp, wb = _scratch(need, dev, workspace)
+    _check(lib.gptq_adapter_matmul(X.data_ptr(), dt, M, ldx, packed.data_ptr(), packed.stride(0), K, N, bits, sp,
+                                   groupsize, ap, lda, a_stride, bp, ldb, b_stride, lp, n_adapters, rank, qp, ip,
+                                   n_requests, out.data_ptr(), ldy, wp, wb, _handle(dev, stream)),
+           "gptq_adapter_matmul")
+    return out
+
+
+def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] Y[positions[t, j]] in fp32; positions outside Y's rows are left out."""
+    dt = _DTYPES.get(Y.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {Y.dtype}")
+    ldy = _rows_of(Y, "Y")
+    dev, (M, N) = Y.device, Y.shape
+    if positions.dim() != 2 or positions.shape != weights.shape:
+        raise ValueError("positions and weights must both be T x topk")
+    pp = _device_tensor(positions, "positions", torch.int32, dev)
+    wp = _device_tensor(weights, "weights", torch.float32, dev)
+    T, topk = positions.shape
+    if out is None:
+        out = torch.empty(T, N, dtype=Y.dtype, device=dev)
+    elif out.shape != (T, N) or out.dtype != Y.dtype:
+        raise ValueError(f"out must be {T} x {N} of Y's dtype")
+    ldo = _rows_of(out, "out", dev)
+    _check(load().gptq_combine(Y.data_ptr(), dt, M, ldy, pp, wp, T, topk, N, out.data_ptr(), ldo,
+                               _handle(dev, stream)), "gptq_combine")
+    return out

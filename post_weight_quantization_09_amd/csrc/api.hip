@@ -10,6 +10,7 @@
 #include "pack.hpp"
 #include "hadamard.hpp"
 #include "act_order.hpp"
+#include "route.hpp"
 #include "timer.hpp"
 
 using namespace gptq;
@@ -151,6 +152,7 @@ size_t gptq_workspace_bytes(gptq_call_t call, int64_t K, int64_t N, int64_t M, u
         case GPTQ_CALL_PREPARE: return prepare_workspace_bytes(K, N);   // N: Hessians of gptq_prepare_groups
         case GPTQ_CALL_ASYM_CORRECTION: return asym_ws(K);
         case GPTQ_CALL_ACT_ORDER: return K > 0 ? act_order_workspace_bytes(K) : 0;
+        case GPTQ_CALL_ROUTE: return route_workspace_bytes(M, K);        // M tokens, K experts
         case GPTQ_CALL_QUANTIZE_LAYER:
             // M: the output-channel groups of gptq_quantize_layer_groups (0 or 1: one)
             return quantize_workspace_bytes(K, N, (flags & 2u) != 0, (flags & GPTQ_FLAG_CAE) != 0, std::max<int64_t>(M, 1));

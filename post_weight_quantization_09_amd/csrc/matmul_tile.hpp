@@ -1,0 +1,268 @@
+// Product of many rows with packed weights: a prompt's rows, an expert with many rows.
+//
+// What bounds it: the matrix cores (2 M K N operations against half a byte per weight).  One workgroup of four waves owns
+// TM rows of one expert and 256 channels; every wave holds its own 64 channels for all TM rows, so no code is converted
+// twice in a workgroup: the words of a 128-k chunk come straight from global memory into registers as operands (nothing
+// of the weights passes through LDS) and serve TM / 16 row tiles.  The rows are laid out once per call by
+// stage_rows_kernel: octets of k in the converted operand's order, [K / 8][row], so that a chunk is 16 contiguous
+// pieces, copied to LDS by DMA and read back as 16-byte operands without bank conflicts; rows are gathered and fp32 rows
+// split in the same pass, and it leaves the row sums that take the codes' excess off again as the accumulators' start (bf16 rows).
+#pragma once
+
+#include "matmul_rows.hpp"
+
+namespace gptq {
+
+typedef __attribute__((address_space(3))) void lds_dma_t;
+
+constexpr int kTileCols = 256;         // channels of a workgroup (outputs: half of them when gated)
+constexpr int kTileGroup = 8;          // row tiles that neighbouring workgroups share a weight tile for
+
+// y += H B^T for the TM rows from r0 on: one product per run of rows with the same adapter.
+template <int PARTS, int RT, int NT, bool GATED>
+__device__ __forceinline__ void add_adapters(const MatmulKernelArgs& p, const LaneChannels<NT, GATED>& ch, int64_t r0,
+                                             int nrow, int lane, f32x4 (&acc)[RT][NT]) {
+    constexpr int HP = PARTS == 1 ? 2 : 3;
+    const int q = lane >> 4;
+    for (int f = 0; f < nrow;) {
+        const int a = __builtin_amdgcn_readfirstlane(p.row_adapter[r0 + f]);
+        int g = f + 1;                                // end of the run, 64 rows at a time
+        while (g < nrow) {
+            const int mine = g + lane < nrow ? p.row_adapter[r0 + g + lane] : -2;
+            const uint64_t other = __ballot(mine != a);
+            if (other) {
+                g += __builtin_ctzll(other);
+                break;
+            }
+            g += 64;
+        }
+        if (g > nrow) g = nrow;
+        if (a >= 0) {
+            for (int k = 0; k < p.rank; k += kStepK) {
+                const int kq = k + 8 * q;
+                bf16x8 b[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    u32x4 v[1] = {{0u, 0u, 0u, 0u}};
+                    if (kq < p.rank)
+                        load_octet<1>(p.B + a * p.b_stride + ch.channel(j) * p.ldb, kq, p.rank, p.bvec, v);
+                    b[j] = __builtin_bit_cast(bf16x8, v[0]);
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    if (16 * t < g && 16 * t + 16 > f) {
+                        const int row = 16 * t + (lane & 15);
+                        float hv[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) hv[i] = 0.f;
+                        if (row >= f && row < g && kq < p.rank) {
+                            const float* h = p.H + (r0 + row) * p.hrank + kq;
+                            const f32x4 u = reinterpret_cast<const f32x4*>(h)[0];
+                            const f32x4 v = reinterpret_cast<const f32x4*>(h)[1];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) { hv[i] = u[i]; hv[4 + i] = v[i]; }
+                        }
+                        u32x4 hp[3];
+                        split3(hv, hp);
+#pragma unroll
+                        for (int i = 0; i < HP; ++i)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) acc[t][j] = mfma16(hp[i], b[j], acc[t][j]);
+                    }
+                }
+            }
+        }
+        f = g;
+    }
+}
+
+template <int BITS, int PARTS, int RT, int GS, bool GATED>
+__global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(MatmulKernelArgs p, int ntn, int ntm) {
+    constexpr int NT = 4, TM = 16 * RT, kGroups = kChunkSteps / GS;
+    constexpr int kOctets = kChunkK / 8;
+    __shared__ __attribute__((aligned(1024))) uint16_t xs[2][PARTS][kOctets][TM][8];
+    __shared__ __attribute__((aligned(1024))) float ss[2][kGroups][PARTS == 1 ? TM : 1];
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // Workgroup b runs on XCD b % 8: each XCD takes a contiguous share of an order in which kTileGroup row tiles sweep
+    // the channels together, so that the tiles in flight on one XCD share rows and words in its L2.
+    const int total = ntn * ntm, share = (total + 7) / 8;
+    const int lin = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= share || lin >= total) return;
+    const int grp = lin / (kTileGroup * ntn), in_grp = lin - grp * kTileGroup * ntn;
+    const int gm = min(kTileGroup, ntm - grp * kTileGroup);
+    const int tm = grp * kTileGroup + in_grp % gm, tn = in_grp / gm;
+
+    const int e = p.tiles[3 * tm];
+    if (e < 0) return;
+    const int64_t r0 = p.tiles[3 * tm + 1], r1 = p.tiles[3 * tm + 2];
+    constexpr int kRun = LaneChannels<NT, GATED>::kRun;
+    const int64_t col0 = (int64_t)tn * (64 * kRun) + wave * (16 * kRun);
+    const int64_t width = GATED ? p.N / 2 : p.N;
+    const LaneChannels<NT, GATED> ch(col0, lane, p.N);
+    if (e == p.E) {                                  // rows of no expert
+        float z[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) z[j] = 0.f;
+        for (int64_t r = r0 + q; r < r1; r += 4) store_values<PARTS, kRun>(p.Y, r * p.ldy + ch.c0, z);
+        return;
+    }
+    const uint32_t* words = p.packed + e * p.p_stride;
+    const float* scales = p.scales + e * p.s_stride;
+    const int nchunks = (int)((p.K + kChunkK - 1) / kChunkK);
+    const int last_word = p.nwords - 1;
+    const int wa = lane_word<BITS>(q), wb = lane_word2<BITS>(q), sh = lane_shift<BITS>(q);
+    constexpr int kLW = kLaneWords<BITS>;
+    const int64_t last_group = (p.K - 1) / (kStepK * GS);
+
+    uint32_t w[kChunkSteps][kLW][NT];
+    float sc[kGroups][NT], s_ch[NT];
+    auto load_words = [&](int chunk) {
+#pragma unroll
+        for (int s = 0; s < kChunkSteps; ++s) {
+            const int at = (chunk * kChunkSteps + s) * BITS;
+            ch.words(words + (int64_t)min(at + wa, last_word) * p.ldp, w[s][0]);
+            if constexpr (kLW == 2) ch.words(words + (int64_t)min(at + wb, last_word) * p.ldp, w[s][1]);
+        }
+        if (!p.per_channel) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                int64_t at = (int64_t)chunk * kGroups + g;
+                at = at < last_group ? at : last_group;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sc[g][j] = scales[at * p.N + ch.channel(j)];
+            }
+        }
+    };
+    const int64_t noct = (int64_t)nchunks * kOctets;
+    constexpr int kRowPieces = TM / 64;              // 64 rows of 16 bytes per DMA instruction
+    constexpr int kPieces = PARTS * kOctets * kRowPieces;
+    auto stage = [&](int chunk, int buf) {
+#pragma unroll
+        for (int i = 0; i < kPieces / 4; ++i) {
+            const int pc = wave * (kPieces / 4) + i;
+            const int part = pc / (kOctets * kRowPieces), rest = pc % (kOctets * kRowPieces);
+            const int o = rest / kRowPieces, h = rest % kRowPieces;
+            const uint16_t* src =
+                p.XT + ((part * noct + (int64_t)chunk * kOctets + o) * p.Mp + r0 + 64 * h + lane) * 8;
+            __builtin_amdgcn_global_load_lds((const void*)src, (lds_dma_t*)&xs[buf][part][o][64 * h][0], 16, 0, 0);
+        }
+        constexpr int kSumPieces = PARTS == 1 ? kGroups * kRowPieces : 0;
+#pragma unroll
+        for (int i = 0; i < (kSumPieces + 3) / 4; ++i) {
+            const int pc = wave + 4 * i;
+            if (pc < kSumPieces) {
+                const int g = pc / kRowPieces, h = pc % kRowPieces;
+                const float* src = p.sums + ((int64_t)chunk * kGroups + g) * p.Mp + r0 + 64 * h + lane;
+                __builtin_amdgcn_global_load_lds((const void*)src, (lds_dma_t*)&ss[buf][g][PARTS == 1 ? 64 * h : 0], 4, 0, 0);
+            }
+        }
+    };
+
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (p.per_channel) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s_ch[j] = scales[ch.channel(j)];
+    }
+    stage(0, 0);
+    load_words(0);
+    if (p.H) add_adapters<PARTS, RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
+
+    for (int c = 0; c < nchunks; ++c) {
+        const int buf = c & 1;
+        // this chunk's rows are in LDS for every wave, and every wave has left the other buffer
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        bf16x8 b[kChunkSteps][NT];
+#pragma unroll
+        for (int s = 0; s < kChunkSteps; ++s)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                b[s][j] = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh)
+                                     : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh);
+        float f[kGroups][NT];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) f[g][j] = p.per_channel ? s_ch[j] : sc[g][j];
+        if (c + 1 < nchunks) {
+            stage(c + 1, buf ^ 1);
+            load_words(c + 1);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                f32x4 start = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (PARTS == 1) start = *reinterpret_cast<const f32x4*>(&ss[buf][g][16 * t + 4 * q]);
+                f32x4 prt[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) prt[j] = start;
+#pragma unroll
+                for (int s = g * GS; s < (g + 1) * GS; ++s)
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        const u32x4 a =
+                            *reinterpret_cast<const u32x4*>(&xs[buf][i][4 * s + q][16 * t + (lane & 15)][0]);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) prt[j] = mfma16(a, b[s][j], prt[j]);
+                    }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(f[g][j], prt[j][i], acc[t][j][i]);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = r0 + 16 * t + 4 * q + i;
+            if (r < r1) {
+                const bool real = source_row(p, r) >= 0;
+                float o[kRun];
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) {
+                    o[j] = acc[t][j][i];
+                    if constexpr (GATED) o[j] = gated(acc[t][j][i], acc[t][kRun + j][i]);
+                    o[j] = real ? o[j] : 0.f;
+                }
+                store_values<PARTS, kRun>(p.Y, r * p.ldy + ch.c0, o);
+            }
+        }
+}
+
+template <int BITS, int PARTS, int RT>
+hipError_t launch_tile_rt(const MatmulKernelArgs& k, int ntm, bool swiglu, hipStream_t stream) {
+    const int64_t width = swiglu ? k.N / 2 : k.N;
+    const int ntn = (int)ceil_div(width, swiglu ? kTileCols / 2 : kTileCols);
+    const unsigned grid = (unsigned)(ceil_div((int64_t)ntn * ntm, 8) * 8);
+#define GPTQ_TILE(GS, GATED) \
+    hipLaunchKernelGGL((matmul_tile_kernel<BITS, PARTS, RT, GS, GATED>), dim3(grid), dim3(256), 0, stream, k, ntn, ntm)
+    if (swiglu) {
+        if (k.group_steps == 1) GPTQ_TILE(1, true);
+        else if (k.group_steps == 2) GPTQ_TILE(2, true);
+        else GPTQ_TILE(4, true);
+    } else {
+        if (k.group_steps == 1) GPTQ_TILE(1, false);
+        else if (k.group_steps == 2) GPTQ_TILE(2, false);
+        else GPTQ_TILE(4, false);
+    }
+#undef GPTQ_TILE
+    return hipGetLastError();
+}
+
+template <int BITS>
+hipError_t launch_tile(const MatmulKernelArgs& k, bool f32, int row_tiles, int ntm, bool swiglu, hipStream_t stream) {
+    if (f32) return launch_tile_rt<BITS, 3, 4>(k, ntm, swiglu, stream);
+    if (row_tiles <= 4) return launch_tile_rt<BITS, 1, 4>(k, ntm, swiglu, stream);
+    return launch_tile_rt<BITS, 1, 8>(k, ntm, swiglu, stream);
+}
+
+}  // namespace gptq
