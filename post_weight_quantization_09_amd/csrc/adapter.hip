@@ -19,7 +19,6 @@ constexpr int kShrinkWaves = 8;
 struct ShrinkArgs {
     const void* X;
     int64_t ldx, M, K;
-    int xvec, avec;
     const uint16_t* A;
     int64_t lda, a_stride;
     const float* alpha;
@@ -72,10 +71,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(ShrinkArgs p)
 #pragma unroll 4
         for (int64_t k = wave * kStepK; k < p.K; k += kShrinkWaves * kStepK) {
             u32x4 x[PARTS], b[1];
-            load_octet<PARTS>(xrow, k + 8 * q, p.K, p.xvec, x);
+            load_octet<PARTS>(xrow, k + 8 * q, p.K, x);
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                load_octet<1>(arow[n], k + 8 * q, p.K, p.avec, b);
+                load_octet<1>(arow[n], k + 8 * q, p.K, b);
 #pragma unroll
                 for (int i = 0; i < PARTS; ++i) acc[n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[n]);
             }
@@ -97,15 +96,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(ShrinkArgs p)
     }
 }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 }  // namespace
 
 hipError_t adapter_shrink(const MatmulArgs& a, float* H, int hrank, int32_t* row_adapter, hipStream_t stream) {
     ShrinkArgs p;
     p.X = a.X; p.ldx = a.ldx; p.M = a.M; p.K = a.K;
-    p.xvec = aligned16(a.X) && a.ldx % (a.f32 ? 4 : 8) == 0;
-    p.avec = aligned16(a.A) && a.lda % 8 == 0 && a.a_stride % 8 == 0;
     p.A = a.A; p.lda = a.lda; p.a_stride = a.a_stride;
     p.alpha = a.alpha; p.n_adapters = a.n_adapters;
     p.rank = a.rank; p.hrank = hrank;

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void stage_rows_kernel(MatmulKernelArgs p, uin
         const int64_t s = r < p.M ? source_row(p, r) : -1;
         if (s >= 0)
             load_octet<PARTS>(static_cast<const char*>(p.X) + s * p.ldx * (PARTS == 1 ? 2 : 4),
-                              (int64_t)chunk * kChunkK + 8 * o, p.K, p.vec, part);
+                              (int64_t)chunk * kChunkK + 8 * o, p.K, part);
         float sum = 0.f;
 #pragma unroll
         for (int d = 0; d < 4; ++d) sum += bf16lo_to_f32(part[0][d]) + bf16hi_to_f32(part[0][d]);
@@ -108,6 +108,18 @@ __global__ __launch_bounds__(256) void stage_rows_kernel(MatmulKernelArgs p, uin
         for (int o = 0; o < 4 * p.group_steps; ++o) s += os[g * 4 * p.group_steps + o][row];
         sums[((int64_t)chunk * groups + g) * p.Mp + r0 + row] = excess * s;
     }
+}
+
+// Z = H B^T for many rows of short requests (single tokens beside each other): one thread per row and four channels.
+__global__ __launch_bounds__(256) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
+    const int lane = threadIdx.x & 63;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), c0 = ((int64_t)blockIdx.y * 64 + lane) * 4;
+    if (r >= p.M || c0 >= p.N) return;
+    LaneChannels<4, false> ch(0, 0, p.N);
+    ch.c0 = c0 < p.N - 4 ? c0 : p.N - 4;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    add_adapter_row<4, false>(p, r, ch, y);
+    *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{y[0], y[1], y[2], y[3]};
 }
 
 // Rows an expert is expected to have; the kernels hold for any split, this only chooses.
@@ -150,47 +162,57 @@ struct Buffers {
     float* sums;
     int32_t* tiles;
     size_t bytes;
-    Buffers(const Plan& p, int64_t M, void* ws) {
+    float* Z;
+    Buffers(const Plan& p, int64_t M, int64_t N, void* ws) {
         Carver c(ws);
         H = p.hrank ? c.take<float>((size_t)M * p.hrank) : nullptr;
         row_adapter = p.hrank ? c.take<int32_t>((size_t)M) : nullptr;
         XT = p.tiles ? c.take<uint16_t>(p.xt_elems) : nullptr;
         sums = p.tiles ? c.take<float>(p.sum_floats) : nullptr;
         tiles = p.tiles ? c.take<int32_t>(3 * (size_t)p.cap) : nullptr;
+        Z = p.tiles && p.hrank ? c.take<float>((size_t)M * N) : nullptr;
         bytes = c.bytes();
     }
 };
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// A tile takes one small product per run of rows with the same adapter: about 1 us each, against M N fp32 values written
+// and read again for Z.  Runs of 32 rows and more (prompts) go the first way, single tokens the second.
+bool short_requests(int64_t M, int64_t n_requests) { return M < 32 * n_requests; }
 
 }  // namespace
 
 size_t matmul_workspace_bytes(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank) {
-    return Buffers(make_plan(f32, M, K, N, experts, rank), M, nullptr).bytes;
+    return Buffers(make_plan(f32, M, K, N, experts, rank), M, N, nullptr).bytes;
 }
 
 hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t stream) {
     const bool lora = a.n_requests > 0 && a.n_adapters > 0;
     const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0);
-    const Buffers buf(plan, a.M, workspace);
+    const Buffers buf(plan, a.M, a.N, workspace);
     MatmulKernelArgs k;
     k.X = a.X; k.ldx = a.ldx; k.x_rows = a.x_rows; k.rows = a.rows; k.M = a.M;
     k.offsets = a.offsets; k.E = a.E;
-    k.vec = aligned16(a.X) && a.ldx % (a.f32 ? 4 : 8) == 0;
     k.packed = a.packed; k.ldp = a.ldp; k.p_stride = a.p_stride; k.K = a.K; k.N = a.N;
     k.nwords = (int)((a.K * a.bits + 31) / 32);
     k.scales = a.scales; k.s_stride = a.s_stride;
     k.group_steps = a.groupsize ? a.groupsize / kStepK : kChunkSteps;
-    k.per_channel = a.groupsize == 0;
+    k.s_row = a.groupsize ? a.N : 0;
+    k.last_group = a.groupsize ? (a.K - 1) / a.groupsize : 0;
     k.Y = a.Y; k.ldy = a.ldy;
     k.H = lora ? buf.H : nullptr;
     k.hrank = plan.hrank; k.row_adapter = buf.row_adapter;
     k.B = a.B; k.ldb = a.ldb; k.b_stride = a.b_stride; k.rank = a.rank;
-    k.bvec = aligned16(a.B) && a.ldb % 8 == 0 && a.b_stride % 8 == 0;
+    k.Z = lora && plan.tiles && short_requests(a.M, a.n_requests) ? buf.Z : nullptr;
     k.XT = buf.XT; k.sums = buf.sums; k.Mp = plan.Mp; k.tiles = buf.tiles;
     if (lora) {
         const hipError_t e = adapter_shrink(a, buf.H, plan.hrank, buf.row_adapter, stream);
         if (e != hipSuccess) return e;
+        if (k.Z) {
+            const dim3 grid((unsigned)ceil_div(a.M, 4), (unsigned)ceil_div(a.N, 256));
+            hipLaunchKernelGGL(adapter_expand_kernel, grid, dim3(256), 0, stream, k, buf.Z);
+            const hipError_t x = hipGetLastError();
+            if (x != hipSuccess) return x;
+        }
     }
     if (plan.tiles) {
         const dim3 grid((unsigned)ceil_div(a.M, 64), (unsigned)plan.nchunks);

@@ -48,24 +48,25 @@ struct MatmulKernelArgs {
     int64_t M;
     const int32_t* offsets;
     int E;
-    int vec;                               // rows of X may be read in 16-byte pieces
     const uint32_t* packed;
     int64_t ldp, p_stride;
     int64_t K, N;
     int nwords;                            // words per channel
     const float* scales;
     int64_t s_stride;
-    int group_steps;                       // MFMA steps per scale (1, 2, 4)
-    int per_channel;
+    int group_steps;                       // MFMA steps per scale (1, 2, 4; per channel 4)
+    int64_t s_row;                         // floats from one group's scales to the next (per channel 0)
+    int64_t last_group;
     void* Y;
     int64_t ldy;
     // adapters: H = alpha A x of every row, M x hrank fp32, and the adapter of every row (-1: none)
     const float* H;
     int hrank;
     const int32_t* row_adapter;
+    const float* Z;                        // H B^T, M x N, where the tile kernel is given it ready; else nullptr
     const uint16_t* B;
     int64_t ldb, b_stride;
-    int rank, bvec;
+    int rank;
     // rows laid out for the tile kernel: PARTS x [K / 8][Mp] octets, and -1.5 2^b sums of x per row and group
     const uint16_t* XT;
     const float* sums;

@@ -117,11 +117,55 @@ struct LaneChannels {
         }
     }
     __device__ __forceinline__ int64_t channel(int j) const { return j < kRun ? c0 + j : half + c0 + (j - kRun); }
+    __device__ __forceinline__ void scales(const float* row, float (&s)[NT]) const {
+        uint32_t u[NT];
+        words(reinterpret_cast<const uint32_t*>(row), u);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j] = __uint_as_float(u[j]);
+    }
 };
 
-template <int BITS, int PARTS, int MT, int NT, bool GATED, int W>
-__global__ __launch_bounds__(64 * W) void matmul_rows_kernel(MatmulKernelArgs p) {
+// y[j] += sum_k H[r][k] B_a[channel j][k] for one row: the adapter's own term where a row stands for itself (single
+// tokens, each with an adapter of its own).
+template <int NT, bool GATED>
+__device__ __forceinline__ void add_adapter_row(const MatmulKernelArgs& p, int64_t r, const LaneChannels<NT, GATED>& ch,
+                                                float (&y)[NT]) {
+    const int a = p.row_adapter[r];
+    if (a < 0) return;
+    const float* h = p.H + r * p.hrank;
+    const uint16_t* B = p.B + a * p.b_stride;
+    const uint16_t* row[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) row[j] = B + ch.channel(j) * p.ldb;
+    const int whole = p.rank & ~7;
+#pragma unroll 2
+    for (int k = 0; k < whole; k += 8) {
+        const f32x4 u = *reinterpret_cast<const f32x4*>(h + k), v = *reinterpret_cast<const f32x4*>(h + k + 4);
+        u32x4 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const u32x4_a2*>(row[j] + k);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float h0 = d < 2 ? u[2 * d] : v[2 * d - 4], h1 = d < 2 ? u[2 * d + 1] : v[2 * d - 3];
+                y[j] = fmaf(h0, bf16lo_to_f32(b[j][d]), y[j]);
+                y[j] = fmaf(h1, bf16hi_to_f32(b[j][d]), y[j]);
+            }
+    }
+    for (int k = whole; k < p.rank; ++k)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) y[j] = fmaf(h[k], __uint_as_float((uint32_t)row[j][k] << 16), y[j]);
+}
+
+// FORM of a product: plain, gated pairs of channels, or plain with adapters.
+enum { kPlain = 0, kGated = 1, kAdapters = 2 };
+
+template <int BITS, int PARTS, int MT, int NT, int FORM, int W>
+__global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
+    constexpr bool GATED = FORM == kGated;
     constexpr int kVals = MT * 4;                    // (row tile, register) items of NT channels
+    constexpr int XR = MT * PARTS >= 4 ? 2 : 4;      // steps of rows in flight
     __shared__ float part[W][kVals * NT][64];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -138,30 +182,28 @@ __global__ __launch_bounds__(64 * W) void matmul_rows_kernel(MatmulKernelArgs p)
     if (lo >= hi) return;
 
     const LaneChannels<NT, GATED> ch(tile0, lane, p.N);
-    const uint32_t* words = p.packed + e * p.p_stride;
-    const float* scales = p.scales + e * p.s_stride;
-    const int nchunks = (int)((p.K + kChunkK - 1) / kChunkK);
-    const int last_word = p.nwords - 1;
-    const int wa = lane_word<BITS>(q), wb = lane_word2<BITS>(q), sh = lane_shift<BITS>(q);
+    const int nfull = (int)(p.K / kChunkK);          // whole chunks
+    const int sh = lane_shift<BITS>(q);
     constexpr int kLW = kLaneWords<BITS>;
-
-    auto load_words = [&](int chunk, uint32_t (&w)[kChunkSteps][kLW][NT]) {
+    constexpr int kXBytes = PARTS == 1 ? 2 : 4;
+    // words: a scalar base that moves with the step, and the lane's own 32-bit offsets
+    const uint32_t* words0 = p.packed + e * p.p_stride;
+    const int64_t step_words = BITS * p.ldp;
+    const uint32_t off[2] = {(uint32_t)(lane_word<BITS>(q) * p.ldp + ch.c0), (uint32_t)(lane_word2<BITS>(q) * p.ldp + ch.c0)};
+    const float* scales = p.scales + e * p.s_stride;
+    // NT words (or scales) of one row: at the lane's channels, gated ones N / 2 further too
+    auto load_pieces = [&](const uint32_t* base, uint32_t at, uint32_t (&v)[NT], int64_t row = 0) {
+        constexpr int R = LaneChannels<NT, GATED>::kRun;
+        uint32_t a[R];
+        WordLoad<R>::run(base + row + at, a);
 #pragma unroll
-        for (int s = 0; s < kChunkSteps; ++s) {
-            const int at = (chunk * kChunkSteps + s) * BITS;
-            const int a = min(at + wa, last_word);   // past the last word x is zero
-            ch.words(words + (int64_t)a * p.ldp, w[s][0]);
-            if constexpr (kLW == 2) {
-                const int b = min(at + wb, last_word);
-                ch.words(words + (int64_t)b * p.ldp, w[s][1]);
-            }
+        for (int j = 0; j < R; ++j) v[j] = a[j];
+        if constexpr (GATED) {
+            WordLoad<R>::run(base + ch.half + row + at, a);
+#pragma unroll
+            for (int j = 0; j < R; ++j) v[R + j] = a[j];
         }
     };
-    float s_ch[NT];
-    if (p.per_channel) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s_ch[j] = scales[ch.channel(j)];
-    }
 
     for (int64_t r0 = lo; r0 < hi; r0 += 16 * MT) {
         const char* xrow[MT];
@@ -169,127 +211,120 @@ __global__ __launch_bounds__(64 * W) void matmul_rows_kernel(MatmulKernelArgs p)
         for (int t = 0; t < MT; ++t) {
             int64_t r = r0 + 16 * t + (lane & 15);
             if (r >= hi) r = hi - 1;                 // a row past the end repeats the last one and is not stored
-            int64_t s = source_row(p, r);
-            xrow[t] = static_cast<const char*>(p.X) + (s < 0 ? 0 : s) * p.ldx * (PARTS == 1 ? 2 : 4);
+            const int64_t s = source_row(p, r);
+            xrow[t] = static_cast<const char*>(p.X) + ((s < 0 ? 0 : s) * p.ldx + 8 * q) * kXBytes;
         }
+        uint32_t w[kChunkSteps][kLW][NT];
+        uint32_t sc[kChunkSteps][NT];
+        RawOctet<PARTS> x[XR][MT];
+        // The chunks' loads: whole chunks from scalar bases, without a bound in sight; the layer's last k apart.
+        auto load_scales = [&](int step, int s) {
+            const int64_t g = step / p.group_steps;
+            const float* row = scales + (g < p.last_group ? g : p.last_group) * p.s_row;
+            load_pieces(reinterpret_cast<const uint32_t*>(row), (uint32_t)ch.c0, sc[s]);
+        };
+        auto load_words = [&](int chunk, int s) {
+            const int step = chunk * kChunkSteps + s;
+            const uint32_t* base = words0 + step * step_words;
+#pragma unroll
+            for (int l = 0; l < kLW; ++l) load_pieces(base, off[l], w[s][l]);
+            if (((s + 1) & (p.group_steps - 1)) == 0) load_scales(step, s);
+        };
+        auto load_x = [&](int chunk, int s) {
+            const int64_t k = ((int64_t)chunk * kChunkSteps + s) * kStepK;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) x[s % XR][t].whole(xrow[t] + k * kXBytes);
+        };
+
         f32x4 acc[MT][NT];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-        // y += H B^T of the rows' adapters: the runs of equal adapters among the tile's rows, dealt out to the waves
-        if (p.H) {
-            constexpr int HP = PARTS == 1 ? 2 : 3;   // parts of H: its error stays far below the output's rounding
+        f32x4 sum[MT], prt[MT][NT];
+        auto multiply = [&](int s) {                 // step s of the chunk in w, x, sc
+            if ((s & (p.group_steps - 1)) == 0) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) prt[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+            u32x4 a[MT][PARTS];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const int64_t t0 = r0 + 16 * t;
-                if (t0 >= hi) break;
-                const int nrow = (int)(hi - t0 < 16 ? hi - t0 : 16);
-                const int mine = (lane & 15) < nrow ? p.row_adapter[t0 + (lane & 15)] : -1;
-                for (int f = 0, run = t; f < nrow; ++run) {
-                    const int a = __builtin_amdgcn_readlane(mine, f);
-                    int g = f + 1;
-                    while (g < nrow && __builtin_amdgcn_readlane(mine, g) == a) ++g;
-                    if (a >= 0 && run % W == wave) {
-                        const bool in = (lane & 15) >= f && (lane & 15) < g;
-                        const float* h = p.H + (t0 + (lane & 15)) * p.hrank;
-                        for (int k = 0; k < p.rank; k += kStepK) {
-                            float hv[8];
+                x[s % XR][t].parts(a[t]);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) hv[i] = 0.f;
-                            const int kq = k + 8 * q;
-                            if (in && kq < p.rank) {
-                                const f32x4 u = *reinterpret_cast<const f32x4*>(h + kq);
-                                const f32x4 v = *reinterpret_cast<const f32x4*>(h + kq + 4);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) { hv[i] = u[i]; hv[4 + i] = v[i]; }
-                            }
-                            u32x4 hp[3];
-                            split3(hv, hp);
-#pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                u32x4 b[1] = {{0u, 0u, 0u, 0u}};
-                                if (kq < p.rank)
-                                    load_octet<1>(p.B + a * p.b_stride + ch.channel(j) * p.ldb, kq, p.rank, p.bvec, b);
-#pragma unroll
-                                for (int i = 0; i < HP; ++i)
-                                    acc[t][j] = mfma16(hp[i], __builtin_bit_cast(bf16x8, b[0]), acc[t][j]);
-                            }
-                        }
-                    }
-                    f = g;
-                }
+                for (int i = 0; i < PARTS; ++i) a[t][i] = pair_order(a[t][i]);
             }
-        }
-
-        uint32_t w[kChunkSteps][kLW][NT];
-        if (wave < nchunks) load_words(wave, w);
-        for (int c = wave; c < nchunks; c += W) {
-            // this chunk's rows
-            u32x4 x[kChunkSteps][MT][PARTS];
+            if constexpr (PARTS == 1) {
 #pragma unroll
-            for (int s = 0; s < kChunkSteps; ++s)
+                for (int t = 0; t < MT; ++t) sum[t] = mfma16(a[t][0], minus_excess_frag<BITS>(), sum[t]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh)
+                                            : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
-                    load_octet<PARTS>(xrow[t], (int64_t)c * kChunkK + s * kStepK + 8 * q, p.K, p.vec, x[s][t]);
-            uint32_t wn[kChunkSteps][kLW][NT];
-            if (c + W < nchunks) load_words(c + W, wn);
-            f32x4 sum[MT], prt[MT][NT];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) prt[t][j] = mfma16(a[t][i], b, prt[t][j]);
+            }
+            if (((s + 1) & (p.group_steps - 1)) == 0) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[t][j][i] = fmaf(__uint_as_float(sc[s][j]), prt[t][j][i] + sum[t][i], acc[t][j][i]);
+            }
+        };
+        if (wave < nfull) {
+#pragma unroll
+            for (int s = 0; s < XR; ++s) load_x(wave, s);
+#pragma unroll
+            for (int s = 0; s < kChunkSteps; ++s) load_words(wave, s);
+        }
+        int c = wave;
+        for (; c + W < nfull; c += W) {
 #pragma unroll
             for (int s = 0; s < kChunkSteps; ++s) {
-                if ((s & (p.group_steps - 1)) == 0) {
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) prt[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    }
-                }
-                bf16x8 b[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    b[j] = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh)
-                                      : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh);
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        const u32x4 a = pair_order(x[s][t][i]);
-                        if constexpr (PARTS == 1) sum[t] = mfma16(a, minus_excess_frag<BITS>(), sum[t]);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) prt[t][j] = mfma16(a, b[j], prt[t][j]);
-                    }
-                if (((s + 1) & (p.group_steps - 1)) == 0) {
-                    float sc[NT];
-                    if (p.per_channel) {
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) sc[j] = s_ch[j];
-                    } else {
-                        const int64_t g = ((int64_t)c * kChunkSteps + s) / p.group_steps;
-                        const int64_t last = (p.K - 1) / (kStepK * p.group_steps);
-                        const float* srow = scales + (g < last ? g : last) * p.N;
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) sc[j] = srow[ch.channel(j)];
-                    }
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[t][j][i] = fmaf(sc[j], prt[t][j][i] + sum[t][i], acc[t][j][i]);
-                }
+                multiply(s);
+                load_x(s + XR < kChunkSteps ? c : c + W, (s + XR) % kChunkSteps);
+                load_words(c + W, s);
             }
+        }
+        if (c < nfull) {
 #pragma unroll
-            for (int s = 0; s < kChunkSteps; ++s)
+            for (int s = 0; s < kChunkSteps; ++s) {
+                multiply(s);
+                if (s + XR < kChunkSteps) load_x(c, s + XR);
+            }
+            c += W;
+        }
+        if (nfull * kChunkK < p.K && nfull % W == wave) {       // the rest of K: past its end x is zero
+            const int last = p.nwords - 1;
+            int step0 = nfull * kChunkSteps;
+            asm volatile("" : "+s"(step0));          // keeps this part's addresses from being computed ahead of the loop
 #pragma unroll
-                for (int l = 0; l < kLW; ++l)
+            for (int s = 0; s < kChunkSteps; ++s) {
+                const int step = step0 + s;
+                const int64_t k = (int64_t)step * kStepK;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) w[s][l][j] = wn[s][l][j];
+                for (int t = 0; t < MT; ++t) x[s % XR][t].some(xrow[t] + k * kXBytes, p.K - k - 8 * q);
+                const uint32_t c0 = (uint32_t)ch.c0;
+                load_pieces(words0, c0, w[s][0], (int64_t)min(step * BITS + lane_word<BITS>(q), last) * p.ldp);
+                if constexpr (kLW == 2)
+                    load_pieces(words0, c0, w[s][1], (int64_t)min(step * BITS + lane_word2<BITS>(q), last) * p.ldp);
+                if (((s + 1) & (p.group_steps - 1)) == 0) load_scales(step, s);
+                multiply(s);
+            }
         }
 
-        __syncthreads();                             // the previous rows' partials have been read
+        if (r0 != lo) __syncthreads();               // the previous rows' partials have been read
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -301,11 +336,13 @@ __global__ __launch_bounds__(64 * W) void matmul_rows_kernel(MatmulKernelArgs p)
             float y[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) y[j] = 0.f;
+#pragma unroll
             for (int s = 0; s < W; ++s)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) y[j] += part[s][v * NT + j][lane];
             const int64_t r = r0 + 16 * (v >> 2) + 4 * q + (v & 3);
             if (r < hi) {
+                if constexpr (FORM == kAdapters) add_adapter_row<NT, GATED>(p, r, ch, y);
                 const bool real = source_row(p, r) >= 0;
                 constexpr int NV = LaneChannels<NT, GATED>::kRun;
                 float o[NV];
@@ -321,33 +358,43 @@ __global__ __launch_bounds__(64 * W) void matmul_rows_kernel(MatmulKernelArgs p)
     }
 }
 
-// Channels per workgroup: 64, or 32 where 64 would leave more than half of the CUs without a workgroup.
+// Channels per workgroup: 64, or 32 where 64 would leave CUs without a workgroup.
 template <int BITS, int PARTS, int MT, int W>
-hipError_t launch_rows_mt(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
+hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
     const int64_t width = swiglu ? k.N / 2 : k.N;
     const unsigned ey = (unsigned)(k.E + (k.offsets ? 1 : 0));
     if (swiglu) {
-        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, true, W>), dim3((unsigned)ceil_div(width, 32), ey),
+        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kGated, W>), dim3((unsigned)ceil_div(width, 32), ey),
                            dim3(64 * W), 0, stream, k);
-    } else if (ceil_div(width, 64) * k.E >= 256) {
-        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, false, W>), dim3((unsigned)ceil_div(width, 64), ey),
-                           dim3(64 * W), 0, stream, k);
+    } else if (ceil_div(width, 64) * k.E >= 224) {
+        const dim3 grid((unsigned)ceil_div(width, 64), ey);
+        if (k.H)
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kAdapters, W>), grid, dim3(64 * W), 0, stream, k);
+        else
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kPlain, W>), grid, dim3(64 * W), 0, stream, k);
     } else {
-        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 2, false, W>), dim3((unsigned)ceil_div(width, 32), ey),
-                           dim3(64 * W), 0, stream, k);
+        const dim3 grid((unsigned)ceil_div(width, 32), ey);
+        if (k.H)
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 2, kAdapters, W>), grid, dim3(64 * W), 0, stream, k);
+        else
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 2, kPlain, W>), grid, dim3(64 * W), 0, stream, k);
     }
     return hipGetLastError();
 }
 
 template <int BITS>
 hipError_t launch_rows(const MatmulKernelArgs& k, bool f32, int row_tiles, bool swiglu, hipStream_t stream) {
+    const int64_t wgs = ceil_div(k.N, 64) * k.E;
     if (f32) {
-        if (row_tiles <= 1) return launch_rows_mt<BITS, 3, 1, 8>(k, swiglu, stream);
-        return launch_rows_mt<BITS, 3, 2, 8>(k, swiglu, stream);
+        if (row_tiles <= 1) return launch_rows_w<BITS, 3, 1, 8>(k, swiglu, stream);
+        return launch_rows_w<BITS, 3, 2, 8>(k, swiglu, stream);
     }
-    if (row_tiles <= 1) return launch_rows_mt<BITS, 1, 1, 16>(k, swiglu, stream);
-    if (row_tiles <= 2) return launch_rows_mt<BITS, 1, 2, 8>(k, swiglu, stream);
-    return launch_rows_mt<BITS, 1, 4, 8>(k, swiglu, stream);
+    if (row_tiles <= 1) {
+        if (wgs >= 1024) return launch_rows_w<BITS, 1, 1, 4>(k, swiglu, stream);
+        return launch_rows_w<BITS, 1, 1, 16>(k, swiglu, stream);
+    }
+    if (row_tiles <= 2) return launch_rows_w<BITS, 1, 2, 8>(k, swiglu, stream);
+    return launch_rows_w<BITS, 1, 4, 8>(k, swiglu, stream);
 }
 
 }  // namespace gptq

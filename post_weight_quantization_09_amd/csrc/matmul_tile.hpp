@@ -18,15 +18,15 @@ typedef __attribute__((address_space(3))) void lds_dma_t;
 constexpr int kTileCols = 256;         // channels of a workgroup (outputs: half of them when gated)
 constexpr int kTileGroup = 8;          // row tiles that neighbouring workgroups share a weight tile for
 
-// y += H B^T for the TM rows from r0 on: one product per run of rows with the same adapter.
+// acc += H B^T for the rows r0 .. r0 + nrow - 1: one product per run of rows with the same adapter (H zero outside it).
 template <int PARTS, int RT, int NT, bool GATED>
-__device__ __forceinline__ void add_adapters(const MatmulKernelArgs& p, const LaneChannels<NT, GATED>& ch, int64_t r0,
-                                             int nrow, int lane, f32x4 (&acc)[RT][NT]) {
-    constexpr int HP = PARTS == 1 ? 2 : 3;
+__device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, const LaneChannels<NT, GATED>& ch, int64_t r0,
+                                                 int nrow, int lane, f32x4 (&acc)[RT][NT]) {
+    constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding
     const int q = lane >> 4;
     for (int f = 0; f < nrow;) {
         const int a = __builtin_amdgcn_readfirstlane(p.row_adapter[r0 + f]);
-        int g = f + 1;                                // end of the run, 64 rows at a time
+        int g = f + 1;                               // end of the run, 64 rows at a time
         while (g < nrow) {
             const int mine = g + lane < nrow ? p.row_adapter[r0 + g + lane] : -2;
             const uint64_t other = __ballot(mine != a);
@@ -37,47 +37,43 @@ __device__ __forceinline__ void add_adapters(const MatmulKernelArgs& p, const La
             g += 64;
         }
         if (g > nrow) g = nrow;
-        if (a >= 0) {
-            for (int k = 0; k < p.rank; k += kStepK) {
-                const int kq = k + 8 * q;
-                bf16x8 b[NT];
+        for (int k = 0; a >= 0 && k < p.rank; k += kStepK) {
+            const int kq = k + 8 * q;
+            bf16x8 b[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    u32x4 v[1] = {{0u, 0u, 0u, 0u}};
-                    if (kq < p.rank)
-                        load_octet<1>(p.B + a * p.b_stride + ch.channel(j) * p.ldb, kq, p.rank, p.bvec, v);
-                    b[j] = __builtin_bit_cast(bf16x8, v[0]);
+            for (int j = 0; j < NT; ++j) {
+                u32x4 v[1];
+                load_octet<1>(p.B + a * p.b_stride + ch.channel(j) * p.ldb, kq, p.rank, v);
+                b[j] = __builtin_bit_cast(bf16x8, v[0]);
+            }
+            const bool has = kq < p.rank;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const int row = 16 * t + (lane & 15);
+                const bool in = has && row >= f && row < g;
+                const f32x4* h = reinterpret_cast<const f32x4*>(p.H + (r0 + (in ? row : f)) * p.hrank + (has ? kq : 0));
+                const f32x4 u = h[0], v = h[1];
+                float hv[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    hv[i] = in ? u[i] : 0.f;
+                    hv[4 + i] = in ? v[i] : 0.f;
                 }
+                u32x4 hp[3];
+                split3(hv, hp);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    if (16 * t < g && 16 * t + 16 > f) {
-                        const int row = 16 * t + (lane & 15);
-                        float hv[8];
+                for (int i = 0; i < HP; ++i)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) hv[i] = 0.f;
-                        if (row >= f && row < g && kq < p.rank) {
-                            const float* h = p.H + (r0 + row) * p.hrank + kq;
-                            const f32x4 u = reinterpret_cast<const f32x4*>(h)[0];
-                            const f32x4 v = reinterpret_cast<const f32x4*>(h)[1];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) { hv[i] = u[i]; hv[4 + i] = v[i]; }
-                        }
-                        u32x4 hp[3];
-                        split3(hv, hp);
-#pragma unroll
-                        for (int i = 0; i < HP; ++i)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j) acc[t][j] = mfma16(hp[i], b[j], acc[t][j]);
-                    }
-                }
+                    for (int j = 0; j < NT; ++j) acc[t][j] = mfma16(hp[i], b[j], acc[t][j]);
             }
         }
         f = g;
     }
 }
 
-template <int BITS, int PARTS, int RT, int GS, bool GATED>
+template <int BITS, int PARTS, int RT, int GS, int FORM>
 __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(MatmulKernelArgs p, int ntn, int ntm) {
+    constexpr bool GATED = FORM == kGated;
     constexpr int NT = 4, TM = 16 * RT, kGroups = kChunkSteps / GS;
     constexpr int kOctets = kChunkK / 8;
     __shared__ __attribute__((aligned(1024))) uint16_t xs[2][PARTS][kOctets][TM][8];
@@ -114,10 +110,8 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     const int last_word = p.nwords - 1;
     const int wa = lane_word<BITS>(q), wb = lane_word2<BITS>(q), sh = lane_shift<BITS>(q);
     constexpr int kLW = kLaneWords<BITS>;
-    const int64_t last_group = (p.K - 1) / (kStepK * GS);
-
     uint32_t w[kChunkSteps][kLW][NT];
-    float sc[kGroups][NT], s_ch[NT];
+    float sc[kGroups][NT];
     auto load_words = [&](int chunk) {
 #pragma unroll
         for (int s = 0; s < kChunkSteps; ++s) {
@@ -125,14 +119,10 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
             ch.words(words + (int64_t)min(at + wa, last_word) * p.ldp, w[s][0]);
             if constexpr (kLW == 2) ch.words(words + (int64_t)min(at + wb, last_word) * p.ldp, w[s][1]);
         }
-        if (!p.per_channel) {
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                int64_t at = (int64_t)chunk * kGroups + g;
-                at = at < last_group ? at : last_group;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) sc[g][j] = scales[at * p.N + ch.channel(j)];
-            }
+        for (int g = 0; g < kGroups; ++g) {
+            const int64_t at = (int64_t)chunk * kGroups + g;
+            ch.scales(scales + (at < p.last_group ? at : p.last_group) * p.s_row, sc[g]);
         }
     };
     const int64_t noct = (int64_t)nchunks * kOctets;
@@ -165,13 +155,8 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (p.per_channel) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s_ch[j] = scales[ch.channel(j)];
-    }
     stage(0, 0);
     load_words(0);
-    if (p.H) add_adapters<PARTS, RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
 
     for (int c = 0; c < nchunks; ++c) {
         const int buf = c & 1;
@@ -188,7 +173,7 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) f[g][j] = p.per_channel ? s_ch[j] : sc[g][j];
+            for (int j = 0; j < NT; ++j) f[g][j] = sc[g][j];
         if (c + 1 < nchunks) {
             stage(c + 1, buf ^ 1);
             load_words(c + 1);
@@ -219,6 +204,9 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
         }
     }
 
+    if constexpr (FORM == kAdapters) {
+        if (!p.Z) add_adapter_runs<PARTS, RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
+    }
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -230,6 +218,7 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
 #pragma unroll
                 for (int j = 0; j < kRun; ++j) {
                     o[j] = acc[t][j][i];
+                    if constexpr (FORM == kAdapters) o[j] += p.Z ? p.Z[r * p.N + ch.channel(j)] : 0.f;
                     if constexpr (GATED) o[j] = gated(acc[t][j][i], acc[t][kRun + j][i]);
                     o[j] = real ? o[j] : 0.f;
                 }
@@ -243,17 +232,18 @@ hipError_t launch_tile_rt(const MatmulKernelArgs& k, int ntm, bool swiglu, hipSt
     const int64_t width = swiglu ? k.N / 2 : k.N;
     const int ntn = (int)ceil_div(width, swiglu ? kTileCols / 2 : kTileCols);
     const unsigned grid = (unsigned)(ceil_div((int64_t)ntn * ntm, 8) * 8);
-#define GPTQ_TILE(GS, GATED) \
-    hipLaunchKernelGGL((matmul_tile_kernel<BITS, PARTS, RT, GS, GATED>), dim3(grid), dim3(256), 0, stream, k, ntn, ntm)
-    if (swiglu) {
-        if (k.group_steps == 1) GPTQ_TILE(1, true);
-        else if (k.group_steps == 2) GPTQ_TILE(2, true);
-        else GPTQ_TILE(4, true);
-    } else {
-        if (k.group_steps == 1) GPTQ_TILE(1, false);
-        else if (k.group_steps == 2) GPTQ_TILE(2, false);
-        else GPTQ_TILE(4, false);
-    }
+#define GPTQ_TILE(GS, FORM) \
+    hipLaunchKernelGGL((matmul_tile_kernel<BITS, PARTS, RT, GS, FORM>), dim3(grid), dim3(256), 0, stream, k, ntn, ntm)
+#define GPTQ_TILE_FORM(FORM)                        \
+    do {                                            \
+        if (k.group_steps == 1) GPTQ_TILE(1, FORM); \
+        else if (k.group_steps == 2) GPTQ_TILE(2, FORM); \
+        else GPTQ_TILE(4, FORM);                    \
+    } while (0)
+    if (swiglu) GPTQ_TILE_FORM(kGated);
+    else if (k.H) GPTQ_TILE_FORM(kAdapters);
+    else GPTQ_TILE_FORM(kPlain);
+#undef GPTQ_TILE_FORM
 #undef GPTQ_TILE
     return hipGetLastError();
 }

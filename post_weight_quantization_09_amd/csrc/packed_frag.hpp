@@ -21,7 +21,9 @@
 
 namespace gptq {
 
-typedef u32x4 __attribute__((aligned(4))) u32x4_a4;      // global 16-byte loads need 4-byte alignment only
+// Global loads take any alignment (the amdhsa target's unaligned access mode); the types say what is promised.
+typedef u32x4 __attribute__((aligned(4))) u32x4_a4;
+typedef u32x4 __attribute__((aligned(2))) u32x4_a2;
 typedef u32x2 __attribute__((aligned(4))) u32x2_a4;
 typedef f32x4 __attribute__((aligned(4))) f32x4_a4;
 typedef f32x2 __attribute__((aligned(4))) f32x2_a4;
@@ -140,34 +142,58 @@ __device__ __forceinline__ void split3(const float (&x)[8], u32x4 (&part)[3]) {
     }
 }
 
-// Eight elements k .. k + 7 of a row as bf16 parts (PARTS = 1: bf16 rows; 3: fp32 rows), zero from K on.  `vec`: the
-// whole row may be read in 16-byte pieces (alignment checked by the host).
+// Eight elements k .. k + 7 of a row as they are in memory (bf16: 16 bytes, fp32: 32), zero from K on.
 template <int PARTS>
-__device__ __forceinline__ void load_octet(const void* row, int64_t k, int64_t K, bool vec, u32x4 (&part)[PARTS]) {
-    if constexpr (PARTS == 1) {
-        const uint16_t* p = static_cast<const uint16_t*>(row) + k;
-        if (vec && k + 8 <= K) {
-            part[0] = *reinterpret_cast<const u32x4*>(p);
+struct RawOctet {
+    u32x4 v[PARTS == 1 ? 1 : 2];
+
+    __device__ __forceinline__ void whole(const char* p) {
+        if constexpr (PARTS == 1) {
+            v[0] = *reinterpret_cast<const u32x4_a2*>(p);
         } else {
-            uint32_t e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = k + i < K ? p[i] : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[0][i] = e[2 * i] | (e[2 * i + 1] << 16);
+            v[0] = reinterpret_cast<const u32x4_a4*>(p)[0];
+            v[1] = reinterpret_cast<const u32x4_a4*>(p)[1];
         }
-    } else {
-        const float* p = static_cast<const float*>(row) + k;
-        float x[8];
-        if (vec && k + 8 <= K) {
-            const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { x[i] = a[i]; x[4 + i] = b[i]; }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = k + i < K ? p[i] : 0.f;
-        }
-        split3(x, part);
     }
+    __device__ __forceinline__ void zero() {
+        v[0] = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (PARTS != 1) v[1] = u32x4{0u, 0u, 0u, 0u};
+    }
+    // `left` elements of the row remain from p on (may be none or negative).
+    __device__ __forceinline__ void some(const char* p, int64_t left) {
+        if (left >= 8) {
+            whole(p);
+            return;
+        }
+        zero();
+#pragma unroll
+        for (int i = 0; i < 7; ++i) {
+            if (i < left) {
+                if constexpr (PARTS == 1)
+                    v[0][i >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+                else
+                    v[i >> 2][i & 3] = reinterpret_cast<const uint32_t*>(p)[i];
+            }
+        }
+    }
+    // As bf16 parts in natural order.
+    __device__ __forceinline__ void parts(u32x4 (&part)[PARTS]) const {
+        if constexpr (PARTS == 1) {
+            part[0] = v[0];
+        } else {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i >> 2][i & 3]);
+            split3(x, part);
+        }
+    }
+};
+
+template <int PARTS>
+__device__ __forceinline__ void load_octet(const void* row, int64_t k, int64_t K, u32x4 (&part)[PARTS]) {
+    RawOctet<PARTS> r;
+    r.some(static_cast<const char*>(row) + k * (PARTS == 1 ? 2 : 4), K - k);
+    r.parts(part);
 }
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, bf16x8 b, f32x4 c) {
