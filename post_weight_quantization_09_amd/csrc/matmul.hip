@@ -1,4 +1,4 @@
-// Products with packed weights: the pass that lays the rows out for the tile kernel, workspace, choice of kernel.
+// Products with packed weights: the pass that prepares the rows, workspace, choice of kernel.
 #include <algorithm>
 
 #include "matmul_launch.hpp"
@@ -9,17 +9,41 @@ namespace gptq {
 namespace {
 
 constexpr int kMaxTileRows = 128;
+constexpr int kStageThreads = 512;
+constexpr int kStageRows = 64;
+
+// What stage_kernel writes.
+struct StageArgs {
+    uint16_t* XT;
+    float* sums;
+    float excess;          // -1.5 2^b
+    int tile, cap;         // rows of a tile, entries of the list
+    int32_t* tiles;
+    int row_blocks;        // workgroups of the rows: row_blocks x chunks (0: rows are not laid out)
+    // adapters
+    const uint16_t* A;
+    int64_t lda, a_stride;
+    const float* alpha;
+    int64_t n_adapters;
+    const int32_t* requests;
+    const int32_t* adapter;
+    int64_t n_requests;
+    int slices;            // workgroups of a request (0: no adapters)
+    float* H;
+    int32_t* row_adapter;
+};
 
 // Row tiles of at most `tile` rows: one list entry (expert, first row, end) per tile, the rows of no expert as expert E,
 // the rest of the list expert -1.  One workgroup.
-__device__ void list_tiles(const MatmulKernelArgs& p, int tile, int cap, int32_t* tiles) {
-    __shared__ int counts[256];
+__device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
+    constexpr int T = kStageThreads;
+    __shared__ int counts[T];
     __shared__ int base;
     const int tid = threadIdx.x;
     if (tid == 0) base = 0;
     __syncthreads();
     const int ranges = p.offsets ? p.E + 2 : 1;
-    for (int f = 0; f < ranges; f += 256) {
+    for (int f = 0; f < ranges; f += T) {
         const int i = f + tid;
         int64_t lo = 0, hi = 0;
         int e = i;
@@ -37,45 +61,42 @@ __device__ void list_tiles(const MatmulKernelArgs& p, int tile, int cap, int32_t
                 hi = i == p.E ? head : p.M;
             }
         }
-        const int n = hi > lo ? (int)((hi - lo + tile - 1) / tile) : 0;
+        const int n = hi > lo ? (int)((hi - lo + a.tile - 1) / a.tile) : 0;
         counts[tid] = n;
         __syncthreads();
-        for (int d = 1; d < 256; d <<= 1) {
+        for (int d = 1; d < T; d <<= 1) {
             const int v = tid >= d ? counts[tid - d] : 0;
             __syncthreads();
             counts[tid] += v;
             __syncthreads();
         }
         const int first = base + counts[tid] - n;
-        for (int t = 0; t < n && first + t < cap; ++t) {
-            tiles[3 * (first + t)] = e;
-            tiles[3 * (first + t) + 1] = (int32_t)(lo + (int64_t)t * tile);
-            tiles[3 * (first + t) + 2] = (int32_t)(lo + (int64_t)(t + 1) * tile < hi ? lo + (int64_t)(t + 1) * tile : hi);
+        for (int t = 0; t < n && first + t < a.cap; ++t) {
+            const int64_t r = lo + (int64_t)t * a.tile;
+            a.tiles[3 * (first + t)] = e;
+            a.tiles[3 * (first + t) + 1] = (int32_t)r;
+            a.tiles[3 * (first + t) + 2] = (int32_t)(r + a.tile < hi ? r + a.tile : hi);
         }
         __syncthreads();
-        if (tid == 255) base += counts[255];
+        if (tid == T - 1) base += counts[T - 1];
         __syncthreads();
     }
-    for (int t = base + tid; t < cap; t += 256) tiles[3 * t] = -1;
+    for (int t = base + tid; t < a.cap; t += T) a.tiles[3 * t] = -1;
 }
 
 // Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times
 // -1.5 2^b.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces along
 // the rows, turned in LDS.  Bound by HBM: every row is read once and written once.
 template <int PARTS>
-__global__ __launch_bounds__(256) void stage_rows_kernel(MatmulKernelArgs p, uint16_t* XT, float* sums, float excess,
-                                                         int tile, int cap, int32_t* tiles) {
-    constexpr int kOctets = kChunkK / 8;
-    __shared__ u32x4 xt[PARTS][kOctets][65];
-    __shared__ float os[kOctets][65];
-    if (blockIdx.x == 0 && blockIdx.y == 0) list_tiles(p, tile, cap, tiles);
+__device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t r0, int chunk, int nchunks, char* lds) {
+    constexpr int kOctets = kChunkK / 8, kPitch = kStageRows + 1;
+    u32x4* xt = reinterpret_cast<u32x4*>(lds);                          // [part][octet][row]
+    float* os = reinterpret_cast<float*>(xt + PARTS * kOctets * kPitch);
     const int tid = threadIdx.x;
-    const int64_t r0 = (int64_t)blockIdx.x * 64;
-    const int chunk = blockIdx.y;
-    const int64_t noct = (int64_t)gridDim.y * kOctets;
+    const int64_t noct = (int64_t)nchunks * kOctets;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = (tid >> 4) + 16 * i, o = tid & 15;
+    for (int i = 0; i < kStageRows * kOctets / kStageThreads; ++i) {
+        const int row = (tid >> 4) + (kStageThreads / 16) * i, o = tid & 15;
         const int64_t r = r0 + row;
         u32x4 part[PARTS];
 #pragma unroll
@@ -88,8 +109,8 @@ __global__ __launch_bounds__(256) void stage_rows_kernel(MatmulKernelArgs p, uin
 #pragma unroll
         for (int d = 0; d < 4; ++d) sum += bf16lo_to_f32(part[0][d]) + bf16hi_to_f32(part[0][d]);
 #pragma unroll
-        for (int j = 0; j < PARTS; ++j) xt[j][o][row] = pair_order(part[j]);
-        os[o][row] = sum;
+        for (int j = 0; j < PARTS; ++j) xt[(j * kOctets + o) * kPitch + row] = pair_order(part[j]);
+        os[o * kPitch + row] = sum;
     }
     __syncthreads();
     const int row = tid & 63;
@@ -97,44 +118,162 @@ __global__ __launch_bounds__(256) void stage_rows_kernel(MatmulKernelArgs p, uin
 #pragma unroll
     for (int j = 0; j < PARTS; ++j)
 #pragma unroll
-        for (int i = 0; i < kOctets / 4; ++i) {
-            const int o = (tid >> 6) + 4 * i;
-            reinterpret_cast<u32x4*>(XT)[(j * noct + (int64_t)chunk * kOctets + o) * p.Mp + r0 + row] = xt[j][o][row];
+        for (int i = 0; i < kOctets / (kStageThreads / 64); ++i) {
+            const int o = (tid >> 6) + (kStageThreads / 64) * i;
+            reinterpret_cast<u32x4*>(a.XT)[(j * noct + (int64_t)chunk * kOctets + o) * p.Mp + r0 + row] =
+                xt[(j * kOctets + o) * kPitch + row];
         }
     if (PARTS > 1) return;                           // fp32 rows: the codes come without the excess
-    const int groups = kChunkSteps / p.group_steps;
-    for (int g = tid >> 6; g < groups; g += 4) {
+    const int per = 4 << p.lg_group, groups = kOctets / per;             // octets of a group
+    for (int g = tid >> 6; g < groups; g += kStageThreads / 64) {
         float s = 0.f;
-        for (int o = 0; o < 4 * p.group_steps; ++o) s += os[g * 4 * p.group_steps + o][row];
-        sums[((int64_t)chunk * groups + g) * p.Mp + r0 + row] = excess * s;
+        for (int o = 0; o < per; ++o) s += os[(g * per + o) * kPitch + row];
+        a.sums[((int64_t)chunk * groups + g) * p.Mp + r0 + row] = a.excess * s;
     }
+}
+
+// The inner half of the low-rank adapters: H[r] = alpha_a (A_a x_r) for the rows r of one request, a its adapter, and
+// the adapter of every row.  Bound by latency and the adapters' bytes for single tokens, by the rows' bytes for prompts.
+// A workgroup takes 16 rows at a time and the whole rank; its waves split K (each 32-k step one matrix product per 16
+// ranks: lane l holds row l % 16 and, of A, rank l % 16, eight consecutive k each, straight from memory; a wave has the
+// loads of kAhead steps in flight) and the partial sums are joined in LDS in a fixed order.  Every request gets `slices`
+// workgroups, so that the launch does not depend on the lengths, which only the device knows.  H stays in fp32.
+template <int PARTS, int NR>
+__device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t req, int slice, char* lds) {
+    constexpr int W = kStageThreads / 64;
+    float* part = reinterpret_cast<float*>(lds);     // [wave][rank and row register][lane]
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (req == a.n_requests) {                       // rows of no request
+        if (slice) return;
+        int64_t head = a.requests[0], tail = a.requests[a.n_requests];
+        head = head < 0 ? 0 : head > p.M ? p.M : head;
+        tail = tail < head ? head : tail > p.M ? p.M : tail;
+        for (int64_t r = tid; r < head; r += kStageThreads) a.row_adapter[r] = -1;
+        for (int64_t r = tail + tid; r < p.M; r += kStageThreads) a.row_adapter[r] = -1;
+        return;
+    }
+    int64_t lo = a.requests[req], hi = a.requests[req + 1];
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > p.M ? p.M : hi;
+    int id = a.adapter[req];
+    if (id < 0 || id >= a.n_adapters) id = -1;
+    const float alpha = id < 0 ? 0.f : a.alpha[id];
+    const int64_t step = 16 * (int64_t)a.slices;
+    for (int64_t r0 = lo + 16 * (int64_t)slice; r0 < hi; r0 += step) {
+        if (tid < 16 && r0 + tid < hi) a.row_adapter[r0 + tid] = id;
+        if (id < 0) continue;
+        int64_t r = r0 + (lane & 15);
+        if (r >= hi) r = hi - 1;
+        const char* xrow = static_cast<const char*>(p.X) + (r * p.ldx + 8 * q) * (PARTS == 1 ? 2 : 4);
+        const uint16_t* arow[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            int rk = 16 * n + (lane & 15);
+            if (rk >= p.rank) rk = p.rank - 1;       // ranks past the end are not stored
+            arow[n] = a.A + id * a.a_stride + rk * a.lda + 8 * q;
+        }
+        f32x4 acc[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // pairs of steps (128 bytes of a bf16 row) are dealt out to the waves, kAhead steps at a time
+        constexpr int kAhead = NR * PARTS <= 4 ? 8 : 4;
+        const int whole = p.K / kStepK;
+        constexpr int kTurn = 2 * W;
+        for (int s0 = 2 * wave; s0 < whole; s0 += kTurn * (kAhead / 2)) {
+            RawOctet<PARTS> x[kAhead];
+            RawOctet<1> b[kAhead][NR];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                int s = s0 + (u >> 1) * kTurn + (u & 1);
+                s = s < whole ? s : s0;              // beyond the end: loaded again and not used
+                x[u].whole(xrow + s * (kStepK * (PARTS == 1 ? 2 : 4)));
+#pragma unroll
+                for (int n = 0; n < NR; ++n) b[u][n].whole(reinterpret_cast<const char*>(arow[n] + s * kStepK));
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (s0 + (u >> 1) * kTurn + (u & 1) < whole) {
+                    u32x4 xp[PARTS];
+                    x[u].parts(xp);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i)
+                            acc[n] = mfma16(xp[i], __builtin_bit_cast(bf16x8, b[u][n].v[0]), acc[n]);
+                }
+            }
+        }
+        if (wave == W - 1 && whole * kStepK < p.K) { // the rest of K
+            u32x4 x[PARTS], b[1];
+            const int k = whole * kStepK, left = p.K - k - 8 * q;
+            load_octet<PARTS>(xrow, k, k + left, x);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                load_octet<1>(arow[n], k, k + left, b);
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) acc[n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[n]);
+            }
+        }
+        __syncthreads();                             // the previous rows' partials have been read
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[(wave * NR * 4 + n * 4 + i) * 64 + lane] = acc[n][i];
+        __syncthreads();
+        for (int v = wave; v < NR * 4; v += W) {
+            float s = 0.f;
+#pragma unroll
+            for (int u = 0; u < W; ++u) s += part[(u * NR * 4 + v) * 64 + lane];
+            const int64_t row = r0 + 4 * q + (v & 3);
+            const int rk = 16 * (v >> 2) + (lane & 15);
+            if (row < hi && rk < p.hrank) a.H[row * p.hrank + rk] = rk < p.rank ? s * alpha : 0.f;
+        }
+    }
+}
+
+// One launch before the product: workgroups of the adapters first (their chains of loads are the longest), then of the
+// rows.  NR 0: no adapters.
+template <int PARTS, int NR>
+__global__ __launch_bounds__(kStageThreads) void stage_kernel(MatmulKernelArgs p, StageArgs a) {
+    constexpr int kLayBytes = PARTS * (kChunkK / 8) * (kStageRows + 1) * 16 + (kChunkK / 8) * (kStageRows + 1) * 4;
+    constexpr int kShrinkBytes = (kStageThreads / 64) * NR * 4 * 64 * 4;
+    __shared__ __attribute__((aligned(16))) char lds[kLayBytes > kShrinkBytes ? kLayBytes : kShrinkBytes];
+    int64_t b = blockIdx.x;
+    if constexpr (NR > 0) {
+        const int64_t n = (a.n_requests + 1) * a.slices;
+        if (b < n) {
+            shrink_rows<PARTS, NR>(p, a, b / a.slices, (int)(b % a.slices), lds);
+            return;
+        }
+        b -= n;
+    }
+    const int nchunks = (p.K + kChunkK - 1) / kChunkK;
+    if (b == (int64_t)a.row_blocks * nchunks) {
+        list_tiles(p, a);
+        return;
+    }
+    lay_out_rows<PARTS>(p, a, b / nchunks * kStageRows, (int)(b % nchunks), nchunks, lds);
 }
 
 // Z = H B^T for many rows of short requests (single tokens beside each other): one thread per row and four channels.
 __global__ __launch_bounds__(256) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
     const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), c0 = ((int64_t)blockIdx.y * 64 + lane) * 4;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t c0 = ((int64_t)blockIdx.y * 64 + lane) * 4;
     if (r >= p.M || c0 >= p.N) return;
     LaneChannels<4, false> ch(0, 0, p.N);
-    ch.c0 = c0 < p.N - 4 ? c0 : p.N - 4;
+    ch.c0 = (uint32_t)(c0 < p.N - 4 ? c0 : p.N - 4);
     float y[4] = {0.f, 0.f, 0.f, 0.f};
     add_adapter_row<4, false>(p, r, ch, y);
     *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{y[0], y[1], y[2], y[3]};
 }
 
-// Rows an expert is expected to have; the kernels hold for any split, this only chooses.
-int64_t rows_per_expert(int64_t M, int64_t experts) { return ceil_div(M, std::max<int64_t>(1, experts)); }
-
-bool use_tiles(int64_t M, int64_t experts) { return rows_per_expert(M, experts) > 64; }
-
-int tile_rows(bool f32, int64_t M, int64_t N, int64_t experts) {
-    if (f32 || ceil_div(M, 128) * ceil_div(N, 256) < 256) return 64;
-    return 128;
-}
+enum Kernel { kRows, kSplit, kTile };
 
 struct Plan {
-    bool tiles;
-    int tile;
+    Kernel kernel;
+    int tile;              // rows of a tile
     int cap;               // entries of the tile list
     int64_t Mp;
     int nchunks;
@@ -142,15 +281,33 @@ struct Plan {
     int hrank;
 };
 
-Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank) {
+// Row tiles of the split kernel: 64 rows fit its registers with one word per step and lane and one scale per 128 k, and
+// halve the conversions of codes; else 32 (64 rows of 3-bit codes in groups of 64 spill: 56 us against TODO).
+int split_row_tiles(bool f32, int64_t mean, int bits, int groupsize) {
+    return !f32 && mean > 32 && (bits == 2 || bits == 4) && (groupsize == 0 || groupsize == 128) ? 4 : 2;
+}
+
+// Which kernel: by the rows an expert has on average (all hold for any split of the rows).  Up to 16 (one operand's
+// rows) the few-rows kernel; then the tile kernel where it has work for every CU twice, else the split kernel.
+Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank, int bits, int groupsize) {
     Plan p;
-    p.tiles = use_tiles(M, experts);
-    p.tile = tile_rows(f32, M, N, experts);
+    const int64_t mean = ceil_div(M, experts);
+    const int big = f32 ? 64 : 128;
+    if (mean <= 16) {
+        p.kernel = kRows;
+        p.tile = 16;
+    } else if (mean > 64 && ceil_div(M, 64) * ceil_div(N, 256) >= 512) {
+        p.kernel = kTile;
+        p.tile = ceil_div(M, big) * ceil_div(N, 256) >= 256 ? big : 64;
+    } else {
+        p.kernel = kSplit;
+        p.tile = 16 * split_row_tiles(f32, mean, bits, groupsize);
+    }
     p.cap = (int)(M / p.tile + std::min<int64_t>(experts + 2, M) + 1);
     p.Mp = (int64_t)align_up((size_t)M + kMaxTileRows, 64);
     p.nchunks = (int)ceil_div(K, kChunkK);
     p.xt_elems = (size_t)(f32 ? 3 : 1) * p.nchunks * kChunkK * p.Mp;
-    p.sum_floats = (size_t)p.nchunks * kChunkSteps * p.Mp;
+    p.sum_floats = f32 ? 0 : (size_t)p.nchunks * kChunkSteps * p.Mp;
     p.hrank = (int)align_up((size_t)rank, 8);
     return p;
 }
@@ -161,86 +318,105 @@ struct Buffers {
     uint16_t* XT;
     float* sums;
     int32_t* tiles;
-    size_t bytes;
     float* Z;
+    size_t bytes;
     Buffers(const Plan& p, int64_t M, int64_t N, void* ws) {
         Carver c(ws);
+        const bool staged = p.kernel != kRows;
         H = p.hrank ? c.take<float>((size_t)M * p.hrank) : nullptr;
         row_adapter = p.hrank ? c.take<int32_t>((size_t)M) : nullptr;
-        XT = p.tiles ? c.take<uint16_t>(p.xt_elems) : nullptr;
-        sums = p.tiles ? c.take<float>(p.sum_floats) : nullptr;
-        tiles = p.tiles ? c.take<int32_t>(3 * (size_t)p.cap) : nullptr;
-        Z = p.tiles && p.hrank ? c.take<float>((size_t)M * N) : nullptr;
+        XT = staged ? c.take<uint16_t>(p.xt_elems) : nullptr;
+        sums = staged ? c.take<float>(p.sum_floats) : nullptr;
+        tiles = staged ? c.take<int32_t>(3 * (size_t)p.cap) : nullptr;
+        Z = p.kernel == kTile && p.hrank ? c.take<float>((size_t)M * N) : nullptr;
         bytes = c.bytes();
     }
 };
 
-// A tile takes one small product per run of rows with the same adapter: about 1 us each, against M N fp32 values written
-// and read again for Z.  Runs of 32 rows and more (prompts) go the first way, single tokens the second.
+// The tile kernel takes one small product per run of rows with the same adapter, about 1 us each, or Z, M N fp32 values
+// written and read again.  Runs of 32 rows and more on average (prompts) go the first way, single tokens the second.
 bool short_requests(int64_t M, int64_t n_requests) { return M < 32 * n_requests; }
+
+template <int PARTS>
+hipError_t launch_stage(const MatmulKernelArgs& k, const StageArgs& a, unsigned grid, hipStream_t stream) {
+#define GPTQ_STAGE(NR) hipLaunchKernelGGL((stage_kernel<PARTS, NR>), dim3(grid), dim3(kStageThreads), 0, stream, k, a)
+    if (!a.slices) GPTQ_STAGE(0);
+    else if (k.rank <= 16) GPTQ_STAGE(1);
+    else if (k.rank <= 32) GPTQ_STAGE(2);
+    else if (k.rank <= 64) GPTQ_STAGE(4);
+    else GPTQ_STAGE(8);
+#undef GPTQ_STAGE
+    return hipGetLastError();
+}
 
 }  // namespace
 
+// For any width and group size: the smaller tiles' list is the longer one.
 size_t matmul_workspace_bytes(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank) {
-    return Buffers(make_plan(f32, M, K, N, experts, rank), M, N, nullptr).bytes;
+    return Buffers(make_plan(f32, M, K, N, experts, rank, 3, 32), M, N, nullptr).bytes;
 }
 
 hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t stream) {
     const bool lora = a.n_requests > 0 && a.n_adapters > 0;
-    const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0);
+    const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0, a.bits, a.groupsize);
     const Buffers buf(plan, a.M, a.N, workspace);
     MatmulKernelArgs k;
     k.X = a.X; k.ldx = a.ldx; k.x_rows = a.x_rows; k.rows = a.rows; k.M = a.M;
     k.offsets = a.offsets; k.E = a.E;
-    k.packed = a.packed; k.ldp = a.ldp; k.p_stride = a.p_stride; k.K = a.K; k.N = a.N;
+    k.packed = a.packed; k.ldp = (uint32_t)a.ldp; k.p_stride = a.p_stride; k.K = (int)a.K; k.N = (int)a.N;
     k.nwords = (int)((a.K * a.bits + 31) / 32);
     k.scales = a.scales; k.s_stride = a.s_stride;
-    k.group_steps = a.groupsize ? a.groupsize / kStepK : kChunkSteps;
-    k.s_row = a.groupsize ? a.N : 0;
-    k.last_group = a.groupsize ? (a.K - 1) / a.groupsize : 0;
+    k.lg_group = a.groupsize == 32 ? 0 : a.groupsize == 64 ? 1 : 2;
+    k.s_row = a.groupsize ? (int)a.N : 0;
+    k.last_group = a.groupsize ? (int)((a.K - 1) / a.groupsize) : 0;
     k.Y = a.Y; k.ldy = a.ldy;
     k.H = lora ? buf.H : nullptr;
     k.hrank = plan.hrank; k.row_adapter = buf.row_adapter;
+    k.Z = lora && plan.kernel == kTile && short_requests(a.M, a.n_requests) ? buf.Z : nullptr;
     k.B = a.B; k.ldb = a.ldb; k.b_stride = a.b_stride; k.rank = a.rank;
-    k.Z = lora && plan.tiles && short_requests(a.M, a.n_requests) ? buf.Z : nullptr;
     k.XT = buf.XT; k.sums = buf.sums; k.Mp = plan.Mp; k.tiles = buf.tiles;
-    if (lora) {
-        const hipError_t e = adapter_shrink(a, buf.H, plan.hrank, buf.row_adapter, stream);
+
+    if (lora || plan.kernel != kRows) {
+        StageArgs s = {};
+        s.XT = buf.XT; s.sums = buf.sums; s.excess = -1.5f * (float)(1 << a.bits);
+        s.tile = plan.tile; s.cap = plan.cap; s.tiles = buf.tiles;
+        int64_t grid = 0;
+        if (plan.kernel != kRows) {
+            s.row_blocks = (int)ceil_div(a.M, kStageRows);
+            grid = (int64_t)s.row_blocks * plan.nchunks + 1;
+        }
+        if (lora) {
+            s.A = a.A; s.lda = a.lda; s.a_stride = a.a_stride; s.alpha = a.alpha; s.n_adapters = a.n_adapters;
+            s.requests = a.requests; s.adapter = a.adapter; s.n_requests = a.n_requests;
+            s.H = buf.H; s.row_adapter = buf.row_adapter;
+            // about 1024 workgroups for the requests in all, no more than the longest could use
+            s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.M, 16), 1024 / a.n_requests));
+            grid += (a.n_requests + 1) * s.slices;
+        }
+        if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
+        hipError_t e = a.f32 ? launch_stage<3>(k, s, (unsigned)grid, stream) : launch_stage<1>(k, s, (unsigned)grid, stream);
         if (e != hipSuccess) return e;
         if (k.Z) {
-            const dim3 grid((unsigned)ceil_div(a.M, 4), (unsigned)ceil_div(a.N, 256));
-            hipLaunchKernelGGL(adapter_expand_kernel, grid, dim3(256), 0, stream, k, buf.Z);
-            const hipError_t x = hipGetLastError();
-            if (x != hipSuccess) return x;
+            const dim3 zgrid((unsigned)ceil_div(a.M, 4), (unsigned)ceil_div(a.N, 256));
+            hipLaunchKernelGGL(adapter_expand_kernel, zgrid, dim3(256), 0, stream, k, buf.Z);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
     }
-    if (plan.tiles) {
-        const dim3 grid((unsigned)ceil_div(a.M, 64), (unsigned)plan.nchunks);
-        const float excess = -1.5f * (float)(1 << a.bits);
-        if (a.f32)
-            hipLaunchKernelGGL((stage_rows_kernel<3>), grid, dim3(256), 0, stream, k, buf.XT, buf.sums, excess,
-                               plan.tile, plan.cap, buf.tiles);
-        else
-            hipLaunchKernelGGL((stage_rows_kernel<1>), grid, dim3(256), 0, stream, k, buf.XT, buf.sums, excess,
-                               plan.tile, plan.cap, buf.tiles);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        switch (a.bits) {
-            case 2: return tile_b2(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);
-            case 3: return tile_b3(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);
-            case 4: return tile_b4(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);
-            case 5: return tile_b5(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);
-            default: return tile_b6(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);
-        }
-    }
-    const int row_tiles = (int)ceil_div(rows_per_expert(a.M, a.E), 16);
+#define GPTQ_WIDTH(B)                                                                                      \
+    do {                                                                                                   \
+        if (plan.kernel == kRows) return rows_b##B(k, a.f32, a.swiglu, stream);                            \
+        if (plan.kernel == kSplit) return split_b##B(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream); \
+        return tile_b##B(k, a.f32, plan.tile / 16, plan.cap, a.swiglu, stream);                            \
+    } while (0)
     switch (a.bits) {
-        case 2: return rows_b2(k, a.f32, row_tiles, a.swiglu, stream);
-        case 3: return rows_b3(k, a.f32, row_tiles, a.swiglu, stream);
-        case 4: return rows_b4(k, a.f32, row_tiles, a.swiglu, stream);
-        case 5: return rows_b5(k, a.f32, row_tiles, a.swiglu, stream);
-        default: return rows_b6(k, a.f32, row_tiles, a.swiglu, stream);
+        case 2: GPTQ_WIDTH(2);
+        case 3: GPTQ_WIDTH(3);
+        case 4: GPTQ_WIDTH(4);
+        case 5: GPTQ_WIDTH(5);
+        default: GPTQ_WIDTH(6);
     }
+#undef GPTQ_WIDTH
 }
 
 }  // namespace gptq

@@ -49,14 +49,15 @@ struct MatmulKernelArgs {
     const int32_t* offsets;
     int E;
     const uint32_t* packed;
-    int64_t ldp, p_stride;
-    int64_t K, N;
+    int64_t p_stride;
+    uint32_t ldp;
+    int K, N;
     int nwords;                            // words per channel
     const float* scales;
     int64_t s_stride;
-    int group_steps;                       // MFMA steps per scale (1, 2, 4; per channel 4)
-    int64_t s_row;                         // floats from one group's scales to the next (per channel 0)
-    int64_t last_group;
+    int lg_group;                          // log2 of the MFMA steps per scale (0, 1, 2; per channel 2)
+    int s_row;                             // floats from one group's scales to the next (per channel 0)
+    int last_group;
     void* Y;
     int64_t ldy;
     // adapters: H = alpha A x of every row, M x hrank fp32, and the adapter of every row (-1: none)

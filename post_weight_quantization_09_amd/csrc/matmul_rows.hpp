@@ -72,20 +72,21 @@ __device__ __forceinline__ void zero_outside(const MatmulKernelArgs& p, int64_t 
 }
 
 // NT neighbouring words of one row of the packed weight (at lane's channels), as one load.
+// (a uniform address and a 32-bit offset of the lane: the load takes both as they are)
 template <int NT>
 struct WordLoad;
 template <>
 struct WordLoad<4> {
-    static __device__ __forceinline__ void run(const uint32_t* p, uint32_t (&w)[4]) {
-        const u32x4 v = *reinterpret_cast<const u32x4_a4*>(p);
+    static __device__ __forceinline__ void run(const uint32_t* row, uint32_t off, uint32_t (&w)[4]) {
+        const u32x4 v = *reinterpret_cast<const u32x4_a4*>(reinterpret_cast<const char*>(row) + 4u * off);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = v[j];
     }
 };
 template <>
 struct WordLoad<2> {
-    static __device__ __forceinline__ void run(const uint32_t* p, uint32_t (&w)[2]) {
-        const u32x2 v = *reinterpret_cast<const u32x2_a4*>(p);
+    static __device__ __forceinline__ void run(const uint32_t* row, uint32_t off, uint32_t (&w)[2]) {
+        const u32x2 v = *reinterpret_cast<const u32x2_a4*>(reinterpret_cast<const char*>(row) + 4u * off);
         w[0] = v[0];
         w[1] = v[1];
     }
@@ -97,32 +98,27 @@ struct WordLoad<2> {
 template <int NT, bool GATED>
 struct LaneChannels {
     static constexpr int kRun = GATED ? NT / 2 : NT;
-    int64_t c0;        // first channel (and first output column)
-    int64_t half;
-    __device__ __forceinline__ LaneChannels(int64_t tile0, int lane, int64_t N) {
+    uint32_t c0;       // first channel (and first output column)
+    uint32_t half;
+    __device__ __forceinline__ LaneChannels(int tile0, int lane, int N) {
         half = GATED ? N / 2 : 0;
-        const int64_t width = GATED ? N / 2 : N;
-        c0 = tile0 + kRun * (lane & 15);
-        if (c0 > width - kRun) c0 = width - kRun;
+        const int width = GATED ? N / 2 : N;
+        const int c = tile0 + kRun * (lane & 15);
+        c0 = c > width - kRun ? width - kRun : c;
     }
-    __device__ __forceinline__ void words(const uint32_t* row, uint32_t (&w)[NT]) const {
+    // NT words (or scales) of one row: `row` is uniform, `off` the lane's own offset into it (c0, or c0 and some rows)
+    __device__ __forceinline__ void words(const uint32_t* row, uint32_t off, uint32_t (&w)[NT]) const {
         if constexpr (GATED) {
             uint32_t a[kRun], b[kRun];
-            WordLoad<kRun>::run(row + c0, a);
-            WordLoad<kRun>::run(row + half + c0, b);
+            WordLoad<kRun>::run(row, off, a);
+            WordLoad<kRun>::run(row + half, off, b);
 #pragma unroll
             for (int j = 0; j < kRun; ++j) { w[j] = a[j]; w[kRun + j] = b[j]; }
         } else {
-            WordLoad<NT>::run(row + c0, w);
+            WordLoad<NT>::run(row, off, w);
         }
     }
-    __device__ __forceinline__ int64_t channel(int j) const { return j < kRun ? c0 + j : half + c0 + (j - kRun); }
-    __device__ __forceinline__ void scales(const float* row, float (&s)[NT]) const {
-        uint32_t u[NT];
-        words(reinterpret_cast<const uint32_t*>(row), u);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s[j] = __uint_as_float(u[j]);
-    }
+    __device__ __forceinline__ uint32_t channel(int j) const { return j < kRun ? c0 + j : half + c0 + (j - kRun); }
 };
 
 // y[j] += sum_k H[r][k] B_a[channel j][k] for one row: the adapter's own term where a row stands for itself (single
@@ -162,16 +158,16 @@ __device__ __forceinline__ void add_adapter_row(const MatmulKernelArgs& p, int64
 enum { kPlain = 0, kGated = 1, kAdapters = 2 };
 
 template <int BITS, int PARTS, int MT, int NT, int FORM, int W>
-__global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
+__global__ __launch_bounds__(64 * W, PARTS == 1 ? 4 : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
     constexpr bool GATED = FORM == kGated;
     constexpr int kVals = MT * 4;                    // (row tile, register) items of NT channels
     constexpr int XR = MT * PARTS >= 4 ? 2 : 4;      // steps of rows in flight
     __shared__ float part[W][kVals * NT][64];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t width = GATED ? p.N / 2 : p.N;
+    const int width = GATED ? p.N / 2 : p.N;
     constexpr int kCols = LaneChannels<NT, GATED>::kRun * 16;
-    const int64_t tile0 = (int64_t)blockIdx.x * kCols;
+    const int tile0 = blockIdx.x * kCols;
     const int e = blockIdx.y;
     if (e == p.E) {
         zero_outside<PARTS>(p, tile0, kCols, width, 64 * W);
@@ -182,28 +178,15 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
     if (lo >= hi) return;
 
     const LaneChannels<NT, GATED> ch(tile0, lane, p.N);
-    const int nfull = (int)(p.K / kChunkK);          // whole chunks
+    const int nfull = p.K / kChunkK;                 // whole chunks
     const int sh = lane_shift<BITS>(q);
     constexpr int kLW = kLaneWords<BITS>;
     constexpr int kXBytes = PARTS == 1 ? 2 : 4;
-    // words: a scalar base that moves with the step, and the lane's own 32-bit offsets
+    const uint32_t base = code_base<BITS>();
+    const int group_mask = (1 << p.lg_group) - 1;
     const uint32_t* words0 = p.packed + e * p.p_stride;
-    const int64_t step_words = BITS * p.ldp;
-    const uint32_t off[2] = {(uint32_t)(lane_word<BITS>(q) * p.ldp + ch.c0), (uint32_t)(lane_word2<BITS>(q) * p.ldp + ch.c0)};
+    const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     const float* scales = p.scales + e * p.s_stride;
-    // NT words (or scales) of one row: at the lane's channels, gated ones N / 2 further too
-    auto load_pieces = [&](const uint32_t* base, uint32_t at, uint32_t (&v)[NT], int64_t row = 0) {
-        constexpr int R = LaneChannels<NT, GATED>::kRun;
-        uint32_t a[R];
-        WordLoad<R>::run(base + row + at, a);
-#pragma unroll
-        for (int j = 0; j < R; ++j) v[j] = a[j];
-        if constexpr (GATED) {
-            WordLoad<R>::run(base + ch.half + row + at, a);
-#pragma unroll
-            for (int j = 0; j < R; ++j) v[R + j] = a[j];
-        }
-    };
 
     for (int64_t r0 = lo; r0 < hi; r0 += 16 * MT) {
         const char* xrow[MT];
@@ -219,16 +202,16 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
         RawOctet<PARTS> x[XR][MT];
         // The chunks' loads: whole chunks from scalar bases, without a bound in sight; the layer's last k apart.
         auto load_scales = [&](int step, int s) {
-            const int64_t g = step / p.group_steps;
-            const float* row = scales + (g < p.last_group ? g : p.last_group) * p.s_row;
-            load_pieces(reinterpret_cast<const uint32_t*>(row), (uint32_t)ch.c0, sc[s]);
+            const int g = step >> p.lg_group;
+            const float* row = scales + (int64_t)(g < p.last_group ? g : p.last_group) * p.s_row;
+            ch.words(reinterpret_cast<const uint32_t*>(row), ch.c0, sc[s]);
         };
         auto load_words = [&](int chunk, int s) {
             const int step = chunk * kChunkSteps + s;
-            const uint32_t* base = words0 + step * step_words;
+            const uint32_t* row = words0 + (int64_t)(step * BITS) * p.ldp;
 #pragma unroll
-            for (int l = 0; l < kLW; ++l) load_pieces(base, off[l], w[s][l]);
-            if (((s + 1) & (p.group_steps - 1)) == 0) load_scales(step, s);
+            for (int l = 0; l < kLW; ++l) ch.words(row, off[l], w[s][l]);
+            if (((s + 1) & group_mask) == 0) load_scales(step, s);
         };
         auto load_x = [&](int chunk, int s) {
             const int64_t k = ((int64_t)chunk * kChunkSteps + s) * kStepK;
@@ -242,9 +225,10 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+        constexpr int kMine = (kVals + W - 1) / W;   // items this wave will join
         f32x4 sum[MT], prt[MT][NT];
         auto multiply = [&](int s) {                 // step s of the chunk in w, x, sc
-            if ((s & (p.group_steps - 1)) == 0) {
+            if ((s & group_mask) == 0) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -265,14 +249,14 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh)
-                                            : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh);
+                const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base)
+                                            : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) prt[t][j] = mfma16(a[t][i], b, prt[t][j]);
             }
-            if (((s + 1) & (p.group_steps - 1)) == 0) {
+            if (((s + 1) & group_mask) == 0) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -315,11 +299,10 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
                 const int64_t k = (int64_t)step * kStepK;
 #pragma unroll
                 for (int t = 0; t < MT; ++t) x[s % XR][t].some(xrow[t] + k * kXBytes, p.K - k - 8 * q);
-                const uint32_t c0 = (uint32_t)ch.c0;
-                load_pieces(words0, c0, w[s][0], (int64_t)min(step * BITS + lane_word<BITS>(q), last) * p.ldp);
+                ch.words(words0, min(step * BITS + lane_word<BITS>(q), last) * p.ldp + ch.c0, w[s][0]);
                 if constexpr (kLW == 2)
-                    load_pieces(words0, c0, w[s][1], (int64_t)min(step * BITS + lane_word2<BITS>(q), last) * p.ldp);
-                if (((s + 1) & (p.group_steps - 1)) == 0) load_scales(step, s);
+                    ch.words(words0, min(step * BITS + lane_word2<BITS>(q), last) * p.ldp + ch.c0, w[s][1]);
+                if (((s + 1) & group_mask) == 0) load_scales(step, s);
                 multiply(s);
             }
         }
@@ -332,7 +315,10 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
 #pragma unroll
                 for (int j = 0; j < NT; ++j) part[wave][(t * 4 + i) * NT + j][lane] = acc[t][j][i];
         __syncthreads();
-        for (int v = wave; v < kVals; v += W) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int v = wave + m * W;
+            if (v >= kVals) break;
             float y[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) y[j] = 0.f;
@@ -358,43 +344,30 @@ __global__ __launch_bounds__(64 * W, (W == 16 || MT == 1) ? 4 : 2) void matmul_r
     }
 }
 
-// Channels per workgroup: 64, or 32 where 64 would leave CUs without a workgroup.
-template <int BITS, int PARTS, int MT, int W>
+// Waves share K: 16 of them where there are few workgroups (latency counts), 4 where there are many (several workgroups
+// per CU then cover each other's start and end).  Channels per workgroup: 64, or 32 where 64 leave CUs without one.
+template <int BITS, int PARTS, int W>
 hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
-    const int64_t width = swiglu ? k.N / 2 : k.N;
+    const int width = swiglu ? k.N / 2 : k.N;
     const unsigned ey = (unsigned)(k.E + (k.offsets ? 1 : 0));
-    if (swiglu) {
-        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kGated, W>), dim3((unsigned)ceil_div(width, 32), ey),
-                           dim3(64 * W), 0, stream, k);
-    } else if (ceil_div(width, 64) * k.E >= 224) {
-        const dim3 grid((unsigned)ceil_div(width, 64), ey);
-        if (k.H)
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kAdapters, W>), grid, dim3(64 * W), 0, stream, k);
-        else
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 4, kPlain, W>), grid, dim3(64 * W), 0, stream, k);
-    } else {
-        const dim3 grid((unsigned)ceil_div(width, 32), ey);
-        if (k.H)
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 2, kAdapters, W>), grid, dim3(64 * W), 0, stream, k);
-        else
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, MT, 2, kPlain, W>), grid, dim3(64 * W), 0, stream, k);
-    }
+    const bool wide = !swiglu && ceil_div(width, 64) * k.E >= 224;
+    const dim3 grid((unsigned)ceil_div(width, wide ? 64 : 32), ey), block(64 * W);
+#define GPTQ_ROWS(NT, FORM) \
+    hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, 1, NT, FORM, W>), grid, block, 0, stream, k)
+    if (swiglu) GPTQ_ROWS(4, kGated);
+    else if (wide && k.H) GPTQ_ROWS(4, kAdapters);
+    else if (wide) GPTQ_ROWS(4, kPlain);
+    else if (k.H) GPTQ_ROWS(2, kAdapters);
+    else GPTQ_ROWS(2, kPlain);
+#undef GPTQ_ROWS
     return hipGetLastError();
 }
 
 template <int BITS>
-hipError_t launch_rows(const MatmulKernelArgs& k, bool f32, int row_tiles, bool swiglu, hipStream_t stream) {
-    const int64_t wgs = ceil_div(k.N, 64) * k.E;
-    if (f32) {
-        if (row_tiles <= 1) return launch_rows_w<BITS, 3, 1, 8>(k, swiglu, stream);
-        return launch_rows_w<BITS, 3, 2, 8>(k, swiglu, stream);
-    }
-    if (row_tiles <= 1) {
-        if (wgs >= 1024) return launch_rows_w<BITS, 1, 1, 4>(k, swiglu, stream);
-        return launch_rows_w<BITS, 1, 1, 16>(k, swiglu, stream);
-    }
-    if (row_tiles <= 2) return launch_rows_w<BITS, 1, 2, 8>(k, swiglu, stream);
-    return launch_rows_w<BITS, 1, 4, 8>(k, swiglu, stream);
+hipError_t launch_rows(const MatmulKernelArgs& k, bool f32, bool swiglu, hipStream_t stream) {
+    if (f32) return launch_rows_w<BITS, 3, 8>(k, swiglu, stream);
+    if (ceil_div(k.N, 64) * k.E >= 1024) return launch_rows_w<BITS, 1, 4>(k, swiglu, stream);
+    return launch_rows_w<BITS, 1, 16>(k, swiglu, stream);
 }
 
 }  // namespace gptq

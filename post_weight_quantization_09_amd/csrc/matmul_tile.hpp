@@ -94,8 +94,7 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     if (e < 0) return;
     const int64_t r0 = p.tiles[3 * tm + 1], r1 = p.tiles[3 * tm + 2];
     constexpr int kRun = LaneChannels<NT, GATED>::kRun;
-    const int64_t col0 = (int64_t)tn * (64 * kRun) + wave * (16 * kRun);
-    const int64_t width = GATED ? p.N / 2 : p.N;
+    const int col0 = tn * (64 * kRun) + wave * (16 * kRun);
     const LaneChannels<NT, GATED> ch(col0, lane, p.N);
     if (e == p.E) {                                  // rows of no expert
         float z[kRun];
@@ -106,23 +105,25 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     }
     const uint32_t* words = p.packed + e * p.p_stride;
     const float* scales = p.scales + e * p.s_stride;
-    const int nchunks = (int)((p.K + kChunkK - 1) / kChunkK);
+    const int nchunks = (p.K + kChunkK - 1) / kChunkK;
     const int last_word = p.nwords - 1;
     const int wa = lane_word<BITS>(q), wb = lane_word2<BITS>(q), sh = lane_shift<BITS>(q);
     constexpr int kLW = kLaneWords<BITS>;
+    const uint32_t base = code_base<BITS>();
     uint32_t w[kChunkSteps][kLW][NT];
-    float sc[kGroups][NT];
+    uint32_t sc[kGroups][NT];
     auto load_words = [&](int chunk) {
 #pragma unroll
         for (int s = 0; s < kChunkSteps; ++s) {
             const int at = (chunk * kChunkSteps + s) * BITS;
-            ch.words(words + (int64_t)min(at + wa, last_word) * p.ldp, w[s][0]);
-            if constexpr (kLW == 2) ch.words(words + (int64_t)min(at + wb, last_word) * p.ldp, w[s][1]);
+            ch.words(words, min(at + wa, last_word) * p.ldp + ch.c0, w[s][0]);
+            if constexpr (kLW == 2) ch.words(words, min(at + wb, last_word) * p.ldp + ch.c0, w[s][1]);
         }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            const int64_t at = (int64_t)chunk * kGroups + g;
-            ch.scales(scales + (at < p.last_group ? at : p.last_group) * p.s_row, sc[g]);
+            const int at = chunk * kGroups + g;
+            const float* row = scales + (int64_t)(at < p.last_group ? at : p.last_group) * p.s_row;
+            ch.words(reinterpret_cast<const uint32_t*>(row), ch.c0, sc[g]);
         }
     };
     const int64_t noct = (int64_t)nchunks * kOctets;
@@ -167,13 +168,13 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
         for (int s = 0; s < kChunkSteps; ++s)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                b[s][j] = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh)
-                                     : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh);
+                b[s][j] = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base)
+                                     : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base);
         float f[kGroups][NT];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) f[g][j] = sc[g][j];
+            for (int j = 0; j < NT; ++j) f[g][j] = __uint_as_float(sc[g][j]);
         if (c + 1 < nchunks) {
             stage(c + 1, buf ^ 1);
             load_words(c + 1);
@@ -236,8 +237,8 @@ hipError_t launch_tile_rt(const MatmulKernelArgs& k, int ntm, bool swiglu, hipSt
     hipLaunchKernelGGL((matmul_tile_kernel<BITS, PARTS, RT, GS, FORM>), dim3(grid), dim3(256), 0, stream, k, ntn, ntm)
 #define GPTQ_TILE_FORM(FORM)                        \
     do {                                            \
-        if (k.group_steps == 1) GPTQ_TILE(1, FORM); \
-        else if (k.group_steps == 2) GPTQ_TILE(2, FORM); \
+        if (k.lg_group == 0) GPTQ_TILE(1, FORM); \
+        else if (k.lg_group == 1) GPTQ_TILE(2, FORM); \
         else GPTQ_TILE(4, FORM);                    \
     } while (0)
     if (swiglu) GPTQ_TILE_FORM(kGated);

@@ -53,21 +53,29 @@ __device__ __forceinline__ uint32_t shl_signed(uint32_t v) {
     else return v >> (-S);
 }
 
+// 2^b in both halves of a vector register: with it there, and the mask in a scalar one, and-or is one instruction (a
+// VALU instruction of gfx950 reads one scalar or literal at most).
+template <int BITS>
+__device__ __forceinline__ uint32_t code_base() {
+    uint32_t base = ((uint32_t)(127 + BITS) << 7) * 0x10001u;
+    asm("" : "+v"(base));
+    return base;
+}
+
 template <int BITS, int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi) {
-    constexpr uint32_t m = ((1u << BITS) - 1u) << (7 - BITS);
-    constexpr uint32_t base = (uint32_t)(127 + BITS) << 7;
+__device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi, uint32_t base) {
+    constexpr uint32_t m = (((1u << BITS) - 1u) << (7 - BITS)) * 0x10001u;
     if constexpr (BITS <= 4) {                // lo holds codes 0..3 from bit 0 and codes 4..7 from bit 16
-        return (shl_signed<7 - BITS - BITS * I>(lo) & (m | (m << 16))) | (base | (base << 16));
+        return (shl_signed<7 - BITS - BITS * I>(lo) & m) | base;
     } else {
         const uint32_t a = shl_signed<7 - BITS - BITS * I>(lo), b = shl_signed<23 - BITS - BITS * I>(hi);
-        return (((a & 0xFFFFu) | (b & 0xFFFF0000u)) & (m | (m << 16))) | (base | (base << 16));
+        return (((a & 0xFFFFu) | (b & 0xFFFF0000u)) & m) | base;
     }
 }
 
 // Eight codes (in words w0, w1 at bit `sh`) -> bf16 values 2^b + c, register i = codes (i, i + 4).
 template <int BITS>
-__device__ __forceinline__ bf16x8 codes_to_frag(uint32_t w0, uint32_t w1, int sh) {
+__device__ __forceinline__ bf16x8 codes_to_frag(uint32_t w0, uint32_t w1, int sh, uint32_t base) {
     uint32_t lo, hi = 0;
     if constexpr (BITS == 4) {
         lo = w0;
@@ -84,18 +92,18 @@ __device__ __forceinline__ bf16x8 codes_to_frag(uint32_t w0, uint32_t w1, int sh
         }
     }
     u32x4 r;
-    r[0] = code_pair<BITS, 0>(lo, hi);
-    r[1] = code_pair<BITS, 1>(lo, hi);
-    r[2] = code_pair<BITS, 2>(lo, hi);
-    r[3] = code_pair<BITS, 3>(lo, hi);
+    r[0] = code_pair<BITS, 0>(lo, hi, base);
+    r[1] = code_pair<BITS, 1>(lo, hi, base);
+    r[2] = code_pair<BITS, 2>(lo, hi, base);
+    r[3] = code_pair<BITS, 3>(lo, hi, base);
     return __builtin_bit_cast(bf16x8, r);
 }
 
 // The same as bf16 values c - z: the excess taken off in fp32 (both steps exact), five more operations per pair.
 template <int BITS>
-__device__ __forceinline__ bf16x8 codes_to_exact_frag(uint32_t w0, uint32_t w1, int sh) {
+__device__ __forceinline__ bf16x8 codes_to_exact_frag(uint32_t w0, uint32_t w1, int sh, uint32_t base) {
     constexpr float excess = 1.5f * (float)(1 << BITS);
-    const u32x4 v = __builtin_bit_cast(u32x4, codes_to_frag<BITS>(w0, w1, sh));
+    const u32x4 v = __builtin_bit_cast(u32x4, codes_to_frag<BITS>(w0, w1, sh, base));
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)

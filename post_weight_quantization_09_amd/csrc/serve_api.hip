@@ -25,6 +25,8 @@ bool layer_ok(const void* X, gptq_dtype_t dtype, int64_t x_rows, int64_t ldx, in
     if (N < 4 || N > kMaxN || bits < 2 || bits > 6 || ldp < N || ldx < K || ldy < width) return false;
     if (groupsize != 0 && groupsize != 32 && groupsize != 64 && groupsize != 128) return false;
     if (M > 0 && (!X || !Y || X == Y || x_rows < 1)) return false;
+    // the kernels address an expert's words by 32-bit byte offsets
+    if ((K * bits + 31) / 32 * ldp > ((int64_t)1 << 30)) return false;
     return ceil_div(M, 64) * ceil_div(N, 128) < (int64_t)1 << 30;
 }
 
