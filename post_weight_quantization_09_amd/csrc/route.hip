@@ -2,8 +2,9 @@
 //
 // Routing, per token t: p = softmax(logits_t); the topk experts with the largest p (ties: the lowest index), weights p
 // or p over their sum; then a stable counting sort of the (token, choice) pairs by expert.  Bound by latency: the data
-// are a few hundred bytes per token.  One wave takes a token: its logits stay in registers (E / 64 per lane), and every
-// choice is one maximum over the wave of a 64-bit key (ordered bits of the logit, then the index reversed).  The sort
+// are a few hundred bytes per token.  One wave takes a token: its logits stay in registers (E / 64 per lane) as
+// integers in the order of the values, and every choice is one maximum over the wave (six DPP steps, no LDS) and the
+// first lane that holds it.  The sort
 // needs, per block of kBlockTokens tokens and expert, which tokens chose it: a bitmap in LDS, whose popcounts are both
 // the block's count and the token's rank, whatever order the waves ran in.  Up to one block of tokens everything is one
 // launch; else a second launch adds up the blocks' counts (each block for itself, from L2) and places the rows.
@@ -33,13 +34,17 @@ struct RouteArgs {
     int nblocks;
 };
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t k) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint64_t o = __shfl_xor(k, d);
-        k = o > k ? o : k;
-    }
-    return k;
+// Maximum over the wave, by data-parallel moves: within rows of 16 lanes, then across them; lane 63 has it.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define GPTQ_DPP_MAX(CTRL) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false))
+    GPTQ_DPP_MAX(0x111);   // from 1, 2, 4, 8 lanes below
+    GPTQ_DPP_MAX(0x112);
+    GPTQ_DPP_MAX(0x114);
+    GPTQ_DPP_MAX(0x118);
+    GPTQ_DPP_MAX(0x142);   // lane 15 of each row to the next row
+    GPTQ_DPP_MAX(0x143);   // lane 31 to the upper half
+#undef GPTQ_DPP_MAX
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -83,59 +88,74 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * kBlockTokens;
     const int nt = (int)(p.T - t0 < kBlockTokens ? p.T - t0 : kBlockTokens);
-    for (int i = wave; i < nt; i += kRouteWaves) {
-        const int64_t t = t0 + i;
-        float x[V];
-        bool wrong = false;
-        float top = -INFINITY;
+    constexpr int kTurns = kBlockTokens / kRouteWaves;
+    float all[kTurns][V];                             // the wave's tokens, loaded together
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+        const int64_t t = t0 + min(wave + u * kRouteWaves, nt - 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = 64 * v + lane;
-            x[v] = -INFINITY;
+            all[u][v] = -INFINITY;
             if (e < p.E) {
-                if (F32) x[v] = static_cast<const float*>(p.logits)[t * p.ld + e];
-                else x[v] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.logits)[t * p.ld + e] << 16);
-                wrong |= !(x[v] < INFINITY);
+                if (F32) all[u][v] = static_cast<const float*>(p.logits)[t * p.ld + e];
+                else all[u][v] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.logits)[t * p.ld + e] << 16);
             }
-            top = fmaxf(top, x[v]);
         }
+    }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int u = 0; u < kTurns; ++u) {
+        const int i = wave + u * kRouteWaves;
+        if (i >= nt) break;
+        const int64_t t = t0 + i;
+        const float (&x)[V] = all[u];
+        uint32_t key[V];                              // 0: not to be chosen (any more)
+        bool wrong = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            wrong |= !(x[v] < INFINITY);
+            key[v] = x[v] > -INFINITY ? ordered(x[v]) : 0u;
+        }
         if (__any(wrong)) {                           // NaN or +infinity: reported, and the token chooses nothing
             if (lane == 0) atomicOr(&bad, 1u);
-            top = -INFINITY;
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = -INFINITY;
+            for (int v = 0; v < V; ++v) key[v] = 0;
         }
-        float sum = 0.f;
-        if (!p.renorm && top > -INFINITY) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum += expf(x[v] - top);
-            sum = wave_sum(sum);
-        }
-        // choice j ends up in lane j
+        // choice j ends up in lane j, its exponential is taken there at the end
         int mine = -1;
-        float weight = 0.f;
+        uint32_t mine_key = 0, top_key = 0;
         for (int j = 0; j < p.topk; ++j) {
-            uint64_t key = 0;
+            uint32_t k = key[0];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const uint64_t k = ((uint64_t)ordered(x[v]) << 32) | (uint32_t) ~(64 * v + lane);
-                if (x[v] > -INFINITY && k > key) key = k;
+            for (int v = 1; v < V; ++v) k = max(k, key[v]);
+            k = wave_max(k);
+            if (k == 0) break;
+            if (j == 0) top_key = k;
+            int e = -1;                               // the first expert with this logit
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                const uint64_t has = __ballot(key[v] == k);
+                if (has) e = 64 * v + __builtin_ctzll(has);
             }
-            key = wave_max(key);
-            if (key == 0) break;
-            const int e = (int)~(uint32_t)key;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (64 * v + lane == e) x[v] = -INFINITY;
-            const float w = expf(unordered((uint32_t)(key >> 32)) - top);
-            if (p.renorm) sum += w;
+                if (64 * v + lane == e) key[v] = 0;
             if (lane == j) {
                 mine = e;
-                weight = w;
+                mine_key = k;
             }
         }
+        const float top = unordered(top_key);
+        const float weight = mine >= 0 ? expf(unordered(mine_key) - top) : 0.f;
+        float sum = weight;
+        if (!p.renorm) {
+            sum = 0.f;
+            if (top_key) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) sum += expf(x[v] - top);
+            }
+        }
+        sum = wave_sum(sum);
         if (lane < p.topk) {
             p.experts[t * p.topk + lane] = mine;
             p.weights[t * p.topk + lane] = mine >= 0 ? weight / sum : 0.f;
