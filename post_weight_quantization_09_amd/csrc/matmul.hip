@@ -19,7 +19,8 @@ struct StageArgs {
     float excess;          // -1.5 2^b
     int tile, cap;         // rows of a tile, entries of the list
     int32_t* tiles;
-    int row_blocks;        // workgroups of the rows: row_blocks x chunks (0: rows are not laid out)
+    int row_blocks;        // workgroups of the rows: row_blocks x nchunks (0: rows are not laid out)
+    int nchunks;
     // adapters
     const uint16_t* A;
     int64_t lda, a_stride;
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(kStageThreads) void stage_kernel(MatmulKernelArgs p
         }
         b -= n;
     }
-    const int nchunks = (p.K + kChunkK - 1) / kChunkK;
+    const int nchunks = a.nchunks;
     if (b == (int64_t)a.row_blocks * nchunks) {
         list_tiles(p, a);
         return;
@@ -293,7 +294,7 @@ int split_row_tiles(bool f32, int64_t mean, int bits, int groupsize) {
 Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank, int bits, int groupsize) {
     Plan p;
     const int64_t mean = ceil_div(M, experts);
-    const int big = f32 ? 64 : 128;
+    const int big = f32 ? 64 : 112;
     if (mean <= 16) {
         p.kernel = kRows;
         p.tile = 16;
@@ -384,6 +385,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
         int64_t grid = 0;
         if (plan.kernel != kRows) {
             s.row_blocks = (int)ceil_div(a.M, kStageRows);
+            s.nchunks = plan.nchunks;
             grid = (int64_t)s.row_blocks * plan.nchunks + 1;
         }
         if (lora) {

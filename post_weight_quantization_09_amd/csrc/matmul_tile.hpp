@@ -1,9 +1,12 @@
 // Product of many rows with packed weights: a prompt's rows, an expert with many rows.
 //
 // What bounds it: the matrix cores (2 M K N operations against half a byte per weight).  One workgroup of four waves owns
-// TM rows of one expert and 256 channels; every wave holds its own 64 channels for all TM rows, so no code is converted
-// twice in a workgroup: the words of a 128-k chunk come straight from global memory into registers as operands (nothing
-// of the weights passes through LDS) and serve TM / 16 row tiles.  The rows are laid out once per call by
+// 16 RT rows of one expert and 256 channels; every wave holds its own 64 channels for all the rows, so no code is
+// converted twice in a workgroup: the words of a 128-k chunk come straight from global memory into registers as operands
+// (nothing of the weights passes through LDS) and serve RT row tiles.  Seven of them: the 256 registers that two waves
+// per SIMD leave each then hold the sums, the chunk's operands and the next step's rows; eight leave no room to read rows
+// ahead (experts 8192 x 28672 x 4096: 1.91 ms against 2.05; adapters 4096 x 8192 x 28672: 2.06 against 2.80), and one
+// wave per SIMD with 512 registers is slower (3.1 ms: half of them are accumulation registers, which cost moves).  The rows are laid out once per call by
 // stage_rows_kernel: octets of k in the converted operand's order, [K / 8][row], so that a chunk is 16 contiguous
 // pieces, copied to LDS by DMA and read back as 16-byte operands without bank conflicts; rows are gathered and fp32 rows
 // split in the same pass, and it leaves the row sums that take the codes' excess off again as the accumulators' start (bf16 rows).
@@ -14,6 +17,23 @@
 namespace gptq {
 
 typedef __attribute__((address_space(3))) void lds_dma_t;
+
+// 64 lanes x BYTES from global memory (a uniform address and the lane's byte offset) into LDS at `lds` + BYTES * lane.
+// The instruction itself and not the compiler's builtin: after the builtin every LDS read waits until the copy has landed,
+// also one from the other buffer (2.05 against 1.80 ms without any copy, 8192 rows x 28672 channels x 4096).  It has no
+// result registers; the kernel waits for it (vmcnt(0) before the barrier after which the buffer is read).  M0, which the
+// compiler may be using, is put back.
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(const void* src, uint32_t off, void* lds) {
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_dma_t*)lds;
+    uint32_t m0;
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0) : "s"(at), "v"(off), "s"(src) : "memory");
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0) : "s"(at), "v"(off), "s"(src) : "memory");
+}
 
 constexpr int kTileCols = 256;         // channels of a workgroup (outputs: half of them when gated)
 constexpr int kTileGroup = 8;          // row tiles that neighbouring workgroups share a weight tile for
@@ -74,7 +94,7 @@ __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, cons
 template <int BITS, int PARTS, int RT, int GS, int FORM>
 __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(MatmulKernelArgs p, int ntn, int ntm) {
     constexpr bool GATED = FORM == kGated;
-    constexpr int NT = 4, TM = 16 * RT, kGroups = kChunkSteps / GS;
+    constexpr int NT = 4, TM = (16 * RT + 63) / 64 * 64, kGroups = kChunkSteps / GS;
     constexpr int kOctets = kChunkK / 8;
     __shared__ __attribute__((aligned(1024))) uint16_t xs[2][PARTS][kOctets][TM][8];
     __shared__ __attribute__((aligned(1024))) float ss[2][kGroups][PARTS == 1 ? TM : 1];
@@ -107,17 +127,28 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     const float* scales = p.scales + e * p.s_stride;
     const int nchunks = (p.K + kChunkK - 1) / kChunkK;
     const int last_word = p.nwords - 1;
-    const int wa = lane_word<BITS>(q), wb = lane_word2<BITS>(q), sh = lane_shift<BITS>(q);
+    const int sh = lane_shift<BITS>(q);
+    const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     constexpr int kLW = kLaneWords<BITS>;
     const uint32_t base = code_base<BITS>();
     uint32_t w[kChunkSteps][kLW][NT];
     uint32_t sc[kGroups][NT];
     auto load_words = [&](int chunk) {
+        if ((chunk + 1) * kChunkSteps * BITS <= p.nwords) {
 #pragma unroll
-        for (int s = 0; s < kChunkSteps; ++s) {
-            const int at = (chunk * kChunkSteps + s) * BITS;
-            ch.words(words, min(at + wa, last_word) * p.ldp + ch.c0, w[s][0]);
-            if constexpr (kLW == 2) ch.words(words, min(at + wb, last_word) * p.ldp + ch.c0, w[s][1]);
+            for (int s = 0; s < kChunkSteps; ++s) {
+                const uint32_t* row = words + (int64_t)((chunk * kChunkSteps + s) * BITS) * p.ldp;
+#pragma unroll
+                for (int l = 0; l < kLW; ++l) ch.words(row, off[l], w[s][l]);
+            }
+        } else {                                     // past the layer's last word x is zero
+#pragma unroll
+            for (int s = 0; s < kChunkSteps; ++s) {
+                const int at = (chunk * kChunkSteps + s) * BITS;
+                ch.words(words, min(at + lane_word<BITS>(q), last_word) * p.ldp + ch.c0, w[s][0]);
+                if constexpr (kLW == 2)
+                    ch.words(words, min(at + lane_word2<BITS>(q), last_word) * p.ldp + ch.c0, w[s][1]);
+            }
         }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
@@ -136,8 +167,8 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
             const int part = pc / (kOctets * kRowPieces), rest = pc % (kOctets * kRowPieces);
             const int o = rest / kRowPieces, h = rest % kRowPieces;
             const uint16_t* src =
-                p.XT + ((part * noct + (int64_t)chunk * kOctets + o) * p.Mp + r0 + 64 * h + lane) * 8;
-            __builtin_amdgcn_global_load_lds((const void*)src, (lds_dma_t*)&xs[buf][part][o][64 * h][0], 16, 0, 0);
+                p.XT + ((part * noct + (int64_t)chunk * kOctets + o) * p.Mp + r0 + 64 * h) * 8;
+            copy_to_lds<16>(src, 16 * lane, &xs[buf][part][o][64 * h][0]);
         }
         constexpr int kSumPieces = PARTS == 1 ? kGroups * kRowPieces : 0;
 #pragma unroll
@@ -145,8 +176,8 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
             const int pc = wave + 4 * i;
             if (pc < kSumPieces) {
                 const int g = pc / kRowPieces, h = pc % kRowPieces;
-                const float* src = p.sums + ((int64_t)chunk * kGroups + g) * p.Mp + r0 + 64 * h + lane;
-                __builtin_amdgcn_global_load_lds((const void*)src, (lds_dma_t*)&ss[buf][g][PARTS == 1 ? 64 * h : 0], 4, 0, 0);
+                const float* src = p.sums + ((int64_t)chunk * kGroups + g) * p.Mp + r0 + 64 * h;
+                copy_to_lds<4>(src, 4 * lane, &ss[buf][g][PARTS == 1 ? 64 * h : 0]);
             }
         }
     };
@@ -179,28 +210,39 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
             stage(c + 1, buf ^ 1);
             load_words(c + 1);
         }
+        // one step of one row tile after the other, its successor's rows on their way out of LDS meanwhile; the order is
+        // pinned (left alone, the scheduler puts every read right before its use)
+        u32x4 a[2][PARTS];
+        f32x4 start[2], prt[NT];
+        auto read_rows = [&](int k, int set) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
+            for (int i = 0; i < PARTS; ++i)
+                a[set][i] = *reinterpret_cast<const u32x4*>(&xs[buf][i][4 * (k % kChunkSteps) + q][16 * (k / kChunkSteps) + (lane & 15)][0]);
+        };
+        auto read_start = [&](int u, int set) {      // of group u, row tile by row tile
+            start[set] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (PARTS == 1)
+                start[set] = *reinterpret_cast<const f32x4*>(&ss[buf][u % kGroups][16 * (u / kGroups) + 4 * q]);
+        };
+        read_rows(0, 0);
+        read_start(0, 0);
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                f32x4 start = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (PARTS == 1) start = *reinterpret_cast<const f32x4*>(&ss[buf][g][16 * t + 4 * q]);
-                f32x4 prt[NT];
+        for (int k = 0; k < RT * kChunkSteps; ++k) {
+            const int t = k / kChunkSteps, s = k % kChunkSteps, u = k / GS;
+            __builtin_amdgcn_sched_barrier(0);
+            if (k + 1 < RT * kChunkSteps) read_rows(k + 1, (k + 1) & 1);
+            if (k % GS == GS - 1 && u + 1 < RT * kGroups) read_start(u + 1, (u + 1) & 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) prt[j] = start;
+            for (int i = 0; i < PARTS; ++i)
 #pragma unroll
-                for (int s = g * GS; s < (g + 1) * GS; ++s)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        const u32x4 a =
-                            *reinterpret_cast<const u32x4*>(&xs[buf][i][4 * s + q][16 * t + (lane & 15)][0]);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) prt[j] = mfma16(a, b[s][j], prt[j]);
-                    }
+                for (int j = 0; j < NT; ++j)
+                    prt[j] = mfma16(a[k & 1][i], b[s][j], k % GS == 0 && i == 0 ? start[u & 1] : prt[j]);
+            if (k % GS == GS - 1) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(f[g][j], prt[j][i], acc[t][j][i]);
+                    for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(f[s / GS][j], prt[j][i], acc[t][j][i]);
             }
         }
     }
@@ -253,7 +295,7 @@ template <int BITS>
 hipError_t launch_tile(const MatmulKernelArgs& k, bool f32, int row_tiles, int ntm, bool swiglu, hipStream_t stream) {
     if (f32) return launch_tile_rt<BITS, 3, 4>(k, ntm, swiglu, stream);
     if (row_tiles <= 4) return launch_tile_rt<BITS, 1, 4>(k, ntm, swiglu, stream);
-    return launch_tile_rt<BITS, 1, 8>(k, ntm, swiglu, stream);
+    return launch_tile_rt<BITS, 1, 7>(k, ntm, swiglu, stream);
 }
 
 }  // namespace gptq
