@@ -3,9 +3,8 @@
 // What bounds it: the packed words are read once from HBM; for up to 16 rows per expert there are at most 32 operations
 // per weight, far below what the matrix cores do in the time of its half byte.  So one workgroup owns 16 NT channels of
 // one expert over all K, its W waves take the 128-k chunks in turn (each wave's words come straight into registers as
-// MFMA operands, the next chunk's loads in flight while one is multiplied), and the W partial sums are joined in LDS in
-// a fixed order: no second launch, no partials in memory, the same bits every time.  MT row tiles of 16 share a wave's
-// operands; more rows than 16 MT loop.
+// MFMA operands, the next chunks' loads in flight while one is multiplied), and the W partial sums are joined in LDS in
+// a fixed order: no second launch, no partials in memory, the same bits every time.  More than 16 rows loop.
 #pragma once
 
 #include "matmul.hpp"
@@ -157,12 +156,12 @@ __device__ __forceinline__ void add_adapter_row(const MatmulKernelArgs& p, int64
 // FORM of a product: plain, gated pairs of channels, or plain with adapters.
 enum { kPlain = 0, kGated = 1, kAdapters = 2 };
 
-template <int BITS, int PARTS, int MT, int NT, int FORM, int W>
-__global__ __launch_bounds__(64 * W, PARTS == 1 ? 4 : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
+template <int BITS, int PARTS, int NT, int GS, int FORM, int W>
+__global__ __launch_bounds__(64 * W, PARTS == 1 ? (W == 16 ? 4 : 3) : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
     constexpr bool GATED = FORM == kGated;
-    constexpr int kVals = MT * 4;                    // (row tile, register) items of NT channels
-    constexpr int XR = MT * PARTS >= 4 ? 2 : 4;      // steps of rows in flight
-    __shared__ float part[W][kVals * NT][64];
+    constexpr int kLW = kLaneWords<BITS>;
+    constexpr int kXBytes = PARTS == 1 ? 2 : 4, kGroups = kChunkSteps / GS;
+    __shared__ float part[W][4 * NT][64];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int width = GATED ? p.N / 2 : p.N;
@@ -180,153 +179,115 @@ __global__ __launch_bounds__(64 * W, PARTS == 1 ? 4 : 2) void matmul_rows_kernel
     const LaneChannels<NT, GATED> ch(tile0, lane, p.N);
     const int nfull = p.K / kChunkK;                 // whole chunks
     const int sh = lane_shift<BITS>(q);
-    constexpr int kLW = kLaneWords<BITS>;
-    constexpr int kXBytes = PARTS == 1 ? 2 : 4;
     const uint32_t base = code_base<BITS>();
-    const int group_mask = (1 << p.lg_group) - 1;
     const uint32_t* words0 = p.packed + e * p.p_stride;
     const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     const float* scales = p.scales + e * p.s_stride;
 
-    for (int64_t r0 = lo; r0 < hi; r0 += 16 * MT) {
-        const char* xrow[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            int64_t r = r0 + 16 * t + (lane & 15);
-            if (r >= hi) r = hi - 1;                 // a row past the end repeats the last one and is not stored
-            const int64_t s = source_row(p, r);
-            xrow[t] = static_cast<const char*>(p.X) + ((s < 0 ? 0 : s) * p.ldx + 8 * q) * kXBytes;
-        }
-        uint32_t w[kChunkSteps][kLW][NT];
-        uint32_t sc[kChunkSteps][NT];
-        RawOctet<PARTS> x[XR][MT];
-        // The chunks' loads: whole chunks from scalar bases, without a bound in sight; the layer's last k apart.
-        auto load_scales = [&](int step, int s) {
-            const int g = step >> p.lg_group;
+    for (int64_t r0 = lo; r0 < hi; r0 += 16) {
+        // words, scales and rows one of the wave's chunks ahead: each step's registers are loaded again as soon as they
+        // have been used
+        uint32_t w[kChunkSteps][kLW][NT], sc[kGroups][NT];
+        RawOctet<PARTS> x[kChunkSteps];
+        auto load_scales = [&](int step, uint32_t (&v)[NT]) {
+            const int g = step / GS;
             const float* row = scales + (int64_t)(g < p.last_group ? g : p.last_group) * p.s_row;
-            ch.words(reinterpret_cast<const uint32_t*>(row), ch.c0, sc[s]);
+            ch.words(reinterpret_cast<const uint32_t*>(row), ch.c0, v);
         };
         auto load_words = [&](int chunk, int s) {
             const int step = chunk * kChunkSteps + s;
             const uint32_t* row = words0 + (int64_t)(step * BITS) * p.ldp;
 #pragma unroll
             for (int l = 0; l < kLW; ++l) ch.words(row, off[l], w[s][l]);
-            if (((s + 1) & group_mask) == 0) load_scales(step, s);
+            if ((s + 1) % GS == 0) load_scales(step, sc[s / GS]);
         };
-        auto load_x = [&](int chunk, int s) {
-            const int64_t k = ((int64_t)chunk * kChunkSteps + s) * kStepK;
+        int64_t mine = r0 + (lane & 15);
+        if (mine >= hi) mine = hi - 1;               // a row past the end repeats the last one and is not stored
+        const int64_t src = source_row(p, mine);
+        const char* xrow = static_cast<const char*>(p.X) + ((src < 0 ? 0 : src) * p.ldx + 8 * q) * kXBytes;
+        auto load_x = [&](int chunk, int s) { x[s].whole(xrow + (chunk * kChunkSteps + s) * (kStepK * kXBytes)); };
+        if (wave < nfull) {                          // in the order of the loop: the waits count loads
 #pragma unroll
-            for (int t = 0; t < MT; ++t) x[s % XR][t].whole(xrow[t] + k * kXBytes);
+            for (int s = 0; s < kChunkSteps; ++s) {
+                load_x(wave, s);
+                load_words(wave, s);
+            }
+        }
+
+        f32x4 acc[NT], sum, prt[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto clear = [&] {
+            sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) prt[j] = f32x4{0.f, 0.f, 0.f, 0.f};
         };
-
-        f32x4 acc[MT][NT];
+        auto multiply = [&](const RawOctet<PARTS>& rows, const uint32_t (&v)[kLW][NT]) {
+            u32x4 a[PARTS];
+            rows.parts(a);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-        constexpr int kMine = (kVals + W - 1) / W;   // items this wave will join
-        f32x4 sum[MT], prt[MT][NT];
-        auto multiply = [&](int s) {                 // step s of the chunk in w, x, sc
-            if ((s & group_mask) == 0) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) prt[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-            }
-            u32x4 a[MT][PARTS];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                x[s % XR][t].parts(a[t]);
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) a[t][i] = pair_order(a[t][i]);
-            }
-            if constexpr (PARTS == 1) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t) sum[t] = mfma16(a[t][0], minus_excess_frag<BITS>(), sum[t]);
-            }
+            for (int i = 0; i < PARTS; ++i) a[i] = pair_order(a[i]);
+            if constexpr (PARTS == 1) sum = mfma16(a[0], minus_excess_frag<BITS>(), sum);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base)
-                                            : codes_to_exact_frag<BITS>(w[s][0][j], w[s][kLW - 1][j], sh, base);
+                const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(v[0][j], v[kLW - 1][j], sh, base)
+                                            : codes_to_exact_frag<BITS>(v[0][j], v[kLW - 1][j], sh, base);
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) prt[t][j] = mfma16(a[t][i], b, prt[t][j]);
-            }
-            if (((s + 1) & group_mask) == 0) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[t][j][i] = fmaf(__uint_as_float(sc[s][j]), prt[t][j][i] + sum[t][i], acc[t][j][i]);
+                for (int i = 0; i < PARTS; ++i) prt[j] = mfma16(a[i], b, prt[j]);
             }
         };
-        if (wave < nfull) {
+        auto add = [&](const uint32_t (&f)[NT]) {
 #pragma unroll
-            for (int s = 0; s < XR; ++s) load_x(wave, s);
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int s = 0; s < kChunkSteps; ++s) load_words(wave, s);
-        }
-        int c = wave;
-        for (; c + W < nfull; c += W) {
+                for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(__uint_as_float(f[j]), prt[j][i] + sum[i], acc[j][i]);
+        };
+        for (int c = wave; c < nfull; c += W) {
+            const bool more = c + W < nfull;
 #pragma unroll
             for (int s = 0; s < kChunkSteps; ++s) {
-                multiply(s);
-                load_x(s + XR < kChunkSteps ? c : c + W, (s + XR) % kChunkSteps);
-                load_words(c + W, s);
+                if (s % GS == 0) clear();
+                multiply(x[s], w[s]);
+                if ((s + 1) % GS == 0) add(sc[s / GS]);
+                __builtin_amdgcn_sched_barrier(0);   // loads moved up would need registers of their own
+                if (more) {
+                    load_x(c + W, s);
+                    load_words(c + W, s);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (c < nfull) {
-#pragma unroll
-            for (int s = 0; s < kChunkSteps; ++s) {
-                multiply(s);
-                if (s + XR < kChunkSteps) load_x(c, s + XR);
-            }
-            c += W;
-        }
-        if (nfull * kChunkK < p.K && nfull % W == wave) {       // the rest of K: past its end x is zero
-            const int last = p.nwords - 1;
-            int step0 = nfull * kChunkSteps;
-            asm volatile("" : "+s"(step0));          // keeps this part's addresses from being computed ahead of the loop
-#pragma unroll
-            for (int s = 0; s < kChunkSteps; ++s) {
-                const int step = step0 + s;
-                const int64_t k = (int64_t)step * kStepK;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) x[s % XR][t].some(xrow[t] + k * kXBytes, p.K - k - 8 * q);
-                ch.words(words0, min(step * BITS + lane_word<BITS>(q), last) * p.ldp + ch.c0, w[s][0]);
+        if (nfull % W == wave) {                     // the rest of K, a step at a time: past its end x is zero
+            for (int step = nfull * kChunkSteps; step * kStepK < p.K; ++step) {
+                const int last = p.nwords - 1;
+                uint32_t v[kLW][NT], f[NT];
+                RawOctet<PARTS> rows;
+                rows.some(xrow + step * (kStepK * kXBytes), p.K - step * kStepK - 8 * q);
+                ch.words(words0, min(step * BITS + lane_word<BITS>(q), last) * p.ldp + ch.c0, v[0]);
                 if constexpr (kLW == 2)
-                    ch.words(words0, min(step * BITS + lane_word2<BITS>(q), last) * p.ldp + ch.c0, w[s][1]);
-                if (((s + 1) & group_mask) == 0) load_scales(step, s);
-                multiply(s);
+                    ch.words(words0, min(step * BITS + lane_word2<BITS>(q), last) * p.ldp + ch.c0, v[1]);
+                load_scales(step, f);
+                clear();
+                multiply(rows, v);
+                add(f);
             }
         }
 
         if (r0 != lo) __syncthreads();               // the previous rows' partials have been read
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) part[wave][(t * 4 + i) * NT + j][lane] = acc[t][j][i];
+            for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[j][i];
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-            const int v = wave + m * W;
-            if (v >= kVals) break;
+        if (wave < 4) {                              // row register `wave` of every lane
             float y[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) y[j] = 0.f;
 #pragma unroll
             for (int s = 0; s < W; ++s)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) y[j] += part[s][v * NT + j][lane];
-            const int64_t r = r0 + 16 * (v >> 2) + 4 * q + (v & 3);
+                for (int j = 0; j < NT; ++j) y[j] += part[s][wave * NT + j][lane];
+            const int64_t r = r0 + 4 * q + wave;
             if (r < hi) {
                 if constexpr (FORM == kAdapters) add_adapter_row<NT, GATED>(p, r, ch, y);
                 const bool real = source_row(p, r) >= 0;
@@ -345,15 +306,23 @@ __global__ __launch_bounds__(64 * W, PARTS == 1 ? 4 : 2) void matmul_rows_kernel
 }
 
 // Waves share K: 16 of them where there are few workgroups (latency counts), 4 where there are many (several workgroups
-// per CU then cover each other's start and end).  Channels per workgroup: 64, or 32 where 64 leave CUs without one.
+// per CU then cover each other's start and end: experts' decode step 82 us with 4, 110 with 8; two chunks of words in
+// flight instead of one 96 us, for want of registers).  Channels per workgroup: 64, or 32 where 64 leave CUs without one.
 template <int BITS, int PARTS, int W>
 hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
     const int width = swiglu ? k.N / 2 : k.N;
     const unsigned ey = (unsigned)(k.E + (k.offsets ? 1 : 0));
     const bool wide = !swiglu && ceil_div(width, 64) * k.E >= 224;
     const dim3 grid((unsigned)ceil_div(width, wide ? 64 : 32), ey), block(64 * W);
-#define GPTQ_ROWS(NT, FORM) \
-    hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, 1, NT, FORM, W>), grid, block, 0, stream, k)
+#define GPTQ_ROWS(NT, FORM)                                                                                              \
+    do {                                                                                                                 \
+        if (k.lg_group == 0)                                                                                             \
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 1, FORM, W>), grid, block, 0, stream, k);      \
+        else if (k.lg_group == 1)                                                                                        \
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 2, FORM, W>), grid, block, 0, stream, k);      \
+        else                                                                                                             \
+            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 4, FORM, W>), grid, block, 0, stream, k);      \
+    } while (0)
     if (swiglu) GPTQ_ROWS(4, kGated);
     else if (wide && k.H) GPTQ_ROWS(4, kAdapters);
     else if (wide) GPTQ_ROWS(4, kPlain);
