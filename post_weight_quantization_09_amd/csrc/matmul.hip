@@ -11,6 +11,7 @@ namespace {
 constexpr int kMaxTileRows = 128;
 constexpr int kStageThreads = 512;
 constexpr int kStageRows = 64;
+constexpr int kMaxKParts = 8;
 
 // What stage_kernel writes.
 struct StageArgs {
@@ -29,7 +30,8 @@ struct StageArgs {
     const int32_t* requests;
     const int32_t* adapter;
     int64_t n_requests;
-    int slices;            // workgroups of a request (0: no adapters)
+    int slices;            // workgroups of a request along its rows (0: no adapters)
+    int k_parts;           // and along K: part z of H is at z * M * hrank
     float* H;
     int32_t* row_adapter;
 };
@@ -193,20 +195,23 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
 
 // The inner half of the low-rank adapters: H[r] = alpha_a (A_a x_r) for the rows r of one request, a its adapter, and
 // the adapter of every row.  Bound by latency and the adapters' bytes for single tokens, by the rows' bytes for prompts.
-// A workgroup takes 16 rows at a time and the whole rank; its waves split K (each 32-k step one matrix product per 16
+// A workgroup takes 16 RS rows at a time and the whole rank; its waves split K (each 32-k step one matrix product per 16
 // ranks: lane l holds row l % 16 and, of A, rank l % 16, eight consecutive k each, straight from memory; a wave has the
 // loads of kAhead steps in flight) and the partial sums are joined in LDS in a fixed order.  A single token is no matrix
 // product: there a wave takes a rank and reads its row of A in whole kilobytes (as operands it would be 64 pieces of 16
-// bytes), products and sums in fp32 (one token, 4096 features, rank 16: TODO against 7.4 us).  Every request gets
-// `slices` workgroups, so that the launch does not depend on the lengths, which only the device knows.  H stays in fp32.
-template <int PARTS, int NR>
-__device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t req, int slice, char* lds) {
-    constexpr int W = kStageThreads / 64;
+// bytes), products and sums in fp32 (one token, 4096 features, rank 16: 4.6 against 7.4 us).  Every request gets
+// `slices` workgroups, so that the launch does not depend on the lengths, which only the device knows.  Prompts take 64
+// rows at a time, since every pass reads A again, and split K over k_parts workgroups; their sums are added where H is
+// used (4096 rows x 28672, rank 64, rows laid out beside it: TODO us against 333 with 16 rows and no split).  H stays in
+// fp32.
+template <int PARTS, int NR, int RS>
+__device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t req, int slice, int z, char* lds) {
+    constexpr int W = kStageThreads / 64, kXBytes = PARTS == 1 ? 2 : 4;
     float* part = reinterpret_cast<float*>(lds);     // [wave][rank and row register][lane]
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (req == a.n_requests) {                       // rows of no request
-        if (slice) return;
+        if (slice || z) return;
         int64_t head = a.requests[0], tail = a.requests[a.n_requests];
         head = head < 0 ? 0 : head > p.M ? p.M : head;
         tail = tail < head ? head : tail > p.M ? p.M : tail;
@@ -220,19 +225,27 @@ __device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64
     int id = a.adapter[req];
     if (id < 0 || id >= a.n_adapters) id = -1;
     const float alpha = id < 0 ? 0.f : a.alpha[id];
-    if (hi - lo == 1) {
+    if (hi - lo == 1 && a.k_parts == 1) {
         if (slice) return;
         if (tid == 0) a.row_adapter[lo] = id;
         if (id >= 0) single_row<PARTS>(p, a, lo, id, alpha, lane, wave);
         return;
     }
-    const int64_t step = 16 * (int64_t)a.slices;
-    for (int64_t r0 = lo + 16 * (int64_t)slice; r0 < hi; r0 += step) {
-        if (tid < 16 && r0 + tid < hi) a.row_adapter[r0 + tid] = id;
+    // this workgroup's steps of K
+    const int whole = p.K / kStepK, per = ((whole + a.k_parts - 1) / a.k_parts + 1) & ~1;
+    const int s_begin = min(z * per, whole), s_end = min(s_begin + per, whole);
+    float* H = a.H + (int64_t)z * p.M * p.hrank;
+    const int64_t step = 16 * RS * (int64_t)a.slices;
+    for (int64_t r0 = lo + 16 * RS * (int64_t)slice; r0 < hi; r0 += step) {
+        if (z == 0 && tid < 16 * RS && r0 + tid < hi) a.row_adapter[r0 + tid] = id;
         if (id < 0) continue;
-        int64_t r = r0 + (lane & 15);
-        if (r >= hi) r = hi - 1;
-        const char* xrow = static_cast<const char*>(p.X) + (r * p.ldx + 8 * q) * (PARTS == 1 ? 2 : 4);
+        const char* xrow[RS];
+#pragma unroll
+        for (int t = 0; t < RS; ++t) {
+            int64_t r = r0 + 16 * t + (lane & 15);
+            if (r >= hi) r = hi - 1;
+            xrow[t] = static_cast<const char*>(p.X) + (r * p.ldx + 8 * q) * kXBytes;
+        }
         const uint16_t* arow[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -240,77 +253,89 @@ __device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64
             if (rk >= p.rank) rk = p.rank - 1;       // ranks past the end are not stored
             arow[n] = a.A + id * a.a_stride + rk * a.lda + 8 * q;
         }
-        f32x4 acc[NR];
+        f32x4 acc[RS][NR];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < RS; ++t)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
         // pairs of steps (128 bytes of a bf16 row) are dealt out to the waves, kAhead steps at a time
-        constexpr int kAhead = NR * PARTS <= 4 ? 8 : 4;
-        const int whole = p.K / kStepK;
+        constexpr int kAhead = RS > 1 || NR * PARTS > 4 ? 2 : 8;
         constexpr int kTurn = 2 * W;
-        for (int s0 = 2 * wave; s0 < whole; s0 += kTurn * (kAhead / 2)) {
-            RawOctet<PARTS> x[kAhead];
+        for (int s0 = s_begin + 2 * wave; s0 < s_end; s0 += kTurn * (kAhead / 2)) {
+            RawOctet<PARTS> x[kAhead][RS];
             RawOctet<1> b[kAhead][NR];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 int s = s0 + (u >> 1) * kTurn + (u & 1);
-                s = s < whole ? s : s0;              // beyond the end: loaded again and not used
-                x[u].whole(xrow + s * (kStepK * (PARTS == 1 ? 2 : 4)));
+                s = s < s_end ? s : s0;              // beyond the end: loaded again and not used
+#pragma unroll
+                for (int t = 0; t < RS; ++t) x[u][t].whole(xrow[t] + s * (kStepK * kXBytes));
 #pragma unroll
                 for (int n = 0; n < NR; ++n) b[u][n].whole(reinterpret_cast<const char*>(arow[n] + s * kStepK));
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (s0 + (u >> 1) * kTurn + (u & 1) < whole) {
-                    u32x4 xp[PARTS];
-                    x[u].parts(xp);
+                if (s0 + (u >> 1) * kTurn + (u & 1) < s_end) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
+                    for (int t = 0; t < RS; ++t) {
+                        u32x4 xp[PARTS];
+                        x[u][t].parts(xp);
 #pragma unroll
-                        for (int i = 0; i < PARTS; ++i)
-                            acc[n] = mfma16(xp[i], __builtin_bit_cast(bf16x8, b[u][n].v[0]), acc[n]);
+                        for (int n = 0; n < NR; ++n)
+#pragma unroll
+                            for (int i = 0; i < PARTS; ++i)
+                                acc[t][n] = mfma16(xp[i], __builtin_bit_cast(bf16x8, b[u][n].v[0]), acc[t][n]);
+                    }
                 }
             }
         }
-        if (wave == W - 1 && whole * kStepK < p.K) { // the rest of K
+        if (z == a.k_parts - 1 && wave == W - 1 && whole * kStepK < p.K) {   // the rest of K
             u32x4 x[PARTS], b[1];
             const int k = whole * kStepK, left = p.K - k - 8 * q;
-            load_octet<PARTS>(xrow, k, k + left, x);
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 load_octet<1>(arow[n], k, k + left, b);
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i) acc[n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[n]);
+                for (int t = 0; t < RS; ++t) {
+                    load_octet<PARTS>(xrow[t], k, k + left, x);
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) acc[t][n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[t][n]);
+                }
             }
         }
-        __syncthreads();                             // the previous rows' partials have been read
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int t = 0; t < RS; ++t) {
+            __syncthreads();                         // the partials before these have been read
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[(wave * NR * 4 + n * 4 + i) * 64 + lane] = acc[n][i];
-        __syncthreads();
-        for (int v = wave; v < NR * 4; v += W) {
-            float s = 0.f;
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int u = 0; u < W; ++u) s += part[(u * NR * 4 + v) * 64 + lane];
-            const int64_t row = r0 + 4 * q + (v & 3);
-            const int rk = 16 * (v >> 2) + (lane & 15);
-            if (row < hi && rk < p.hrank) a.H[row * p.hrank + rk] = rk < p.rank ? s * alpha : 0.f;
+                for (int i = 0; i < 4; ++i) part[(wave * NR * 4 + n * 4 + i) * 64 + lane] = acc[t][n][i];
+            __syncthreads();
+            for (int v = wave; v < NR * 4; v += W) {
+                float s = 0.f;
+#pragma unroll
+                for (int u = 0; u < W; ++u) s += part[(u * NR * 4 + v) * 64 + lane];
+                const int64_t row = r0 + 16 * t + 4 * q + (v & 3);
+                const int rk = 16 * (v >> 2) + (lane & 15);
+                if (row < hi && rk < p.hrank) H[row * p.hrank + rk] = rk < p.rank ? s * alpha : 0.f;
+            }
         }
     }
 }
 
 // One launch before the product: workgroups of the adapters first (their chains of loads are the longest), then of the
 // rows.  NR 0: no adapters.
-template <int PARTS, int NR>
-__global__ __launch_bounds__(kStageThreads) void stage_kernel(MatmulKernelArgs p, StageArgs a) {
+template <int PARTS, int NR, int RS>
+__global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArgs p, StageArgs a) {
     constexpr int kLayBytes = PARTS * (kChunkK / 8) * (kStageRows + 1) * 16 + (kChunkK / 8) * (kStageRows + 1) * 4;
     constexpr int kShrinkBytes = (kStageThreads / 64) * NR * 4 * 64 * 4;
     __shared__ __attribute__((aligned(16))) char lds[kLayBytes > kShrinkBytes ? kLayBytes : kShrinkBytes];
     int64_t b = blockIdx.x;
     if constexpr (NR > 0) {
-        const int64_t n = (a.n_requests + 1) * a.slices;
+        const int64_t per = (int64_t)a.slices * a.k_parts, n = (a.n_requests + 1) * per;
         if (b < n) {
-            shrink_rows<PARTS, NR>(p, a, b / a.slices, (int)(b % a.slices), lds);
+            const int in = (int)(b % per);
+            shrink_rows<PARTS, NR, RS>(p, a, b / per, in / a.k_parts, in % a.k_parts, lds);
             return;
         }
         b -= n;
@@ -346,6 +371,7 @@ struct Plan {
     int nchunks;
     size_t xt_elems, sum_floats;
     int hrank;
+    int k_parts;
 };
 
 // Row tiles of the split kernel: 64 rows fit its registers with one word per step and lane and one scale per 128 k, and
@@ -357,7 +383,8 @@ int split_row_tiles(bool f32, int64_t mean, int bits, int groupsize) {
 // Which kernel: by the rows an expert has on average (all hold for any split of the rows).  Up to 16 (one operand's
 // rows) the few-rows kernel; then the tile kernel where it has work for every CU, else the split kernel (1531 rows x
 // 4099 channels, 408 tiles of 64 x 256: 120 us against 193; 512 x 2048, 64 tiles: 83 against 44).
-Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank, int bits, int groupsize) {
+Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank, int64_t n_requests, int bits,
+               int groupsize) {
     Plan p;
     const int64_t mean = ceil_div(M, experts);
     const int big = f32 ? 64 : 112;
@@ -377,6 +404,10 @@ Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64
     p.xt_elems = (size_t)(f32 ? 3 : 1) * p.nchunks * kChunkK * p.Mp;
     p.sum_floats = f32 ? 0 : (size_t)p.nchunks * kChunkSteps * p.Mp;
     p.hrank = (int)align_up((size_t)rank, 8);
+    // H in parts of K: for prompts, where 64-row passes alone would leave most of the GPU without one
+    p.k_parts = 1;
+    if (p.kernel == kTile && M >= 64 * n_requests)
+        p.k_parts = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)kMaxKParts, 512 / ceil_div(M, 64), K / 1024}));
     return p;
 }
 
@@ -391,7 +422,7 @@ struct Buffers {
     Buffers(const Plan& p, int64_t M, int64_t N, void* ws) {
         Carver c(ws);
         const bool staged = p.kernel != kRows;
-        H = p.hrank ? c.take<float>((size_t)M * p.hrank) : nullptr;
+        H = p.hrank ? c.take<float>((size_t)M * p.hrank * p.k_parts) : nullptr;
         row_adapter = p.hrank ? c.take<int32_t>((size_t)M) : nullptr;
         XT = staged ? c.take<uint16_t>(p.xt_elems) : nullptr;
         sums = staged ? c.take<float>(p.sum_floats) : nullptr;
@@ -406,27 +437,33 @@ struct Buffers {
 bool short_requests(int64_t M, int64_t n_requests) { return M < 32 * n_requests; }
 
 template <int PARTS>
-hipError_t launch_stage(const MatmulKernelArgs& k, const StageArgs& a, unsigned grid, hipStream_t stream) {
-#define GPTQ_STAGE(NR) hipLaunchKernelGGL((stage_kernel<PARTS, NR>), dim3(grid), dim3(kStageThreads), 0, stream, k, a)
-    if (!a.slices) GPTQ_STAGE(0);
-    else if (k.rank <= 16) GPTQ_STAGE(1);
-    else if (k.rank <= 32) GPTQ_STAGE(2);
-    else if (k.rank <= 64) GPTQ_STAGE(4);
-    else GPTQ_STAGE(8);
+hipError_t launch_stage(const MatmulKernelArgs& k, const StageArgs& a, bool long_rows, unsigned grid, hipStream_t stream) {
+#define GPTQ_STAGE(NR, RS) hipLaunchKernelGGL((stage_kernel<PARTS, NR, RS>), dim3(grid), dim3(kStageThreads), 0, stream, k, a)
+#define GPTQ_STAGE_RS(NR)             \
+    do {                              \
+        if (long_rows) GPTQ_STAGE(NR, 4); \
+        else GPTQ_STAGE(NR, 1);       \
+    } while (0)
+    if (!a.slices) GPTQ_STAGE(0, 1);
+    else if (k.rank <= 16) GPTQ_STAGE_RS(1);
+    else if (k.rank <= 32) GPTQ_STAGE_RS(2);
+    else if (k.rank <= 64) GPTQ_STAGE_RS(4);
+    else GPTQ_STAGE_RS(8);
+#undef GPTQ_STAGE_RS
 #undef GPTQ_STAGE
     return hipGetLastError();
 }
 
 }  // namespace
 
-// For any width and group size: the smaller tiles' list is the longer one.
+// For any width, group size and requests: the smaller tiles' list is the longer one, one request has the most parts of H.
 size_t matmul_workspace_bytes(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank) {
-    return Buffers(make_plan(f32, M, K, N, experts, rank, 3, 32), M, N, nullptr).bytes;
+    return Buffers(make_plan(f32, M, K, N, experts, rank, 1, 3, 32), M, N, nullptr).bytes;
 }
 
 hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t stream) {
     const bool lora = a.n_requests > 0 && a.n_adapters > 0;
-    const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0, a.bits, a.groupsize);
+    const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0, lora ? a.n_requests : 1, a.bits, a.groupsize);
     const Buffers buf(plan, a.M, a.N, workspace);
     MatmulKernelArgs k;
     k.X = a.X; k.ldx = a.ldx; k.x_rows = a.x_rows; k.rows = a.rows; k.M = a.M;
@@ -439,7 +476,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
     k.last_group = a.groupsize ? (int)((a.K - 1) / a.groupsize) : 0;
     k.Y = a.Y; k.ldy = a.ldy;
     k.H = lora ? buf.H : nullptr;
-    k.hrank = plan.hrank; k.row_adapter = buf.row_adapter;
+    k.h_parts = plan.k_parts; k.hrank = plan.hrank; k.row_adapter = buf.row_adapter;
     k.Z = lora && plan.kernel == kTile && short_requests(a.M, a.n_requests) ? buf.Z : nullptr;
     k.B = a.B; k.ldb = a.ldb; k.b_stride = a.b_stride; k.rank = a.rank;
     k.XT = buf.XT; k.sums = buf.sums; k.Mp = plan.Mp; k.tiles = buf.tiles;
@@ -449,6 +486,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
         s.XT = buf.XT; s.sums = buf.sums; s.excess = -1.5f * (float)(1 << a.bits);
         s.tile = plan.tile; s.cap = plan.cap; s.tiles = buf.tiles;
         int64_t grid = 0;
+        bool long_rows = false;
         if (plan.kernel != kRows) {
             s.row_blocks = (int)ceil_div(a.M, kStageRows);
             s.nchunks = plan.nchunks;
@@ -458,12 +496,16 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
             s.A = a.A; s.lda = a.lda; s.a_stride = a.a_stride; s.alpha = a.alpha; s.n_adapters = a.n_adapters;
             s.requests = a.requests; s.adapter = a.adapter; s.n_requests = a.n_requests;
             s.H = buf.H; s.row_adapter = buf.row_adapter;
-            // about 1024 workgroups for the requests in all, no more than the longest could use
-            s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.M, 16), 1024 / a.n_requests));
-            grid += (a.n_requests + 1) * s.slices;
+            // workgroups for the requests: about 1024 in all, no more than the longest could use
+            long_rows = plan.k_parts > 1;
+            const int rows = long_rows ? 64 : 16;
+            s.k_parts = plan.k_parts;
+            s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.M, rows), 1024 / (a.n_requests * s.k_parts)));
+            grid += (a.n_requests + 1) * s.slices * s.k_parts;
         }
         if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
-        hipError_t e = a.f32 ? launch_stage<3>(k, s, (unsigned)grid, stream) : launch_stage<1>(k, s, (unsigned)grid, stream);
+        hipError_t e = a.f32 ? launch_stage<3>(k, s, long_rows, (unsigned)grid, stream)
+                             : launch_stage<1>(k, s, long_rows, (unsigned)grid, stream);
         if (e != hipSuccess) return e;
         if (k.Z) {
             const dim3 zgrid((unsigned)ceil_div(a.M, 4), (unsigned)ceil_div(a.N, 256));

@@ -60,9 +60,10 @@ struct MatmulKernelArgs {
     int last_group;
     void* Y;
     int64_t ldy;
-    // adapters: H = alpha A x of every row, M x hrank fp32, and the adapter of every row (-1: none)
+    // adapters: H = alpha A x of every row, M x hrank fp32, in h_parts parts to be added (more than one only for the tile
+    // kernel's runs), and the adapter of every row (-1: none)
     const float* H;
-    int hrank;
+    int hrank, h_parts;
     const int32_t* row_adapter;
     const float* Z;                        // H B^T, M x N, where the tile kernel is given it ready; else nullptr
     const uint16_t* B;

@@ -72,7 +72,12 @@ __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, cons
                 const int row = 16 * t + (lane & 15);
                 const bool in = has && row >= f && row < g;
                 const f32x4* h = reinterpret_cast<const f32x4*>(p.H + (r0 + (in ? row : f)) * p.hrank + (has ? kq : 0));
-                const f32x4 u = h[0], v = h[1];
+                f32x4 u = h[0], v = h[1];
+                for (int z = 1; z < p.h_parts; ++z) {
+                    const f32x4* hz = h + (int64_t)z * p.M * p.hrank / 4;
+                    u += hz[0];
+                    v += hz[1];
+                }
                 float hv[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
