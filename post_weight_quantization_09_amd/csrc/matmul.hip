@@ -1,5 +1,6 @@
 // Products with packed weights: the pass that prepares the rows, workspace, choice of kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "matmul_launch.hpp"
 #include "matmul_rows.hpp"
@@ -107,7 +108,7 @@ __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int6
         const int64_t s = r < p.M ? source_row(p, r) : -1;
         if (s >= 0)
             load_octet<PARTS>(static_cast<const char*>(p.X) + s * p.ldx * (PARTS == 1 ? 2 : 4),
-                              (int64_t)chunk * kChunkK + 8 * o, p.K, part);
+                              chunk * kChunkK + 8 * o, p.K, part);
         float sum = 0.f;
 #pragma unroll
         for (int d = 0; d < 4; ++d) sum += bf16lo_to_f32(part[0][d]) + bf16hi_to_f32(part[0][d]);
@@ -149,6 +150,30 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
         for (int k0 = 0; k0 < p.K; k0 += kLoads * 512) {
             RawOctet<PARTS> x[kLoads];
             RawOctet<1> b[2][kLoads];
+            auto add = [&](auto masked) {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int k = k0 + u * 512 + 8 * lane, skip = k - min(k, p.K - 8);
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        float x0, x1;
+                        if constexpr (PARTS == 1) {
+                            x0 = bf16lo_to_f32(x[u].v[0][d]);
+                            x1 = bf16hi_to_f32(x[u].v[0][d]);
+                        } else {
+                            x0 = __uint_as_float(x[u].v[d >> 1][2 * (d & 1)]);
+                            x1 = __uint_as_float(x[u].v[d >> 1][2 * (d & 1) + 1]);
+                        }
+                        if constexpr (decltype(masked)::value) {
+                            x0 = 2 * d >= skip ? x0 : 0.f;
+                            x1 = 2 * d + 1 >= skip ? x1 : 0.f;
+                        }
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            sum[n] = fmaf(x1, bf16hi_to_f32(b[n][u].v[0][d]), fmaf(x0, bf16lo_to_f32(b[n][u].v[0][d]), sum[n]));
+                    }
+                }
+            };
             if (k0 + kLoads * 512 <= p.K) {
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
@@ -157,31 +182,26 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
 #pragma unroll
                     for (int n = 0; n < 2; ++n) b[n][u].whole(arow[n] + k * 2);
                 }
-            } else {
+                add(std::integral_constant<bool, false>{});
+            } else if (p.K >= 8) {                   // the last octet is read from further left, what is another's masked
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
-                    const int k = k0 + u * 512 + 8 * lane;
-                    x[u].some(xrow + k * kXBytes, p.K - k);
+                    const int at = min(k0 + u * 512 + 8 * lane, p.K - 8);
+                    x[u].whole(xrow + at * kXBytes);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) b[n][u].some(arow[n] + k * 2, p.K - k);
+                    for (int n = 0; n < 2; ++n) b[n][u].whole(arow[n] + at * 2);
                 }
-            }
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    float x0, x1;
-                    if constexpr (PARTS == 1) {
-                        x0 = bf16lo_to_f32(x[u].v[0][d]);
-                        x1 = bf16hi_to_f32(x[u].v[0][d]);
-                    } else {
-                        x0 = __uint_as_float(x[u].v[d >> 1][2 * (d & 1)]);
-                        x1 = __uint_as_float(x[u].v[d >> 1][2 * (d & 1) + 1]);
-                    }
+                add(std::integral_constant<bool, true>{});
+            } else if (lane == 0) {                  // rows shorter than an octet
+                for (int k = 0; k < p.K; ++k) {
+                    float xv;
+                    if constexpr (PARTS == 1) xv = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(xrow)[k] << 16);
+                    else xv = reinterpret_cast<const float*>(xrow)[k];
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
-                        sum[n] = fmaf(x1, bf16hi_to_f32(b[n][u].v[0][d]), fmaf(x0, bf16lo_to_f32(b[n][u].v[0][d]), sum[n]));
+                        sum[n] = fmaf(xv, __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(arow[n])[k] << 16), sum[n]);
                 }
+            }
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -197,8 +217,8 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
 // the adapter of every row.  Bound by latency and the adapters' bytes for single tokens, by the rows' bytes for prompts.
 // A workgroup takes 16 RS rows at a time and the whole rank; its waves split K (each 32-k step one matrix product per 16
 // ranks: lane l holds row l % 16 and, of A, rank l % 16, eight consecutive k each, straight from memory; a wave has the
-// loads of kAhead steps in flight) and the partial sums are joined in LDS in a fixed order.  A single token is no matrix
-// product: there a wave takes a rank and reads its row of A in whole kilobytes (as operands it would be 64 pieces of 16
+// loads of kAhead steps in flight) and the partial sums are joined in LDS in a fixed order.  One to four tokens are no
+// matrix product: there a wave takes a rank and reads its row of A in whole kilobytes (as operands it would be 64 pieces of 16
 // bytes), products and sums in fp32 (one token, 4096 features, rank 16: 4.6 against 7.4 us).  Every request gets
 // `slices` workgroups, so that the launch does not depend on the lengths, which only the device knows.  Prompts take 64
 // rows at a time, since every pass reads A again, and split K over k_parts workgroups; their sums are added where H is
@@ -225,10 +245,11 @@ __device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64
     int id = a.adapter[req];
     if (id < 0 || id >= a.n_adapters) id = -1;
     const float alpha = id < 0 ? 0.f : a.alpha[id];
-    if (hi - lo == 1 && a.k_parts == 1) {
-        if (slice) return;
-        if (tid == 0) a.row_adapter[lo] = id;
-        if (id >= 0) single_row<PARTS>(p, a, lo, id, alpha, lane, wave);
+    if (hi - lo <= 4 && a.k_parts == 1) {
+        for (int64_t r = lo + slice; r < hi; r += a.slices) {
+            if (tid == 0) a.row_adapter[r] = id;
+            if (id >= 0) single_row<PARTS>(p, a, r, id, alpha, lane, wave);
+        }
         return;
     }
     // this workgroup's steps of K
@@ -348,17 +369,97 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
     lay_out_rows<PARTS>(p, a, b / nchunks * kStageRows, (int)(b % nchunks), nchunks, lds);
 }
 
-// Z = H B^T for many rows of short requests (single tokens beside each other): one thread per row and four channels.
-__global__ __launch_bounds__(256) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
-    const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t c0 = ((int64_t)blockIdx.y * 64 + lane) * 4;
-    if (r >= p.M || c0 >= p.N) return;
-    LaneChannels<4, false> ch(0, 0, p.N);
-    ch.c0 = (uint32_t)(c0 < p.N - 4 ? c0 : p.N - 4);
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    add_adapter_row<4, false>(p, r, ch, y);
-    *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{y[0], y[1], y[2], y[3]};
+// Z = H B^T for many rows of short requests (single tokens beside each other).  A wave takes 64 rows and 64 channels: for
+// every adapter among the rows, wherever they are, one matrix product with H masked to its rows, so that B is read once
+// for all of them (row by row it is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us
+// against TODO).  The next operands are on their way while one set is multiplied.
+template <int PARTS>
+__global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
+    constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding
+    constexpr int RT = 4, NT = 4, kMaxOctets = 16;
+    __shared__ u32x4 hs[HP][kMaxOctets][64];         // H of the rows as operands
+    __shared__ int list[64];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t r0 = (int64_t)blockIdx.x * 64;
+    const int mine = r0 + lane < p.M ? p.row_adapter[r0 + lane] : -1;   // adapter of row `lane`
+    if (wave == 0) {                                 // the distinct adapters, in the order of their first rows
+        bool first = mine >= 0;
+        for (int i = 0; i < 63; ++i) first = first && !(i < lane && __builtin_amdgcn_readlane(mine, i) == mine);
+        const uint64_t m = __ballot(first);
+        if (first) list[__popcll(m & ((1ull << lane) - 1))] = mine;
+        if (lane == 0) count = __popcll(m);
+    }
+    for (int o = wave; o < p.hrank / 8; o += 4) {
+        float hv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hv[i] = mine >= 0 ? p.H[(r0 + lane) * p.hrank + 8 * o + i] : 0.f;
+        u32x4 part[3];
+        split3(hv, part);
+#pragma unroll
+        for (int i = 0; i < HP; ++i) hs[i][o][lane] = part[i];
+    }
+    __syncthreads();
+    const LaneChannels<NT, false> ch((blockIdx.y * 4 + wave) * 64, lane, p.N);
+    const int n = __builtin_amdgcn_readfirstlane(count);
+    int ids[RT];
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        ids[t] = __shfl(mine, 16 * t + (lane & 15));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const char* Bc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) Bc[j] = reinterpret_cast<const char*>(p.B + ch.channel(j) * p.ldb + 8 * q);
+    const int steps = (p.rank + kStepK - 1) / kStepK, items = n * steps;
+    int which = 0, step = 0;                         // of the next item
+    RawOctet<1> b[NT];
+    auto load = [&] {
+        const int64_t id = __builtin_amdgcn_readfirstlane(list[which]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            b[j].some(Bc[j] + (id * p.b_stride + step * kStepK) * 2, p.rank - step * kStepK - 8 * q, p.rank);
+        if (++step == steps) {
+            step = 0;
+            ++which;
+        }
+    };
+    if (items) load();
+    for (int item = 0, id = 0, at = 0, now = 0; item < items; ++item) {
+        id = __builtin_amdgcn_readfirstlane(list[now]);
+        bf16x8 bv[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) bv[j] = __builtin_bit_cast(bf16x8, b[j].v[0]);
+        if (item + 1 < items) load();
+        const int o = min(4 * at + q, p.hrank / 8 - 1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const bool in = ids[t] == id && 4 * at + q < p.hrank / 8;
+#pragma unroll
+            for (int i = 0; i < HP; ++i) {
+                u32x4 a = hs[i][o][16 * t + (lane & 15)];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) a[d] = in ? a[d] : 0u;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[t][j] = mfma16(a, bv[j], acc[t][j]);
+            }
+        }
+        if (++at == steps) {
+            at = 0;
+            ++now;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = r0 + 16 * t + 4 * q + i;
+            if (r < p.M)
+                *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{acc[t][0][i], acc[t][1][i], acc[t][2][i], acc[t][3][i]};
+        }
 }
 
 enum Kernel { kRows, kSplit, kTile };
@@ -387,7 +488,8 @@ Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64
                int groupsize) {
     Plan p;
     const int64_t mean = ceil_div(M, experts);
-    const int big = f32 ? 64 : 112;
+    // 112 rows where an expert fills several such tiles (the last one is half empty on average), else 64
+    const int big = f32 || mean < 256 ? 64 : 112;
     if (mean <= 16) {
         p.kernel = kRows;
         p.tile = 16;
@@ -500,7 +602,8 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
             long_rows = plan.k_parts > 1;
             const int rows = long_rows ? 64 : 16;
             s.k_parts = plan.k_parts;
-            s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.M, rows), 1024 / (a.n_requests * s.k_parts)));
+            s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(ceil_div(a.M, rows), std::min<int64_t>(a.M, 4)),
+                                                                     1024 / (a.n_requests * s.k_parts)));
             grid += (a.n_requests + 1) * s.slices * s.k_parts;
         }
         if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
@@ -508,8 +611,9 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
                              : launch_stage<1>(k, s, long_rows, (unsigned)grid, stream);
         if (e != hipSuccess) return e;
         if (k.Z) {
-            const dim3 zgrid((unsigned)ceil_div(a.M, 4), (unsigned)ceil_div(a.N, 256));
-            hipLaunchKernelGGL(adapter_expand_kernel, zgrid, dim3(256), 0, stream, k, buf.Z);
+            const dim3 zgrid((unsigned)ceil_div(a.M, 64), (unsigned)ceil_div(a.N, 256));
+            if (a.f32) hipLaunchKernelGGL(adapter_expand_kernel<3>, zgrid, dim3(256), 0, stream, k, buf.Z);
+            else hipLaunchKernelGGL(adapter_expand_kernel<1>, zgrid, dim3(256), 0, stream, k, buf.Z);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

@@ -132,32 +132,39 @@ __device__ __forceinline__ void add_adapter_row(const MatmulKernelArgs& p, int64
     const uint16_t* row[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) row[j] = B + ch.channel(j) * p.ldb;
-    const int whole = p.rank & ~7;
-#pragma unroll 2
-    for (int k = 0; k < whole; k += 8) {
-        const f32x4 u = *reinterpret_cast<const f32x4*>(h + k), v = *reinterpret_cast<const f32x4*>(h + k + 4);
+    if (p.rank < 8) {
+        for (int k = 0; k < p.rank; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) y[j] = fmaf(h[k], __uint_as_float((uint32_t)row[j][k] << 16), y[j]);
+        return;
+    }
+    // octets of ranks; the last one moves back to end with the rank, what it repeats counts as zero
+#pragma unroll 4
+    for (int k = 0; k < p.rank; k += 8) {
+        const int at = min(k, p.rank - 8);
+        float hv[8];
+        const f32x4 u = *reinterpret_cast<const f32x4_a4*>(h + at), v = *reinterpret_cast<const f32x4_a4*>(h + at + 4);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) hv[d] = at + d >= k ? (d < 4 ? u[d & 3] : v[d & 3]) : 0.f;
         u32x4 b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const u32x4_a2*>(row[j] + k);
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const u32x4_a2*>(row[j] + at);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                const float h0 = d < 2 ? u[2 * d] : v[2 * d - 4], h1 = d < 2 ? u[2 * d + 1] : v[2 * d - 3];
-                y[j] = fmaf(h0, bf16lo_to_f32(b[j][d]), y[j]);
-                y[j] = fmaf(h1, bf16hi_to_f32(b[j][d]), y[j]);
+                y[j] = fmaf(hv[2 * d], bf16lo_to_f32(b[j][d]), y[j]);
+                y[j] = fmaf(hv[2 * d + 1], bf16hi_to_f32(b[j][d]), y[j]);
             }
     }
-    for (int k = whole; k < p.rank; ++k)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) y[j] = fmaf(h[k], __uint_as_float((uint32_t)row[j][k] << 16), y[j]);
 }
 
 // FORM of a product: plain, gated pairs of channels, or plain with adapters.
 enum { kPlain = 0, kGated = 1, kAdapters = 2 };
 
 template <int BITS, int PARTS, int NT, int GS, int FORM, int W>
-__global__ __launch_bounds__(64 * W, PARTS == 1 ? (W == 16 ? 4 : 3) : 2) void matmul_rows_kernel(MatmulKernelArgs p) {
+__global__ __launch_bounds__(64 * W, W == 16 ? 4 : W == 4 && GS == 4 && kLaneWords<BITS> == 1 ? 3 : 2)
+void matmul_rows_kernel(MatmulKernelArgs p) {
     constexpr bool GATED = FORM == kGated;
     constexpr int kLW = kLaneWords<BITS>;
     constexpr int kXBytes = PARTS == 1 ? 2 : 4, kGroups = kChunkSteps / GS;
@@ -257,12 +264,13 @@ __global__ __launch_bounds__(64 * W, PARTS == 1 ? (W == 16 ? 4 : 3) : 2) void ma
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (nfull % W == wave) {                     // the rest of K, a step at a time: past its end x is zero
-            for (int step = nfull * kChunkSteps; step * kStepK < p.K; ++step) {
+        {   // the rest of K, a step for each of the next waves: past its end x is zero
+            const int step = nfull * kChunkSteps + (wave + W - nfull % W) % W;
+            if (step * kStepK < p.K) {
                 const int last = p.nwords - 1;
                 uint32_t v[kLW][NT], f[NT];
                 RawOctet<PARTS> rows;
-                rows.some(xrow + step * (kStepK * kXBytes), p.K - step * kStepK - 8 * q);
+                rows.some(xrow + step * (kStepK * kXBytes), p.K - step * kStepK - 8 * q, p.K);
                 ch.words(words0, min(step * BITS + lane_word<BITS>(q), last) * p.ldp + ch.c0, v[0]);
                 if constexpr (kLW == 2)
                     ch.words(words0, min(step * BITS + lane_word2<BITS>(q), last) * p.ldp + ch.c0, v[1]);
@@ -305,38 +313,39 @@ __global__ __launch_bounds__(64 * W, PARTS == 1 ? (W == 16 ? 4 : 3) : 2) void ma
     }
 }
 
-// Waves share K: 16 of them where there are few workgroups (latency counts), 4 where there are many (several workgroups
-// per CU then cover each other's start and end: experts' decode step 82 us with 4, 110 with 8; two chunks of words in
-// flight instead of one 96 us, for want of registers).  Channels per workgroup: 64, or 32 where 64 leave CUs without one.
-template <int BITS, int PARTS, int W>
-hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
+// Channels per workgroup: 64, or 32 where 64 leave CUs without one.  Waves that share K: 16 in the narrow kernel with one
+// word per step and lane, whose registers allow it (latency counts); 8 in the others; 4 where there are many workgroups,
+// several of which then share a CU and cover each other's start and end (experts' decode step 82 us with 4, 110 with 8).
+template <int BITS, int PARTS, int NT, int FORM, int W>
+hipError_t launch_rows_form(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
     const int width = swiglu ? k.N / 2 : k.N;
-    const unsigned ey = (unsigned)(k.E + (k.offsets ? 1 : 0));
-    const bool wide = !swiglu && ceil_div(width, 64) * k.E >= 224;
-    const dim3 grid((unsigned)ceil_div(width, wide ? 64 : 32), ey), block(64 * W);
-#define GPTQ_ROWS(NT, FORM)                                                                                              \
-    do {                                                                                                                 \
-        if (k.lg_group == 0)                                                                                             \
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 1, FORM, W>), grid, block, 0, stream, k);      \
-        else if (k.lg_group == 1)                                                                                        \
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 2, FORM, W>), grid, block, 0, stream, k);      \
-        else                                                                                                             \
-            hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 4, FORM, W>), grid, block, 0, stream, k);      \
-    } while (0)
-    if (swiglu) GPTQ_ROWS(4, kGated);
-    else if (wide && k.H) GPTQ_ROWS(4, kAdapters);
-    else if (wide) GPTQ_ROWS(4, kPlain);
-    else if (k.H) GPTQ_ROWS(2, kAdapters);
-    else GPTQ_ROWS(2, kPlain);
-#undef GPTQ_ROWS
+    const dim3 grid((unsigned)ceil_div(width, NT == 4 && !swiglu ? 64 : 32), (unsigned)(k.E + (k.offsets ? 1 : 0)));
+    const dim3 block(64 * W);
+    if (k.lg_group == 0)
+        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 1, FORM, W>), grid, block, 0, stream, k);
+    else if (k.lg_group == 1)
+        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 2, FORM, W>), grid, block, 0, stream, k);
+    else
+        hipLaunchKernelGGL((matmul_rows_kernel<BITS, PARTS, NT, 4, FORM, W>), grid, block, 0, stream, k);
     return hipGetLastError();
+}
+
+template <int BITS, int PARTS, int WIDE, int NARROW>
+hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
+    if (swiglu) return launch_rows_form<BITS, PARTS, 4, kGated, WIDE>(k, swiglu, stream);
+    if (ceil_div(k.N, 64) * k.E >= 224) {
+        if (k.H) return launch_rows_form<BITS, PARTS, 4, kAdapters, WIDE>(k, swiglu, stream);
+        return launch_rows_form<BITS, PARTS, 4, kPlain, WIDE>(k, swiglu, stream);
+    }
+    if (k.H) return launch_rows_form<BITS, PARTS, 2, kAdapters, NARROW>(k, swiglu, stream);
+    return launch_rows_form<BITS, PARTS, 2, kPlain, NARROW>(k, swiglu, stream);
 }
 
 template <int BITS>
 hipError_t launch_rows(const MatmulKernelArgs& k, bool f32, bool swiglu, hipStream_t stream) {
-    if (f32) return launch_rows_w<BITS, 3, 8>(k, swiglu, stream);
-    if (ceil_div(k.N, 64) * k.E >= 1024) return launch_rows_w<BITS, 1, 4>(k, swiglu, stream);
-    return launch_rows_w<BITS, 1, 16>(k, swiglu, stream);
+    if (f32) return launch_rows_w<BITS, 3, 8, 8>(k, swiglu, stream);
+    if (ceil_div(k.N, 64) * k.E >= 1024) return launch_rows_w<BITS, 1, 4, 4>(k, swiglu, stream);
+    return launch_rows_w<BITS, 1, 8, kLaneWords<BITS> == 1 ? 16 : 8>(k, swiglu, stream);
 }
 
 }  // namespace gptq

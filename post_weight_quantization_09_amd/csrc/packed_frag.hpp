@@ -167,22 +167,54 @@ struct RawOctet {
         v[0] = u32x4{0u, 0u, 0u, 0u};
         if constexpr (PARTS != 1) v[1] = u32x4{0u, 0u, 0u, 0u};
     }
-    // `left` elements of the row remain from p on (may be none or negative).
-    __device__ __forceinline__ void some(const char* p, int64_t left) {
+    // `left` of the row's `all` elements remain from p on (may be none or negative).  The last octet is loaded whole, from
+    // further left, and moved; only rows shorter than an octet go element by element.
+    __device__ __forceinline__ void some(const char* p, int left, int all) {
         if (left >= 8) {
             whole(p);
             return;
         }
-        zero();
+        if (left <= 0) {
+            zero();
+            return;
+        }
+        if (all < 8) {
+            zero();
+            for (int i = 0; i < left; ++i) {
+                if constexpr (PARTS == 1) {
+                    const uint32_t e = reinterpret_cast<const uint16_t*>(p)[i];
 #pragma unroll
-        for (int i = 0; i < 7; ++i) {
-            if (i < left) {
-                if constexpr (PARTS == 1)
-                    v[0][i >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-                else
-                    v[i >> 2][i & 3] = reinterpret_cast<const uint32_t*>(p)[i];
+                    for (int d = 0; d < 4; ++d) v[0][d] |= i >> 1 == d ? e << (16 * (i & 1)) : 0u;
+                } else {
+                    const uint32_t e = reinterpret_cast<const uint32_t*>(p)[i];
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) v[d >> 2][d & 3] = i == d ? e : v[d >> 2][d & 3];
+                }
+            }
+            return;
+        }
+        const int by = 8 - left;                     // 1 .. 7 elements down
+        whole(p - by * (PARTS == 1 ? 2 : 4));
+        constexpr int kWords = PARTS == 1 ? 4 : 8;
+        uint32_t u[kWords];
+#pragma unroll
+        for (int d = 0; d < kWords; ++d) u[d] = v[d >> 2][d & 3];
+        if constexpr (PARTS == 1) {
+            if (by & 1) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) u[d] = (u[d] >> 16) | (d < 3 ? u[d + 1] << 16 : 0u);
             }
         }
+        const int words = PARTS == 1 ? by >> 1 : by;
+#pragma unroll
+        for (int step = 1; step < kWords; step <<= 1) {
+            if (words & step) {
+#pragma unroll
+                for (int d = 0; d < kWords; ++d) u[d] = d + step < kWords ? u[d + step] : 0u;
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kWords; ++d) v[d >> 2][d & 3] = u[d];
     }
     // As bf16 parts in natural order.
     __device__ __forceinline__ void parts(u32x4 (&part)[PARTS]) const {
@@ -198,9 +230,9 @@ struct RawOctet {
 };
 
 template <int PARTS>
-__device__ __forceinline__ void load_octet(const void* row, int64_t k, int64_t K, u32x4 (&part)[PARTS]) {
+__device__ __forceinline__ void load_octet(const void* row, int k, int K, u32x4 (&part)[PARTS]) {
     RawOctet<PARTS> r;
-    r.some(static_cast<const char*>(row) + k * (PARTS == 1 ? 2 : 4), K - k);
+    r.some(static_cast<const char*>(row) + (int64_t)k * (PARTS == 1 ? 2 : 4), K - k, K);
     r.parts(part);
 }
 
