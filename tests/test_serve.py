@@ -242,6 +242,48 @@ def test_expert_matmul_repeats_bit_for_bit_and_in_a_graph(counts):
     assert torch.equal(out, ref)
 
 
+# Enough tiles for the kernel of many rows: 64-row tiles, and 112-row tiles where an expert has several of them.
+TILE_CASES = [[300, 0, 500, 1, 250], [600, 1300]]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts", TILE_CASES)
+@pytest.mark.parametrize("bits,groupsize", [(2, 0), (2, 32), (3, 64), (3, 128), (4, 0), (4, 32), (4, 64), (4, 128), (5, 0),
+                                            (5, 32), (6, 64), (6, 128)])
+def test_expert_matmul_tiles(bits, groupsize, counts, dtype):
+    y, ref, bound = expert_case(counts, 135, 4201, bits, groupsize, dtype, gather=True, lead=3, trail=70, seed=bits)
+    close(y, ref, bound, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts", TILE_CASES)
+@pytest.mark.parametrize("K", [1, 128, 260])
+def test_expert_matmul_tiles_gated(K, counts, dtype):
+    y, ref, bound = expert_case(counts, K, 4202, 4, 64, dtype, swiglu=True, seed=K)
+    close(y, ref, bound, dtype)
+
+
+@gpu
+def test_expert_matmul_tiles_repeat_and_graph():
+    codes, scales, W, s = layer(256, 4096, 4, 128, 7, E=2)
+    X, p, sc = rows_of(1900, 256, BF16, 1).to(DEV), packed_on(codes, 4, DEV), scales.to(DEV)
+    off = torch.tensor([0, 900, 1900], dtype=torch.int32, device=DEV)
+    ref = g.gptq_expert_matmul(X, p, sc, off, 4, groupsize=128)
+    out, ws = torch.empty_like(ref), torch.empty(g.gptq_matmul_workspace_bytes(BF16, 1900, 256, 4096, experts=2),
+                                                 dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.gptq_expert_matmul(X, p, sc, off, 4, groupsize=128, out=out, workspace=ws)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        ws.fill_(0x7F)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(ref, g.gptq_expert_matmul(X, p, sc, off, 4, groupsize=128))
+
+
 # ---------------------------------------------------------------------------------------------------------- adapters
 
 def adapter_case(lengths, ids, K, N, bits, groupsize, rank, dtype, n_adapters=3, lead=0, trail=0, seed=0, slices=False):
@@ -305,6 +347,26 @@ def test_adapter_matmul_many_requests_of_one_token(n):
     ids = [(7 * i) % 11 - 1 for i in range(n)]      # 9 is past the last adapter
     y, ref, bound = adapter_case([1] * n, ids, 256, 96, 4, 128, 16, BF16, n_adapters=9)
     close(y, ref, bound, BF16)
+
+
+# Prompts (A x in parts of K, one product per run of rows) and single tokens (by distinct adapter) in the many-rows kernel.
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,K,rank", [([900, 0, 130, 500], 2100, 24), ([700, 30, 800], 4099, 70),
+                                            ([1] * 400 + [3] * 300, 200, 9), ([40] * 35, 333, 128), ([1300], 1, 3)])
+def test_adapter_matmul_tiles(lengths, K, rank, dtype):
+    ids = [(5 * i + 1) % 8 - 1 for i in range(len(lengths))]
+    y, ref, bound = adapter_case(lengths, ids, K, 4102, 4, 128, rank, dtype, n_adapters=6, lead=2, trail=5, seed=rank)
+    close(y, ref, bound, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("K", [1, 5, 7, 8, 9, 31, 33, 511, 513, 4103])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths", [[1, 2, 4], [5, 17]])
+def test_adapter_matmul_lengths(K, lengths, dtype):
+    y, ref, bound = adapter_case(lengths, [0, 2, 1][:len(lengths)], K, 37, 4, 0, 12, dtype, seed=K)
+    close(y, ref, bound, dtype)
 
 
 @gpu
