@@ -475,11 +475,24 @@ def _device_tensor(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch
 
 def _rows_of(t: torch.Tensor, name: str, device=None) -> int:
     """The leading dimension of a 2-D tensor of rows with unit column stride, on the GPU."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be on the GPU of the other tensors")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if t.is_contiguous():
+        return t.shape[1] or 1
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _output(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, width: int):
+    """`out` checked, or a new rows x width tensor of `like`'s dtype and GPU; and its leading dimension."""
+    if out is None:
+        return like.new_empty((rows, width)), width
+    if out.shape != (rows, width) or out.dtype != like.dtype:
+        raise ValueError(f"out must be {rows} x {width} of dtype {like.dtype}")
+    return out, _rows_of(out, "out", like.device)
 
 
 # the current stream's handle without a Stream object around it (0.1 us instead of 1.9)
@@ -569,11 +582,7 @@ def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
     if rows is not None:
         rp, M = _device_tensor(rows, "rows", torch.int32, dev), rows.numel()
     width = N // 2 if swiglu else N
-    if out is None:
-        out = torch.empty(M, width, dtype=X.dtype, device=dev)
-    elif out.shape != (M, width) or out.dtype != X.dtype:
-        raise ValueError(f"out must be {M} x {width} of X's dtype")
-    ldy = _rows_of(out, "out", dev)
+    out, ldy = _output(out, X, M, width)
     lib = load()
     need = 0 if workspace is not None else lib.gptq_matmul_workspace_bytes(dt, M, K, N, E, 0)
     workspace, wp, wb = _scratch(need, dev, workspace)
@@ -630,11 +639,7 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
             raise ValueError("alpha must hold one entry per adapter, requests one more than adapter")
         if n_adapters == 0 or n_requests == 0:
             rank = 0
-    if out is None:
-        out = torch.empty(M, N, dtype=X.dtype, device=dev)
-    elif out.shape != (M, N) or out.dtype != X.dtype:
-        raise ValueError(f"out must be {M} x {N} of X's dtype")
-    ldy = _rows_of(out, "out", dev)
+    out, ldy = _output(out, X, M, N)
     lib = load()
     need = 0 if workspace is not None else lib.gptq_matmul_workspace_bytes(dt, M, K, N, 1, rank)
     workspace, wp, wb = _scratch(need, dev, workspace)
@@ -658,11 +663,7 @@ def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor
     pp = _device_tensor(positions, "positions", torch.int32, dev)
     wp = _device_tensor(weights, "weights", torch.float32, dev)
     T, topk = positions.shape
-    if out is None:
-        out = torch.empty(T, N, dtype=Y.dtype, device=dev)
-    elif out.shape != (T, N) or out.dtype != Y.dtype:
-        raise ValueError(f"out must be {T} x {N} of Y's dtype")
-    ldo = _rows_of(out, "out", dev)
+    out, ldo = _output(out, Y, T, N)
     _check(load().gptq_combine(Y.data_ptr(), dt, M, ldy, pp, wp, T, topk, N, out.data_ptr(), ldo,
                                _handle(dev, stream)), "gptq_combine")
     return out
