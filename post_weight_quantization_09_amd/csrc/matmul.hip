@@ -370,9 +370,9 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
 }
 
 // Z = H B^T for many rows of short requests (single tokens beside each other).  A wave takes 64 rows and 64 channels: for
-// every adapter among the rows, wherever they are, one matrix product with H masked to its rows, so that B is read once
-// for all of them (row by row it is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us
-// against 55).  The next operands are on their way while one set is multiplied.
+// every adapter among the rows, wherever they are, one matrix product of which its rows are kept (and not one with other
+// rows of H zero: an infinite or NaN value of B would reach them), so that B is read once for all of them (row by row it
+// is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us against 55).  The next operands are on their way while one set is multiplied.
 template <int PARTS>
 __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
     constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding
@@ -403,13 +403,14 @@ __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs
     __syncthreads();
     const LaneChannels<NT, false> ch((blockIdx.y * 4 + wave) * 64, lane, p.N);
     const int n = __builtin_amdgcn_readfirstlane(count);
-    int ids[RT];
-    f32x4 acc[RT][NT];
+    int ids[RT][4];                                  // adapters of the rows that this lane has sums of
+    f32x4 acc[RT][NT], out[RT][NT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        ids[t] = __shfl(mine, 16 * t + (lane & 15));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) ids[t][i] = __shfl(mine, 16 * t + 4 * q + i);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] = out[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const char* Bc[NT];
 #pragma unroll
@@ -437,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs
         const int o = min(4 * at + q, p.hrank / 8 - 1);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            const bool in = ids[t] == id && 4 * at + q < p.hrank / 8;
+            const bool in = 4 * at + q < p.hrank / 8;
 #pragma unroll
             for (int i = 0; i < HP; ++i) {
                 u32x4 a = hs[i][o][16 * t + (lane & 15)];
@@ -450,6 +451,14 @@ __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs
         if (++at == steps) {
             at = 0;
             ++now;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out[t][j][i] = ids[t][i] == id ? acc[t][j][i] : out[t][j][i];
+                    acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
         }
     }
 #pragma unroll
@@ -458,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs
         for (int i = 0; i < 4; ++i) {
             const int64_t r = r0 + 16 * t + 4 * q + i;
             if (r < p.M)
-                *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{acc[t][0][i], acc[t][1][i], acc[t][2][i], acc[t][3][i]};
+                *reinterpret_cast<f32x4_a4*>(Z + r * p.N + ch.c0) = f32x4{out[t][0][i], out[t][1][i], out[t][2][i], out[t][3][i]};
         }
 }
 

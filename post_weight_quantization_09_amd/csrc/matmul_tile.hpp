@@ -38,7 +38,8 @@ __device__ __forceinline__ void copy_to_lds(const void* src, uint32_t off, void*
 constexpr int kTileCols = 256;         // channels of a workgroup (outputs: half of them when gated)
 constexpr int kTileGroup = 8;          // row tiles that neighbouring workgroups share a weight tile for
 
-// acc += H B^T for the rows r0 .. r0 + nrow - 1: one product per run of rows with the same adapter (H zero outside it).
+// acc += H B^T for the rows r0 .. r0 + nrow - 1: one product per run of rows with the same adapter, added to the rows of
+// the run alone (zero rows of H would not do: an infinite or NaN value of B would reach the other rows as 0 * inf).
 template <int PARTS, int RT, int NT, bool GATED>
 __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, const LaneChannels<NT, GATED>& ch, int64_t r0,
                                                  int nrow, int lane, f32x4 (&acc)[RT][NT]) {
@@ -69,6 +70,7 @@ __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, cons
             const bool has = kq < p.rank;
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
+                if (16 * t >= g || 16 * t + 16 <= f) continue;
                 const int row = 16 * t + (lane & 15);
                 const bool in = has && row >= f && row < g;
                 const f32x4* h = reinterpret_cast<const f32x4*>(p.H + (r0 + (in ? row : f)) * p.hrank + (has ? kq : 0));
@@ -86,10 +88,19 @@ __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, cons
                 }
                 u32x4 hp[3];
                 split3(hv, hp);
+                f32x4 sum[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < HP; ++i)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[t][j] = mfma16(hp[i], b[j], acc[t][j]);
+                    for (int j = 0; j < NT; ++j) sum[j] = mfma16(hp[i], b[j], sum[j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int to = 16 * t + 4 * q + i;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[t][j][i] += to >= f && to < g ? sum[j][i] : 0.f;
+                }
             }
         }
         f = g;

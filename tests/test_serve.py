@@ -385,6 +385,42 @@ def test_adapter_matmul_strided_adapters(lengths):
     close(y, ref, bound, BF16)
 
 
+# Infinities and NaN in one request's adapter or rows reach no row of another request, whatever kernel takes them.
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,N", [([1] * 6, 70), ([20, 9, 3, 12], 70), ([500, 3, 90, 700], 3900), ([1] * 700 + [2] * 200, 3900)])
+def test_adapter_matmul_non_finite_requests_stay_alone(lengths, N, dtype):
+    K, rank, n = 168, 20, 3
+    codes, scales, W, s = layer(K, N, 4, 0, 3)
+    ids = [i % n for i in range(len(lengths))]
+    offsets = np.concatenate([[0], np.cumsum(lengths)])
+    M = int(offsets[-1])
+    owner = torch.tensor(np.repeat(ids, lengths))
+    X, A, B = rows_of(M, K, dtype, 1), rows_of(n * rank, K, BF16, 2).view(n, rank, K), rows_of(n * N, rank, BF16, 3).view(n, N, rank)
+    args = (packed_on(codes, 4, DEV)[0], scales[0].to(DEV), 4)
+
+    def run(X, A, B):
+        return g.gptq_adapter_matmul(X.to(DEV), *args, A=A.to(DEV), B=B.to(DEV), alpha=torch.ones(n, device=DEV),
+                                     requests=torch.tensor(offsets, dtype=torch.int32, device=DEV),
+                                     adapter=torch.tensor(ids, dtype=torch.int32, device=DEV)).cpu()
+
+    fine = run(X, A, B)
+    bad = B.clone()
+    bad[1, ::7, 3], bad[1, 1::7, 19] = math.inf, math.nan
+    y = run(X, A, bad)
+    assert torch.equal(y[owner != 1], fine[owner != 1])
+    mine = y[owner == 1]
+    assert not mine[:, ::7].isfinite().any() and mine[:, 1::7].isnan().all() and mine[:, 2::7].isfinite().all()
+    bad = A.clone()
+    bad[1, 5, 100] = math.nan
+    y = run(X, bad, B)
+    assert torch.equal(y[owner != 1], fine[owner != 1]) and y[owner == 1].isnan().all()
+    bad = X.clone()
+    bad[M - 1, 7] = math.nan
+    y = run(bad, A, B)
+    assert torch.equal(y[:-1], fine[:-1]) and y[-1].isnan().all()
+
+
 @gpu
 @pytest.mark.parametrize("M", [1, 3, 70])
 def test_adapter_matmul_without_adapters_is_the_dequantised_product(M):
