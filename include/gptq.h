@@ -401,7 +401,8 @@ gptq_status_t gptq_unpack_codes(const uint32_t* packed, int64_t ldp, int64_t K, 
  *   (its p is 0); where fewer than topk are left, the last choices are experts = positions = -1 with weight 0.
  *   The choices are then sorted by expert, stably (an expert's rows are in the order of the tokens).
  *
- *   logits     device, T x E, dtype, leading dimension ld >= E.   T >= 0.   E 1..1024.   topk 1..32 (may exceed E).
+ *   logits     device, T x E, dtype, leading dimension ld >= E.   T 0..2^27, T * topk <= 2^30.   E 1..1024.
+ *              topk 1..32 (may exceed E).
  *   weights    device fp32[T * topk].        experts   device int32[T * topk].
  *   offsets    device int32[E + 1]: expert e has rows [offsets[e], offsets[e + 1]).
  *   rows       device int32[T * topk]: the token of every row; -1 from offsets[E] on.

@@ -1,4 +1,6 @@
 // C ABI of the serving calls: routing, products with packed weights, joining (see include/gptq.h).
+#include <algorithm>
+
 #include "matmul.hpp"
 #include "route.hpp"
 #include "timer.hpp"
@@ -14,6 +16,7 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
 
 bool dtype_ok(gptq_dtype_t d) { return d == GPTQ_DTYPE_F32 || d == GPTQ_DTYPE_BF16; }
 
+constexpr int64_t kMaxTokens = (int64_t)1 << 27;      // of gptq_route: a launch has fewer than 2^32 threads
 constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 22, kMaxN = (int64_t)1 << 22;
 constexpr int64_t kMaxExperts = 16384, kMaxRequests = (int64_t)1 << 24;
 
@@ -45,7 +48,7 @@ gptq_status_t gptq_route(const void* logits, gptq_dtype_t dtype, int64_t T, int6
                          unsigned flags, float* weights, int32_t* experts, int32_t* offsets, int32_t* rows,
                          int32_t* positions, void* workspace, size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dtype) || T < 0 || E < 1 || E > kRouteMaxExperts || ld < E) return GPTQ_ERR_ARG;
-    if (topk < 1 || topk > kRouteMaxTopk || T > kMaxRows / topk || !offsets) return GPTQ_ERR_ARG;
+    if (topk < 1 || topk > kRouteMaxTopk || T > std::min(kMaxRows / topk, kMaxTokens) || !offsets) return GPTQ_ERR_ARG;
     if (flags & ~GPTQ_FLAG_RENORM) return GPTQ_ERR_ARG;
     if (T > 0 && (!logits || !weights || !experts || !rows || !positions)) return GPTQ_ERR_ARG;
     if (!ws_ok(workspace, workspace_bytes, route_workspace_bytes(T, E))) return GPTQ_ERR_WORKSPACE;

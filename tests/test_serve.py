@@ -475,6 +475,30 @@ def test_route(T, E, topk, dtype, renorm):
     check_route(out, x.double().numpy(), topk, renorm)
 
 
+# Experts around the lanes' shares, choices around the 16 that 16 lanes keep.
+@gpu
+@pytest.mark.parametrize("T,E,topk", [(63, 16, 16), (70, 17, 2), (200, 33, 16), (200, 33, 17), (130, 100, 1), (129, 127, 5),
+                                      (67, 129, 7), (66, 200, 20)])
+def test_route_lanes(T, E, topk):
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(T + E)).mul(4).round().div(4)     # ties
+    check_route(g.gptq_route(x.to(DEV), topk), x.double().numpy(), topk, False)
+
+
+@gpu
+def test_route_of_many_blocks_of_tokens():
+    T, E = 131200, 1024
+    x = torch.randn(T, E, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    x[:, 512:] -= 1                                  # experts of unlike shares
+    out = g.gptq_route(x, 1)
+    top = x.max(1, keepdim=True).values
+    ex = (x == top).int().argmax(1)                  # the first of equal ones
+    order = ex.sort(stable=True).indices
+    assert torch.equal(out["experts"][:, 0].long(), ex)
+    assert torch.equal(out["rows"].long(), order)
+    assert torch.equal(out["offsets"].long()[1:], torch.bincount(ex, minlength=E).cumsum(0))
+    assert torch.equal(out["rows"][out["positions"][:, 0].long()].long(), torch.arange(T, device=DEV))
+
+
 @gpu
 @pytest.mark.parametrize("T", [3, 200])
 def test_route_masks(T):
@@ -666,6 +690,17 @@ def test_adapter_matmul_workspace():
     need = g.gptq_matmul_workspace_bytes(BF16, 8, 64, 32, rank=16)
     assert adapter_args(wsb=need - 1) == g.GPTQ_ERR_WORKSPACE
     assert adapter_args(M=0, ws=None) == g.GPTQ_OK
+
+
+@gpu
+def test_combine_more_tokens_than_one_launch_takes():
+    T, N = (1 << 23) + 5, 4
+    Y = torch.arange(16, dtype=F32, device=DEV).view(4, N)
+    pos = (torch.arange(T, dtype=torch.int32, device=DEV) % 5 - 1).view(T, 1)
+    w = torch.arange(T, dtype=F32, device=DEV).view(T, 1) % 64
+    out = g.gptq_combine(Y, pos, w)
+    ref = torch.where(pos < 0, torch.zeros((), device=DEV), w * Y[pos.clamp(min=0).long().view(-1)])
+    assert torch.equal(out, ref)                     # products of small integers: exact
 
 
 def test_route_refuses():
