@@ -2,9 +2,11 @@
 // products with too few tiles for the tile kernel to fill the GPU.
 //
 // What bounds it: between the two others - every weight serves up to 64 rows, so the matrix cores and the conversion of
-// codes take about as long as the words do from HBM.  One workgroup owns 16 MT rows of one expert and 64 channels over
-// all K; its eight waves take the 128-k chunks in turn and join their sums in LDS in a fixed order, as in the few-rows
-// kernel, so a product of 64 rows and 4096 channels already has 64 workgroups of 8 waves without partials in memory.
+// codes take about as long as the words do from HBM (64 rows x 14336 channels x 4096, 4 bits: 17 us, 30 MB of words at
+// 1.8 TB/s; 782 rows of 16 experts x 1411 x 1990, 3 bits in groups of 64: 28 us, 155 TFLOP/s).  One workgroup owns 16 MT
+// rows of one expert and 64 channels over all K; its W waves take the 128-k chunks in turn and join their sums in LDS in
+// a fixed order, as in the few-rows kernel, so a product of 64 rows and 4096 channels already has 64 workgroups of 8
+// waves without partials in memory.
 // Rows come from stage_rows (matmul.hip) as whole operands: one contiguous kilobyte per 16 rows and 32 k, where the rows
 // as they lie would be 64 pieces of 16 bytes.
 #pragma once
@@ -13,12 +15,10 @@
 
 namespace gptq {
 
-constexpr int kSplitWaves = 8;
-
-template <int BITS, int PARTS, int MT, int GS, int FORM>
-__global__ __launch_bounds__(64 * kSplitWaves, 2) void matmul_split_kernel(MatmulKernelArgs p) {
+template <int BITS, int PARTS, int MT, int GS, int FORM, int W>
+__global__ __launch_bounds__(64 * W, 2) void matmul_split_kernel(MatmulKernelArgs p) {
     constexpr bool GATED = FORM == kGated;
-    constexpr int NT = 4, W = kSplitWaves, kVals = MT * 4, kGroups = kChunkSteps / GS;
+    constexpr int NT = 4, kVals = MT * 4, kGroups = kChunkSteps / GS;
     constexpr int XR = 2;                            // steps of rows in flight
     constexpr int kLW = kLaneWords<BITS>;
     __shared__ float part[W][kVals * NT][64];
@@ -171,16 +171,26 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void matmul_split_kernel(Matmu
     }
 }
 
-template <int BITS, int PARTS, int MT, int GS>
-hipError_t launch_split_gs(const MatmulKernelArgs& k, int ntm, bool swiglu, hipStream_t stream) {
-    const dim3 grid((unsigned)ceil_div(swiglu ? k.N / 2 : k.N, swiglu ? 32 : 64), (unsigned)ntm), block(64 * kSplitWaves);
+template <int BITS, int PARTS, int MT, int GS, int W>
+hipError_t launch_split_waves(const MatmulKernelArgs& k, int ntm, bool swiglu, hipStream_t stream) {
+    const dim3 grid((unsigned)ceil_div(swiglu ? k.N / 2 : k.N, swiglu ? 32 : 64), (unsigned)ntm), block(64 * W);
 #define GPTQ_SPLIT(FORM) \
-    hipLaunchKernelGGL((matmul_split_kernel<BITS, PARTS, MT, GS, FORM>), grid, block, 0, stream, k)
+    hipLaunchKernelGGL((matmul_split_kernel<BITS, PARTS, MT, GS, FORM, W>), grid, block, 0, stream, k)
     if (swiglu) GPTQ_SPLIT(kGated);
     else if (k.H) GPTQ_SPLIT(kAdapters);
     else GPTQ_SPLIT(kPlain);
 #undef GPTQ_SPLIT
     return hipGetLastError();
+}
+
+// Eight waves share K while every CU has one workgroup at most; beyond that four do, so that more workgroups share a CU
+// and fewer partial sums are joined (87 rows x 3552 channels x 9496, 168 workgroups: 45 us with eight waves, 67 with
+// four; 1127 rows of 23 experts x 24256 x 128: 275 against 117; 782 rows of 16 experts x 1411 x 1990: the same).
+template <int BITS, int PARTS, int MT, int GS>
+hipError_t launch_split_gs(const MatmulKernelArgs& k, int ntm, bool swiglu, hipStream_t stream) {
+    const int64_t groups = ceil_div(swiglu ? k.N / 2 : k.N, swiglu ? 32 : 64) * (ceil_div(k.M, 16 * MT) + k.E / 2);
+    if (groups > 256) return launch_split_waves<BITS, PARTS, MT, GS, 4>(k, ntm, swiglu, stream);
+    return launch_split_waves<BITS, PARTS, MT, GS, 8>(k, ntm, swiglu, stream);
 }
 
 // row_tiles: 2, or 4 as split_row_tiles() allows.

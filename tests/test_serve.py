@@ -195,6 +195,15 @@ def test_expert_matmul_keeps_to_its_rows(M, offsets):
         close(guard[1:M + 1], ref, bound, BF16)
 
 
+# More workgroups than CUs: four waves share K.
+@gpu
+@pytest.mark.parametrize("dtype,bits,groupsize,swiglu", [(BF16, 4, 128, False), (BF16, 3, 64, False), (BF16, 5, 32, True),
+                                                         (BF16, 2, 0, True), (F32, 4, 0, False), (F32, 6, 64, True)])
+def test_expert_matmul_tens_of_rows_wide(dtype, bits, groupsize, swiglu):
+    y, ref, bound = expert_case([40, 65, 0, 33, 1], 709, 5450, bits, groupsize, dtype, swiglu=swiglu, gather=True, seed=9)
+    close(y, ref, bound, dtype)
+
+
 @gpu
 @pytest.mark.parametrize("M", [9, 150])
 @pytest.mark.parametrize("dtype", [BF16, F32])
