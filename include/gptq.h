@@ -9,6 +9,7 @@
  *   3. gptq_asym_correction     P1 = [(A U^T) masked strictly upper] U               ([R] item 3)
  *   4. gptq_quantize_layer      shared-order column loop with lazy block updates     ([T] sections 3-5)
  *      gptq_quantize_layer_groups  the same for output-channel groups with a Hessian each ([G])
+ * and computes with the packed layers: gptq_route, gptq_expert_matmul, gptq_adapter_matmul, gptq_combine.
  *
  * Sources, cited by page title and section:
  *   [T] GPTQ tutorial page "GPTQ：量化一个权重之后怎样补偿输出误差" (charlestar.github.io, 2026-10-15); its
@@ -432,12 +433,15 @@ size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int
  *              are written as zeros.
  *   E          1 .. 16384 experts.
  *   packed     device uint32, word w of channel n of expert e at packed[e * p_stride + w * ldp + n]; ldp >= N,
- *              p_stride >= gptq_packed_words(K, bits) * ldp (E > 1).
+ *              p_stride >= gptq_packed_words(K, bits) * ldp (E > 1); gptq_packed_words(K, bits) * ldp <= 2^30.
  *   K          1 .. 2^22.   N: 4 .. 2^22 channels (even with GPTQ_FLAG_SWIGLU).   bits 2..6.
  *   scales     device fp32, contiguous N per expert (groups: ceil(K / groupsize) x N), expert e at e * s_stride.
  *   groupsize  0, 32, 64 or 128 consecutive k that share a scale.
  *   Y          device, M x N (N / 2 with GPTQ_FLAG_SWIGLU), dtype, leading dimension ldy; not X.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, E, 0).
+ * Sums are fp32, of x (2^bits + code) for bf16 rows and of x (code - z) for fp32 rows, times the scale every 128 k or
+ * scale group.  A row with an infinity or NaN gives no finite value (NaN also where the exact one is an infinity); no
+ * other row is touched.
  * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_rows, int64_t ldx, const int32_t* rows,
@@ -460,7 +464,8 @@ gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_ro
  *   adapter    device int32[n_requests]; -1 (or any value outside [0, n_adapters)): no adapter.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, 1, rank).
  * A x is summed and kept in fp32 (it enters the second product in bf16 parts: two for bf16 rows, with an error 2^-17 of
- * the adapter's term, exactly three for fp32 rows).  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ * the adapter's term, exactly three for fp32 rows).  An infinity or NaN in a request's rows or adapter stays in that
+ * request.  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, int64_t ldx, const uint32_t* packed,
                                   int64_t ldp, int64_t K, int64_t N, int bits, const float* scales, int64_t groupsize,
@@ -481,7 +486,7 @@ gptq_status_t gptq_combine(const void* Y, gptq_dtype_t dtype, int64_t M, int64_t
 
 /*
  * gptq_device_status - the error latched on the device by the latest gptq_prepare, gptq_prepare_groups,
- * gptq_quantize_layer or gptq_quantize_layer_groups call that used `workspace` (the refusal convention of [T]
+ * gptq_quantize_layer, gptq_quantize_layer_groups or gptq_route call that used `workspace` (the refusal convention of [T]
  * section 7: a non-finite input or a non-positive pivot is an error, reported and not repaired).
  *
  *   workspace  the device workspace given to that call (its 256-byte head holds the status word), or NULL for
