@@ -490,6 +490,13 @@ int split_row_tiles(bool f32, int64_t mean, int bits, int groupsize) {
     return !f32 && mean > 32 && (bits == 2 || bits == 4) && (groupsize == 0 || groupsize == 128) ? 4 : 2;
 }
 
+// Rows of the tile kernel's tiles: 112 where an expert fills several such tiles (the last one is half empty on average)
+// and a lane's operand is one word; else 64 (fp32 rows take three operands; with two words per operand seven row tiles
+// spill: 4096 rows of 4 experts x 14336 x 2048, 3 bits in groups of 32: 606 us against 393; per channel 402 against 323).
+int big_tile_rows(bool f32, int64_t mean, int bits) {
+    return !f32 && mean >= 256 && (bits == 2 || bits == 4) ? 112 : 64;
+}
+
 // Which kernel: by the rows an expert has on average (all hold for any split of the rows).  Up to 16 (one operand's
 // rows) the few-rows kernel; then the tile kernel where it has work for every CU, else the split kernel (1531 rows x
 // 4099 channels, 408 tiles of 64 x 256: 120 us against 193; 512 x 2048, 64 tiles: 83 against 44).
@@ -497,8 +504,7 @@ Plan make_plan(bool f32, int64_t M, int64_t K, int64_t N, int64_t experts, int64
                int groupsize) {
     Plan p;
     const int64_t mean = ceil_div(M, experts);
-    // 112 rows where an expert fills several such tiles (the last one is half empty on average), else 64
-    const int big = f32 || mean < 256 ? 64 : 112;
+    const int big = big_tile_rows(f32, mean, bits);
     if (mean <= 16) {
         p.kernel = kRows;
         p.tile = 16;

@@ -3,7 +3,8 @@
 // What bounds it: the matrix cores (2 M K N operations against half a byte per weight).  One workgroup of four waves owns
 // 16 RT rows of one expert and 256 channels; every wave holds its own 64 channels for all the rows, so no code is
 // converted twice in a workgroup: the words of a 128-k chunk come straight from global memory into registers as operands
-// (nothing of the weights passes through LDS) and serve RT row tiles.  Seven of them: the 256 registers that two waves
+// (nothing of the weights passes through LDS) and serve RT row tiles.  Seven of them (four for small experts and for codes
+// of two words an operand, see big_tile_rows in matmul.hip): the 256 registers that two waves
 // per SIMD leave each then hold the sums, the chunk's operands and the next step's rows; eight leave no room to read rows
 // ahead (experts 8192 x 28672 x 4096: 1.91 ms against 2.05; adapters 4096 x 8192 x 28672: 2.06 against 2.80), and one
 // wave per SIMD with 512 registers is slower (3.1 ms: half of them are accumulation registers, which cost moves).  The rows are laid out once per call by
@@ -307,11 +308,14 @@ hipError_t launch_tile_rt(const MatmulKernelArgs& k, int ntm, bool swiglu, hipSt
     return hipGetLastError();
 }
 
+// row_tiles: 4, or 7 as big_tile_rows() allows.
 template <int BITS>
 hipError_t launch_tile(const MatmulKernelArgs& k, bool f32, int row_tiles, int ntm, bool swiglu, hipStream_t stream) {
     if (f32) return launch_tile_rt<BITS, 3, 4>(k, ntm, swiglu, stream);
-    if (row_tiles <= 4) return launch_tile_rt<BITS, 1, 4>(k, ntm, swiglu, stream);
-    return launch_tile_rt<BITS, 1, 7>(k, ntm, swiglu, stream);
+    if constexpr (kLaneWords<BITS> == 1) {
+        if (row_tiles == 7) return launch_tile_rt<BITS, 1, 7>(k, ntm, swiglu, stream);
+    }
+    return launch_tile_rt<BITS, 1, 4>(k, ntm, swiglu, stream);
 }
 
 }  // namespace gptq
