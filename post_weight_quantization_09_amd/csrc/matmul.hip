@@ -90,7 +90,8 @@ __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
 
 // Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times
 // -1.5 2^b.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces along
-// the rows, turned in LDS.  Bound by HBM: every row is read once and written once.
+// the rows, turned in LDS.  Bound by HBM: every row is read once and written once (8192 gathered rows x 4096, bf16: 27.5 us,
+// 4.9 TB/s).
 template <int PARTS>
 __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t r0, int chunk, int nchunks, char* lds) {
     constexpr int kOctets = kChunkK / 8, kPitch = kStageRows + 1;
@@ -372,7 +373,8 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
 // Z = H B^T for many rows of short requests (single tokens beside each other).  A wave takes 64 rows and 64 channels: for
 // every adapter among the rows, wherever they are, one matrix product of which its rows are kept (and not one with other
 // rows of H zero: an infinite or NaN value of B would reach them), so that B is read once for all of them (row by row it
-// is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us against 55).  The next operands are on their way while one set is multiplied.
+// is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us against 55).  The next
+// operands are on their way while one set is multiplied.
 template <int PARTS>
 __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
     constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding

@@ -2,12 +2,12 @@
 // products with too few tiles for the tile kernel to fill the GPU.
 //
 // What bounds it: between the two others - every weight serves up to 64 rows, so the matrix cores and the conversion of
-// codes take about as long as the words do from HBM (64 rows x 14336 channels x 4096, 4 bits: 17 us, 30 MB of words at
-// 1.8 TB/s; 782 rows of 16 experts x 1411 x 1990, 3 bits in groups of 64: 28 us, 155 TFLOP/s).  One workgroup owns 16 MT
+// codes take about as long as the words do from HBM (64 rows x 14336 channels x 4096, 4 bits: 19.5 us with rank 16
+// adapters, 30 MB of words at 1.5 TB/s; 782 rows of 16 experts x 1411 x 1990, 3 bits in groups of 64: 29.5 us, 149 TFLOP/s).  One workgroup owns 16 MT
 // rows of one expert and 64 channels over all K; its W waves take the 128-k chunks in turn and join their sums in LDS in
 // a fixed order, as in the few-rows kernel, so a product of 64 rows and 4096 channels already has 64 workgroups of 8
 // waves without partials in memory.
-// Rows come from stage_rows (matmul.hip) as whole operands: one contiguous kilobyte per 16 rows and 32 k, where the rows
+// Rows come from stage_kernel (matmul.hip) as whole operands: one contiguous kilobyte per 16 rows and 32 k, where the rows
 // as they lie would be 64 pieces of 16 bytes.
 #pragma once
 

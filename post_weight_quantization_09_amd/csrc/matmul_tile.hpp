@@ -7,8 +7,9 @@
 // of two words an operand, see big_tile_rows in matmul.hip): the 256 registers that two waves
 // per SIMD leave each then hold the sums, the chunk's operands and the next step's rows; eight leave no room to read rows
 // ahead (experts 8192 x 28672 x 4096: 1.91 ms against 2.05; adapters 4096 x 8192 x 28672: 2.06 against 2.80), and one
-// wave per SIMD with 512 registers is slower (3.1 ms: half of them are accumulation registers, which cost moves).  The rows are laid out once per call by
-// stage_rows_kernel: octets of k in the converted operand's order, [K / 8][row], so that a chunk is 16 contiguous
+// wave per SIMD with 512 registers is slower (3.1 ms: half of them are accumulation registers, which cost moves).  That is
+// 1.0 PFLOP/s: the matrix units are busy 48% of the cycles at 2.0 GHz.  The rows are laid out once per call by
+// stage_kernel: octets of k in the converted operand's order, [K / 8][row], so that a chunk is 16 contiguous
 // pieces, copied to LDS by DMA and read back as 16-byte operands without bank conflicts; rows are gathered and fp32 rows
 // split in the same pass, and it leaves the row sums that take the codes' excess off again as the accumulators' start (bf16 rows).
 #pragma once
