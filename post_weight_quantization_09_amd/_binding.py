@@ -2,10 +2,15 @@
 
 Argument marshalling only: every step of the path runs in the library's HIP kernels.  torch supplies
 device memory (tensors, workspace) and the current HIP stream.  The functions carry the C names.
+
+`stream` (a torch.cuda.Stream, default the current one) is where a call's work is enqueued: inputs have to be ready
+there, and what the call allocates is that stream's memory, as for torch's own operations inside torch.cuda.stream().
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import Optional
 
@@ -128,6 +133,23 @@ def _stream(device, stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_its_stream(call):
+    """A call given a stream runs with that stream as the current one, so that what it allocates (workspace, outputs)
+    comes from that stream's memory and, once released, goes to later work on that stream alone.  Taken from the current
+    stream's, a block could be handed out again there while the kernels still use it."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+
+    return run
+
+
 def _workspace(call, K, N, M, flags, device, workspace):
     need = gptq_workspace_bytes(call, K, N, M, flags)
     if workspace is None:
@@ -190,6 +212,7 @@ def gptq_timer_read() -> dict:
     return {c: (float(ms[i]), int(cnt[i])) for i, c in enumerate(GPTQ_TIMER_CLASSES)}
 
 
+@_on_its_stream
 def gptq_accumulate_hessian(H: torch.Tensor, X: torch.Tensor, row_scale: Optional[torch.Tensor] = None,
                             X_float: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
                             workspace: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -212,6 +235,7 @@ def gptq_accumulate_hessian(H: torch.Tensor, X: torch.Tensor, row_scale: Optiona
     _check(st, "gptq_accumulate_hessian")
 
 
+@_on_its_stream
 def gptq_prepare(H: torch.Tensor, percdamp: float, dead: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None, stream=None, sync: bool = True):
     """In place H -> U.  Returns (dead uint8[K], damp, n_dead).  sync=False passes no host outputs: the call then
@@ -233,6 +257,7 @@ def gptq_prepare(H: torch.Tensor, percdamp: float, dead: Optional[torch.Tensor] 
     return dead, float(damp.value), int(n_dead.value)
 
 
+@_on_its_stream
 def gptq_prepare_groups(H: torch.Tensor, percdamp: float, dead: Optional[torch.Tensor] = None,
                         workspace: Optional[torch.Tensor] = None, stream=None, sync: bool = True):
     """In place H[g] -> U[g] for every group g of H (groups x K x K, each K x K matrix contiguous).
@@ -259,6 +284,7 @@ def gptq_prepare_groups(H: torch.Tensor, percdamp: float, dead: Optional[torch.T
     return dead, [float(x) for x in damps], [int(x) for x in n_dead]
 
 
+@_on_its_stream
 def gptq_asym_correction(U: torch.Tensor, A: torch.Tensor, P1: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     K = U.shape[0]
@@ -276,6 +302,7 @@ def gptq_asym_correction(U: torch.Tensor, A: torch.Tensor, P1: Optional[torch.Te
     return P1
 
 
+@_on_its_stream
 def gptq_quantize_layer(W: torch.Tensor, U: torch.Tensor, bits: int, dead: Optional[torch.Tensor] = None,
                         P1: Optional[torch.Tensor] = None, blocksize: int = 128,
                         scales: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
@@ -306,6 +333,7 @@ def gptq_quantize_layer(W: torch.Tensor, U: torch.Tensor, bits: int, dead: Optio
                      stream, cae, perm, groupsize, static_groups, mse, g_idx, check)
 
 
+@_on_its_stream
 def gptq_quantize_layer_groups(W: torch.Tensor, U: torch.Tensor, bits: int, dead: Optional[torch.Tensor] = None,
                                P1: Optional[torch.Tensor] = None, blocksize: int = 128,
                                scales: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
@@ -381,6 +409,7 @@ def gptq_packed_words(K: int, bits: int) -> int:
     return int(load().gptq_packed_words(int(K), int(bits)))
 
 
+@_on_its_stream
 def gptq_pack_codes(codes: torch.Tensor, bits: int, packed: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """codes: K x N uint8 view (any strides) -> packed words, ceil(K*bits/32) x N, held as int32 (bit patterns of
     the uint32 words)."""
@@ -398,6 +427,7 @@ def gptq_pack_codes(codes: torch.Tensor, bits: int, packed: Optional[torch.Tenso
     return packed
 
 
+@_on_its_stream
 def gptq_unpack_codes(packed: torch.Tensor, K: int, bits: int, scales: Optional[torch.Tensor] = None,
                       codes: Optional[torch.Tensor] = None, W_hat: Optional[torch.Tensor] = None,
                       stream=None) -> dict:
@@ -423,6 +453,7 @@ def gptq_unpack_codes(packed: torch.Tensor, K: int, bits: int, scales: Optional[
     return {"codes": codes, "W_hat": W_hat}
 
 
+@_on_its_stream
 def gptq_hadamard_rotate(x: torch.Tensor, signs: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     """Rows of x (R x K, unit column stride, fp32 or bf16) -> (row * signs) H_K / sqrt(K); out=x rotates in place."""
@@ -441,6 +472,7 @@ def gptq_hadamard_rotate(x: torch.Tensor, signs: Optional[torch.Tensor] = None, 
     return out
 
 
+@_on_its_stream
 def gptq_act_order(H: torch.Tensor, A: Optional[torch.Tensor] = None, perm: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Act-order: returns perm (int32[K]) and permutes H (and A) in place to H[perm][:, perm]."""
@@ -461,7 +493,8 @@ def gptq_act_order(H: torch.Tensor, A: Optional[torch.Tensor] = None, perm: Opti
 
 # --- serving the packed layers -------------------------------------------------------------------------------------
 # These calls are short (a few microseconds on the GPU for single tokens), so their marshalling is kept to plain
-# integers: addresses and the stream handle go to ctypes as they are.
+# integers: addresses and the stream handle go to ctypes as they are.  Given a stream, a call runs again with that stream
+# as the current one (as _on_its_stream does, without a wrapper around the calls that are given none).
 
 _DTYPES = {torch.float32: GPTQ_DTYPE_F32, torch.bfloat16: GPTQ_DTYPE_BF16}
 
@@ -499,9 +532,14 @@ def _output(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, width: i
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _handle(device, stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+def _current(stream, t: torch.Tensor):
+    """The context in which `stream` is the current one."""
+    if stream.device != t.device:
+        raise ValueError(f"stream must be one of {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _handle(device) -> int:
     if _current_handle is not None:
         return _current_handle(device.index)
     return torch.cuda.current_stream(device).cuda_stream
@@ -529,6 +567,9 @@ def gptq_route(logits: torch.Tensor, topk: int, renorm: bool = False, workspace:
     Returns dict(weights fp32[T, topk], experts int32[T, topk], offsets int32[E + 1], rows int32[T * topk], positions
     int32[T, topk]).  Stream-ordered: a NaN or +infinity logit is latched in `workspace` (gptq_device_status).
     """
+    if stream is not None:
+        with _current(stream, logits):
+            return gptq_route(logits, topk, renorm, workspace)
     ld = _rows_of(logits, "logits")
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
@@ -546,7 +587,7 @@ def gptq_route(logits: torch.Tensor, topk: int, renorm: bool = False, workspace:
     workspace, wp, wb = _scratch(need, dev, workspace)
     at = ints.data_ptr()
     _check(lib.gptq_route(logits.data_ptr(), dt, T, E, ld, topk, GPTQ_FLAG_RENORM if renorm else 0, weights.data_ptr(),
-                          at, at + 12 * n, at + 8 * n, at + 4 * n, wp, wb, _handle(dev, stream)), "gptq_route")
+                          at, at + 12 * n, at + 8 * n, at + 4 * n, wp, wb, _handle(dev)), "gptq_route")
     return {"weights": weights, "experts": experts.view(T, topk), "offsets": offsets, "rows": rows,
             "positions": positions.view(T, topk)}
 
@@ -561,6 +602,9 @@ def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
     E x groups x N with groupsize.  rows: int32[M], None for M = len(X) rows as they are.  swiglu: out is M x N / 2,
     silu(first half) * second half.
     """
+    if stream is not None:
+        with _current(stream, X):
+            return gptq_expert_matmul(X, packed, scales, offsets, bits, rows, groupsize, swiglu, out, workspace)
     dt = _DTYPES.get(X.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {X.dtype}")
@@ -589,7 +633,7 @@ def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
     _check(lib.gptq_expert_matmul(X.data_ptr(), dt, x_rows, ldx, rp, M, op, E, packed.data_ptr(), packed.stride(1),
                                   packed.stride(0), K, N, bits, sp, groups * N, groupsize,
                                   GPTQ_FLAG_SWIGLU if swiglu else 0, out.data_ptr(), ldy, wp, wb,
-                                  _handle(dev, stream)), "gptq_expert_matmul")
+                                  _handle(dev)), "gptq_expert_matmul")
     return out
 
 
@@ -604,6 +648,9 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     adapters x rank x K, B: bf16 adapters x N x rank, alpha: fp32[adapters].  requests: int32[R + 1] row offsets,
     adapter: int32[R] (-1: none).  Without A the plain product.
     """
+    if stream is not None:
+        with _current(stream, X):
+            return gptq_adapter_matmul(X, packed, scales, bits, groupsize, A, B, alpha, requests, adapter, out, workspace)
     dt = _DTYPES.get(X.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {X.dtype}")
@@ -645,7 +692,7 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     workspace, wp, wb = _scratch(need, dev, workspace)
     _check(lib.gptq_adapter_matmul(X.data_ptr(), dt, M, ldx, packed.data_ptr(), packed.stride(0), K, N, bits, sp,
                                    groupsize, ap, lda, a_stride, bp, ldb, b_stride, lp, n_adapters, rank, qp, ip,
-                                   n_requests, out.data_ptr(), ldy, wp, wb, _handle(dev, stream)),
+                                   n_requests, out.data_ptr(), ldy, wp, wb, _handle(dev)),
            "gptq_adapter_matmul")
     return out
 
@@ -653,6 +700,9 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
 def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] Y[positions[t, j]] in fp32; positions outside Y's rows are left out."""
+    if stream is not None:
+        with _current(stream, Y):
+            return gptq_combine(Y, positions, weights, out)
     dt = _DTYPES.get(Y.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {Y.dtype}")
@@ -665,5 +715,5 @@ def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor
     T, topk = positions.shape
     out, ldo = _output(out, Y, T, N)
     _check(load().gptq_combine(Y.data_ptr(), dt, M, ldy, pp, wp, T, topk, N, out.data_ptr(), ldo,
-                               _handle(dev, stream)), "gptq_combine")
+                               _handle(dev)), "gptq_combine")
     return out
