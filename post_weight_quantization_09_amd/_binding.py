@@ -519,6 +519,16 @@ def _rows_of(t: torch.Tensor, name: str, device=None) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
+def _matrices(t: torch.Tensor, name: str):
+    """Address, leading dimension and stride from one to the next of the matrices t[0], t[1], ...  A dimension of size one
+    has any stride; one that repeats or overlaps rows (expand) is refused, the library would read past them."""
+    n, rows, cols = t.shape
+    row, whole = t.stride(1) if rows > 1 else cols, t.stride(0)
+    if (cols > 1 and t.stride(2) != 1) or row < cols or (n > 1 and whole < rows * row):
+        raise ValueError(f"{name} must be matrices of rows with unit column stride, none of them overlapping")
+    return t.data_ptr(), row, whole if n > 1 else rows * row
+
+
 def _output(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, width: int):
     """`out` checked, or a new rows x width tensor of `like`'s dtype and GPU; and its leading dimension."""
     if out is None:
@@ -670,14 +680,13 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     if A is not None:
         if B is None or alpha is None or requests is None or adapter is None:
             raise ValueError("adapters need A, B, alpha, requests and adapter")
+        if A.dim() != 3 or A.shape[2] != K or A.dtype != torch.bfloat16 or A.device != dev:
+            raise ValueError("A must be bf16 adapters x rank x K")
         n_adapters, rank = A.shape[0], A.shape[1]
-        if A.dim() != 3 or A.shape[2] != K or A.dtype != torch.bfloat16 or A.stride(2) != 1 or A.device != dev:
-            raise ValueError("A must be bf16 adapters x rank x K with unit stride along K")
-        if B.shape != (n_adapters, N, rank) or B.dtype != torch.bfloat16 or B.device != dev or \
-                (rank > 1 and B.stride(2) != 1):
-            raise ValueError("B must be bf16 adapters x N x rank with unit stride along the rank")
-        ap, lda, a_stride = A.data_ptr(), max(A.stride(1), K), A.stride(0)
-        bp, ldb, b_stride = B.data_ptr(), max(B.stride(1), rank), B.stride(0)
+        if B.shape != (n_adapters, N, rank) or B.dtype != torch.bfloat16 or B.device != dev:
+            raise ValueError("B must be bf16 adapters x N x rank")
+        ap, lda, a_stride = _matrices(A, "A")
+        bp, ldb, b_stride = _matrices(B, "B")
         lp = _device_tensor(alpha, "alpha", torch.float32, dev)
         qp = _device_tensor(requests, "requests", torch.int32, dev)
         ip = _device_tensor(adapter, "adapter", torch.int32, dev)

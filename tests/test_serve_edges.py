@@ -102,3 +102,45 @@ def test_quantising_on_another_stream_with_its_own_buffers():
     torch.cuda.synchronize()
     for a, b in zip(want, behind_a_busy_stream(run, 64 << 20)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------------------------------------- views
+
+@gpu
+@pytest.mark.parametrize("M", [2, 20])
+def test_expanded_adapters_are_refused(M):
+    """A view that repeats rows has no leading dimension: read as dense it would run out of its memory."""
+    K, N, r = 64, 32, 8
+    X, p, s = rows_of(M, K, BF16, 1).to(DEV), torch.zeros(8, N, dtype=torch.int32, device=DEV), torch.ones(N, device=DEV)
+    full = dict(A=torch.zeros(1, r, K, dtype=BF16, device=DEV), B=torch.zeros(1, N, r, dtype=BF16, device=DEV),
+                alpha=torch.ones(1, device=DEV), requests=ints([0, M]), adapter=ints([0]))
+    assert bool((g.gptq_adapter_matmul(X, p, s, 4, **full) == g.gptq_adapter_matmul(X, p, s, 4)).all())
+    two = dict(full, alpha=torch.ones(2, device=DEV), A=full["A"].repeat(2, 1, 1), B=full["B"].repeat(2, 1, 1))
+    z = lambda *shape: torch.zeros(*shape, dtype=BF16, device=DEV)
+    for args in (dict(full, A=z(1, 1, K).expand(1, r, K)), dict(full, B=z(1, 1, r).expand(1, N, r)),
+                 dict(full, B=z(1, N, 1).expand(1, N, r)), dict(full, A=z(1, r, 1).expand(1, r, K)),
+                 dict(full, A=z(r * K).as_strided((1, r, K), (r * K, K - 1, 1))),
+                 dict(two, A=z(1, r, K).expand(2, r, K)), dict(two, B=z(1, N, r).expand(2, N, r)),
+                 dict(full, A=z(r, K)), dict(full, A=z(K)), dict(full, A=z(1, K, r).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            g.gptq_adapter_matmul(X, p, s, 4, **args)
+
+
+@gpu
+@pytest.mark.parametrize("M", [2, 20])
+def test_adapters_with_dimensions_of_size_one(M):
+    """Any stride is right along a dimension of size one (rank 1, one adapter)."""
+    K, N = 72, 32
+    codes, scales, W, s = layer(K, N, 4, 0, 2)
+    X, gen = rows_of(M, K, BF16, 1), torch.Generator().manual_seed(1)
+    a, b = torch.randn(K, generator=gen).to(BF16), torch.randn(N, generator=gen).to(BF16)
+    A = torch.empty(5, K, dtype=BF16, device=DEV)[2].copy_(a).as_strided((1, 1, K), (1, 3, 1))
+    wide = torch.zeros(N, 7, dtype=BF16, device=DEV)
+    wide[:, 3] = b.to(DEV)
+    B = wide[:, 3:4].as_strided((1, N, 1), (2, 7, 5), 3)
+    y = g.gptq_adapter_matmul(X.to(DEV), packed_on(codes, 4, DEV)[0], scales[0].to(DEV), 4, A=A, B=B,
+                              alpha=torch.ones(1, device=DEV), requests=ints([0, M]), adapter=ints([0]))
+    inner = X.double() @ a.double()[:, None]
+    term = (X.double().abs() @ a.double().abs()[:, None]) * b.double().abs()
+    # A x: at most 64 roundings of 2^-24 on a term's way, 2^-17 where it enters in two bf16 parts
+    close(y, X.double() @ W[0] + inner * b.double(), slack(X, s[0], 4, BF16, K) + 2.0 ** -16 * term, BF16)
