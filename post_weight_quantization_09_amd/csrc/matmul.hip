@@ -38,11 +38,12 @@ struct StageArgs {
 };
 
 // Row tiles of at most `tile` rows: one list entry (expert, first row, end) per tile, the rows of no expert as expert E,
-// the rest of the list expert -1.  One workgroup.
+// the rest of the list expert -1.  One workgroup.  Offsets out of order give more tiles than the list has entries, up to E
+// times the rows' tiles: they are counted in 64 bits, so that what is left out is what comes past the end.
 __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
     constexpr int T = kStageThreads;
-    __shared__ int counts[T];
-    __shared__ int base;
+    __shared__ int64_t counts[T];
+    __shared__ int64_t base;
     const int tid = threadIdx.x;
     if (tid == 0) base = 0;
     __syncthreads();
@@ -69,12 +70,12 @@ __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
         counts[tid] = n;
         __syncthreads();
         for (int d = 1; d < T; d <<= 1) {
-            const int v = tid >= d ? counts[tid - d] : 0;
+            const int64_t v = tid >= d ? counts[tid - d] : 0;
             __syncthreads();
             counts[tid] += v;
             __syncthreads();
         }
-        const int first = base + counts[tid] - n;
+        const int64_t first = base + counts[tid] - n;
         for (int t = 0; t < n && first + t < a.cap; ++t) {
             const int64_t r = lo + (int64_t)t * a.tile;
             a.tiles[3 * (first + t)] = e;
@@ -85,7 +86,7 @@ __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
         if (tid == T - 1) base += counts[T - 1];
         __syncthreads();
     }
-    for (int t = base + tid; t < a.cap; t += T) a.tiles[3 * t] = -1;
+    for (int64_t t = base + tid; t < a.cap; t += T) a.tiles[3 * t] = -1;
 }
 
 // Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times

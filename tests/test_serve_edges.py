@@ -144,3 +144,23 @@ def test_adapters_with_dimensions_of_size_one(M):
     term = (X.double().abs() @ a.double().abs()[:, None]) * b.double().abs()
     # A x: at most 64 roundings of 2^-24 on a term's way, 2^-17 where it enters in two bf16 parts
     close(y, X.double() @ W[0] + inner * b.double(), slack(X, s[0], 4, BF16, K) + 2.0 ** -16 * term, BF16)
+
+
+# ---------------------------------------------------------------------------------------------------- steering lists
+
+@gpu
+def test_offsets_out_of_order_over_many_experts_keep_to_the_tile_list():
+    """8192 of 16384 experts claim all of 2^25 rows: 2^31 row tiles and more, of which the list holds its share."""
+    M, K, N, E = 1 << 25, 8, 4, 1 << 14
+    X = torch.zeros(M, K, dtype=BF16, device=DEV)
+    p, s = torch.zeros(E, 1, N, dtype=torch.int32, device=DEV), torch.ones(E, N, device=DEV)
+    off = ints([0]).repeat(E + 1)
+    off[1::2] = M
+    out = torch.full((M + 2, N), 5.0, dtype=BF16, device=DEV)
+    need = g.gptq_matmul_workspace_bytes(BF16, M, K, N, experts=E)
+    ws = torch.empty(need + 4096, dtype=torch.uint8, device=DEV)
+    ws[need:] = 0xA5
+    g.gptq_expert_matmul(X, p, s, off, 4, out=out[1:M + 1], workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert bool((out[0] == 5).all()) and bool((out[M + 1] == 5).all()) and bool((ws[need:] == 0xA5).all())
+    assert bool((out[1:M + 1] == 0).all())           # expert 0 owns every row, and its rows of X are zero
