@@ -463,9 +463,8 @@ gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_ro
  *   requests   device int32[n_requests + 1], non-decreasing, clamped to [0, M]; rows outside have no adapter.
  *   adapter    device int32[n_requests]; -1 (or any value outside [0, n_adapters)): no adapter.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, 1, rank).
- * A x is summed and kept in fp32 (it enters the second product in bf16 parts: two for bf16 rows, with an error 2^-17 of
- * the adapter's term, exactly three for fp32 rows).  An infinity or NaN in a request's rows or adapter stays in that
- * request.  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ * A x is summed and kept in fp32, and enters the second product with all of its bits (as fp32, or as three bf16 parts
+ * on the matrix cores).  An infinity or NaN in a request's rows or adapter stays in that request.  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, int64_t ldx, const uint32_t* packed,
                                   int64_t ldp, int64_t K, int64_t N, int bits, const float* scales, int64_t groupsize,

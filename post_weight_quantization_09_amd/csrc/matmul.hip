@@ -376,9 +376,8 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
 // rows of H zero: an infinite or NaN value of B would reach them), so that B is read once for all of them (row by row it
 // is read again for every token: 266 tokens of 13 adapters, rank 68, 15296 channels: 200 us against 55).  The next
 // operands are on their way while one set is multiplied.
-template <int PARTS>
 __global__ __launch_bounds__(256, 2) void adapter_expand_kernel(MatmulKernelArgs p, float* Z) {
-    constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding
+    constexpr int HP = 3;                            // parts of H: exactly its fp32 value
     constexpr int RT = 4, NT = 4, kMaxOctets = 16;
     __shared__ u32x4 hs[HP][kMaxOctets][64];         // H of the rows as operands
     __shared__ int list[64];
@@ -630,8 +629,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
         if (e != hipSuccess) return e;
         if (k.Z) {
             const dim3 zgrid((unsigned)ceil_div(a.M, 64), (unsigned)ceil_div(a.N, 256));
-            if (a.f32) hipLaunchKernelGGL(adapter_expand_kernel<3>, zgrid, dim3(256), 0, stream, k, buf.Z);
-            else hipLaunchKernelGGL(adapter_expand_kernel<1>, zgrid, dim3(256), 0, stream, k, buf.Z);
+            hipLaunchKernelGGL(adapter_expand_kernel, zgrid, dim3(256), 0, stream, k, buf.Z);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

@@ -42,10 +42,10 @@ constexpr int kTileGroup = 8;          // row tiles that neighbouring workgroups
 
 // acc += H B^T for the rows r0 .. r0 + nrow - 1: one product per run of rows with the same adapter, added to the rows of
 // the run alone (zero rows of H would not do: an infinite or NaN value of B would reach the other rows as 0 * inf).
-template <int PARTS, int RT, int NT, bool GATED>
+template <int RT, int NT, bool GATED>
 __device__ __forceinline__ void add_adapter_runs(const MatmulKernelArgs& p, const LaneChannels<NT, GATED>& ch, int64_t r0,
                                                  int nrow, int lane, f32x4 (&acc)[RT][NT]) {
-    constexpr int HP = PARTS == 1 ? 2 : 3;           // parts of H: its error stays far below the output's rounding
+    constexpr int HP = 3;                            // parts of H: exactly its fp32 value
     const int q = lane >> 4;
     for (int f = 0; f < nrow;) {
         const int a = __builtin_amdgcn_readfirstlane(p.row_adapter[r0 + f]);
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     }
 
     if constexpr (FORM == kAdapters) {
-        if (!p.Z) add_adapter_runs<PARTS, RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
+        if (!p.Z) add_adapter_runs<RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t)

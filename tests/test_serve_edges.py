@@ -164,3 +164,23 @@ def test_offsets_out_of_order_over_many_experts_keep_to_the_tile_list():
     torch.cuda.synchronize()
     assert bool((out[0] == 5).all()) and bool((out[M + 1] == 5).all()) and bool((ws[need:] == 0xA5).all())
     assert bool((out[1:M + 1] == 0).all())           # expert 0 owns every row, and its rows of X are zero
+
+
+# ---------------------------------------------------------------------------------------------------------- numerics
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,N", [([1, 2], 70), ([5, 3], 70), ([30, 40], 70), ([900, 600], 4102), ([1] * 1000 + [2] * 200, 4102)])
+def test_inner_products_of_adapters_keep_all_their_bits(lengths, N, dtype):
+    """A x = (1 + 2^-9 + 2^-20, 1 + 2^-9) with B = (1, -1): 2^-20, exactly, which 16 bits of A x would lose."""
+    K, M = 40, sum(lengths)
+    codes = torch.full((K, N), 8, dtype=torch.uint8, device=DEV)     # a layer of zeros
+    x = torch.zeros(M, K, device=DEV)
+    x[:, 0], x[:, 17], x[:, 39] = 1, 2.0 ** -9, 2.0 ** -20
+    A = torch.zeros(1, 2, K, device=DEV)
+    A[0, 0], A[0, 1, :20] = 1, 1
+    B = torch.tensor([1.0, -1.0], device=DEV).expand(1, N, 2).to(BF16).contiguous()
+    y = g.gptq_adapter_matmul(x.to(dtype), g.gptq_pack_codes(codes, 4), torch.ones(N, device=DEV), 4, A=A.to(BF16), B=B,
+                              alpha=torch.ones(1, device=DEV), requests=ints(np.concatenate([[0], np.cumsum(lengths)]).tolist()),
+                              adapter=ints([0] * len(lengths)))
+    assert bool((y == 2.0 ** -20).all()), (y.min().item(), y.max().item())
