@@ -132,7 +132,8 @@ __device__ __forceinline__ u32x4 pair_order(u32x4 v) {
     return r;
 }
 
-// Eight fp32 values as three bf16 parts whose sum is exact (24 = 3 x 8 mantissa bits): part p in natural order.
+// Eight fp32 values as three bf16 parts whose sum is exact (24 = 3 x 8 mantissa bits): part p in natural order.  They
+// are cut off, not rounded: rounded up, the parts of values near the largest one would be infinite, or their sum on the way.
 // A non-finite value goes into the first part as it is; its remainders, NaN by then, are taken as zero.
 __device__ __forceinline__ void split3(const float (&x)[8], u32x4 (&part)[3]) {
     float r[8];
@@ -142,7 +143,7 @@ __device__ __forceinline__ void split3(const float (&x)[8], u32x4 (&part)[3]) {
     for (int p = 0; p < 3; ++p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            part[p][i] = pack_bf16x2_rne(r[2 * i], r[2 * i + 1]);
+            part[p][i] = __builtin_amdgcn_perm(__float_as_uint(r[2 * i + 1]), __float_as_uint(r[2 * i]), 0x07060302u);
             const float a = r[2 * i] - bf16lo_to_f32(part[p][i]), b = r[2 * i + 1] - bf16hi_to_f32(part[p][i]);
             r[2 * i] = a == a ? a : 0.f;
             r[2 * i + 1] = b == b ? b : 0.f;

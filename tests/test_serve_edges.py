@@ -184,3 +184,36 @@ def test_inner_products_of_adapters_keep_all_their_bits(lengths, N, dtype):
                               alpha=torch.ones(1, device=DEV), requests=ints(np.concatenate([[0], np.cumsum(lengths)]).tolist()),
                               adapter=ints([0] * len(lengths)))
     assert bool((y == 2.0 ** -20).all()), (y.min().item(), y.max().item())
+
+
+# The largest values: what the products hold on the way must not overflow where the result does not.
+@gpu
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_fp32_rows_with_one_value_up_to_the_largest(M):
+    """x = +-max and a little below in one place: a bf16 part rounded from it would be infinite."""
+    K, N = 8, 4100 if M > 1000 else 70
+    gen = torch.Generator().manual_seed(M)
+    codes = torch.randint(7, 10, (K, N), generator=gen).to(torch.uint8)
+    X = torch.randn(M, K, generator=gen)
+    r = torch.arange(M)
+    X[r, r % K] = torch.finfo(F32).max * (1 - (r % 5) * 2.0 ** -10) * ((r % 2) * 2.0 - 1)
+    s = torch.full((K, N), 2.0 ** -20, dtype=torch.float64)
+    y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes[None], 4, DEV), torch.full((1, N), 2.0 ** -20, device=DEV), ints([0, M]), 4)
+    close(y, X.double() @ (s * (codes.double() - 8)), slack(X, s, 4, F32, K), F32)
+
+
+@gpu
+@pytest.mark.parametrize("lengths", [[1], [30], [900, 700]])
+def test_inner_products_of_adapters_up_to_the_largest_value(lengths):
+    """A x = max in fp32, where bf16 would round to infinity; B = 2^-20."""
+    K, N, M = 8, 4100 if len(lengths) > 1 else 70, sum(lengths)
+    x = torch.zeros(M, K, device=DEV)
+    x[:, 0] = torch.finfo(F32).max
+    A, B = torch.zeros(1, 1, K, dtype=BF16, device=DEV), torch.full((1, N, 1), 2.0 ** -20, dtype=BF16, device=DEV)
+    A[0, 0, 0] = 1
+    y = g.gptq_adapter_matmul(x, g.gptq_pack_codes(torch.full((K, N), 8, dtype=torch.uint8, device=DEV), 4),
+                              torch.ones(N, device=DEV), 4, A=A, B=B, alpha=torch.ones(1, device=DEV),
+                              requests=ints([0] + np.cumsum(lengths).tolist()), adapter=ints([0] * len(lengths)))
+    want = torch.finfo(F32).max * 2.0 ** -20
+    # three products of parts, added up in fp32
+    assert bool(((y.double() - want).abs() <= 3 * 2.0 ** -24 * want).all())
