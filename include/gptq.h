@@ -440,8 +440,9 @@ size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int
  *   Y          device, M x N (N / 2 with GPTQ_FLAG_SWIGLU), dtype, leading dimension ldy; not X.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, E, 0).
  * Sums are fp32, of x (2^bits + code) for bf16 rows and of x (code - z) for fp32 rows, times the scale every 128 k or
- * scale group.  A row with an infinity or NaN gives no finite value (NaN also where the exact one is an infinity); no
- * other row is touched.
+ * scale group.  They are kept times 2^-(bits+8): finite rows overflow only where their result does, and results below
+ * 2^-100 lose relative precision.  A row with an infinity or NaN gives no finite value (NaN also where the exact one is
+ * an infinity); no other row is touched.
  * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_rows, int64_t ldx, const int32_t* rows,

@@ -18,7 +18,6 @@ constexpr int kMaxKParts = 8;
 struct StageArgs {
     uint16_t* XT;
     float* sums;
-    float excess;          // -1.5 2^b
     int tile, cap;         // rows of a tile, entries of the list
     int32_t* tiles;
     int row_blocks;        // workgroups of the rows: row_blocks x nchunks (0: rows are not laid out)
@@ -90,7 +89,7 @@ __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
 }
 
 // Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times
-// -1.5 2^b.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces along
+// -1.5 2^-8, the codes' excess.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces along
 // the rows, turned in LDS.  Bound by HBM: every row is read once and written once (8192 gathered rows x 4096, bf16: 27.5 us,
 // 4.9 TB/s).
 template <int PARTS>
@@ -98,6 +97,7 @@ __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int6
     constexpr int kOctets = kChunkK / 8, kPitch = kStageRows + 1;
     u32x4* xt = reinterpret_cast<u32x4*>(lds);                          // [part][octet][row]
     float* os = reinterpret_cast<float*>(xt + PARTS * kOctets * kPitch);
+    constexpr float kMinusExcess = -1.5f / (float)(1 << -kCodeExponent);
     const int tid = threadIdx.x;
     const int64_t noct = (int64_t)nchunks * kOctets;
 #pragma unroll
@@ -113,7 +113,7 @@ __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int6
                               chunk * kChunkK + 8 * o, p.K, part);
         float sum = 0.f;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) sum += bf16lo_to_f32(part[0][d]) + bf16hi_to_f32(part[0][d]);
+        for (int d = 0; d < 4; ++d) sum += kMinusExcess * bf16lo_to_f32(part[0][d]) + kMinusExcess * bf16hi_to_f32(part[0][d]);
 #pragma unroll
         for (int j = 0; j < PARTS; ++j) xt[(j * kOctets + o) * kPitch + row] = pair_order(part[j]);
         os[o * kPitch + row] = sum;
@@ -134,7 +134,7 @@ __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int6
     for (int g = tid >> 6; g < groups; g += kStageThreads / 64) {
         float s = 0.f;
         for (int o = 0; o < per; ++o) s += os[(g * per + o) * kPitch + row];
-        a.sums[((int64_t)chunk * groups + g) * p.Mp + r0 + row] = a.excess * s;
+        a.sums[((int64_t)chunk * groups + g) * p.Mp + r0 + row] = s;
     }
 }
 
@@ -602,7 +602,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
 
     if (lora || plan.kernel != kRows) {
         StageArgs s = {};
-        s.XT = buf.XT; s.sums = buf.sums; s.excess = -1.5f * (float)(1 << a.bits);
+        s.XT = buf.XT; s.sums = buf.sums;
         s.tile = plan.tile; s.cap = plan.cap; s.tiles = buf.tiles;
         int64_t grid = 0;
         bool long_rows = false;

@@ -69,7 +69,7 @@ struct MatmulKernelArgs {
     const uint16_t* B;
     int64_t ldb, b_stride;
     int rank;
-    // rows laid out for the tile kernel: PARTS x [K / 8][Mp] octets, and -1.5 2^b sums of x per row and group
+    // rows laid out for the tile kernel: PARTS x [K / 8][Mp] octets, and per row and group the sum of x times -1.5 2^-8
     const uint16_t* XT;
     const float* sums;
     int64_t Mp;

@@ -188,7 +188,7 @@ void matmul_rows_kernel(MatmulKernelArgs p) {
     const LaneChannels<NT, GATED> ch(tile0, lane, p.N);
     const int nfull = p.K / kChunkK;                 // whole chunks
     const int sh = lane_shift<BITS>(q);
-    const uint32_t base = code_base<BITS>();
+    const uint32_t base = code_base();
     const uint32_t* words0 = p.packed + e * p.p_stride;
     const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     const float* scales = p.scales + e * p.s_stride;
@@ -236,7 +236,7 @@ void matmul_rows_kernel(MatmulKernelArgs p) {
             rows.parts(a);
 #pragma unroll
             for (int i = 0; i < PARTS; ++i) a[i] = pair_order(a[i]);
-            if constexpr (PARTS == 1) sum = mfma16(a[0], minus_excess_frag<BITS>(), sum);
+            if constexpr (PARTS == 1) sum = mfma16(a[0], minus_excess_frag(), sum);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const bf16x8 b = PARTS == 1 ? codes_to_frag<BITS>(v[0][j], v[kLW - 1][j], sh, base)
@@ -297,6 +297,8 @@ void matmul_rows_kernel(MatmulKernelArgs p) {
             for (int s = 0; s < W; ++s)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) y[j] += part[s][wave * NT + j][lane];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) y[j] *= kCodeUnits<BITS>;
             const int64_t r = r0 + 4 * q + wave;
             if (r < hi) {
                 if constexpr (FORM == kAdapters) add_adapter_row<NT, GATED>(p, r, ch, y);

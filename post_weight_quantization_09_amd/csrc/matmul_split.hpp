@@ -38,7 +38,7 @@ __global__ __launch_bounds__(64 * W, 2) void matmul_split_kernel(MatmulKernelArg
     }
     const int nchunks = (p.K + kChunkK - 1) / kChunkK;
     const int sh = lane_shift<BITS>(q);
-    const uint32_t base = code_base<BITS>();
+    const uint32_t base = code_base();
     const uint32_t* words0 = p.packed + e * p.p_stride;
     const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     const float* scales = p.scales + e * p.s_stride;
@@ -155,6 +155,8 @@ __global__ __launch_bounds__(64 * W, 2) void matmul_split_kernel(MatmulKernelArg
         for (int s = 0; s < W; ++s)
 #pragma unroll
             for (int j = 0; j < NT; ++j) y[j] += part[s][v * NT + j][lane];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) y[j] *= kCodeUnits<BITS>;
         const int64_t r = r0 + 16 * (v >> 2) + 4 * q + (v & 3);
         if (r < r1) {
             if constexpr (FORM == kAdapters) add_adapter_row<NT, GATED>(p, r, ch, y);

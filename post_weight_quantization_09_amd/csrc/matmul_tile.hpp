@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
     const int sh = lane_shift<BITS>(q);
     const uint32_t off[2] = {lane_word<BITS>(q) * p.ldp + ch.c0, lane_word2<BITS>(q) * p.ldp + ch.c0};
     constexpr int kLW = kLaneWords<BITS>;
-    const uint32_t base = code_base<BITS>();
+    const uint32_t base = code_base();
     uint32_t w[kChunkSteps][kLW][NT];
     uint32_t sc[kGroups][NT];
     auto load_words = [&](int chunk) {
@@ -265,6 +265,12 @@ __global__ __launch_bounds__(256, PARTS == 1 ? 2 : 1) void matmul_tile_kernel(Ma
         }
     }
 
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][j][i] *= kCodeUnits<BITS>;
     if constexpr (FORM == kAdapters) {
         if (!p.Z) add_adapter_runs<RT, NT, GATED>(p, ch, r0, (int)(r1 - r0), lane, acc);
     }

@@ -6,15 +6,17 @@
 // A lane takes the same words of NT neighbouring channels with one 16- (8-) byte load; product j of the NT products
 // then covers channels 4 (l % 16) + j, and the lane ends up with NT consecutive channels of each of its rows.
 //
-// A code is turned into bf16 by writing its b <= 6 bits at the top of the mantissa of 2^b: the value 2^b + c is exact,
-// and costs one shift and one and-or per pair of codes.  Codes i and i + 4 of the eight share a register (they sit 16
-// bits apart in a 4-bit word), so the A operand is given in the same order of k.  The excess is taken off again in
-// fp32:  sum_k x_k (c_k - z) = sum_k x_k (2^b + c_k) - 1.5 2^b sum_k x_k,  with the row sums of x from a product with
-// the constant -1.5 2^b (exact in bf16) or from the pass that lays x out.  It is done for every 128 k (or scale group),
-// so the partial sums stay near the size of their result.  That leaves an error of 1e-6 to 4e-6 of the result
-// (against 64 bits), which bf16 output cannot show (its own rounding is 1.7e-3) but fp32 output would: fp32 rows, whose
-// three parts make three products per conversion anyway, get c - z itself as operand.  Scales multiply the fp32 partial
-// sums: no weight is rounded.
+// A code is turned into bf16 by writing its b <= 6 bits at the top of the mantissa of 2^-8: the value u (2^b + c), with
+// u = 2^-(b+8), is exact and costs one shift and one and-or per pair of codes.  Codes i and i + 4 of the eight share a
+// register (they sit 16 bits apart in a 4-bit word), so the A operand is given in the same order of k.  The excess is taken
+// off again in fp32:  sum_k x_k (c_k - z) = sum_k x_k (2^b + c_k) - 1.5 2^b sum_k x_k,  with the row sums of x from a
+// product with the constant -1.5 2^b u (exact in bf16) or from the pass that lays x out.  It is done for every 128 k (or
+// scale group), so the partial sums stay near the size of their result.  That leaves an error of 1e-6 to 4e-6 of the
+// result (against 64 bits), which bf16 output cannot show (its own rounding is 1.7e-3) but fp32 output would: fp32 rows,
+// whose three parts make three products per conversion anyway, get u (c - z) itself as operand.  Scales multiply the fp32
+// partial sums: no weight is rounded.
+// The factor u keeps every sum of 128 products below the largest x, so that rows up to the largest value stay finite
+// where their result is; 1/u multiplies the finished sums, exactly.
 #pragma once
 
 #include "gptq_common.hpp"
@@ -53,11 +55,15 @@ __device__ __forceinline__ uint32_t shl_signed(uint32_t v) {
     else return v >> (-S);
 }
 
-// 2^b in both halves of a vector register: with it there, and the mask in a scalar one, and-or is one instruction (a
-// VALU instruction of gfx950 reads one scalar or literal at most).
+// The exponent of every code's value u (2^b + c) = 2^-8 (1 + c / 2^b), and 1/u.
+constexpr int kCodeExponent = -8;
 template <int BITS>
+constexpr float kCodeUnits = (float)(1 << (BITS - kCodeExponent));
+
+// 2^-8 in both halves of a vector register: with it there, and the mask in a scalar one, and-or is one instruction (a
+// VALU instruction of gfx950 reads one scalar or literal at most).
 __device__ __forceinline__ uint32_t code_base() {
-    uint32_t base = ((uint32_t)(127 + BITS) << 7) * 0x10001u;
+    uint32_t base = ((uint32_t)(127 + kCodeExponent) << 7) * 0x10001u;
     asm("" : "+v"(base));
     return base;
 }
@@ -73,7 +79,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t lo, uint32_t hi, uint32_t
     }
 }
 
-// Eight codes (in words w0, w1 at bit `sh`) -> bf16 values 2^b + c, register i = codes (i, i + 4).
+// Eight codes (in words w0, w1 at bit `sh`) -> bf16 values u (2^b + c), register i = codes (i, i + 4).
 template <int BITS>
 __device__ __forceinline__ bf16x8 codes_to_frag(uint32_t w0, uint32_t w1, int sh, uint32_t base) {
     uint32_t lo, hi = 0;
@@ -99,10 +105,10 @@ __device__ __forceinline__ bf16x8 codes_to_frag(uint32_t w0, uint32_t w1, int sh
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// The same as bf16 values c - z: the excess taken off in fp32 (both steps exact), five more operations per pair.
+// The same as bf16 values u (c - z): the excess taken off in fp32 (both steps exact), five more operations per pair.
 template <int BITS>
 __device__ __forceinline__ bf16x8 codes_to_exact_frag(uint32_t w0, uint32_t w1, int sh, uint32_t base) {
-    constexpr float excess = 1.5f * (float)(1 << BITS);
+    constexpr float excess = 1.5f / (float)(1 << -kCodeExponent);
     const u32x4 v = __builtin_bit_cast(u32x4, codes_to_frag<BITS>(w0, w1, sh, base));
     u32x4 r;
 #pragma unroll
@@ -112,14 +118,10 @@ __device__ __forceinline__ bf16x8 codes_to_exact_frag(uint32_t w0, uint32_t w1, 
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// -1.5 2^b in both halves of a register (exact: 2^b (1 + 1/2)).
-template <int BITS>
-constexpr uint32_t kMinusExcess = 0x80008000u | (((uint32_t)(127 + BITS) << 7) | 0x40u) * 0x10001u;
-
-template <int BITS>
+// -1.5 2^b u in both halves of a register (exact: 2^-8 (1 + 1/2)).
 __device__ __forceinline__ bf16x8 minus_excess_frag() {
-    const u32x4 r = {kMinusExcess<BITS>, kMinusExcess<BITS>, kMinusExcess<BITS>, kMinusExcess<BITS>};
-    return __builtin_bit_cast(bf16x8, r);
+    constexpr uint32_t v = 0x80008000u | (((uint32_t)(127 + kCodeExponent) << 7) | 0x40u) * 0x10001u;
+    return __builtin_bit_cast(bf16x8, u32x4{v, v, v, v});
 }
 
 // Eight consecutive bf16 in natural order -> register i = elements (i, i + 4).

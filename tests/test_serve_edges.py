@@ -217,3 +217,47 @@ def test_inner_products_of_adapters_up_to_the_largest_value(lengths):
     want = torch.finfo(F32).max * 2.0 ** -20
     # three products of parts, added up in fp32
     assert bool(((y.double() - want).abs() <= 3 * 2.0 ** -24 * want).all())
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_fp32_rows_up_to_the_largest_value(M):
+    """x = +-max: a bf16 part rounded from it would be infinite.  Weights 2^-20 (c - 8) with c - 8 in {-1, 0, 1}."""
+    K, N = 8, 4100 if M > 1000 else 70
+    gen = torch.Generator().manual_seed(M)
+    codes = torch.randint(7, 10, (K, N), generator=gen).to(torch.uint8)
+    sign = torch.randint(0, 2, (M, K), generator=gen) * 2.0 - 1
+    X = sign * torch.finfo(F32).max
+    X[:, 1:4] *= 0.999                               # on both sides of the last value that bf16 rounds down
+    X[:, 4:] *= 2.0 ** -30
+    y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes[None], 4, DEV), torch.full((1, N), 2.0 ** -20, device=DEV), ints([0, M]), 4)
+    W = 2.0 ** -20 * (codes.double() - 8)
+    close(y, X.double() @ W, slack(X, torch.full((K, N), 2.0 ** -20, dtype=torch.float64), 4, F32, K), F32)
+
+
+@gpu
+@pytest.mark.parametrize("bits,groupsize", [(2, 0), (3, 32), (4, 128), (5, 64), (6, 0)])
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_bf16_rows_up_to_the_largest_value(M, bits, groupsize):
+    """Every x is +-max, and a third of the rows have one sign alone: 128 codes at the top of the grid, unscaled, pass it."""
+    K, N = 300, 4100 if M > 1000 else 70
+    codes, scales, W, s = layer(K, N, bits, groupsize, M)
+    X = torch.randint(0, 2, (M, K), generator=torch.Generator().manual_seed(M)) * 2.0 - 1
+    X[::3] = 1
+    X = (X * torch.finfo(BF16).max).to(BF16)
+    W, s, scales = W * 2.0 ** -12, s * 2.0 ** -12, scales * 2.0 ** -12
+    y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes, bits, DEV), scales.to(DEV), ints([0, M]), bits, groupsize=groupsize)
+    close(y, X.double() @ W[0], slack(X, s[0], bits, BF16, K), BF16)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_small_values(M, dtype):
+    """Rows of about 2^-80 and a scale of 2^-6: no product falls below the normal numbers."""
+    K, N = 300, 4100 if M > 1000 else 70
+    codes, scales, W, s = layer(K, N, 4, 64, M)
+    X = (rows_of(M, K, F32, 1) * 2.0 ** -80).to(dtype)
+    y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes, 4, DEV), scales.to(DEV), ints([0, M]), 4, groupsize=64)
+    y, ref = y.double().cpu() * 2.0 ** 80, X.double() @ W[0] * 2.0 ** 80
+    close(y, ref, slack(X, s[0], 4, dtype, K) * 2.0 ** 80, dtype)
