@@ -9,7 +9,9 @@
 // 13.0 us with one token per wave, 7.4 with four).  The sort needs, per block of kBlockTokens tokens and expert,
 // which tokens chose it: a bitmap in LDS, whose popcounts are both the block's count and the token's rank, whatever order
 // the waves ran in.  Up to one block of tokens everything is one launch (one token: 3.4 us); else a second launch adds up
-// the blocks' counts, a byte each (each block for itself, from L2: 6.8 us with 32-bit counts, 5.6 with bytes), and places the rows.
+// the blocks' counts, a byte each (each block for itself, from L2: 6.8 us with 32-bit counts, 5.6 with bytes), and places
+// the rows.  That grows with the square of the tokens, so many blocks are first added up by groups of 64, whose sums are
+// scanned (2^20 tokens, 128 experts, 8 choices: 462 us).
 #include "route.hpp"
 
 #include <algorithm>
@@ -20,6 +22,7 @@ namespace {
 
 constexpr int kBlockTokens = 64;
 constexpr int kRouteWaves = 16;
+constexpr int kGroupBlocks = 64;        // blocks whose counts are summed together where there are many
 
 struct RouteArgs {
     const void* logits;
@@ -34,6 +37,8 @@ struct RouteArgs {
     uint8_t* counts;        // [block][E, rounded up to 4]
     uint32_t* bad;          // [block]
     int nblocks;
+    int32_t* before;        // [group][E]: an expert's tokens in the groups of blocks before; only where grouped
+    int32_t* whole;         // [E]: an expert's tokens
 };
 
 // Maximum over 16 lanes (in all of them), or over the wave, by data-parallel moves.
@@ -242,7 +247,55 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     }
 }
 
-// Second launch: the first row of every expert for this block, then the rows of its tokens.
+// Many blocks: an expert's tokens in every group of kGroupBlocks blocks.  A thread takes four experts.
+__global__ __launch_bounds__(256) void group_counts_kernel(RouteArgs p) {
+    const int words = (p.E + 3) >> 2, word = threadIdx.x;
+    if (word >= words) return;
+    const int64_t k0 = (int64_t)blockIdx.x * kGroupBlocks;
+    const int n = (int)min((int64_t)kGroupBlocks, p.nblocks - k0);
+    const uint32_t* counts = reinterpret_cast<const uint32_t*>(p.counts) + k0 * words + word;
+    uint32_t w[2] = {0, 0};                           // experts 0 and 2, 1 and 3: 64 counts of at most 64 fit 16 bits
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const uint32_t c = counts[(int64_t)k * words];
+        w[0] += c & 0x00FF00FFu;
+        w[1] += (c >> 8) & 0x00FF00FFu;
+    }
+    int32_t* to = p.before + (int64_t)blockIdx.x * p.E + 4 * word;
+    for (int i = 0; i < 4 && 4 * word + i < p.E; ++i) to[i] = (int)(w[i & 1] >> (i & 2 ? 16 : 0) & 0xFFFFu);
+}
+
+// Then, for 32 experts a workgroup, their sums over the groups before, in place, and over all.
+__global__ __launch_bounds__(1024) void scan_groups_kernel(RouteArgs p) {
+    constexpr int kParts = 32, kAhead = 8;
+    __shared__ int sums[kParts][32];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int ngroups = (p.nblocks + kGroupBlocks - 1) / kGroupBlocks, per = (ngroups + kParts - 1) / kParts;
+    const int g0 = min(part * per, ngroups), g1 = e < p.E ? min(g0 + per, ngroups) : g0;
+    int sum = 0;
+#pragma unroll 8
+    for (int g = g0; g < g1; ++g) sum += p.before[(int64_t)g * p.E + e];
+    sums[part][lane] = sum;
+    __syncthreads();
+    int at = 0;
+    for (int q = 0; q < part; ++q) at += sums[q][lane];
+    for (int g = g0; g < g1; g += kAhead) {
+        int v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v[i] = g + i < g1 ? p.before[(int64_t)(g + i) * p.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (g + i < g1) {
+                p.before[(int64_t)(g + i) * p.E + e] = at;
+                at += v[i];
+            }
+    }
+    if (part == kParts - 1 && e < p.E) p.whole[e] = at;
+}
+
+// Last launch: the first row of every expert for this block, then the rows of its tokens.  It adds up the counts of all
+// blocks or, GROUPED, those of its group's blocks before it.
+template <bool GROUPED>
 __global__ __launch_bounds__(64 * kRouteWaves) void place_kernel(RouteArgs p) {
     __shared__ int before[kRouteMaxExperts], whole[kRouteMaxExperts];
     __shared__ int scratch[kRouteWaves];
@@ -261,16 +314,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void place_kernel(RouteArgs p) {
             rank[u] = p.positions[t0 * p.topk + i];
         }
     }
-    for (int e = tid; e < kRouteMaxExperts; e += nthreads) before[e] = whole[e] = 0;
+    const int64_t group = blockIdx.x / kGroupBlocks;
+    const int begin = GROUPED ? (int)group * kGroupBlocks : 0, blocks_end = GROUPED ? (int)blockIdx.x : p.nblocks;
+    for (int e = tid; e < kRouteMaxExperts; e += nthreads) {
+        before[e] = GROUPED && e < p.E ? p.before[group * p.E + e] : 0;
+        whole[e] = 0;
+    }
     __syncthreads();
     // threads side by side take four experts each; what is left of the workgroup splits the blocks
     const int words = (p.E + 3) >> 2, parts = nthreads / words, part = tid / words, word = tid - part * words;
     const uint32_t* counts = reinterpret_cast<const uint32_t*>(p.counts) + word;
     constexpr int kSum = 512;                         // bytes of at most 64 that 16 bits hold the sum of
     if (part < parts) {
-        for (int k0 = part; k0 < p.nblocks; k0 += kSum * parts) {
+        for (int k0 = begin + part; k0 < blocks_end; k0 += kSum * parts) {
             uint32_t w[2] = {0, 0}, b[2] = {0, 0};    // experts 0 and 2, 1 and 3
-            const int end = (int)min((int64_t)p.nblocks, k0 + (int64_t)kSum * parts);
+            const int end = (int)min((int64_t)blocks_end, k0 + (int64_t)kSum * parts);
 #pragma unroll 8
             for (int k = k0; k < end; k += parts) {
                 const uint32_t c = counts[(int64_t)k * words], c0 = c & 0x00FF00FFu, c1 = (c >> 8) & 0x00FF00FFu;
@@ -288,7 +346,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void place_kernel(RouteArgs p) {
         }
     }
     __syncthreads();
-    const int n = tid < p.E ? whole[tid] : 0;         // E <= 1024 threads
+    const int n = tid < p.E ? GROUPED ? p.whole[tid] : whole[tid] : 0;      // E <= 1024 threads
     const int upto = block_scan(n, scratch);
     if (tid < p.E) {
         before[tid] += upto - n;
@@ -377,10 +435,16 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* Y, int64_t M, 
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether the blocks' counts are first added up by groups, two short launches more, or by every block for itself, which
+// reads blocks^2 E bytes from L2 (1024 blocks, 64 experts: 24 us the second way, 31 the first; 256 experts: 77 and 71;
+// 2048 blocks, 8 experts: 54 and 42; 16384 blocks, 128 experts: 2785 and 462).
+bool counts_by_groups(int64_t blocks, int64_t E) { return blocks > 1024 || blocks * blocks * E > (int64_t)1 << 27; }
+
 struct RouteBuffers {
     DevStatus* status;
     uint8_t* counts;
     uint32_t* bad;
+    int32_t *before, *whole;
     size_t bytes;
     RouteBuffers(int64_t T, int64_t E, void* ws) {
         const size_t blocks = (size_t)ceil_div(T, kBlockTokens);
@@ -388,6 +452,9 @@ struct RouteBuffers {
         status = c.take<DevStatus>(1);
         counts = c.take<uint8_t>(blocks > 1 ? blocks * align_up((size_t)E, 4) : 0);
         bad = c.take<uint32_t>(blocks > 1 ? blocks : 0);
+        const bool grouped = counts_by_groups(blocks, E);
+        before = grouped ? c.take<int32_t>((blocks + kGroupBlocks - 1) / kGroupBlocks * (size_t)E) : nullptr;
+        whole = grouped ? c.take<int32_t>((size_t)E) : nullptr;
         bytes = c.bytes();
     }
 };
@@ -409,6 +476,7 @@ hipError_t route(const void* logits, bool f32, int64_t T, int64_t E, int64_t ld,
     p.weights = weights; p.experts = experts; p.offsets = offsets; p.rows = rows; p.positions = positions;
     p.status = buf.status; p.counts = buf.counts; p.bad = buf.bad;
     p.nblocks = (int)ceil_div(T, kBlockTokens);
+    p.before = buf.before; p.whole = buf.whole;
     const dim3 grid((unsigned)p.nblocks), block(64 * kRouteWaves);
 #define GPTQ_ROUTE(LANES, V)                                                                      \
     do {                                                                                          \
@@ -429,7 +497,12 @@ hipError_t route(const void* logits, bool f32, int64_t T, int64_t E, int64_t ld,
     if (p.nblocks > 1) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(place_kernel, grid, block, 0, stream, p);
+        if (p.before) {
+            hipLaunchKernelGGL(group_counts_kernel, dim3((unsigned)ceil_div(p.nblocks, kGroupBlocks)), dim3(256), 0, stream, p);
+            hipLaunchKernelGGL(scan_groups_kernel, dim3((unsigned)ceil_div(E, 32)), dim3(1024), 0, stream, p);
+        }
+        if (p.before) hipLaunchKernelGGL(place_kernel<true>, grid, block, 0, stream, p);
+        else hipLaunchKernelGGL(place_kernel<false>, grid, block, 0, stream, p);
     }
     return hipGetLastError();
 }

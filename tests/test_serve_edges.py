@@ -261,3 +261,57 @@ def test_small_values(M, dtype):
     y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes, 4, DEV), scales.to(DEV), ints([0, M]), 4, groupsize=64)
     y, ref = y.double().cpu() * 2.0 ** 80, X.double() @ W[0] * 2.0 ** 80
     close(y, ref, slack(X, s[0], 4, dtype, K) * 2.0 ** 80, dtype)
+
+
+# -------------------------------------------------------------------------------------------------- many tokens routed
+
+def route_on_device(x, topk):
+    """The definition by sorts on the GPU: experts, offsets, rows, positions."""
+    T, E = x.shape
+    v, ex = torch.sort(x, dim=1, descending=True, stable=True)
+    v, ex = v[:, :topk], ex[:, :topk]
+    ex = torch.where(v > -math.inf, ex, torch.full_like(ex, E))
+    flat = ex.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    counts = torch.bincount(flat, minlength=E + 1)
+    n = int(counts[:E].sum())
+    pos = torch.empty_like(order)
+    pos[order] = torch.arange(order.numel(), device=x.device)
+    rows = torch.where(torch.arange(order.numel(), device=x.device) < n, order // topk, -1)
+    return (torch.where(ex < E, ex, -1), torch.cat([counts.new_zeros(1), counts[:E].cumsum(0)]), rows,
+            torch.where(flat < E, pos, -1).view(T, topk))
+
+
+# Around 1024 blocks of 64 tokens (or blocks^2 experts = 2^27) and groups of 64 blocks, where the placing of the rows changes.
+@gpu
+@pytest.mark.parametrize("T,E,topk", [(65536, 128, 2), (65536, 129, 2), (65537, 5, 2), (69632, 64, 3), (69633, 64, 3),
+                                      (32768, 9, 2), (32769, 9, 2), (36864, 130, 1), (36865, 64, 8), (262144 + 63, 33, 3),
+                                      (300001, 1, 1), (40000, 1023, 4), (1 << 20, 8, 2)])
+def test_route_of_many_tokens(T, E, topk):
+    x = torch.randn(T, E, device=DEV, generator=torch.Generator(DEV).manual_seed(T))
+    x[T // 3:T // 2, :E // 2 + 1] = -math.inf        # a stretch of tokens with few experts, or none
+    need = g.gptq_workspace_bytes(g.GPTQ_CALL_ROUTE, E, 0, T)
+    ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = g.gptq_route(x, topk, workspace=ws[:need])
+    ex, off, rows, pos = route_on_device(x, min(topk, E))
+    assert torch.equal(out["experts"].long(), ex) and torch.equal(out["offsets"].long(), off)
+    assert torch.equal(out["rows"].long(), rows) and torch.equal(out["positions"].long(), pos)
+    assert bool((ws[need:] == 0xA5).all())
+
+
+@gpu
+def test_route_takes_time_in_proportion_to_its_tokens():
+    """Four times the tokens: four times the time, not sixteen."""
+    def us(T):
+        x = torch.randn(T, 64, device=DEV)
+        ws = torch.empty(g.gptq_workspace_bytes(g.GPTQ_CALL_ROUTE, 64, 0, T), dtype=torch.uint8, device=DEV)
+        best = math.inf
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.gptq_route(x, 2, workspace=ws)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    assert us(1 << 21) < 8 * us(1 << 19)
