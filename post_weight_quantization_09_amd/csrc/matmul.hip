@@ -32,6 +32,7 @@ struct StageArgs {
     int64_t n_requests;
     int slices;            // workgroups of a request along its rows (0: no adapters)
     int k_parts;           // and along K: part z of H is at z * M * hrank
+    int64_t windows;       // of one pass's rows, for what is longer (0: no request can be)
     float* H;
     int32_t* row_adapter;
 };
@@ -221,16 +222,113 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
 // ranks: lane l holds row l % 16 and, of A, rank l % 16, eight consecutive k each, straight from memory; a wave has the
 // loads of kAhead steps in flight) and the partial sums are joined in LDS in a fixed order.  One to four tokens are no
 // matrix product: there a wave takes a rank and reads its row of A in whole kilobytes (as operands it would be 64 pieces of 16
-// bytes), products and sums in fp32 (one token, 4096 features, rank 16: 4.6 against 7.4 us).  Every request gets
-// `slices` workgroups, so that the launch does not depend on the lengths, which only the device knows.  Prompts take 64
-// rows at a time, since every pass reads A again, and split K over k_parts workgroups; their sums are added where H is
-// used (4096 rows x 28672, rank 64, rows laid out beside it: 230 us against 333 with 16 rows and no split).  H stays in
-// fp32.
+// bytes), products and sums in fp32 (one token, 4096 features, rank 16: 4.6 against 7.4 us).  Prompts take 64 rows at a
+// time, since every pass reads A again, and split K over k_parts workgroups; their sums are added where H is used (4096
+// rows x 28672, rank 64, rows laid out beside it: 230 us against 333 with 16 rows and no split).  H stays in fp32.
+//
+// The launch cannot depend on the lengths, which only the device knows.  Every request gets `slices` workgroups, which
+// take one pass each; what is longer is left to `windows` workgroups, one per 16 RS rows of X, which look up the requests
+// that reach into theirs (one request of 3841 rows beside 255 of one, 4096 features, rank 16: 53 us; 494
+// with the request's own workgroups alone).
+
+// One pass: the rows r0 .. min(r0 + 16 RS, hi) - 1, for adapter `id`, over this workgroup's part z of K.
 template <int PARTS, int NR, int RS>
-__device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t req, int slice, int z, char* lds) {
+__device__ void shrink_pass(const MatmulKernelArgs& p, const StageArgs& a, int id, float alpha, int64_t r0, int64_t hi, int z,
+                            char* lds) {
     constexpr int W = kStageThreads / 64, kXBytes = PARTS == 1 ? 2 : 4;
     float* part = reinterpret_cast<float*>(lds);     // [wave][rank and row register][lane]
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int whole = p.K / kStepK, per = ((whole + a.k_parts - 1) / a.k_parts + 1) & ~1;
+    const int s_begin = min(z * per, whole), s_end = min(s_begin + per, whole);
+    float* H = a.H + (int64_t)z * p.M * p.hrank;
+    const char* xrow[RS];
+#pragma unroll
+    for (int t = 0; t < RS; ++t) {
+        int64_t r = r0 + 16 * t + (lane & 15);
+        if (r >= hi) r = hi - 1;
+        xrow[t] = static_cast<const char*>(p.X) + (r * p.ldx + 8 * q) * kXBytes;
+    }
+    const uint16_t* arow[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        int rk = 16 * n + (lane & 15);
+        if (rk >= p.rank) rk = p.rank - 1;           // ranks past the end are not stored
+        arow[n] = a.A + id * a.a_stride + rk * a.lda + 8 * q;
+    }
+    f32x4 acc[RS][NR];
+#pragma unroll
+    for (int t = 0; t < RS; ++t)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // pairs of steps (128 bytes of a bf16 row) are dealt out to the waves, kAhead steps at a time
+    constexpr int kAhead = RS > 1 || NR * PARTS > 4 ? 2 : 8;
+    constexpr int kTurn = 2 * W;
+    for (int s0 = s_begin + 2 * wave; s0 < s_end; s0 += kTurn * (kAhead / 2)) {
+        RawOctet<PARTS> x[kAhead][RS];
+        RawOctet<1> b[kAhead][NR];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            int s = s0 + (u >> 1) * kTurn + (u & 1);
+            s = s < s_end ? s : s0;                  // beyond the end: loaded again and not used
+#pragma unroll
+            for (int t = 0; t < RS; ++t) x[u][t].whole(xrow[t] + s * (kStepK * kXBytes));
+#pragma unroll
+            for (int n = 0; n < NR; ++n) b[u][n].whole(reinterpret_cast<const char*>(arow[n] + s * kStepK));
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (s0 + (u >> 1) * kTurn + (u & 1) < s_end) {
+#pragma unroll
+                for (int t = 0; t < RS; ++t) {
+                    u32x4 xp[PARTS];
+                    x[u][t].parts(xp);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i)
+                            acc[t][n] = mfma16(xp[i], __builtin_bit_cast(bf16x8, b[u][n].v[0]), acc[t][n]);
+                }
+            }
+        }
+    }
+    if (z == a.k_parts - 1 && wave == W - 1 && whole * kStepK < p.K) {   // the rest of K
+        u32x4 x[PARTS], b[1];
+        const int k = whole * kStepK, left = p.K - k - 8 * q;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            load_octet<1>(arow[n], k, k + left, b);
+#pragma unroll
+            for (int t = 0; t < RS; ++t) {
+                load_octet<PARTS>(xrow[t], k, k + left, x);
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) acc[t][n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[t][n]);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RS; ++t) {
+        __syncthreads();                             // the partials before these have been read
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[(wave * NR * 4 + n * 4 + i) * 64 + lane] = acc[t][n][i];
+        __syncthreads();
+        for (int v = wave; v < NR * 4; v += W) {
+            float s = 0.f;
+#pragma unroll
+            for (int u = 0; u < W; ++u) s += part[(u * NR * 4 + v) * 64 + lane];
+            const int64_t row = r0 + 16 * t + 4 * q + (v & 3);
+            const int rk = 16 * (v >> 2) + (lane & 15);
+            if (row < hi && rk < p.hrank) H[row * p.hrank + rk] = rk < p.rank ? s * alpha : 0.f;
+        }
+    }
+}
+
+// The rows of request `req`: their adapter, and one pass of A x per workgroup (single tokens: all of it).
+template <int PARTS, int NR, int RS>
+__device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t req, int slice, int z, char* lds) {
+    const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (req == a.n_requests) {                       // rows of no request
         if (slice || z) return;
@@ -254,95 +352,53 @@ __device__ void shrink_rows(const MatmulKernelArgs& p, const StageArgs& a, int64
         }
         return;
     }
-    // this workgroup's steps of K
-    const int whole = p.K / kStepK, per = ((whole + a.k_parts - 1) / a.k_parts + 1) & ~1;
-    const int s_begin = min(z * per, whole), s_end = min(s_begin + per, whole);
-    float* H = a.H + (int64_t)z * p.M * p.hrank;
-    const int64_t step = 16 * RS * (int64_t)a.slices;
-    for (int64_t r0 = lo + 16 * RS * (int64_t)slice; r0 < hi; r0 += step) {
-        if (z == 0 && tid < 16 * RS && r0 + tid < hi) a.row_adapter[r0 + tid] = id;
-        if (id < 0) continue;
-        const char* xrow[RS];
-#pragma unroll
-        for (int t = 0; t < RS; ++t) {
-            int64_t r = r0 + 16 * t + (lane & 15);
-            if (r >= hi) r = hi - 1;
-            xrow[t] = static_cast<const char*>(p.X) + (r * p.ldx + 8 * q) * kXBytes;
+    if (z == 0)
+        for (int64_t r = lo + slice * kStageThreads + tid; r < hi; r += (int64_t)a.slices * kStageThreads) a.row_adapter[r] = id;
+    const int64_t r0 = lo + 16 * RS * (int64_t)slice;
+    if (id >= 0 && r0 < hi) shrink_pass<PARTS, NR, RS>(p, a, id, alpha, r0, hi, z, lds);
+}
+
+// The rows of one window that their requests' own workgroups do not reach.  The requests are looked through side by side, from
+// the one that the window's first row belongs to (found by halving) where they are many.
+template <int PARTS, int NR, int RS>
+__device__ void shrink_window(const MatmulKernelArgs& p, const StageArgs& a, int64_t window, int z, char* lds) {
+    constexpr int T = kStageThreads;
+    __shared__ int list[T], count;
+    const int tid = threadIdx.x;
+    const int64_t w0 = window * 16 * RS, w1 = w0 + 16 * RS < p.M ? w0 + 16 * RS : p.M;
+    const int64_t reach = 16 * RS * (int64_t)a.slices;
+    int64_t q = 0;
+    if (a.n_requests > T) {
+        int64_t past = a.n_requests;
+        while (past - q > 1) {
+            const int64_t mid = (q + past) / 2;
+            if (a.requests[mid] <= w0) q = mid;
+            else past = mid;
         }
-        const uint16_t* arow[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            int rk = 16 * n + (lane & 15);
-            if (rk >= p.rank) rk = p.rank - 1;       // ranks past the end are not stored
-            arow[n] = a.A + id * a.a_stride + rk * a.lda + 8 * q;
+    }
+    for (; q < a.n_requests; q += T) {
+        if (tid == 0) count = 0;
+        __syncthreads();
+        auto span = [&](int64_t req, int64_t& begin, int64_t& end) {
+            int64_t lo = a.requests[req], hi = a.requests[req + 1];
+            lo = lo < 0 ? 0 : lo;
+            begin = lo + reach > w0 ? lo + reach : w0;
+            end = hi < w1 ? hi : w1;
+        };
+        int64_t begin = 0, end = 0;
+        if (q + tid < a.n_requests) span(q + tid, begin, end);
+        if (begin < end) list[atomicAdd(&count, 1)] = (int)(q + tid);    // in any order: each has rows of its own
+        __syncthreads();
+        const int n = count;
+        for (int i = 0; i < n; ++i) {
+            const int64_t req = list[i];
+            span(req, begin, end);
+            const int id = a.adapter[req];
+            if (id < 0 || id >= a.n_adapters) continue;
+            shrink_pass<PARTS, NR, RS>(p, a, id, a.alpha[id], begin, end, z, lds);
         }
-        f32x4 acc[RS][NR];
-#pragma unroll
-        for (int t = 0; t < RS; ++t)
-#pragma unroll
-            for (int n = 0; n < NR; ++n) acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // pairs of steps (128 bytes of a bf16 row) are dealt out to the waves, kAhead steps at a time
-        constexpr int kAhead = RS > 1 || NR * PARTS > 4 ? 2 : 8;
-        constexpr int kTurn = 2 * W;
-        for (int s0 = s_begin + 2 * wave; s0 < s_end; s0 += kTurn * (kAhead / 2)) {
-            RawOctet<PARTS> x[kAhead][RS];
-            RawOctet<1> b[kAhead][NR];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                int s = s0 + (u >> 1) * kTurn + (u & 1);
-                s = s < s_end ? s : s0;              // beyond the end: loaded again and not used
-#pragma unroll
-                for (int t = 0; t < RS; ++t) x[u][t].whole(xrow[t] + s * (kStepK * kXBytes));
-#pragma unroll
-                for (int n = 0; n < NR; ++n) b[u][n].whole(reinterpret_cast<const char*>(arow[n] + s * kStepK));
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (s0 + (u >> 1) * kTurn + (u & 1) < s_end) {
-#pragma unroll
-                    for (int t = 0; t < RS; ++t) {
-                        u32x4 xp[PARTS];
-                        x[u][t].parts(xp);
-#pragma unroll
-                        for (int n = 0; n < NR; ++n)
-#pragma unroll
-                            for (int i = 0; i < PARTS; ++i)
-                                acc[t][n] = mfma16(xp[i], __builtin_bit_cast(bf16x8, b[u][n].v[0]), acc[t][n]);
-                    }
-                }
-            }
-        }
-        if (z == a.k_parts - 1 && wave == W - 1 && whole * kStepK < p.K) {   // the rest of K
-            u32x4 x[PARTS], b[1];
-            const int k = whole * kStepK, left = p.K - k - 8 * q;
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                load_octet<1>(arow[n], k, k + left, b);
-#pragma unroll
-                for (int t = 0; t < RS; ++t) {
-                    load_octet<PARTS>(xrow[t], k, k + left, x);
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc[t][n] = mfma16(x[i], __builtin_bit_cast(bf16x8, b[0]), acc[t][n]);
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < RS; ++t) {
-            __syncthreads();                         // the partials before these have been read
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[(wave * NR * 4 + n * 4 + i) * 64 + lane] = acc[t][n][i];
-            __syncthreads();
-            for (int v = wave; v < NR * 4; v += W) {
-                float s = 0.f;
-#pragma unroll
-                for (int u = 0; u < W; ++u) s += part[(u * NR * 4 + v) * 64 + lane];
-                const int64_t row = r0 + 16 * t + 4 * q + (v & 3);
-                const int rk = 16 * (v >> 2) + (lane & 15);
-                if (row < hi && rk < p.hrank) H[row * p.hrank + rk] = rk < p.rank ? s * alpha : 0.f;
-            }
-        }
+        if (q + T < a.n_requests && a.requests[q + T] >= w1) return;
+        __syncthreads();                             // the list has been read
     }
 }
 
@@ -362,6 +418,11 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
             return;
         }
         b -= n;
+        if (b < a.windows * a.k_parts) {
+            shrink_window<PARTS, NR, RS>(p, a, b / a.k_parts, (int)(b % a.k_parts), lds);
+            return;
+        }
+        b -= a.windows * a.k_parts;
     }
     const int nchunks = a.nchunks;
     if (b == (int64_t)a.row_blocks * nchunks) {
@@ -621,7 +682,8 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
             s.k_parts = plan.k_parts;
             s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(ceil_div(a.M, rows), std::min<int64_t>(a.M, 4)),
                                                                      1024 / (a.n_requests * s.k_parts)));
-            grid += (a.n_requests + 1) * s.slices * s.k_parts;
+            s.windows = (int64_t)rows * s.slices < a.M ? ceil_div(a.M, rows) : 0;
+            grid += ((a.n_requests + 1) * s.slices + s.windows) * s.k_parts;
         }
         if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
         hipError_t e = a.f32 ? launch_stage<3>(k, s, long_rows, (unsigned)grid, stream)

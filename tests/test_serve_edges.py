@@ -315,3 +315,64 @@ def test_route_takes_time_in_proportion_to_its_tokens():
             best = min(best, a.elapsed_time(b))
         return best
     assert us(1 << 21) < 8 * us(1 << 19)
+
+
+# ---------------------------------------------------------------------------------- long requests beside single tokens
+
+def mixed(lengths, ids, K, N, rank, dtype, seed=0):
+    """A call's tensors, and its result and bound in 64 bits, for adapters that repeat among many requests."""
+    M, n = sum(lengths), 5
+    codes, scales, W, s = layer(K, N, 4, 128, seed)
+    X, gen = rows_of(M, K, dtype, seed + 1), torch.Generator().manual_seed(seed + 2)
+    A = (torch.randn(n, rank, K, generator=gen) / math.sqrt(K)).to(BF16)
+    B = (torch.randn(n, N, rank, generator=gen) * 0.3).to(BF16)
+    alpha = torch.rand(n, generator=gen) + 0.5
+    owner = torch.tensor(np.repeat(ids, lengths))
+    ref, bound = X.double() @ W[0], slack(X, s[0], 4, dtype, K)
+    for a in range(n):
+        r = owner == a
+        x, al = X[r].double(), alpha[a].double()
+        inner = x.abs() @ A[a].double().abs().t()
+        # A x: an fp32 sum of at most (16 + K / 256 + 16) roundings on a term's way; times alpha, times B: 8 more
+        ref[r] += al * (x @ A[a].double().t()) @ B[a].double().t()
+        bound[r] += (16 + -(-K // 256) + 16 + 8) * 2.0 ** -24 * al * inner @ B[a].double().abs().t()
+    call = dict(X=X.to(DEV), packed=packed_on(codes, 4, DEV)[0], scales=scales[0].to(DEV), bits=4, groupsize=128, A=A.to(DEV),
+                B=B.to(DEV), alpha=alpha.to(DEV), requests=ints([0] + np.cumsum(lengths).tolist()), adapter=ints(ids))
+    return call, ref, bound
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,N", [([1] * 40 + [700] + [1] * 60, 70), ([700] + [1] * 200, 70), ([1] * 200 + [65, 300], 70),
+                                       ([1] * 600 + [1500] + [0] * 700 + [1] * 30, 70), ([5] * 300, 70),
+                                       ([1] * 255 + [3841], 4100), ([2500] + [1] * 30 + [0] * 5, 4100),
+                                       ([1] * 1100 + [2000, 33, 1000] + [2] * 5, 4100)])
+def test_adapter_matmul_long_requests_beside_single_tokens(lengths, N, dtype):
+    ids = [(3 * i) % 6 - 1 for i in range(len(lengths))]
+    ids[int(np.argmax(lengths))] = 2
+    call, ref, bound = mixed(lengths, ids, 333, N, 20, dtype)
+    close(g.gptq_adapter_matmul(**call), ref, bound, dtype)
+
+
+@gpu
+def test_a_long_request_beside_single_tokens_is_shared_out():
+    """The same rows with one adapter, as 256 requests of 16 and as one of 3841 beside 255 of one: alike in time."""
+    K, M, n = 4096, 4096, 256
+    X, p = torch.randn(M, K, device=DEV).to(BF16), torch.zeros(K // 8, 64, dtype=torch.int32, device=DEV)
+    A, B = torch.zeros(1, 16, K, dtype=BF16, device=DEV), torch.zeros(1, 64, 16, dtype=BF16, device=DEV)
+    s, al, ad = torch.ones(64, device=DEV), torch.ones(1, device=DEV), ints([0] * n)
+    ws = torch.empty(g.gptq_matmul_workspace_bytes(BF16, M, K, 64, rank=16), dtype=torch.uint8, device=DEV)
+
+    def us(lengths):
+        req = ints([0] + np.cumsum(lengths).tolist())
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                g.gptq_adapter_matmul(X, p, s, 4, A=A, B=B, alpha=al, requests=req, adapter=ad, workspace=ws)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    assert us([1] * 255 + [3841]) < 3 * us([16] * 256)
