@@ -426,9 +426,9 @@ size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int
  *   Y[r] = X[rows[r]] W_e  for r in [offsets[e], offsets[e + 1]); with GPTQ_FLAG_SWIGLU
  *   Y[r][n] = silu(y_n) y_{n + N/2}, n < N/2, silu(g) = g / (1 + e^-g), in fp32 before the one rounding.
  *
- *   X          device, x_rows x K, dtype, leading dimension ldx >= K.
+ *   X          device, x_rows x K, dtype, leading dimension ldx >= K.   x_rows at least 1 where M is.
  *   rows       NULL (row r of X; x_rows >= M), or device int32[M]; a value outside [0, x_rows) gives a zero row.
- *   M          rows of Y, 0 .. 2^30.
+ *   M          rows of Y, 0 .. 2^30; with more than 64 an expert on average (M / 64 + E + 3) ceil(N / 256) < 2^24.
  *   offsets    device int32[E + 1], non-decreasing; clamped to [0, M].  Rows before offsets[0] and from offsets[E] on
  *              are written as zeros.
  *   E          1 .. 16384 experts.
@@ -460,12 +460,13 @@ gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_ro
  *   A          device bf16, rank x K per adapter (the layout of an nn.Linear weight), row i of adapter a at
  *              A + a * a_stride + i * lda; lda >= K.
  *   B          device bf16, N x rank per adapter, row n of adapter a at B + a * b_stride + n * ldb; ldb >= rank.
- *   alpha      device fp32[n_adapters].      rank 1..128 (smaller ones: zero rows of A).
+ *   alpha      device fp32[n_adapters], at most 2^24.      rank 1..128 (smaller ones: zero rows of A).
  *   requests   device int32[n_requests + 1], non-decreasing, clamped to [0, M]; rows outside have no adapter.
- *   adapter    device int32[n_requests]; -1 (or any value outside [0, n_adapters)): no adapter.
+ *   adapter    device int32[n_requests], at most 2^24; -1 (or any value outside [0, n_adapters)): no adapter.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, 1, rank).
  * A x is summed and kept in fp32, and enters the second product with all of its bits (as fp32, or as three bf16 parts
- * on the matrix cores).  An infinity or NaN in a request's rows or adapter stays in that request.  Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ * on the matrix cores).  An infinity or NaN in a request's rows or adapter stays in that request.
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, int64_t ldx, const uint32_t* packed,
                                   int64_t ldp, int64_t K, int64_t N, int bits, const float* scales, int64_t groupsize,

@@ -22,6 +22,7 @@ struct StageArgs {
     int32_t* tiles;
     int row_blocks;        // workgroups of the rows: row_blocks x nchunks (0: rows are not laid out)
     int nchunks;
+    int64_t workgroups;    // of the launch, counted along x, then y
     // adapters
     const uint16_t* A;
     int64_t lda, a_stride;
@@ -409,7 +410,8 @@ __global__ __launch_bounds__(kStageThreads, 2) void stage_kernel(MatmulKernelArg
     constexpr int kLayBytes = PARTS * (kChunkK / 8) * (kStageRows + 1) * 16 + (kChunkK / 8) * (kStageRows + 1) * 4;
     constexpr int kShrinkBytes = (kStageThreads / 64) * NR * 4 * 64 * 4;
     __shared__ __attribute__((aligned(16))) char lds[kLayBytes > kShrinkBytes ? kLayBytes : kShrinkBytes];
-    int64_t b = blockIdx.x;
+    int64_t b = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+    if (b >= a.workgroups) return;
     if constexpr (NR > 0) {
         const int64_t per = (int64_t)a.slices * a.k_parts, n = (a.n_requests + 1) * per;
         if (b < n) {
@@ -617,8 +619,12 @@ struct Buffers {
 bool short_requests(int64_t M, int64_t n_requests) { return M < 32 * n_requests; }
 
 template <int PARTS>
-hipError_t launch_stage(const MatmulKernelArgs& k, const StageArgs& a, bool long_rows, unsigned grid, hipStream_t stream) {
-#define GPTQ_STAGE(NR, RS) hipLaunchKernelGGL((stage_kernel<PARTS, NR, RS>), dim3(grid), dim3(kStageThreads), 0, stream, k, a)
+hipError_t launch_stage(const MatmulKernelArgs& k, const StageArgs& a, bool long_rows, hipStream_t stream) {
+    constexpr int64_t kMost = 1 << 22;               // a launch has fewer than 2^32 threads along x
+    const int64_t turns = ceil_div(a.workgroups, kMost);
+    if (turns > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)std::min(a.workgroups, kMost), (unsigned)turns);
+#define GPTQ_STAGE(NR, RS) hipLaunchKernelGGL((stage_kernel<PARTS, NR, RS>), grid, dim3(kStageThreads), 0, stream, k, a)
 #define GPTQ_STAGE_RS(NR)             \
     do {                              \
         if (long_rows) GPTQ_STAGE(NR, 4); \
@@ -665,12 +671,11 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
         StageArgs s = {};
         s.XT = buf.XT; s.sums = buf.sums;
         s.tile = plan.tile; s.cap = plan.cap; s.tiles = buf.tiles;
-        int64_t grid = 0;
         bool long_rows = false;
         if (plan.kernel != kRows) {
             s.row_blocks = (int)ceil_div(a.M, kStageRows);
             s.nchunks = plan.nchunks;
-            grid = (int64_t)s.row_blocks * plan.nchunks + 1;
+            s.workgroups = (int64_t)s.row_blocks * plan.nchunks + 1;
         }
         if (lora) {
             s.A = a.A; s.lda = a.lda; s.a_stride = a.a_stride; s.alpha = a.alpha; s.n_adapters = a.n_adapters;
@@ -683,11 +688,9 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
             s.slices = (int)std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(ceil_div(a.M, rows), std::min<int64_t>(a.M, 4)),
                                                                      1024 / (a.n_requests * s.k_parts)));
             s.windows = (int64_t)rows * s.slices < a.M ? ceil_div(a.M, rows) : 0;
-            grid += ((a.n_requests + 1) * s.slices + s.windows) * s.k_parts;
+            s.workgroups += ((a.n_requests + 1) * s.slices + s.windows) * s.k_parts;
         }
-        if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
-        hipError_t e = a.f32 ? launch_stage<3>(k, s, long_rows, (unsigned)grid, stream)
-                             : launch_stage<1>(k, s, long_rows, (unsigned)grid, stream);
+        hipError_t e = a.f32 ? launch_stage<3>(k, s, long_rows, stream) : launch_stage<1>(k, s, long_rows, stream);
         if (e != hipSuccess) return e;
         if (k.Z) {
             const dim3 zgrid((unsigned)ceil_div(a.M, 64), (unsigned)ceil_div(a.N, 256));

@@ -18,19 +18,24 @@ bool dtype_ok(gptq_dtype_t d) { return d == GPTQ_DTYPE_F32 || d == GPTQ_DTYPE_BF
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 27;      // of gptq_route: a launch has fewer than 2^32 threads
 constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxK = (int64_t)1 << 22, kMaxN = (int64_t)1 << 22;
-constexpr int64_t kMaxExperts = 16384, kMaxRequests = (int64_t)1 << 24;
+constexpr int64_t kMaxExperts = 16384, kMaxRequests = (int64_t)1 << 24, kMaxAdapters = (int64_t)1 << 24;
+
+// The launch over tiles of 64 rows x 256 channels has fewer than 2^32 threads.
+bool tiles_ok(int64_t M, int64_t N, int64_t E) {
+    return ceil_div(M, E) <= 64 || (ceil_div(M, 64) + E + 3) * ceil_div(N, 256) < (int64_t)1 << 24;
+}
 
 // The checks that gptq_expert_matmul and gptq_adapter_matmul share.
 bool layer_ok(const void* X, gptq_dtype_t dtype, int64_t x_rows, int64_t ldx, int64_t M, const uint32_t* packed,
               int64_t ldp, int64_t K, int64_t N, int bits, const float* scales, int64_t groupsize, int64_t width,
-              const void* Y, int64_t ldy) {
+              const void* Y, int64_t ldy, int64_t E) {
     if (!dtype_ok(dtype) || !packed || !scales || M < 0 || M > kMaxRows || K < 1 || K > kMaxK) return false;
     if (N < 4 || N > kMaxN || bits < 2 || bits > 6 || ldp < N || ldx < K || ldy < width) return false;
     if (groupsize != 0 && groupsize != 32 && groupsize != 64 && groupsize != 128) return false;
     if (M > 0 && (!X || !Y || X == Y || x_rows < 1)) return false;
     // the kernels address an expert's words by 32-bit byte offsets
     if ((K * bits + 31) / 32 * ldp > ((int64_t)1 << 30)) return false;
-    return ceil_div(M, 64) * ceil_div(N, 128) < (int64_t)1 << 30;
+    return tiles_ok(M, N, E);
 }
 
 }  // namespace
@@ -41,6 +46,7 @@ size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int
                                    int64_t rank) {
     if (!dtype_ok(dtype) || M < 1 || M > kMaxRows || K < 1 || K > kMaxK || N < 1 || N > kMaxN) return 0;
     if (experts < 1 || experts > kMaxExperts || rank < 0 || rank > 128) return 0;
+    if (!tiles_ok(M, N, experts)) return 0;
     return matmul_workspace_bytes(dtype == GPTQ_DTYPE_F32, M, K, N, experts, rank);
 }
 
@@ -67,9 +73,9 @@ gptq_status_t gptq_expert_matmul(const void* X, gptq_dtype_t dtype, int64_t x_ro
     if (flags & ~GPTQ_FLAG_SWIGLU) return GPTQ_ERR_ARG;
     const bool swiglu = (flags & GPTQ_FLAG_SWIGLU) != 0;
     if (swiglu && N % 2 != 0) return GPTQ_ERR_ARG;
-    if (!layer_ok(X, dtype, x_rows, ldx, M, packed, ldp, K, N, bits, scales, groupsize, swiglu ? N / 2 : N, Y, ldy))
-        return GPTQ_ERR_ARG;
     if (!offsets || E < 1 || E > kMaxExperts || (!rows && x_rows < M)) return GPTQ_ERR_ARG;
+    if (!layer_ok(X, dtype, x_rows, ldx, M, packed, ldp, K, N, bits, scales, groupsize, swiglu ? N / 2 : N, Y, ldy, E))
+        return GPTQ_ERR_ARG;
     const int64_t groups = groupsize ? ceil_div(K, groupsize) : 1;
     if (E > 1 && (p_stride < (K * bits + 31) / 32 * ldp || s_stride < groups * N)) return GPTQ_ERR_ARG;
     if (M == 0) return GPTQ_OK;
@@ -91,8 +97,8 @@ gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, 
                                   int64_t b_stride, const float* alpha, int64_t n_adapters, int64_t rank,
                                   const int32_t* requests, const int32_t* adapter, int64_t n_requests, void* Y,
                                   int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!layer_ok(X, dtype, M, ldx, M, packed, ldp, K, N, bits, scales, groupsize, N, Y, ldy)) return GPTQ_ERR_ARG;
-    if (n_adapters < 0 || n_requests < 0 || n_requests > kMaxRequests || n_adapters > ((int64_t)1 << 24))
+    if (!layer_ok(X, dtype, M, ldx, M, packed, ldp, K, N, bits, scales, groupsize, N, Y, ldy, 1)) return GPTQ_ERR_ARG;
+    if (n_adapters < 0 || n_requests < 0 || n_requests > kMaxRequests || n_adapters > kMaxAdapters)
         return GPTQ_ERR_ARG;
     const bool lora = n_adapters > 0 && n_requests > 0;
     if (lora) {

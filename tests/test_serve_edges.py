@@ -376,3 +376,36 @@ def test_a_long_request_beside_single_tokens_is_shared_out():
             best = min(best, a.elapsed_time(b))
         return best
     assert us([1] * 255 + [3841]) < 3 * us([16] * 256)
+
+
+# ------------------------------------------------------------------------------------------------------------- limits
+
+@gpu
+def test_more_requests_than_one_launch_has_threads_for():
+    """2^23 requests and more, nearly all of them empty."""
+    K, N, n = 64, 32, (1 << 23) + 70
+    codes, scales, W, s = layer(K, N, 4, 0, 2)
+    X = rows_of(40, K, BF16, 1)
+    A = torch.ones(2, 3, K, dtype=BF16, device=DEV)
+    B = torch.ones(2, N, 3, dtype=BF16, device=DEV)
+    req = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    req[1 << 22:] = 5
+    req[n - 3:] = 39
+    ad = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    ad[(1 << 22) - 1], ad[n - 4] = 0, 1              # rows 0 .. 4 and 5 .. 38
+    y = g.gptq_adapter_matmul(X.to(DEV), packed_on(codes, 4, DEV)[0], scales[0].to(DEV), 4, A=A, B=B,
+                              alpha=torch.tensor([1.0, -2.0], device=DEV), requests=req, adapter=ad)
+    ref, x = X.double() @ W[0], X.double()
+    ref[:5] += 3 * x[:5].sum(1, keepdim=True)
+    ref[5:39] -= 6 * x[5:39].sum(1, keepdim=True)
+    close(y, ref, slack(X, s[0], 4, BF16, K) + 40 * 2.0 ** -24 * 6 * x.abs().sum(1, keepdim=True), BF16)
+
+
+def test_sizes_past_a_launch_are_refused():
+    """The tile launch's threads: an argument error, not one of the launch."""
+    from test_serve import expert_args
+    assert expert_args(M=1 << 30, xr=8, rows=0x100000, K=64, N=32) == g.GPTQ_ERR_ARG
+    assert g.gptq_matmul_workspace_bytes(BF16, 1 << 30, 64, 32, experts=2) == 0
+    assert expert_args(M=(1 << 30) - 64 * 5, xr=8, rows=0x100000, wsb=0) == g.GPTQ_ERR_ARG
+    assert expert_args(M=(1 << 30) - 64 * 6, xr=8, rows=0x100000, wsb=0) == g.GPTQ_ERR_WORKSPACE
+    assert expert_args(M=128, xr=128, E=1 << 14, N=1 << 22, ldp=1 << 22, ps=1 << 25, ss=1 << 22, ldy=1 << 22, wsb=0) != g.GPTQ_ERR_ARG
