@@ -519,6 +519,14 @@ def _rows_of(t: torch.Tensor, name: str, device=None) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
+def _no_gradient(*tensors):
+    """The serving calls have no backward pass: a gradient that would end here is refused, not dropped."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("the serving calls have no gradient: detach the tensors, or call under torch.no_grad()")
+
+
 def _matrices(t: torch.Tensor, name: str):
     """Address, leading dimension and stride from one to the next of the matrices t[0], t[1], ...  A dimension of size one
     has any stride; one that repeats or overlaps rows (expand) is refused, the library would read past them."""
@@ -580,6 +588,7 @@ def gptq_route(logits: torch.Tensor, topk: int, renorm: bool = False, workspace:
     if stream is not None:
         with _current(stream, logits):
             return gptq_route(logits, topk, renorm, workspace)
+    _no_gradient(logits)
     ld = _rows_of(logits, "logits")
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
@@ -615,6 +624,7 @@ def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
     if stream is not None:
         with _current(stream, X):
             return gptq_expert_matmul(X, packed, scales, offsets, bits, rows, groupsize, swiglu, out, workspace)
+    _no_gradient(X, scales, out)
     dt = _DTYPES.get(X.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {X.dtype}")
@@ -661,6 +671,7 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     if stream is not None:
         with _current(stream, X):
             return gptq_adapter_matmul(X, packed, scales, bits, groupsize, A, B, alpha, requests, adapter, out, workspace)
+    _no_gradient(X, scales, A, B, alpha, out)
     dt = _DTYPES.get(X.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {X.dtype}")
@@ -712,6 +723,7 @@ def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor
     if stream is not None:
         with _current(stream, Y):
             return gptq_combine(Y, positions, weights, out)
+    _no_gradient(Y, weights, out)
     dt = _DTYPES.get(Y.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {Y.dtype}")

@@ -409,3 +409,27 @@ def test_sizes_past_a_launch_are_refused():
     assert expert_args(M=(1 << 30) - 64 * 5, xr=8, rows=0x100000, wsb=0) == g.GPTQ_ERR_ARG
     assert expert_args(M=(1 << 30) - 64 * 6, xr=8, rows=0x100000, wsb=0) == g.GPTQ_ERR_WORKSPACE
     assert expert_args(M=128, xr=128, E=1 << 14, N=1 << 22, ldp=1 << 22, ps=1 << 25, ss=1 << 22, ldy=1 << 22, wsb=0) != g.GPTQ_ERR_ARG
+
+
+@gpu
+def test_gradients_are_refused():
+    X = torch.zeros(4, 64, dtype=BF16, device=DEV)
+    p, s, off = torch.zeros(8, 32, dtype=torch.int32, device=DEV), torch.ones(32, device=DEV), ints([0, 4])
+    A, B = torch.zeros(1, 8, 64, dtype=BF16, device=DEV), torch.zeros(1, 32, 8, dtype=BF16, device=DEV)
+    x, w, pos = torch.randn(4, 8, device=DEV), torch.ones(4, 1, device=DEV), ints([[0], [1], [2], [3]])
+    al, ad = torch.ones(1, device=DEV), ints([0])
+    for t, call in ((X, lambda t: g.gptq_adapter_matmul(t, p, s, 4)), (s, lambda t: g.gptq_adapter_matmul(X, p, t, 4)),
+                    (A, lambda t: g.gptq_adapter_matmul(X, p, s, 4, A=t, B=B, alpha=al, requests=off, adapter=ad)),
+                    (B, lambda t: g.gptq_adapter_matmul(X, p, s, 4, A=A, B=t, alpha=al, requests=off, adapter=ad)),
+                    (al, lambda t: g.gptq_adapter_matmul(X, p, s, 4, A=A, B=B, alpha=t, requests=off, adapter=ad)),
+                    (X, lambda t: g.gptq_expert_matmul(t, p[None], s[None], off, 4)), (x, lambda t: g.gptq_route(t, 1)),
+                    (X, lambda t: g.gptq_combine(t, pos, w)), (w, lambda t: g.gptq_combine(X, pos, t))):
+        call(t)
+        leaf = t.clone().requires_grad_()
+        with pytest.raises(ValueError):
+            call(leaf)
+        with pytest.raises(ValueError):
+            call(leaf * 1)
+        call(leaf.detach())
+        with torch.no_grad():
+            call(leaf)
