@@ -651,6 +651,7 @@ hipError_t packed_matmul(const MatmulArgs& a, void* workspace, hipStream_t strea
     const bool lora = a.n_requests > 0 && a.n_adapters > 0;
     const Plan plan = make_plan(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0, lora ? a.n_requests : 1, a.bits, a.groupsize);
     const Buffers buf(plan, a.M, a.N, workspace);
+    if (buf.bytes > matmul_workspace_bytes(a.f32, a.M, a.K, a.N, a.E, lora ? a.rank : 0)) return hipErrorInvalidValue;
     MatmulKernelArgs k;
     k.X = a.X; k.ldx = a.ldx; k.x_rows = a.x_rows; k.rows = a.rows; k.M = a.M;
     k.offsets = a.offsets; k.E = a.E;

@@ -433,3 +433,140 @@ def test_gradients_are_refused():
         call(leaf.detach())
         with torch.no_grad():
             call(leaf)
+
+
+# ------------------------------------------------------------------------- adapters: buffers, repeats, graphs, bad lists
+
+# few rows; tens of rows; prompts (one product per run of rows); short requests (by distinct adapter, through Z)
+PATHS = [([1, 2, 0, 3], 70), ([20, 0, 9, 13], 70), ([900, 5, 600], 4100), ([1] * 700 + [2] * 200, 4100)]
+
+
+def ids_of(lengths):
+    return [(3 * i + 1) % 6 - 1 for i in range(len(lengths))]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths,N", PATHS)
+@pytest.mark.parametrize("rank", [3, 70])
+def test_adapter_matmul_on_a_workspace_of_the_stated_size(lengths, N, rank, dtype):
+    """Filled with NaN, nothing past its end is touched, and two calls give the same bits."""
+    call, ref, bound = mixed(lengths, ids_of(lengths), 333, N, rank, dtype)
+    need = g.gptq_matmul_workspace_bytes(dtype, sum(lengths), 333, N, rank=rank)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    y = g.gptq_adapter_matmul(**call, workspace=ws[:need])
+    close(y, ref, bound, dtype)
+    assert bool((ws[need:] == 0xFF).all())
+    ws[:need] = 0x7F
+    assert torch.equal(y, g.gptq_adapter_matmul(**call, workspace=ws[:need]))
+    assert torch.equal(y, g.gptq_adapter_matmul(**call))
+
+
+@gpu
+@pytest.mark.parametrize("lengths,N", PATHS)
+def test_adapter_matmul_in_a_graph(lengths, N):
+    call, ref, bound = mixed(lengths, ids_of(lengths), 333, N, 20, BF16)
+    ws = torch.empty(g.gptq_matmul_workspace_bytes(BF16, sum(lengths), 333, N, rank=20), dtype=torch.uint8, device=DEV)
+    want = g.gptq_adapter_matmul(**call)
+    close(want, ref, bound, BF16)
+    out, graph = torch.empty_like(want), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.gptq_adapter_matmul(**call, out=out, workspace=ws)
+    first = call["X"].clone()
+    for i in range(3):
+        call["X"].copy_(first if i == 1 else first * (i + 2))
+        call["adapter"].copy_(call["adapter"].flip(0))           # other adapters, other lengths, the same graph
+        call["requests"].copy_(call["requests"][-1] - call["requests"].flip(0))
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, g.gptq_adapter_matmul(**call))
+
+
+@gpu
+@pytest.mark.parametrize("lengths,N", PATHS)
+@pytest.mark.parametrize("how", ["outside", "swapped", "wild"])
+def test_adapter_matmul_keeps_to_its_rows(lengths, N, how):
+    """Requests outside [0, M] or out of order, adapters that do not exist: nothing outside the buffers, lists in order right."""
+    n, M = len(lengths), sum(lengths)
+    call, ref, bound = mixed(lengths, ids_of(lengths), 96, N, 20, BF16)
+    plain = g.gptq_adapter_matmul(**{k: call[k] for k in ("X", "packed", "scales", "bits", "groupsize")})
+    full = g.gptq_adapter_matmul(**call)
+    req = call["requests"].clone()
+    gen = torch.Generator().manual_seed(n)
+    if how == "outside":
+        req[0], req[n] = -7, M + 1000
+    elif how == "swapped":
+        req = req.flip(0)
+    else:
+        req = torch.randint(-2 ** 31, 2 ** 31 - 1, (n + 1,), generator=gen).to(torch.int32).to(DEV)
+        call["adapter"] = torch.randint(-2 ** 31, 2 ** 31 - 1, (n,), generator=gen).to(torch.int32).to(DEV)
+    call["requests"] = req.contiguous()
+    need = g.gptq_matmul_workspace_bytes(BF16, M, 96, N, rank=20)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    guard = torch.full((M + 2, N), 5.0, dtype=BF16, device=DEV)
+    g.gptq_adapter_matmul(**call, out=guard[1:M + 1], workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert bool((guard[0] == 5).all()) and bool((guard[M + 1] == 5).all()) and bool((ws[need:] == 0xFF).all())
+    if how == "outside":
+        assert torch.equal(guard[1:M + 1], full)
+    if how == "wild":                                # no adapter exists: the plain product
+        assert torch.equal(guard[1:M + 1], plain)
+
+
+# ---------------------------------------------------------------------------------- skewed experts, far-away addresses
+
+# By the average these are few rows (16), tens of rows (64) and many; one expert has nearly all of them.
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("E,M,N", [(128, 2048, 70), (128, 2049, 70), (64, 4096, 130), (8, 1200, 4100)])
+def test_expert_matmul_skewed(E, M, N, dtype):
+    K, bits = 96, 4
+    counts = [0] * E
+    counts[E // 3], counts[E // 2], counts[E - 1] = M - M // 8 - 3, M // 8, 3
+    codes, scales, W, s = layer(K, N, bits, 32, 5, E=E)
+    X, off = rows_of(M, K, dtype, 1), np.concatenate([[0], np.cumsum(counts)])
+    y = g.gptq_expert_matmul(X.to(DEV), packed_on(codes, bits, DEV), scales.to(DEV), ints(off.tolist()), bits, groupsize=32)
+    ref, bound = torch.zeros(M, N, dtype=torch.float64), torch.zeros(M, N, dtype=torch.float64)
+    for e in np.nonzero(counts)[0]:
+        r = slice(off[e], off[e + 1])
+        ref[r], bound[r] = X[r].double() @ W[e], slack(X[r], s[e], bits, dtype, K)
+    close(y, ref, bound, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("bits,K,groupsize", [(4, 256, 64), (6, 32, 0), (3, 70, 32), (5, 160, 128)])
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_words_at_the_end_of_the_largest_layer(M, bits, K, groupsize):
+    """2^30 words of one layer, 4 GiB: the channels are a view whose rows are as far apart as that allows."""
+    N = 4100 if M > 1000 else 70
+    nw = (K * bits + 31) // 32
+    ldp = (1 << 30) // nw
+    whole = torch.empty(nw * ldp, dtype=torch.int32, device=DEV)
+    packed = whole.view(nw, ldp)[:, ldp - N:]
+    codes, scales, W, s = layer(K, N, bits, groupsize, M)
+    packed.copy_(packed_on(codes, bits, DEV)[0])
+    X = rows_of(M, K, BF16, 1)
+    y = g.gptq_adapter_matmul(X.to(DEV), packed, scales[0].to(DEV), bits, groupsize=groupsize)
+    close(y, X.double() @ W[0], slack(X, s[0], bits, BF16, K), BF16)
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 40, 1500])
+def test_experts_past_four_gigabytes(M):
+    """The words, rows and results of the last experts lie beyond 32-bit offsets."""
+    E, K, N = 9, 64, 4100 if M > 1000 else 70
+    codes, scales, W, s = layer(K, N, 4, 0, M, E=E)
+    stride = 1 << 28                                 # words: 1 GiB an expert
+    packed = torch.empty((E - 1) * stride + 8 * N, dtype=torch.int32, device=DEV).as_strided((E, 8, N), (stride, N, 1))
+    packed.copy_(packed_on(codes, 4, DEV))
+    ld = -(-(1 << 32) // M) + 64
+    X, wide = rows_of(M, K, BF16, 1), torch.empty(M * ld, dtype=BF16, device=DEV).view(M, ld)
+    wide[:, 7:7 + K] = X.to(DEV)
+    out = torch.empty(M * ld, dtype=BF16, device=DEV).view(M, ld)[:, 1:1 + N] if ld > N else None
+    off = [0] * 7 + [M // 3, M // 2, M]              # experts 6, 7 and 8
+    y = g.gptq_expert_matmul(wide[:, 7:7 + K], packed, scales.to(DEV), ints(off), 4, out=out)
+    ref = torch.cat([X[off[e]:off[e + 1]].double() @ W[e] for e in (6, 7, 8)])
+    bound = torch.cat([slack(X[off[e]:off[e + 1]], s[e], 4, BF16, K) for e in (6, 7, 8)])
+    close(y, ref, bound, BF16)
