@@ -317,9 +317,11 @@ void matmul_rows_kernel(MatmulKernelArgs p) {
     }
 }
 
-// Channels per workgroup: 64, or 32 where 64 leave CUs without one.  Waves that share K: 16 in the narrow kernel with one
-// word per step and lane, whose registers allow it (latency counts); 8 in the others; 4 where there are many workgroups,
-// several of which then share a CU and cover each other's start and end (experts' decode step 82 us with 4, 110 with 8).
+// Channels per workgroup: 32 while every such workgroup has a CU of its own, else 64 (one token x 4096, 4 bits, 8192
+// channels: 6.6 us with 32, 8.6 with 64; 10240 channels: 10.8 and 8.8; 16 rows: 8.7 and 9.4, 15.1 and 9.6; fp32 rows and 3
+// bits alike).  Waves that share K: 16 in the narrow kernel with one word per step and lane, whose registers allow it
+// (latency counts); 8 in the others; 4 where there are many workgroups, several of which then share a CU and cover each
+// other's start and end (experts' decode step 82 us with 4, 110 with 8).
 template <int BITS, int PARTS, int NT, int FORM, int W>
 hipError_t launch_rows_form(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
     const int width = swiglu ? k.N / 2 : k.N;
@@ -339,7 +341,7 @@ hipError_t launch_rows_form(const MatmulKernelArgs& k, bool swiglu, hipStream_t 
 template <int BITS, int PARTS, int WIDE, int NARROW>
 hipError_t launch_rows_w(const MatmulKernelArgs& k, bool swiglu, hipStream_t stream) {
     if (swiglu) return launch_rows_form<BITS, PARTS, 4, kGated, WIDE>(k, swiglu, stream);
-    if (ceil_div(k.N, 64) * k.E >= 224) {
+    if (ceil_div(k.N, 32) * k.E > 256) {
         if (k.H) return launch_rows_form<BITS, PARTS, 4, kAdapters, WIDE>(k, swiglu, stream);
         return launch_rows_form<BITS, PARTS, 4, kPlain, WIDE>(k, swiglu, stream);
     }
