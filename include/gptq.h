@@ -418,7 +418,8 @@ gptq_status_t gptq_route(const void* logits, gptq_dtype_t dtype, int64_t T, int6
                          int32_t* positions, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace of gptq_expert_matmul (rank 0) and of gptq_adapter_matmul (experts 1; rank 0 without adapters) for M >= 1
- * rows; 0 for sizes that those calls refuse. */
+ * rows, whatever the offsets and requests (with a rank it counts M x N fp32 for short requests beside many rows); 0 for
+ * sizes that those calls refuse. */
 size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int64_t N, int64_t experts, int64_t rank);
 
 /*
@@ -437,7 +438,7 @@ size_t gptq_matmul_workspace_bytes(gptq_dtype_t dtype, int64_t M, int64_t K, int
  *   K          1 .. 2^22.   N: 4 .. 2^22 channels (even with GPTQ_FLAG_SWIGLU).   bits 2..6.
  *   scales     device fp32, contiguous N per expert (groups: ceil(K / groupsize) x N), expert e at e * s_stride.
  *   groupsize  0, 32, 64 or 128 consecutive k that share a scale.
- *   Y          device, M x N (N / 2 with GPTQ_FLAG_SWIGLU), dtype, leading dimension ldy; not X.
+ *   Y          device, M x N (N / 2 with GPTQ_FLAG_SWIGLU), dtype, leading dimension ldy; no element of it is one of X.
  *   workspace  device scratch of gptq_matmul_workspace_bytes(dtype, M, K, N, E, 0).
  * Sums are fp32, of x (2^bits + code) for bf16 rows and of x (code - z) for fp32 rows, times the scale every 128 k or
  * scale group.  They are kept times 2^-(bits+8): finite rows overflow only where their result does, and results below

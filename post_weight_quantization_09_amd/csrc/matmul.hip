@@ -90,10 +90,10 @@ __device__ void list_tiles(const MatmulKernelArgs& p, const StageArgs& a) {
     for (int64_t t = base + tid; t < a.cap; t += T) a.tiles[3 * t] = -1;
 }
 
-// Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times
-// -1.5 2^-8, the codes' excess.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces along
-// the rows, turned in LDS.  Bound by HBM: every row is read once and written once (8192 gathered rows x 4096, bf16: 27.5 us,
-// 4.9 TB/s).
+// Rows -> [part][K / 8][Mp] octets in the operand's order of k, with each row's sums over the scale groups times -1.5 2^-8,
+// the codes' excess.  64 rows x 128 k per workgroup: rows are read in 16-byte pieces along k and written in 16-byte pieces
+// along the rows, turned in LDS.  Bound by HBM: every row is read once and written once (8192 gathered rows x 4096, bf16:
+// 27.5 us, 4.9 TB/s).
 template <int PARTS>
 __device__ void lay_out_rows(const MatmulKernelArgs& p, const StageArgs& a, int64_t r0, int chunk, int nchunks, char* lds) {
     constexpr int kOctets = kChunkK / 8, kPitch = kStageRows + 1;
@@ -225,12 +225,12 @@ __device__ void single_row(const MatmulKernelArgs& p, const StageArgs& a, int64_
 // matrix product: there a wave takes a rank and reads its row of A in whole kilobytes (as operands it would be 64 pieces of 16
 // bytes), products and sums in fp32 (one token, 4096 features, rank 16: 4.6 against 7.4 us).  Prompts take 64 rows at a
 // time, since every pass reads A again, and split K over k_parts workgroups; their sums are added where H is used (4096
-// rows x 28672, rank 64, rows laid out beside it: 230 us against 333 with 16 rows and no split).  H stays in fp32.
+// rows x 28672, rank 64, rows laid out beside it: 240 us against 333 with 16 rows and no split).  H stays in fp32.
 //
 // The launch cannot depend on the lengths, which only the device knows.  Every request gets `slices` workgroups, which
 // take one pass each; what is longer is left to `windows` workgroups, one per 16 RS rows of X, which look up the requests
-// that reach into theirs (one request of 3841 rows beside 255 of one, 4096 features, rank 16: 53 us; 494
-// with the request's own workgroups alone).
+// that reach into theirs (one request of 3841 rows beside 255 of one, 4096 features, rank 16: 53 us; 494 with the
+// request's own workgroups alone).
 
 // One pass: the rows r0 .. min(r0 + 16 RS, hi) - 1, for adapter `id`, over this workgroup's part z of K.
 template <int PARTS, int NR, int RS>

@@ -1,4 +1,4 @@
-// Host interface of the products with packed weights (matmul_rows.hpp, matmul_tile.hpp, adapter.hip, matmul.hip).
+// Host interface of the products with packed weights (matmul.hip; kernels in matmul_rows.hpp, matmul_split.hpp, matmul_tile.hpp).
 #pragma once
 
 #include "gptq_common.hpp"

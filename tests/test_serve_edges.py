@@ -142,7 +142,7 @@ def test_adapters_with_dimensions_of_size_one(M):
                               alpha=torch.ones(1, device=DEV), requests=ints([0, M]), adapter=ints([0]))
     inner = X.double() @ a.double()[:, None]
     term = (X.double().abs() @ a.double().abs()[:, None]) * b.double().abs()
-    # A x: at most 64 roundings of 2^-24 on a term's way, 2^-17 where it enters in two bf16 parts
+    # A x: at most 64 roundings of 2^-24 on a term's way; 2^-16 covers them many times over
     close(y, X.double() @ W[0] + inner * b.double(), slack(X, s[0], 4, BF16, K) + 2.0 ** -16 * term, BF16)
 
 
