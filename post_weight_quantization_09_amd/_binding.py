@@ -154,6 +154,8 @@ def _workspace(call, K, N, M, flags, device, workspace):
     need = gptq_workspace_bytes(call, K, N, M, flags)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be contiguous, on the GPU of the other tensors")
     return workspace, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
 
 
@@ -566,8 +568,8 @@ def _handle(device) -> int:
 def _scratch(need: int, device, workspace: Optional[torch.Tensor]):
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError("workspace must be on the GPU of the other tensors")
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be contiguous, on the GPU of the other tensors")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

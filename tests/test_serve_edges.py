@@ -570,3 +570,19 @@ def test_experts_past_four_gigabytes(M):
     ref = torch.cat([X[off[e]:off[e + 1]].double() @ W[e] for e in (6, 7, 8)])
     bound = torch.cat([slack(X[off[e]:off[e + 1]], s[e], 4, BF16, K) for e in (6, 7, 8)])
     close(y, ref, bound, BF16)
+
+
+@gpu
+def test_workspaces_that_are_no_memory_of_their_own_are_refused():
+    """A view that repeats one byte, or skips some, has fewer bytes than its elements say."""
+    K = 128
+    X, p, s = torch.zeros(70, K, dtype=BF16, device=DEV), torch.zeros(K // 8, 32, dtype=torch.int32, device=DEV), torch.ones(32, device=DEV)
+    H, off = torch.eye(K, device=DEV), ints([0, 70])
+    for ws in (torch.empty(1, dtype=torch.uint8, device=DEV).expand(1 << 24), torch.empty(1 << 25, dtype=torch.uint8, device=DEV)[::2],
+               torch.empty(1 << 24, dtype=torch.uint8)):
+        for call in (lambda: g.gptq_adapter_matmul(X, p, s, 4, workspace=ws), lambda: g.gptq_route(X, 2, workspace=ws),
+                     lambda: g.gptq_expert_matmul(X, p[None], s[None], off, 4, workspace=ws),
+                     lambda: g.gptq_prepare(H, 0.01, workspace=ws), lambda: g.gptq_accumulate_hessian(H, X, workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
+    assert torch.equal(H, torch.eye(K, device=DEV))
