@@ -133,17 +133,31 @@ def _stream(device, stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# the current device, without its Python wrapper
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether another GPU than the tensor's is the current one: a launch on the null stream would go there."""
+    return t.is_cuda and t.device.index != _device_now()
+
+
 def _on_its_stream(call):
     """A call given a stream runs with that stream as the current one, so that what it allocates (workspace, outputs)
     comes from that stream's memory and, once released, goes to later work on that stream alone.  Taken from the current
-    stream's, a block could be handed out again there while the kernels still use it."""
-    at = list(inspect.signature(call).parameters).index("stream")
+    stream's, a block could be handed out again there while the kernels still use it.  Likewise a call whose first tensor
+    is on another GPU than the current one runs with that GPU as the current one."""
+    names = list(inspect.signature(call).parameters)
+    at = names.index("stream")
 
     @functools.wraps(call)
     def run(*args, **kw):
         stream = args[at] if len(args) > at else kw.get("stream")
         if stream is None:
-            return call(*args, **kw)
+            first = args[0] if args else kw.get(names[0])
+            if not (isinstance(first, torch.Tensor) and _elsewhere(first)):
+                return call(*args, **kw)
+            stream = torch.cuda.current_stream(first.device)
         with torch.cuda.stream(stream):
             return call(*args, **kw)
 
@@ -182,6 +196,7 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
+@_on_its_stream
 def gptq_device_status(workspace: torch.Tensor, stream=None, check: bool = False) -> int:
     """Synchronises the stream and returns the status latched in `workspace` by the latest prepare / quantize call
     that used it (GPTQ_OK, GPTQ_ERR_NONFINITE or GPTQ_ERR_NOT_PD); check=True raises GptqError instead of
@@ -495,8 +510,8 @@ def gptq_act_order(H: torch.Tensor, A: Optional[torch.Tensor] = None, perm: Opti
 
 # --- serving the packed layers -------------------------------------------------------------------------------------
 # These calls are short (a few microseconds on the GPU for single tokens), so their marshalling is kept to plain
-# integers: addresses and the stream handle go to ctypes as they are.  Given a stream, a call runs again with that stream
-# as the current one (as _on_its_stream does, without a wrapper around the calls that are given none).
+# integers: addresses and the stream handle go to ctypes as they are.  Given a stream, or tensors of another GPU than the
+# current one, a call runs again with that stream as the current one (as _on_its_stream does, without its wrapper).
 
 _DTYPES = {torch.float32: GPTQ_DTYPE_F32, torch.bfloat16: GPTQ_DTYPE_BF16}
 
@@ -553,7 +568,9 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _current(stream, t: torch.Tensor):
-    """The context in which `stream` is the current one."""
+    """The context in which `stream`, or the current stream of the tensor's GPU, is the current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
     if stream.device != t.device:
         raise ValueError(f"stream must be one of {t.device}")
     return torch.cuda.stream(stream)
@@ -587,7 +604,7 @@ def gptq_route(logits: torch.Tensor, topk: int, renorm: bool = False, workspace:
     Returns dict(weights fp32[T, topk], experts int32[T, topk], offsets int32[E + 1], rows int32[T * topk], positions
     int32[T, topk]).  Stream-ordered: a NaN or +infinity logit is latched in `workspace` (gptq_device_status).
     """
-    if stream is not None:
+    if stream is not None or _elsewhere(logits):
         with _current(stream, logits):
             return gptq_route(logits, topk, renorm, workspace)
     _no_gradient(logits)
@@ -623,7 +640,7 @@ def gptq_expert_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
     E x groups x N with groupsize.  rows: int32[M], None for M = len(X) rows as they are.  swiglu: out is M x N / 2,
     silu(first half) * second half.
     """
-    if stream is not None:
+    if stream is not None or _elsewhere(X):
         with _current(stream, X):
             return gptq_expert_matmul(X, packed, scales, offsets, bits, rows, groupsize, swiglu, out, workspace)
     _no_gradient(X, scales, out)
@@ -670,7 +687,7 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     adapters x rank x K, B: bf16 adapters x N x rank, alpha: fp32[adapters].  requests: int32[R + 1] row offsets,
     adapter: int32[R] (-1: none).  Without A the plain product.
     """
-    if stream is not None:
+    if stream is not None or _elsewhere(X):
         with _current(stream, X):
             return gptq_adapter_matmul(X, packed, scales, bits, groupsize, A, B, alpha, requests, adapter, out, workspace)
     _no_gradient(X, scales, A, B, alpha, out)
@@ -722,7 +739,7 @@ def gptq_adapter_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
 def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] Y[positions[t, j]] in fp32; positions outside Y's rows are left out."""
-    if stream is not None:
+    if stream is not None or _elsewhere(Y):
         with _current(stream, Y):
             return gptq_combine(Y, positions, weights, out)
     _no_gradient(Y, weights, out)
