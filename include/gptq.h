@@ -9,7 +9,8 @@
  *   3. gptq_asym_correction     P1 = [(A U^T) masked strictly upper] U               ([R] item 3)
  *   4. gptq_quantize_layer      shared-order column loop with lazy block updates     ([T] sections 3-5)
  *      gptq_quantize_layer_groups  the same for output-channel groups with a Hessian each ([G])
- * and computes with the packed layers: gptq_route, gptq_expert_matmul, gptq_adapter_matmul, gptq_combine.
+ * and computes with the packed layers: gptq_route, gptq_expert_matmul, gptq_adapter_matmul, gptq_combine; and, between the
+ * projections of a served layer, gptq_rotary, gptq_cache_write, gptq_cache_read, gptq_cache_attention.
  *
  * Sources, cited by page title and section:
  *   [T] GPTQ tutorial page "GPTQ：量化一个权重之后怎样补偿输出误差" (charlestar.github.io, 2026-10-15); its
@@ -485,6 +486,114 @@ gptq_status_t gptq_adapter_matmul(const void* X, gptq_dtype_t dtype, int64_t M, 
  */
 gptq_status_t gptq_combine(const void* Y, gptq_dtype_t dtype, int64_t M, int64_t ldy, const int32_t* positions,
                            const float* weights, int64_t T, int topk, int64_t N, void* out, int64_t ldo, void* stream);
+
+/*
+ * Between the packed projections of a served layer: rotary positions, the cache of keys and values, and the attention
+ * of new tokens over it.  As the calls above these are asynchronous, allocate nothing, may be captured into a HIP graph and
+ * give the same bits for the same inputs; slots, tables, lengths and positions live on the device, and an entry outside its
+ * range selects nothing, as stated at each.  Rows are given by two strides in elements (of a token or request, of a head;
+ * any >= 0 for what is read); rows that are written must not share elements.  At most 1024 heads.
+ */
+
+/* Scalings of gptq_rotary_frequencies. */
+#define GPTQ_ROTARY_PLAIN  0   /* f_i = base^(-2 i / rot) */
+#define GPTQ_ROTARY_LINEAR 1   /* f_i / factor: positions interpolated */
+#define GPTQ_ROTARY_BASE   2   /* base * factor^(rot / (rot - 2)) in base's place */
+#define GPTQ_ROTARY_RAMP   3   /* pairs of at least `high` turns over `original` positions as they are, of at most `low` f_i / factor,
+                                  a ramp over the pairs between; magnitude 0.1 ln(factor) + 1 */
+#define GPTQ_ROTARY_BANDS  4   /* the same by frequency: share (original f_i / 2 pi - low) / (high - low), in [0, 1], as it is */
+
+#define GPTQ_FLAG_INTERLEAVED 1u   /* gptq_rotary: pairs (2 i, 2 i + 1) instead of (i, i + rot / 2) */
+
+/*
+ * gptq_rotary_frequencies - the frequencies (radians per position) of the rot / 2 pairs, for plain or scaled contexts; a
+ * host-side query in 64 bits, whose result the caller copies to the device once.
+ *   rot        even, 2..1024.   base > 1.   factor >= 1 (except PLAIN).   original >= 1, 0 < low < high (RAMP: usually 1 and
+ *              32; BANDS: 1 and 4; otherwise unused).
+ *   freqs      host double[rot / 2].   magnitude: host, may be NULL; gptq_rotary's factor (1 except for RAMP).
+ * Errors: GPTQ_ERR_ARG.
+ */
+gptq_status_t gptq_rotary_frequencies(int64_t rot, double base, int scaling, double factor, double original, double low,
+                                      double high, double* freqs, float* magnitude);
+
+/*
+ * gptq_rotary - the first rot elements of every row turned by its token's position, the others copied:
+ *   (a, b) -> factor (a cos - b sin, b cos + a sin) of the angle positions[t] * freqs[i],  i < rot / 2.
+ * Angles are reduced in 64 bits; products and sums are fp32, with one rounding to bf16.
+ *   X          device, T x H x D, dtype.   T 0..2^22, D 1..1024, rot even, 2..D.
+ *   positions  device int32[T], any value.   freqs: device double[rot / 2], finite, of size at most 2^20.
+ *   flags      GPTQ_FLAG_INTERLEAVED or 0.
+ *   Y          device, T x H x D, dtype; X itself with its strides (in place), or no element of it.
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_rotary(const void* X, gptq_dtype_t dtype, int64_t T, int64_t H, int64_t D, int64_t x_ts, int64_t x_hs,
+                          const int32_t* positions, const double* freqs, int64_t rot, float factor, unsigned flags,
+                          void* Y, int64_t y_ts, int64_t y_hs, void* stream);
+
+/*
+ * The cache: pages of page_size tokens, each with one block of bytes per head, at pages + page * page_stride + head *
+ * head_stride; slot s is place s % page_size of page s / page_size.  With Dp the smallest of 64, 96, 128, 192, 256 that is
+ * at least D, and b bits (16: bf16 values; 8 and 4: codes in two's complement with a scale s per token, value s c):
+ *   keys         page_size rows of Dp b / 8 bytes; with 4 bits a byte holds dimensions 2 i (low half) and 2 i + 1;
+ *   values       for every eight tokens Dp x 8 entries, those of a dimension side by side: the operand order of the
+ *                attention's matrix products; with 4 bits Dp / 2 x 8 bytes of dimensions 2 i and 2 i + 1 of a token;
+ *   key scales   fp32[page_size] (8 and 4 bits);   value scales   fp32[page_size].
+ * Dimensions from D on are zeros.  The grid is that of gptq_quantize_layer (symmetric, z = 2^(b-1), c here is code - z):
+ * s = max(absmax / (2^(b-1) - 1/2), 2^-126) rounded to fp32, c = x / s rounded to nearest, ties to even, exactly, clipped to
+ * [-2^(b-1), 2^(b-1) - 1].  A row with a NaN or infinity gets s = NaN: it reads back as NaN.  16 bits: x rounded to nearest.
+ *   bits 4, 8 or 16.   D a multiple of 8, 8..256.   page_size a multiple of 16, 16..65536.   n_pages >= 1,
+ *   n_pages * page_size < 2^31.   pages 16-byte aligned, strides multiples of 16 bytes; blocks must not overlap.
+ */
+
+/* Bytes of one head's block of a page; 0 for sizes that the cache refuses. */
+size_t gptq_cache_block_bytes(int64_t page_size, int64_t D, int bits);
+
+/*
+ * gptq_cache_write - keys and values of T tokens (T x H x D each, dtype) quantised into their slots.
+ *   slots   device int32[T]; a slot outside [0, n_pages * page_size) is not written (padding).  The others differ from one
+ *           another: where two tokens name one slot, what it holds afterwards is unspecified.   T 0..2^22.
+ * Nothing but those slots is written.  Errors: GPTQ_ERR_ARG, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_cache_write(const void* K, const void* V, gptq_dtype_t dtype, int64_t T, int64_t H, int64_t D,
+                               int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, const int32_t* slots, int bits,
+                               void* pages, int64_t n_pages, int64_t page_stride, int64_t head_stride,
+                               int64_t page_size, void* stream);
+
+/*
+ * gptq_cache_read - the values that T slots hold, as T x H x D rows of dtype (s c in fp32, then rounded); zeros for a slot
+ * outside [0, n_pages * page_size).  K and V: no element of one is one of the other.   Errors: GPTQ_ERR_ARG, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_cache_read(const void* pages, int64_t n_pages, int64_t page_stride, int64_t head_stride,
+                              int64_t page_size, int bits, const int32_t* slots, int64_t T, int64_t H, int64_t D, void* K,
+                              void* V, gptq_dtype_t dtype, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                              void* stream);
+
+/* Workspace of gptq_cache_attention, whatever the lengths; 0 for sizes that it refuses. */
+size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D);
+
+/*
+ * gptq_cache_attention - attention of one new token of each of R requests over its cached tokens (its own among them):
+ *   out[r][i] = sum_t p_t v_t,  p = softmax over t of scale q[r][i] . k_t,  k, v of head i / (Hq / H),
+ * over the tokens t in [max(0, n - window), n) (window 0: [0, n)), n = lengths[r].
+ *   Q          device, R x Hq x D, dtype.   R 0..65536.   Hq a multiple of H, at most 1024.   scale: finite.
+ *   table      device int32, the page of tokens [j page_size, (j + 1) page_size) of request r at table[r * ld_table + j],
+ *              j < max_pages; tokens of a page outside [0, n_pages) are left out.   max_pages * page_size < 2^31.
+ *   lengths    device int32[R], clamped to [0, max_pages * page_size].
+ *   out        device, R x Hq x D, dtype; not Q.   lse: NULL, or device fp32[R * Hq]: ln sum_t exp(scale q . k_t).
+ *   workspace  device scratch of gptq_attention_workspace_bytes(R, Hq, H, D).
+ * A request without a token to attend to gets zeros, and lse -infinity; so does one whose scores are all -infinity.  Slots that
+ * no length reaches may hold anything.  A NaN or infinity in q, or in a key or value that is attended to, gives values that are
+ * not finite in the rows that it enters and touches no others.  Scores, softmax and sums are fp32, over the exact codes;
+ * scales multiply scores and probabilities.  For bf16 rows a probability (times its value's scale) enters the second product
+ * as bf16; for fp32 rows q and the probabilities enter as three bf16 parts each.
+ * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
+ */
+gptq_status_t gptq_cache_attention(const void* Q, gptq_dtype_t dtype, int64_t R, int64_t Hq, int64_t H, int64_t D,
+                                   int64_t q_rs, int64_t q_hs, const void* pages, int64_t n_pages, int64_t page_stride,
+                                   int64_t head_stride, int64_t page_size, int bits, const int32_t* table,
+                                   int64_t ld_table, int64_t max_pages, const int32_t* lengths, float scale,
+                                   int64_t window, void* out, int64_t o_rs, int64_t o_hs, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /*
  * gptq_device_status - the error latched on the device by the latest gptq_prepare, gptq_prepare_groups,

@@ -28,8 +28,11 @@ GPTQ_FLAG_STATIC_GROUPS = 8
 GPTQ_FLAG_MSE = 16
 GPTQ_FLAG_RENORM = 1
 GPTQ_FLAG_SWIGLU = 1
+GPTQ_FLAG_INTERLEAVED = 1
+GPTQ_ROTARY_PLAIN, GPTQ_ROTARY_LINEAR, GPTQ_ROTARY_BASE, GPTQ_ROTARY_RAMP, GPTQ_ROTARY_BANDS = range(5)
 
-_i64, _f32, _u32, _ptr, _size = ctypes.c_int64, ctypes.c_float, ctypes.c_uint, ctypes.c_void_p, ctypes.c_size_t
+_i64, _f32, _f64, _u32, _ptr, _size = (ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_uint, ctypes.c_void_p,
+                                       ctypes.c_size_t)
 
 _SIGNATURES = {
     "gptq_version": (ctypes.c_char_p, []),
@@ -69,6 +72,18 @@ _SIGNATURES = {
                                            _ptr, _i64, _ptr, _size, _ptr]),
     "gptq_combine": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _ptr, _ptr, _i64, ctypes.c_int, _i64, _ptr, _i64,
                                     _ptr]),
+    "gptq_rotary_frequencies": (ctypes.c_int, [_i64, _f64, ctypes.c_int, _f64, _f64, _f64, _f64, _ptr, _ptr]),
+    "gptq_rotary": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _ptr, _ptr, _i64, _f32, _u32, _ptr,
+                                   _i64, _i64, _ptr]),
+    "gptq_cache_block_bytes": (_size, [_i64, _i64, ctypes.c_int]),
+    "gptq_cache_write": (ctypes.c_int, [_ptr, _ptr, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _ptr,
+                                        ctypes.c_int, _ptr, _i64, _i64, _i64, _i64, _ptr]),
+    "gptq_cache_read": (ctypes.c_int, [_ptr, _i64, _i64, _i64, _i64, ctypes.c_int, _ptr, _i64, _i64, _i64, _ptr, _ptr,
+                                       ctypes.c_int, _i64, _i64, _i64, _i64, _ptr]),
+    "gptq_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64]),
+    "gptq_cache_attention": (ctypes.c_int, [_ptr, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, _i64, _ptr, _i64, _i64, _i64,
+                                            _i64, ctypes.c_int, _ptr, _i64, _i64, _ptr, _f32, _i64, _ptr, _i64, _i64,
+                                            _ptr, _ptr, _size, _ptr]),
     "gptq_timer_enable": (ctypes.c_int, [ctypes.c_int]),
     "gptq_timer_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)]),
 }
@@ -756,4 +771,187 @@ def gptq_combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor
     out, ldo = _output(out, Y, T, N)
     _check(load().gptq_combine(Y.data_ptr(), dt, M, ldy, pp, wp, T, topk, N, out.data_ptr(), ldo,
                                _handle(dev)), "gptq_combine")
+    return out
+
+
+# --- between the packed projections of a served layer: rotary positions, the cache, the attention over it -----------
+
+_ROTARY_SCALINGS = {"plain": GPTQ_ROTARY_PLAIN, "linear": GPTQ_ROTARY_LINEAR, "base": GPTQ_ROTARY_BASE,
+                    "ramp": GPTQ_ROTARY_RAMP, "bands": GPTQ_ROTARY_BANDS}
+# a stored row's elements, by head size
+_STORED = {D: next(n for n in (64, 96, 128, 192, 256) if n >= D) for D in range(8, 257, 8)}
+
+
+def _heads(t: torch.Tensor, name: str, device) -> tuple:
+    """Strides from token to token and head to head of a T x H x D tensor with unit element stride, on the GPU."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on the GPU of the other tensors")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be tokens x heads x elements with unit element stride")
+    return t.stride(0), t.stride(1)
+
+
+def _row_type(t: torch.Tensor) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return dt
+
+
+def _pages(pages: torch.Tensor, H: int, D: int, bits: int, device) -> tuple:
+    """Page count, strides and page size of a uint8 pages x heads x block tensor."""
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.device != device or not pages.is_cuda:
+        raise ValueError("pages must be uint8 pages x heads x bytes on the GPU of the other tensors")
+    n, heads, block = pages.shape
+    if heads != H or pages.stride(2) != 1:
+        raise ValueError(f"pages must hold {H} heads, each a contiguous block")
+    if bits not in (4, 8, 16) or D not in _STORED:
+        raise ValueError("bits must be 4, 8 or 16, and the head size a multiple of 8 up to 256")
+    slot = 2 * (_STORED[D] * bits // 8) + (8 if bits < 16 else 0)
+    if block < 1 or block % slot != 0:
+        raise ValueError(f"blocks of {block} bytes hold no whole number of slots of {slot} (gptq_cache_block_bytes)")
+    return n, pages.stride(0), pages.stride(1), block // slot
+
+
+def gptq_rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                            original: float = 8192.0, low: float = 1.0, high: Optional[float] = None, device=None):
+    """(freqs float64[rot / 2], factor): radians per position of every pair, and gptq_rotary's factor on cos and sin.
+
+    scaling: "plain", "linear", "base", "ramp" (high 32 unless given) or "bands" (high 4); see include/gptq.h.
+    """
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)}")
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
+    freqs = torch.empty(max(int(rot) // 2, 0), dtype=torch.float64)
+    magnitude = _f32(1.0)
+    _check(load().gptq_rotary_frequencies(int(rot), float(base), _ROTARY_SCALINGS[scaling], float(factor), float(original),
+                                          float(low), float(high), freqs.data_ptr(), ctypes.addressof(magnitude)),
+           "gptq_rotary_frequencies")
+    return (freqs if device is None else freqs.to(device)), float(magnitude.value)
+
+
+def gptq_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
+                factor: float = 1.0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The first 2 len(freqs) elements of every row of x (T x H x D) turned by positions (int32[T]), the others copied.
+
+    Pairs (i, i + rot / 2), or neighbours with interleaved.  out=x turns in place.
+    """
+    if stream is not None or _elsewhere(x):
+        with _current(stream, x):
+            return gptq_rotary(x, positions, freqs, interleaved, factor, out)
+    _no_gradient(x, freqs, out)
+    dt, dev = _row_type(x), x.device
+    x_ts, x_hs = _heads(x, "x", dev)
+    T, H, D = x.shape
+    pp = _device_tensor(positions, "positions", torch.int32, dev)
+    fp = _device_tensor(freqs, "freqs", torch.float64, dev)
+    if positions.numel() != T or freqs.dim() != 1:
+        raise ValueError("positions must hold an entry per token, freqs be a vector")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must match x")
+    y_ts, y_hs = _heads(out, "out", dev)
+    _check(load().gptq_rotary(x.data_ptr(), dt, T, H, D, x_ts, x_hs, pp, fp, 2 * freqs.numel(), factor,
+                              GPTQ_FLAG_INTERLEAVED if interleaved else 0, out.data_ptr(), y_ts, y_hs, _handle(dev)),
+           "gptq_rotary")
+    return out
+
+
+def gptq_cache_block_bytes(page_size: int, D: int, bits: int) -> int:
+    """Bytes of one head's block of a page; 0 for sizes that the cache refuses."""
+    return int(load().gptq_cache_block_bytes(int(page_size), int(D), int(bits)))
+
+
+def gptq_cache_write(k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor, slots: torch.Tensor, bits: int,
+                     stream=None) -> None:
+    """Keys and values (T x H x D) quantised into slots (int32[T]; outside the pages: not written) of `pages`.
+
+    pages: uint8 pages x H x gptq_cache_block_bytes(page_size, D, bits).
+    """
+    if stream is not None or _elsewhere(k):
+        with _current(stream, k):
+            return gptq_cache_write(k, v, pages, slots, bits)
+    _no_gradient(k, v)
+    dt, dev = _row_type(k), k.device
+    k_ts, k_hs = _heads(k, "k", dev)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("v must match k")
+    v_ts, v_hs = _heads(v, "v", dev)
+    T, H, D = k.shape
+    n, ps, hs, size = _pages(pages, H, D, bits, dev)
+    sp = _device_tensor(slots, "slots", torch.int32, dev)
+    if slots.numel() != T:
+        raise ValueError("slots must hold an entry per token")
+    _check(load().gptq_cache_write(k.data_ptr(), v.data_ptr(), dt, T, H, D, k_ts, k_hs, v_ts, v_hs, sp, bits,
+                                   pages.data_ptr(), n, ps, hs, size, _handle(dev)), "gptq_cache_write")
+
+
+def gptq_cache_read(pages: torch.Tensor, slots: torch.Tensor, D: int, bits: int, dtype: torch.dtype = torch.bfloat16,
+                    stream=None) -> tuple:
+    """(k, v), T x H x D each: what the slots (int32[T]) hold; zeros for a slot outside the pages."""
+    if stream is not None or _elsewhere(pages):
+        with _current(stream, pages):
+            return gptq_cache_read(pages, slots, D, bits, dtype)
+    if pages.dim() != 3:
+        raise ValueError("pages must be uint8 pages x heads x bytes")
+    dev, H, T = pages.device, pages.shape[1], slots.numel()
+    n, ps, hs, size = _pages(pages, H, D, bits, dev)
+    sp = _device_tensor(slots, "slots", torch.int32, dev)
+    k, v = torch.empty((2, T, H, D), dtype=dtype, device=dev)
+    _check(load().gptq_cache_read(pages.data_ptr(), n, ps, hs, size, bits, sp, T, H, D, k.data_ptr(), v.data_ptr(),
+                                  _row_type(k), H * D, D, H * D, D, _handle(dev)), "gptq_cache_read")
+    return k, v
+
+
+def gptq_attention_workspace_bytes(R: int, Hq: int, H: int, D: int) -> int:
+    """Bytes of workspace of gptq_cache_attention; 0 for sizes that it refuses."""
+    return int(load().gptq_attention_workspace_bytes(int(R), int(Hq), int(H), int(D)))
+
+
+def gptq_cache_attention(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, bits: int,
+                         scale: Optional[float] = None, window: int = 0, out: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """out[r] (Hq x D): attention of request r's new token q[r] over its lengths[r] cached tokens.
+
+    q: R x Hq x D (fp32 or bf16).  pages: as gptq_cache_write left them, H heads with Hq a multiple of H.  table: int32 R x
+    pages per request.  lengths: int32[R].  scale: 1 / sqrt(D) unless given.  window: only the last `window` tokens.
+    lse: fp32 R x Hq, written if given.
+    """
+    if stream is not None or _elsewhere(q):
+        with _current(stream, q):
+            return gptq_cache_attention(q, pages, table, lengths, bits, scale, window, out, lse, workspace)
+    _no_gradient(q, out, lse)
+    dt, dev = _row_type(q), q.device
+    q_rs, q_hs = _heads(q, "q", dev)
+    R, Hq, D = q.shape
+    if pages.dim() != 3:
+        raise ValueError("pages must be uint8 pages x heads x bytes")
+    H = pages.shape[1]
+    n, ps, hs, size = _pages(pages, H, D, bits, dev)
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or table.device != dev \
+            or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be int32 requests x pages with unit column stride on the GPU of q")
+    lp = _device_tensor(lengths, "lengths", torch.int32, dev)
+    if lengths.numel() != R:
+        raise ValueError("lengths must hold an entry per request")
+    if out is None:
+        out = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q")
+    o_rs, o_hs = _heads(out, "out", dev)
+    ep = None
+    if lse is not None:
+        ep = _device_tensor(lse, "lse", torch.float32, dev)
+        if lse.numel() != R * Hq:
+            raise ValueError("lse must hold an entry per request and head")
+    lib = load()
+    need = 0 if workspace is not None else lib.gptq_attention_workspace_bytes(R, Hq, H, D)
+    workspace, wp, wb = _scratch(need, dev, workspace)
+    _check(lib.gptq_cache_attention(q.data_ptr(), dt, R, Hq, H, D, q_rs, q_hs, pages.data_ptr(), n, ps, hs, size, bits,
+                                    table.data_ptr(), table.stride(0), table.shape[1], lp,
+                                    D ** -0.5 if scale is None else scale, window, out.data_ptr(), o_rs, o_hs, ep, wp, wb,
+                                    _handle(dev)), "gptq_cache_attention")
     return out

@@ -1,0 +1,898 @@
+"""Rotary positions, the paged cache of keys and values, and the attention over it.
+
+Bounds, elementwise, from the kernels' arithmetic (u = 2^-24; one rounding of the output: u |y| for fp32, 2^-8 |y| for
+bf16):
+  * rotary: the fraction of a turn is rounded to fp32 (2^-25 of a turn, 2 pi 2^-25 < 4 u of an angle), its cosine and sine
+    are within 4 u, times the factor u, a product and a fused product-sum 2 u: 11 u factor (|a| + |b|); the angle itself
+    carries three roundings in 64 bits, here and once more in the reference: 6 * 2^-53 of it.
+  * cache: none.  Codes and scales are held to their definition bit by bit, values to s c rounded once.
+  * attention: a score is a sum of D products, each of which meets at most 8 sequential matrix products and 5 levels within
+    one, the scales' products and the multiplication by scale log2(e): es = 20 u scale sum |q k|, and u of the score
+    itself when the largest is taken off (2 es + 4 u |score|).  A probability is then off by that relative part and 4 u of
+    its exponential.  Sums over the tokens: one rounding per 32 tokens of a wave, then the joins: (n / 32 + 64) u.  bf16
+    rows round each probability times its value's scale to bf16 once: 2^-8.  All of it times sum p |v|.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_09_amd as g
+
+gpu = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def ints(v, dev=DEV):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
+
+
+def gen_rows(shape, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=gen) * torch.exp(0.4 * torch.randn(shape[-1], generator=gen))).to(dtype)
+
+
+# ----------------------------------------------------------------------------------------------------------- rotary
+
+def rotary64(x, positions, freqs, rot, interleaved, factor):
+    x, y = x.double(), x.double().clone()
+    angle = positions.double()[:, None, None] * freqs.double()
+    c, s = factor * torch.cos(angle), factor * torch.sin(angle)
+    first = slice(0, rot, 2) if interleaved else slice(0, rot // 2)
+    second = slice(1, rot, 2) if interleaved else slice(rot // 2, rot)
+    a, b = x[..., first], x[..., second]
+    y[..., first], y[..., second] = a * c - b * s, b * c + a * s
+    bound = torch.zeros_like(y)
+    size = factor * (a.abs() + b.abs()) * (11 * U + 6 * 2.0 ** -53 * angle.abs())
+    bound[..., first], bound[..., second] = size, size
+    return y, bound
+
+
+def assert_rotary(y, x, positions, freqs, rot, interleaved, factor):
+    ref, bound = rotary64(x, positions, freqs, rot, interleaved, factor)
+    unit = 2.0 ** -8 if x.dtype == BF16 else U
+    y = y.cpu()
+    assert torch.equal(y[..., rot:], x[..., rot:])
+    off = (y.double() - ref).abs()
+    assert (off <= unit * ref.abs() + (1 + unit) * bound + 1e-37).all(), off.max()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,D,rot", [(1, 1, 2, 2), (1, 40, 128, 128), (3, 5, 80, 32), (7, 3, 96, 96), (64, 11, 64, 64), (65, 2, 72, 18),
+                                       (130, 9, 256, 64), (2, 1, 7, 6), (5, 4, 128, 30), (300, 40, 128, 128), (33, 7, 100, 50),
+                                       (2, 2, 1000, 1000), (1, 1000, 16, 8)])
+def test_rotary(T, H, D, rot, interleaved, dtype):
+    x = gen_rows((T, H, D), dtype, T + D)
+    positions = torch.arange(T, dtype=torch.int32) * 977 % 131072
+    freqs, factor = g.gptq_rotary_frequencies(rot, 500000.0, "ramp", 4.0, 4096.0)
+    y = g.gptq_rotary(x.to(DEV), positions.to(DEV), freqs.to(DEV), interleaved, factor)
+    assert_rotary(y, x, positions, freqs, rot, interleaved, factor)
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rotary_far_and_negative_positions(dtype, interleaved):
+    positions = torch.tensor([0, 1, -1, 2 ** 20, 2 ** 24 + 1, -(2 ** 24), 2 ** 31 - 1, -(2 ** 31)], dtype=torch.int32)
+    freqs, factor = g.gptq_rotary_frequencies(64)
+    x = gen_rows((8, 3, 64), dtype, 1)
+    y = g.gptq_rotary(x.to(DEV), positions.to(DEV), freqs.to(DEV), interleaved, factor)
+    assert_rotary(y, x, positions, freqs, 64, interleaved, factor)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_rotary_of_views_and_in_place(offset, interleaved, dtype):
+    """Query and key heads of a fused projection's output, in place; the value heads behind them stay."""
+    T, D = 21, 64
+    fused = gen_rows((T, 8 * D + offset), dtype, 3)
+    dev = fused.to(DEV)
+    positions = torch.arange(T, dtype=torch.int32) + 5000
+    freqs, factor = g.gptq_rotary_frequencies(48)
+    view = dev[:, offset:].unflatten(1, (8, D))[:, :6]
+    assert g.gptq_rotary(view, positions.to(DEV), freqs.to(DEV), interleaved, factor, out=view) is view
+    x = fused[:, offset:].unflatten(1, (8, D))
+    after = dev.cpu()[:, offset:].unflatten(1, (8, D))
+    assert_rotary(after[:, :6], x[:, :6].contiguous(), positions, freqs, 48, interleaved, factor)
+    assert torch.equal(after[:, 6:], x[:, 6:]) and torch.equal(dev.cpu()[:, :offset], fused[:, :offset])
+    # heads first, tokens second, and one row for all tokens
+    y = g.gptq_rotary(x.transpose(0, 1).contiguous().to(DEV).transpose(0, 1), positions.to(DEV), freqs.to(DEV), interleaved, factor,
+                      out=torch.empty(8, T, D, dtype=dtype, device=DEV).transpose(0, 1))
+    assert_rotary(y, x.contiguous(), positions, freqs, 48, interleaved, factor)
+    same = x[:1].contiguous()
+    y = g.gptq_rotary(same.to(DEV).expand(T, 8, D), positions.to(DEV), freqs.to(DEV), interleaved, factor)
+    assert_rotary(y, same.expand(T, 8, D).contiguous(), positions, freqs, 48, interleaved, factor)
+
+
+@gpu
+def test_rotary_keeps_what_is_not_finite_in_its_pair():
+    x = gen_rows((4, 2, 64), F32, 2)
+    x[1, 0, 3], x[2, 1, 60] = math.nan, math.inf
+    freqs, _ = g.gptq_rotary_frequencies(64)
+    y = g.gptq_rotary(x.to(DEV), ints([3, 4, 5, 6]), freqs.to(DEV)).cpu()
+    bad = torch.zeros(4, 2, 64, dtype=torch.bool)
+    bad[1, 0, [3, 35]], bad[2, 1, [28, 60]] = True, True
+    assert torch.equal(~torch.isfinite(y), bad)
+
+
+@gpu
+def test_rotary_of_no_tokens():
+    freqs, _ = g.gptq_rotary_frequencies(64)
+    assert g.gptq_rotary(torch.empty(0, 3, 64, device=DEV), ints([]), freqs.to(DEV)).shape == (0, 3, 64)
+
+
+def test_rotary_frequencies():
+    plain, one = g.gptq_rotary_frequencies(128, 10000.0)
+    i = torch.arange(64, dtype=torch.float64)
+    assert one == 1.0 and torch.allclose(plain, 10000.0 ** (-i / 64), rtol=1e-14, atol=0)
+    linear, one = g.gptq_rotary_frequencies(128, 10000.0, "linear", 4.0)
+    assert one == 1.0 and torch.allclose(linear, plain / 4, rtol=1e-14, atol=0)
+    changed, one = g.gptq_rotary_frequencies(128, 10000.0, "base", 4.0)
+    assert one == 1.0 and torch.allclose(changed, (10000.0 * 4.0 ** (128 / 126)) ** (-i / 64), rtol=1e-14, atol=0)
+    assert abs(changed[-1] / plain[-1] * 4 - 1) < 1e-12             # the slowest pair is stretched by the whole factor
+    ramp, m = g.gptq_rotary_frequencies(128, 10000.0, "ramp", 8.0, 4096.0)
+    turns = 4096.0 * plain / (2 * math.pi)
+    assert abs(m - (0.1 * math.log(8.0) + 1)) < 1e-6
+    assert torch.equal(ramp[turns > 40], plain[turns > 40]) and torch.allclose(ramp[turns < 0.8], plain[turns < 0.8] / 8, rtol=1e-14, atol=0)
+    assert ((ramp <= plain) & (ramp >= plain / 8 * (1 - 1e-14))).all() and (ramp.diff() < 0).all()
+    bands, one = g.gptq_rotary_frequencies(128, 500000.0, "bands", 8.0, 8192.0)
+    plain = 500000.0 ** (-i / 64)
+    length = 2 * math.pi / plain
+    share = ((8192.0 / length - 1.0) / 3.0).clamp(0, 1)
+    assert one == 1.0 and torch.allclose(bands, share * plain + (1 - share) * plain / 8, rtol=1e-13, atol=0)
+
+
+def test_rotary_frequencies_refusals():
+    for kw in (dict(rot=0), dict(rot=3), dict(rot=1026), dict(rot=8, base=1.0), dict(rot=8, base=math.inf), dict(rot=8, base=math.nan),
+               dict(rot=8, scaling="linear", factor=0.5), dict(rot=8, scaling="ramp", factor=math.nan),
+               dict(rot=8, scaling="ramp", factor=2.0, original=0.0), dict(rot=8, scaling="bands", factor=2.0, low=4.0),
+               dict(rot=8, scaling="bands", factor=2.0, low=0.0), dict(rot=8, scaling="bands", factor=2.0, high=math.inf)):
+        with pytest.raises(g.GptqError):
+            g.gptq_rotary_frequencies(**kw)
+    with pytest.raises(ValueError):
+        g.gptq_rotary_frequencies(8, scaling="else")
+
+
+# ------------------------------------------------------------------------------------------------------------ cache
+
+def stored(D):
+    return min(n for n in (64, 96, 128, 192, 256) if n >= D)
+
+
+def grid64(x, bits):
+    """Scales (fp32 bits) and codes of rows by the definition, exactly (in rationals of 64-bit floats)."""
+    x = x.double().numpy()
+    half = 2.0 ** (bits - 1)
+    with np.errstate(invalid="ignore", over="ignore"):
+        s = (np.abs(x).max(-1) / (half - 0.5)).astype(np.float32)
+    s = np.maximum(s, np.float32(2.0 ** -126))
+    fine = np.isfinite(x).all(-1)
+    with np.errstate(invalid="ignore"):
+        c = np.rint(x / s.astype(np.float64)[..., None])           # a quotient of 24-bit numbers is never rounded onto a tie
+    c = np.where(fine[..., None], np.clip(c, -half, half - 1), 0).astype(np.int64)
+    return np.where(fine, s, np.float32(np.nan)), c
+
+
+def write64(pages, x_k, x_v, slots, bits, ps):
+    """What gptq_cache_write leaves in `pages` (numpy uint8 pages x H x block), place by place."""
+    T, H, D = x_k.shape
+    Dp = stored(D)
+    part = ps * Dp * bits // 8
+    for which, x in ((0, x_k), (1, x_v)):
+        if bits == 16:
+            units = x.to(BF16).view(torch.int16).numpy().astype(np.int64) & 0xFFFF
+        else:
+            s, units = grid64(x, bits)
+        full = np.zeros((T, H, Dp), np.int64)
+        full[..., :D] = units
+        for t in range(T):
+            slot = int(slots[t])
+            if slot < 0 or slot >= pages.shape[0] * ps:
+                continue
+            p, i = divmod(slot, ps)
+            d = np.arange(Dp)
+            for h in range(H):
+                block = pages[p, h]
+                if bits == 16:
+                    at = (part + ((i // 8 * Dp + d) * 8 + i % 8) * 2) if which else i * Dp * 2 + 2 * d
+                    block[at], block[at + 1] = full[t, h] & 255, full[t, h] >> 8
+                elif bits == 8:
+                    block[(part + (i // 8 * Dp + d) * 8 + i % 8) if which else i * Dp + d] = full[t, h] & 255
+                else:
+                    two = (full[t, h, 0::2] & 15) | (full[t, h, 1::2] & 15) << 4
+                    d2 = np.arange(Dp // 2)
+                    block[(part + (i // 8 * (Dp // 2) + d2) * 8 + i % 8) if which else i * Dp // 2 + d2] = two
+                if bits < 16:
+                    at = 2 * part + which * 4 * ps + 4 * i
+                    block[at:at + 4] = np.frombuffer(np.float32(s[t, h]).tobytes(), np.uint8)
+    return pages
+
+
+def values64(x, bits):
+    if bits == 16:
+        return x.to(BF16).double()
+    s, c = grid64(x, bits)
+    return torch.from_numpy(s.astype(np.float64)[..., None] * c)
+
+
+def new_pages(P, H, ps, D, bits, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randint(0, 256, (P, H, g.gptq_cache_block_bytes(ps, D, bits)), generator=gen, dtype=torch.uint8)
+
+
+def same_bytes(got, want, ps, D, bits):
+    """Equal, but for the bits of a NaN (a scale, or a value kept in bf16)."""
+    if bits == 16:
+        a, b = got.contiguous().view(BF16), want.contiguous().view(BF16)
+        assert ((a.view(torch.int16) == b.view(torch.int16)) | (a.isnan() & b.isnan())).all()
+        return
+    if bits < 16:
+        n = 2 * ps * stored(D) * bits // 8
+        a, b = (t[..., n:].contiguous().view(F32) for t in (got, want))
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(0.0).view(torch.int32), b.nan_to_num(0.0).view(torch.int32))
+        got, want = got[..., :n], want[..., :n]
+    assert torch.equal(got, want)
+
+
+def check_cache(k, v, slots, pages, bits, ps):
+    """Written and read on the GPU against the definition; returns the pages there."""
+    D = k.shape[-1]
+    dev = pages.to(DEV)
+    g.gptq_cache_write(k.to(DEV), v.to(DEV), dev, ints(slots), bits)
+    want = torch.from_numpy(write64(pages.numpy().copy(), k, v, slots, bits, ps))
+    same_bytes(dev.cpu(), want, ps, D, bits)
+    inside = [0 <= s < pages.shape[0] * ps for s in slots]
+    for dtype in (F32, BF16):
+        got = g.gptq_cache_read(dev, ints(slots), D, bits, dtype)
+        for y, x in zip(got, (k, v)):
+            ref = values64(x, bits)
+            ref[~torch.tensor(inside, dtype=torch.bool)] = 0.0
+            ref = ref.float().to(dtype)
+            assert y.shape == x.shape and y.dtype == dtype
+            assert torch.equal(y.cpu().isnan(), ref.isnan()) and torch.equal(y.cpu().nan_to_num(0.0), ref.nan_to_num(0.0))
+    return dev
+
+
+SLOTS = {
+    "one": lambda n, rng: [int(rng.integers(n))],
+    "scattered": lambda n, rng: [int(s) for s in rng.permutation(n)[:37]],
+    "run": lambda n, rng: list(range(3, 3 + 45)),
+    "aligned": lambda n, rng: list(range(16, 16 + 48)),
+    "runs": lambda n, rng: list(range(5, 14)) + list(range(40, 57)) + list(range(24, 40)) + [1, 0],
+    "padded": lambda n, rng: [-1, 7, 8, -5, n, 9, 10, 2 ** 31 - 1, 11, -(2 ** 31)] + list(range(64, 81)) + [-1] * 9,
+    "backwards": lambda n, rng: list(range(60, 20, -1)),
+}
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("how", sorted(SLOTS))
+@pytest.mark.parametrize("H,D,ps", [(1, 64, 16), (3, 128, 48), (2, 72, 16), (5, 8, 32), (2, 256, 16)])
+def test_cache(H, D, ps, how, bits, dtype):
+    P = -(-96 // ps)
+    slots = SLOTS[how](P * ps, np.random.default_rng(D))
+    k, v = gen_rows((len(slots), H, D), dtype, 1), gen_rows((len(slots), H, D), dtype, 2)
+    check_cache(k, v, slots, new_pages(P, H, ps, D, bits), bits, ps)
+
+
+@gpu
+@pytest.mark.parametrize("D", list(range(8, 257, 8)))
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_cache_of_every_head_size(D, bits):
+    slots = list(range(30, 51)) + [3]
+    k, v = gen_rows((22, 3, D), BF16, D), gen_rows((22, 3, D), BF16, D + 1)
+    check_cache(k, v, slots, new_pages(4, 3, 16, D, bits), bits, 16)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+def test_cache_rounds_exactly(bits):
+    """Values on, and next to, the borders between codes; scales that are no powers of two."""
+    half = 2.0 ** (bits - 1)
+    rng = np.random.default_rng(3)
+    rows = []
+    for i in range(64):
+        top = np.float32(rng.uniform(1, 2) * 2.0 ** rng.integers(-30, 30))
+        s = np.float32(np.float64(top) / (half - 0.5))
+        c = rng.integers(-int(half) + 1, int(half) - 1, 128) + 0.5
+        x = (c * np.float64(s)).astype(np.float32)                 # as near to a border as fp32 comes
+        x = np.nextafter(x, np.float32(np.inf) * rng.choice([-1, 1], 128).astype(np.float32), dtype=np.float32) if i % 3 == 1 else x
+        x[i] = top
+        rows.append(x)
+    # scales that are powers of two: exact ties, to even
+    for e in (-100, 0, 100):
+        x = np.float32(2.0 ** e) * (np.arange(128, dtype=np.float32) % (2 * half - 1) - (half - 1) + 0.5)
+        x[0] = np.float32(2.0 ** e * (half - 0.5))
+        rows.append(x.astype(np.float32))
+    k = torch.from_numpy(np.stack(rows)).view(-1, 1, 128)
+    check_cache(k, k.flip(0), list(range(k.shape[0])), new_pages(5, 1, 16, 128, bits), bits, 16)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_cache_of_extreme_rows(bits, dtype):
+    big, tiny = torch.finfo(dtype).max, 2.0 ** -133
+    k = gen_rows((16, 2, 64), F32, 5)
+    k[0] = 0.0
+    k[1] = -0.0
+    k[2] = big
+    k[3, :, ::2], k[3, :, 1::2] = -big, big
+    k[4] *= 2.0 ** 120
+    k[5] = tiny
+    k[6, 0, 5], k[7, 1, 63] = math.nan, -math.inf
+    k[8, 0, 0] = math.inf
+    k[9] *= 2.0 ** -125
+    k[10] *= 2.0 ** -130
+    k[11] = 0.0
+    k[11, :, 7] = -tiny
+    k = k.to(dtype)
+    check_cache(k, k.flip(0).contiguous(), list(range(8, 24)), new_pages(2, 2, 16, 64, bits), bits, 16)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_cache_of_views(bits):
+    """Keys and values inside a fused projection's rows; pages of one layer among several, and heads before pages."""
+    T, H, D, ps = 19, 3, 64, 16
+    fused = gen_rows((T, 1 + 4 * H * D), BF16, 7)
+    k, v = fused[:, 1 + H * D:].unflatten(1, (3 * H, D))[:, :H], fused[:, 1 + H * D:].unflatten(1, (3 * H, D))[:, H:2 * H]
+    dev = fused.to(DEV)
+    kd, vd = dev[:, 1 + H * D:].unflatten(1, (3 * H, D))[:, :H], dev[:, 1 + H * D:].unflatten(1, (3 * H, D))[:, H:2 * H]
+    slots = list(range(9, 9 + T))
+    block = g.gptq_cache_block_bytes(ps, D, bits)
+    for shape, view in (((4, 2, H, block), lambda p: p[:, 1]), ((H, 4, block), lambda p: p.transpose(0, 1))):
+        pages = torch.randint(0, 256, shape, dtype=torch.uint8)
+        on = pages.to(DEV)
+        g.gptq_cache_write(kd, vd, view(on), ints(slots), bits)
+        want = view(pages).numpy().copy()
+        write64(want, k.contiguous(), v.contiguous(), slots, bits, ps)
+        same_bytes(view(on).cpu().contiguous(), torch.from_numpy(want), ps, D, bits)
+        if len(shape) == 4:
+            assert torch.equal(on[:, 0].cpu(), pages[:, 0])
+        got = g.gptq_cache_read(view(on), ints(slots), D, bits, F32)
+        assert torch.equal(got[0].cpu(), values64(k, bits).float()) and torch.equal(got[1].cpu(), values64(v, bits).float())
+
+
+@gpu
+def test_cache_past_four_gigabytes():
+    H, D, ps, bits = 8, 128, 64, 8
+    block = g.gptq_cache_block_bytes(ps, D, bits)
+    P = (5 << 30) // (H * block)
+    pages = torch.zeros(P, H, block, dtype=torch.uint8, device=DEV)
+    slots = [P * ps - 1, P * ps - 2, 0, P * ps - 9, P * ps]
+    k, v = gen_rows((5, H, D), BF16, 1), gen_rows((5, H, D), BF16, 2)
+    g.gptq_cache_write(k.to(DEV), v.to(DEV), pages, ints(slots), bits)
+    got = g.gptq_cache_read(pages, ints(slots), D, bits, F32)
+    for y, x in zip(got, (k, v)):
+        assert torch.equal(y[:4].cpu(), values64(x, bits).float()[:4]) and not y[4].any()
+    assert int((pages != 0).any(-1).any(-1).sum()) == 2
+    q = gen_rows((1, H, D), BF16, 3).to(DEV)
+    table, n = torch.full((1, 3), P - 1, dtype=torch.int32, device=DEV), ints([2 * ps])
+    one = g.gptq_cache_attention(q, pages, table, n, bits)
+    few = g.gptq_cache_attention(q, pages[P - 1:], torch.zeros_like(table), n, bits)
+    assert torch.equal(one, few) and one.any()
+
+
+@gpu
+def test_cache_of_no_tokens_and_a_slot_named_twice():
+    pages = new_pages(2, 2, 16, 64, 8)
+    dev = pages.to(DEV)
+    empty = torch.empty(0, 2, 64, device=DEV)
+    g.gptq_cache_write(empty, empty, dev, ints([]), 8)
+    assert torch.equal(dev.cpu(), pages)
+    k, v = g.gptq_cache_read(dev, ints([]), 64, 8, F32)
+    assert k.shape == v.shape == (0, 2, 64)
+    x = gen_rows((20, 2, 64), F32, 1).to(DEV)
+    g.gptq_cache_write(x, x, dev, ints([4] * 20), 8)                # whatever slot 4 holds, the others are as they were
+    after = g.gptq_cache_read(dev, ints([i for i in range(32) if i != 4]), 64, 8, F32)
+    before = g.gptq_cache_read(pages.to(DEV), ints([i for i in range(32) if i != 4]), 64, 8, F32)
+    for a, b in zip(after, before):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32)) or torch.equal(a.nan_to_num(0.5), b.nan_to_num(0.5))
+
+
+# -------------------------------------------------------------------------------------------------------- attention
+
+def filled(lengths, H, D, ps, bits, seed, spare=2, stale=math.nan, extra=1):
+    """Pages of requests in shuffled order, what the slots hold (64 bits), and the table (CPU)."""
+    per = [-(-n // ps) for n in lengths]
+    P = sum(per) + spare
+    rng = np.random.default_rng(seed)
+    order = rng.permutation(P)
+    table = np.full((len(lengths), max(per + [0]) + extra), -1, np.int32)
+    used, holder = 0, np.zeros(P, np.int64)
+    for r, n in enumerate(per):
+        table[r, :n] = order[used:used + n]
+        for j in range(n):
+            holder[table[r, j]] = min(ps, lengths[r] - j * ps)
+        used += n
+    k, v = gen_rows((P * ps, H, D), BF16, seed + 1), gen_rows((P * ps, H, D), BF16, seed + 2)
+    old = torch.from_numpy(np.arange(P * ps) % ps >= holder[np.arange(P * ps) // ps])
+    k[old], v[old] = stale, stale
+    pages = torch.zeros(P, H, g.gptq_cache_block_bytes(ps, D, bits), dtype=torch.uint8, device=DEV)
+    g.gptq_cache_write(k.to(DEV), v.to(DEV), pages, torch.arange(P * ps, dtype=torch.int32, device=DEV), bits)
+    return pages, values64(k, bits).view(P, ps, H, D), values64(v, bits).view(P, ps, H, D), torch.from_numpy(table)
+
+
+def attend64(q, k, v, table, lengths, ps, scale, window, dtype):
+    R, Hq, D = q.shape
+    P, H = k.shape[0], k.shape[2]
+    out, lse = torch.zeros(R, Hq, D, dtype=torch.float64), torch.full((R, Hq), -math.inf, dtype=torch.float64)
+    bound, lse_bound = torch.zeros_like(out), torch.zeros_like(lse)
+    for r in range(R):
+        n = min(max(int(lengths[r]), 0), table.shape[1] * ps)
+        t = torch.arange(max(0, n - window) if window else 0, n)
+        page = table[r, t // ps].long()
+        t, page = t[(page >= 0) & (page < P)], page[(page >= 0) & (page < P)]
+        if not len(t):
+            continue
+        kr, vr = (x[page, t % ps].repeat_interleave(Hq // H, 1) for x in (k, v))            # tokens x Hq x D
+        s = torch.einsum("hd,thd->ht", q[r].double(), kr) * scale
+        size = torch.einsum("hd,thd->ht", q[r].double().abs(), kr.abs()) * abs(scale)
+        p = torch.softmax(s, -1)
+        out[r], lse[r] = torch.einsum("ht,thd->hd", p, vr), torch.logsumexp(s, -1)
+        es = (40 * U * size + 4 * U * s.abs()).amax(-1, keepdim=True)                       # of a score and the largest one
+        rel = 2 * es + (8 + n / 32 + 64) * U + (2.0 ** -8 if dtype == BF16 else 0.0)
+        bound[r] = rel * torch.einsum("ht,thd->hd", p, vr.abs())
+        lse_bound[r] = (es + (8 + n / 32 + 64) * U).squeeze(-1) + 4 * U * lse[r].abs()
+    return out, lse, bound, lse_bound
+
+
+def check_attention(lengths, Hq, H, D, ps, bits, dtype, window=0, scale=None, seed=0, q=None, given=None, at=None, **kw):
+    """`given`: lengths that the call gets instead of those of the pages; `at`: a change of the table."""
+    pages, k, v, table = filled(lengths, H, D, ps, bits, seed, **kw)
+    R = len(lengths)
+    lengths = given or lengths
+    if at:
+        at(table)
+    q = gen_rows((R, Hq, D), dtype, seed + 9) if q is None else q
+    lse = torch.full((R, Hq), 7.0, device=DEV)
+    out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints(lengths), bits, scale, window, lse=lse)
+    used = D ** -0.5 if scale is None else scale
+    ref, ref_lse, bound, lse_bound = attend64(q, k, v, table, lengths, ps, used, window, dtype)
+    unit = 2.0 ** -8 if dtype == BF16 else U
+    assert out.shape == q.shape and out.dtype == dtype
+    off = (out.cpu().double() - ref).abs()
+    assert (off <= unit * ref.abs() + (1 + unit) * bound + 1e-30).all(), (off - unit * ref.abs() - bound).max()
+    empty = ref_lse == -math.inf
+    assert torch.equal(lse.cpu() == -math.inf, empty) and not out.cpu()[empty].any()
+    off = (lse.cpu().double() - ref_lse).abs()[~empty]
+    assert (off <= lse_bound[~empty] + U).all(), off.max()
+    norm = ref.norm().item()
+    if norm > 0:
+        assert (out.cpu().double() - ref).norm().item() <= (2.0 ** -8 if dtype == BF16 else 4e-6) * norm
+    return out
+
+
+LENGTHS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("Hq,H,D,ps", [(8, 2, 128, 16), (3, 3, 64, 48), (5, 1, 96, 16), (16, 1, 80, 32), (17, 1, 64, 16), (40, 2, 128, 64),
+                                       (2, 1, 8, 16), (6, 3, 256, 16), (4, 4, 160, 16), (33, 1, 256, 32)])
+def test_attention(Hq, H, D, ps, bits, dtype):
+    check_attention(LENGTHS, Hq, H, D, ps, bits, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("D", list(range(8, 257, 8)))
+def test_attention_of_every_head_size(D, bits):
+    check_attention([5, 70, 0, 33], 4, 2, D, 16, bits, BF16, seed=D)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("window", [1, 2, 16, 31, 33, 64, 200, 1000])
+def test_attention_window(window, bits, dtype):
+    check_attention(LENGTHS, 4, 2, 64, 16, bits, dtype, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("lengths", [[20000], [3, 0, 9000, 1, 70, 0, 0, 5], [1] * 300, [0] * 9, [700] * 40, [4097, 1, 4095] * 3])
+def test_attention_over_long_and_uneven_lengths(lengths, bits, dtype):
+    check_attention(lengths, 8, 2, 64, 32, bits, dtype, seed=len(lengths))
+
+
+@gpu
+def test_attention_of_many_requests():
+    rng = np.random.default_rng(0)
+    check_attention([int(n) for n in rng.integers(0, 40, 1500)], 2, 1, 64, 16, 8, BF16)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_leaves_out_pages_that_do_not_exist(bits):
+    def at(table):
+        table[1, 1], table[2, 0], table[3, :], table[0, 0] = -7, 10 ** 6, 2 ** 31 - 1, -(2 ** 31)
+    check_attention([100, 70, 48, 33], 4, 2, 64, 16, bits, F32, at=at)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_clamps_lengths(bits):
+    """Below zero nothing; past the table's pages all of them (entries behind a request's own are -1)."""
+    check_attention([33, 64, 5, 0], 4, 2, 64, 16, bits, F32, given=[-5, 2 ** 31 - 1, 5, -(2 ** 31)], stale=0.5)
+    check_attention([64, 64], 4, 2, 64, 16, bits, F32, given=[65, 2 ** 31 - 1], extra=0)
+    check_attention([64, 64], 4, 2, 64, 16, bits, F32, given=[2 ** 31 - 1, 70], window=10, extra=0)
+
+
+@gpu
+def test_attention_without_pages_in_the_table():
+    pages = new_pages(1, 1, 16, 64, 8).to(DEV)
+    lse = torch.zeros(3, 2, device=DEV)
+    out = g.gptq_cache_attention(torch.randn(3, 2, 64, device=DEV), pages, torch.empty(3, 0, dtype=torch.int32, device=DEV),
+                                 ints([0, 5, 9]), 8, lse=lse)
+    assert not out.any() and (lse == -math.inf).all()
+    assert g.gptq_cache_attention(torch.randn(0, 2, 64, device=DEV), pages, torch.empty(0, 4, dtype=torch.int32, device=DEV),
+                                  ints([]), 8).shape == (0, 2, 64)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_of_large_and_small_queries(bits, dtype):
+    """The scale brings the scores back to size one: no sum on the way may overflow or vanish."""
+    for size in (2.0 ** 110, 2.0 ** -100):
+        q = (gen_rows((4, 4, 64), F32, 1) * size).to(dtype)
+        check_attention([33, 100, 1, 64], 4, 2, 64, 16, bits, dtype, scale=0.125 / size, q=q)
+    check_attention([33, 100, 1, 64], 4, 2, 64, 16, bits, dtype, scale=0.0)
+    check_attention([33, 100, 1, 64], 4, 2, 64, 16, bits, dtype, scale=-0.2)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_with_scores_far_apart(bits, dtype):
+    """Scores in the thousands: one token takes it all, and others vanish without a trace."""
+    pages, k, v, table = filled([200, 90], 2, 64, 16, bits, 3)
+    q = k[table[:, 1].long(), 3].repeat_interleave(2, 1).to(dtype) * 40.0
+    out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints([200, 90]), bits, 1.0)
+    ref, _, bound, _ = attend64(q, k, v, table, [200, 90], 16, 1.0, 0, dtype)
+    unit = 2.0 ** -8 if dtype == BF16 else U
+    assert ((out.cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound + 1e-30).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_keeps_what_is_not_finite_to_its_rows(bits, dtype):
+    H, D, ps = 2, 64, 16
+    lengths = [100, 100, 100, 40]
+    pages, k, v, table = filled(lengths, H, D, ps, bits, 5)
+    q = gen_rows((4, 4, D), dtype, 1)
+    clean = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints(lengths), bits).cpu()
+    q[3, 1, 7] = math.nan
+    bad = gen_rows((2, H, D), BF16, 2)
+    bad[0, 1, 5], bad[1, 0, 9] = math.nan, math.inf
+    good = gen_rows((2, H, D), BF16, 2)
+    at = [int(table[0, 2]) * ps + 3, int(table[1, 6]) * ps + 3]       # a key of request 0, a value of request 1 (its last token but zero)
+    g.gptq_cache_write(bad[:1].to(DEV), good[:1].to(DEV), pages, ints(at[:1]), bits)
+    g.gptq_cache_write(good[1:].to(DEV), bad[1:].to(DEV), pages, ints(at[1:]), bits)
+    out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints(lengths), bits).cpu()
+    fine = torch.isfinite(out)
+    assert not fine[0, 2:].any() and fine[0, :2].all()               # key head 1 of request 0
+    if bits == 16:
+        assert not fine[1, :2, 9].any() and int((~fine[1]).sum()) == 2
+    else:
+        assert not fine[1, :2].any() and fine[1, 2:].all()
+    assert not fine[3, 1].any() and int((~fine[3]).sum()) == D
+    assert torch.equal(out[2], clean[2]) and torch.equal(out[3, [0, 2, 3]], clean[3, [0, 2, 3]])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_of_views(bits, dtype):
+    """Queries inside a fused projection's rows, output into wider rows, one layer's pages, a table with more columns."""
+    lengths = [50, 0, 300, 17]
+    pages, k, v, table = filled(lengths, 2, 64, 16, bits, 4)
+    layers = torch.randint(0, 256, (pages.shape[0], 3, *pages.shape[1:]), dtype=torch.uint8, device=DEV)
+    layers[:, 1] = pages
+    fused = torch.randn(4, 1 + 8 * 64, device=DEV).to(dtype)
+    q = fused[:, 1:].unflatten(1, (8, 64))[:, 2:6]
+    wide = torch.full((4, 9, 65), 3.0, device=DEV, dtype=dtype)
+    tables = torch.full((4, table.shape[1] + 5), 10 ** 6, dtype=torch.int32, device=DEV)
+    tables[:, 2:2 + table.shape[1]] = table.to(DEV)
+    plain = g.gptq_cache_attention(q.contiguous(), pages, table.to(DEV), ints(lengths), bits)
+    got = g.gptq_cache_attention(q, layers[:, 1], tables[:, 2:2 + table.shape[1]], ints(lengths), bits, out=wide[:, 3:7, :64])
+    assert torch.equal(got, plain)
+    wide[:, 3:7, :64] = 3.0
+    assert (wide == 3.0).all()
+    heads = pages.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(g.gptq_cache_attention(q, heads, table.to(DEV), ints(lengths), bits), plain)
+    back = g.gptq_cache_attention(q.transpose(0, 1).contiguous().transpose(0, 1), pages, table.to(DEV), ints(lengths), bits,
+                                  out=torch.empty(4, 4, 64, device=DEV, dtype=dtype).transpose(0, 1))
+    assert torch.equal(back, plain)
+
+
+# --------------------------------------------------------------------------------------------------------- together
+
+def layer_step(x, positions, slots, table, lengths, pages, bits, freqs, factor, Hq, H, D, workspace=None):
+    """What a served layer does between its projections: x holds query, key and value heads."""
+    qk = x[:, :Hq + H]
+    g.gptq_rotary(qk, positions, freqs, factor=factor, out=qk)
+    g.gptq_cache_write(x[:, Hq:Hq + H], x[:, Hq + H:], pages, slots, bits)
+    return g.gptq_cache_attention(x[:, :Hq], pages, table, lengths, bits, workspace=workspace)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_prompts_then_tokens(bits, dtype):
+    """Prompts written, then decode steps; against all of it in 64 bits from the rotated rows that the calls return."""
+    Hq, H, D, ps, R = 6, 2, 64, 16, 3
+    freqs, factor = g.gptq_rotary_frequencies(D, 10000.0)
+    freqs = freqs.to(DEV)
+    lengths = [37, 5, 64]
+    table = torch.randperm(R * 8).view(R, 8).int()
+    pages = torch.zeros(R * 8, H, g.gptq_cache_block_bytes(ps, D, bits), dtype=torch.uint8, device=DEV)
+    slot = lambda r, t: int(table[r, t // ps]) * ps + t % ps  # noqa: E731
+    keys, values = [[] for _ in range(R)], [[] for _ in range(R)]
+    gen = torch.Generator().manual_seed(0)
+    prompt = torch.randn(sum(lengths), 2 * H, D, generator=gen).to(dtype).to(DEV)
+    where = [(r, t) for r in range(R) for t in range(lengths[r])]
+    k = g.gptq_rotary(prompt[:, :H], ints([t for _, t in where]), freqs, factor=factor)
+    g.gptq_cache_write(k, prompt[:, H:], pages, ints([slot(r, t) for r, t in where]), bits)
+    for i, (r, t) in enumerate(where):
+        keys[r].append(k[i].cpu())
+        values[r].append(prompt[i, H:].cpu())
+    for step in range(20):
+        x = torch.randn(R, Hq + 2 * H, D, generator=gen).to(dtype).to(DEV)
+        out = layer_step(x, ints(lengths), ints([slot(r, n) for r, n in enumerate(lengths)]), table.to(DEV),
+                         ints([n + 1 for n in lengths]), pages, bits, freqs, factor, Hq, H, D)
+        lengths = [n + 1 for n in lengths]
+        for r in range(R):
+            keys[r].append(x[r, Hq:Hq + H].cpu())
+            values[r].append(x[r, Hq + H:].cpu())
+            kr, vr = (values64(torch.stack(z), bits).view(1, -1, H, D) for z in (keys[r], values[r]))
+            n = lengths[r]
+            ref, _, bound, _ = attend64(x[r:r + 1, :Hq].cpu(), kr, vr, torch.zeros(1, 1, dtype=torch.int32), [n], n, D ** -0.5, 0, dtype)
+            unit = 2.0 ** -8 if dtype == BF16 else U
+            assert ((out[r:r + 1].cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound + 1e-30).all()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_a_step_in_a_graph(bits):
+    """Captured once, replayed as lengths grow (past a split of the work), each replay against the eager calls."""
+    Hq, H, D, ps, R = 8, 2, 128, 16, 4
+    freqs, factor = g.gptq_rotary_frequencies(D)
+    freqs = freqs.to(DEV)
+    start = [100, 0, 3000, 31]
+    pages, _, _, table = filled(start, H, D, ps, bits, 1, spare=8, stale=0.0, extra=3)
+    free = [p for p in range(pages.shape[0]) if not (table == p).any()]
+    for r, n in enumerate(start):
+        table[r, -(-n // ps):][:2] = torch.tensor(free[2 * r:2 * r + 2], dtype=torch.int32)
+    table = table.to(DEV)
+    x, positions, slots, lengths = torch.zeros(R, Hq + 2 * H, D, dtype=BF16, device=DEV), ints([0] * R), ints([-1] * R), ints([1] * R)
+    ws = torch.empty(g.gptq_attention_workspace_bytes(R, Hq, H, D), dtype=torch.uint8, device=DEV)
+    eager = pages.clone()
+    layer_step(x, positions, slots, table, lengths, pages, bits, freqs, factor, Hq, H, D, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer_step(x, positions, slots, table, lengths, pages, bits, freqs, factor, Hq, H, D, ws)
+    for step in range(18):
+        now = [n + step for n in start]
+        fresh = torch.randn(R, Hq + 2 * H, D, device=DEV).to(BF16)
+        where = [int(table[r, n // ps]) * ps + n % ps for r, n in enumerate(now)]
+        x.copy_(fresh)
+        positions.copy_(ints(now))
+        slots.copy_(ints(where))
+        lengths.copy_(ints([n + 1 for n in now]))
+        graph.replay()
+        want = layer_step(fresh, ints(now), ints(where), table, ints([n + 1 for n in now]), eager, bits, freqs, factor, Hq, H, D)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(pages, eager)
+
+
+@gpu
+def test_two_graphs_may_share_a_workspace():
+    """Replayed one after the other on one stream."""
+    ws = torch.empty(g.gptq_attention_workspace_bytes(40, 8, 2, 64), dtype=torch.uint8, device=DEV)
+    made = []
+    for lengths, bits in (([5000], 8), ([200] * 40, 16)):
+        pages, _, _, table = filled(lengths, 2, 64, 16, bits, 2)
+        q, table, n = torch.randn(len(lengths), 8, 64, device=DEV), table.to(DEV), ints(lengths)
+        want = g.gptq_cache_attention(q, pages, table, n, bits)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = g.gptq_cache_attention(q, pages, table, n, bits, workspace=ws)
+        made.append((graph, out, want, (q, pages, table, n)))
+    for _ in range(3):
+        for graph, out, want, _ in made:
+            out.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _ in made:
+            assert torch.equal(out, want)
+
+
+@gpu
+def test_calls_on_another_stream():
+    lengths = [3000, 10]
+    pages, _, _, table = filled(lengths, 2, 64, 16, 8, 2)
+    table, n = table.to(DEV), ints(lengths)
+    x = torch.randn(2, 8, 64, device=DEV)
+    freqs = g.gptq_rotary_frequencies(64)[0].to(DEV)
+    q = g.gptq_rotary(x, n, freqs)
+    want = g.gptq_cache_attention(q, pages, table, n, 8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3                                    # the current stream is behind
+    got_q = g.gptq_rotary(x, n, freqs, stream=side)
+    got = g.gptq_cache_attention(got_q, pages, table, n, 8, stream=side)
+    k, v = g.gptq_cache_read(pages, ints([1, 2]), 64, 8, F32, stream=side)
+    g.gptq_cache_write(k, v, pages, ints([1, 2]), 8, stream=side)
+    side.synchronize()
+    assert torch.equal(got_q, q) and torch.equal(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_the_same_call_gives_the_same_bits(bits):
+    lengths = [0, 9000, 1, 33, 700, 701]
+    pages, _, _, table = filled(lengths, 4, 128, 16, bits, 2)
+    q = torch.randn(6, 16, 128, device=DEV)
+    calls = [g.gptq_cache_attention(q, pages, table.to(DEV), ints(lengths), bits) for _ in range(5)]
+    assert all(torch.equal(c, calls[0]) for c in calls)
+
+
+@gpu
+def test_attention_on_a_workspace_of_the_stated_size():
+    lengths, R = [9000, 0, 40, 5] * 20, 80
+    pages, _, _, table = filled(lengths, 2, 128, 16, 8, 2)
+    q = torch.randn(R, 34, 128, device=DEV)
+    want = g.gptq_cache_attention(q, pages, table.to(DEV), ints(lengths), 8)
+    need = g.gptq_attention_workspace_bytes(R, 34, 2, 128)
+    around = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    got = g.gptq_cache_attention(q, pages, table.to(DEV), ints(lengths), 8, workspace=around[256:256 + need])
+    assert torch.equal(got, want) and (around[:256] == 0xA5).all() and (around[256 + need:] == 0xA5).all()
+    with pytest.raises(g.GptqError):
+        g.gptq_cache_attention(q, pages, table.to(DEV), ints(lengths), 8, workspace=around[256:256 + need - 1])
+
+
+# --------------------------------------------------------------------------------------------------------- refusals
+
+FAKE, OUT = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x900000)   # never dereferenced: validation fails first
+
+
+def change(call, base, names, **kw):
+    args = list(base)
+    for k, v in kw.items():
+        args[names.index(k)] = v
+    return call(*args)
+
+
+ROTARY = ["X", "dtype", "T", "H", "D", "x_ts", "x_hs", "positions", "freqs", "rot", "factor", "flags", "Y", "y_ts", "y_hs", "stream"]
+WRITE = ["K", "V", "dtype", "T", "H", "D", "k_ts", "k_hs", "v_ts", "v_hs", "slots", "bits", "pages", "n", "ps", "hs", "size", "stream"]
+READ = ["pages", "n", "ps", "hs", "size", "bits", "slots", "T", "H", "D", "K", "V", "dtype", "k_ts", "k_hs", "v_ts", "v_hs", "stream"]
+ATTEND = ["Q", "dtype", "R", "Hq", "H", "D", "q_rs", "q_hs", "pages", "n", "ps", "hs", "size", "bits", "table", "ld", "max_pages", "lengths",
+          "scale", "window", "out", "o_rs", "o_hs", "lse", "ws", "ws_bytes", "stream"]
+
+
+def test_rotary_refusals():
+    base = (FAKE, 1, 4, 2, 64, 128, 64, FAKE, FAKE, 64, 1.0, 0, OUT, 128, 64, None)
+    for kw in (dict(dtype=2), dict(T=-1), dict(T=(1 << 22) + 1), dict(H=0), dict(H=1025), dict(D=0), dict(D=1025), dict(rot=0), dict(rot=63),
+               dict(rot=66), dict(flags=2), dict(X=None), dict(Y=None), dict(positions=None), dict(freqs=None), dict(x_ts=-1), dict(y_hs=-1),
+               dict(y_hs=63), dict(y_ts=127), dict(y_ts=0), dict(Y=FAKE, x_ts=129), dict(Y=FAKE, x_hs=32), dict(x_ts=1 << 41)):
+        assert change(g.load().gptq_rotary, base, ROTARY, **kw) == g.GPTQ_ERR_ARG, kw
+    assert change(g.load().gptq_rotary, base, ROTARY, T=0, X=None, Y=None, positions=None) == g.GPTQ_OK
+
+
+def test_cache_refusals():
+    block = g.gptq_cache_block_bytes(32, 64, 8)
+    assert block == 2 * 32 * 64 + 8 * 32
+    bad_pages = (dict(bits=2), dict(bits=5), dict(D=0), dict(D=12), dict(D=264), dict(H=0), dict(H=1025), dict(size=0), dict(size=8), dict(size=24),
+                 dict(size=65552), dict(pages=None), dict(pages=ctypes.c_void_p(0x100008)), dict(n=0), dict(n=1 << 26), dict(ps=block),
+                 dict(hs=block - 16), dict(hs=block + 8), dict(ps=3 * block + 8), dict(hs=0))
+    write = (FAKE, FAKE, 1, 4, 2, 64, 128, 64, 128, 64, FAKE, 8, FAKE, 10, 2 * block, block, 32, None)
+    for kw in bad_pages + (dict(K=None), dict(V=None), dict(slots=None), dict(T=-1), dict(T=(1 << 22) + 1), dict(dtype=5), dict(k_ts=-1), dict(v_hs=-1)):
+        assert change(g.load().gptq_cache_write, write, WRITE, **kw) == g.GPTQ_ERR_ARG, kw
+    read = (FAKE, 10, 2 * block, block, 32, 8, FAKE, 4, 2, 64, FAKE, OUT, 1, 128, 64, 128, 64, None)
+    for kw in bad_pages + (dict(K=None), dict(V=None), dict(V=FAKE), dict(slots=None), dict(T=-1), dict(dtype=5), dict(k_ts=0), dict(v_hs=32)):
+        assert change(g.load().gptq_cache_read, read, READ, **kw) == g.GPTQ_ERR_ARG, kw
+    for call, base, names in ((g.load().gptq_cache_write, write, WRITE), (g.load().gptq_cache_read, read, READ)):
+        assert change(call, base, names, T=0, K=None, V=None, slots=None) == g.GPTQ_OK
+    for args in ((0, 64, 8), (8, 64, 8), (17, 64, 8), (65552, 64, 8), (16, 0, 8), (16, 257, 8), (16, 12, 8), (16, 64, 6), (16, 64, 32)):
+        assert g.gptq_cache_block_bytes(*args) == 0
+    for D, Dp in ((8, 64), (64, 64), (72, 96), (104, 128), (136, 192), (200, 256), (256, 256)):
+        assert g.gptq_cache_block_bytes(48, D, 16) == 48 * Dp * 4 and g.gptq_cache_block_bytes(48, D, 4) == 48 * (Dp + 8)
+
+
+def test_attention_refusals():
+    block = g.gptq_cache_block_bytes(32, 64, 8)
+    need = g.gptq_attention_workspace_bytes(4, 8, 2, 64)
+    base = (FAKE, 1, 4, 8, 2, 64, 512, 64, FAKE, 10, 2 * block, block, 32, 8, FAKE, 7, 7, FAKE, 0.125, 0, OUT, 512, 64, None, FAKE, need, None)
+    call = g.load().gptq_cache_attention
+    for kw in (dict(dtype=2), dict(R=-1), dict(R=65537), dict(Hq=0), dict(Hq=1), dict(Hq=7), dict(Hq=1026), dict(H=0), dict(D=20), dict(D=512),
+               dict(bits=6), dict(size=40), dict(n=0), dict(pages=None), dict(hs=block - 16), dict(ps=block), dict(Q=None), dict(out=None),
+               dict(out=FAKE), dict(table=None), dict(lengths=None), dict(ld=-1), dict(max_pages=-1), dict(max_pages=1 << 26), dict(window=-1),
+               dict(scale=math.inf), dict(scale=math.nan), dict(q_rs=-1), dict(o_rs=0), dict(o_hs=60)):
+        assert change(call, base, ATTEND, **kw) == g.GPTQ_ERR_ARG, kw
+    for kw in (dict(ws=None), dict(ws=ctypes.c_void_p(0x100010)), dict(ws_bytes=need - 1)):
+        assert change(call, base, ATTEND, **kw) == g.GPTQ_ERR_WORKSPACE, kw
+    assert change(call, base, ATTEND, R=0, Q=None, out=None, lengths=None, table=None, ws=None) == g.GPTQ_OK
+    for args in ((0, 8, 2, 64), (65537, 8, 2, 64), (1, 7, 2, 64), (1, 1, 2, 64), (1, 2048, 2, 64), (1, 8, 2, 12), (1, 8, 0, 64)):
+        assert g.gptq_attention_workspace_bytes(*args) == 0
+
+
+def test_tensors_on_the_cpu_are_refused():
+    """Before any launch, by the binding."""
+    freqs, _ = g.gptq_rotary_frequencies(64)
+    x = torch.zeros(2, 2, 64)
+    pages = torch.zeros(2, 2, g.gptq_cache_block_bytes(16, 64, 8), dtype=torch.uint8)
+    at = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: g.gptq_rotary(x, at, freqs), lambda: g.gptq_cache_write(x, x, pages, at, 8), lambda: g.gptq_cache_read(pages, at, 64, 8),
+                 lambda: g.gptq_cache_attention(x, pages, at.view(2, 1), at, 8)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@gpu
+def test_refusals_of_the_binding():
+    freqs = g.gptq_rotary_frequencies(64)[0].to(DEV)
+    x = torch.zeros(2, 2, 64, device=DEV)
+    pages = torch.zeros(3, 2, g.gptq_cache_block_bytes(16, 64, 8), dtype=torch.uint8, device=DEV)
+    at, table = ints([0, 1]), ints([[0, 1], [2, 0]])
+    bad = [
+        lambda: g.gptq_rotary(x.half(), at, freqs), lambda: g.gptq_rotary(x[0], at, freqs), lambda: g.gptq_rotary(x, at.long(), freqs),
+        lambda: g.gptq_rotary(x, at[:1], freqs), lambda: g.gptq_rotary(x, at, freqs.float()), lambda: g.gptq_rotary(x, at, freqs.cpu()),
+        lambda: g.gptq_rotary(x.transpose(1, 2), at, freqs), lambda: g.gptq_rotary(x, at, freqs, out=x[:1]),
+        lambda: g.gptq_rotary(x, at, freqs, out=torch.zeros(2, 2, 64, device=DEV, dtype=BF16)),
+        lambda: g.gptq_rotary(x, at, freqs, out=torch.zeros(1, 2, 64, device=DEV).expand(2, 2, 64)),
+        lambda: g.gptq_rotary(x[..., :32], at, freqs),
+        lambda: g.gptq_cache_write(x, x[:1], pages, at, 8), lambda: g.gptq_cache_write(x, x.to(BF16), pages, at, 8),
+        lambda: g.gptq_cache_write(x, x, pages, at[:1], 8), lambda: g.gptq_cache_write(x, x, pages, at.long(), 8),
+        lambda: g.gptq_cache_write(x, x, pages, at, 16), lambda: g.gptq_cache_write(x, x, pages, at, 3),
+        lambda: g.gptq_cache_write(x, x, pages[:, :1], at, 8), lambda: g.gptq_cache_write(x, x, pages.float(), at, 8),
+        lambda: g.gptq_cache_write(x, x, pages[:1].expand(3, -1, -1), at, 8), lambda: g.gptq_cache_write(x, x, pages.cpu(), at, 8),
+        lambda: g.gptq_cache_write(x[..., :60], x[..., :60], pages, at, 8), lambda: g.gptq_cache_write(x, x, pages[:, :, 8:], at, 8),
+        lambda: g.gptq_cache_read(pages, at, 63, 8), lambda: g.gptq_cache_read(pages, at.long(), 64, 8), lambda: g.gptq_cache_read(pages, at, 64, 8, torch.half),
+        lambda: g.gptq_cache_read(pages[0], at, 64, 8), lambda: g.gptq_cache_read(pages[:0], at, 64, 8),
+        lambda: g.gptq_cache_attention(x[:, :1], pages, table, at, 8), lambda: g.gptq_cache_attention(x, pages, table[:1], at, 8),
+        lambda: g.gptq_cache_attention(x, pages, table.long(), at, 8), lambda: g.gptq_cache_attention(x, pages, table.t(), at, 8),
+        lambda: g.gptq_cache_attention(x, pages, table, at[:1], 8), lambda: g.gptq_cache_attention(x, pages, table, at, 8, out=x),
+        lambda: g.gptq_cache_attention(x, pages, table, at, 8, out=x[:1]), lambda: g.gptq_cache_attention(x, pages, table, at, 8, window=-1),
+        lambda: g.gptq_cache_attention(x, pages, table, at, 8, scale=math.nan),
+        lambda: g.gptq_cache_attention(x, pages, table, at, 8, lse=torch.zeros(3, device=DEV)),
+        lambda: g.gptq_cache_attention(x, pages, table, at, 8, lse=torch.zeros(2, 2, device=DEV, dtype=torch.float64)),
+        lambda: g.gptq_cache_attention(x, pages, table, at, 8, workspace=torch.zeros(256, dtype=torch.uint8)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, g.GptqError)):
+            call()
+            raise AssertionError(f"call {i} was accepted")
+
+
+@gpu
+def test_gradients_are_refused():
+    freqs = g.gptq_rotary_frequencies(64)[0].to(DEV)
+    x = torch.zeros(1, 2, 64, device=DEV, requires_grad=True)
+    plain = x.detach()
+    pages = torch.zeros(3, 2, g.gptq_cache_block_bytes(16, 64, 8), dtype=torch.uint8, device=DEV)
+    for call in (lambda: g.gptq_rotary(x, ints([0]), freqs), lambda: g.gptq_cache_write(x, plain, pages, ints([0]), 8),
+                 lambda: g.gptq_cache_write(plain, x, pages, ints([0]), 8), lambda: g.gptq_cache_attention(x, pages, ints([[0]]), ints([1]), 8)):
+        with pytest.raises(ValueError):
+            call()
+        with torch.no_grad():
+            call()
