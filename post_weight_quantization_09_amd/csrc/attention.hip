@@ -1,8 +1,8 @@
-// Attention of one new token of every request over its pages.
-//
-// One pass over the tokens: with m the largest score so far, l = sum e^(score - m) and o = sum e^(score - m) v, a larger score
-// rescales l and o by e^(old m - new m).  The waves of a workgroup take the tokens in turn and join their (m, l, o) in LDS.
-#include "context.hpp"
+// Attention of new tokens over their pages: the launch, and the join of sums that several workgroups hold
+// (kernels in attention_kernel.hpp).
+#include <algorithm>
+
+#include "attention.hpp"
 
 namespace gptq {
 
@@ -10,96 +10,82 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-struct AttentionKernelArgs {
-    const void* q;
-    void* out;
-    int64_t q_rs, q_hs, o_rs, o_hs;
-    int R, Hq, H, D, Dp;
-    const uint8_t* pages;
-    int64_t n_pages, page_stride, head_stride;
-    int page_size;
-    const int32_t* table;
-    int64_t ld_table, max_pages;
-    const int32_t* lengths;
-    float scale;
-    int64_t window;
-    float* lse;
-};
+// A wave joins one query head of the segment that begins in workgroup blockIdx.x and ends in a later one.
+template <typename E>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
+    const AttentionRecord rec = a.records[blockIdx.x];
+    if (rec.request < 0) return;
+    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
+    const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
+    const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads + row;
+    if (row >= heads) return;
+    const int first = blockIdx.x, parts = rec.last - first + 1;
+    const auto place = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 64) top = fmaxf(top, a.partial_ml[place(i) * 2]);
+    for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
+    const float from = top == -INFINITY ? 0.0f : top;
+    float whole = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < parts; ++i) {
+        const int64_t p = place(i);
+        const float keep = __builtin_amdgcn_exp2f(a.partial_ml[p * 2] - from);
+        whole += keep * a.partial_ml[p * 2 + 1];
+        for (int z = 0; z < 4; ++z)
+            if (lane + 64 * z < Dp) o[z] += keep * a.partial_o[p * Dp + lane + 64 * z];
+    }
+    E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs;
+    for (int z = 0; z < 4; ++z)
+        if (lane + 64 * z < a.D) to[lane + 64 * z] = (E)(whole == 0.0f ? 0.0f : o[z] / whole);
+    if (a.lse && lane == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+}
 
-template <typename E, int BITS>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionKernelArgs a) {
-    __shared__ float part[4][256 + 2];
-    const int hq = blockIdx.x, r = blockIdx.y, h = hq / (a.Hq / a.H);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = min((int64_t)max(a.lengths[r], 0), a.max_pages * a.page_size);
-    const int64_t first = a.window > 0 && n > a.window ? n - a.window : 0;
-    const E* q = static_cast<const E*>(a.q) + r * a.q_rs + hq * a.q_hs;
-    float qv[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < 4; ++i) qv[i] = lane + 64 * i < a.D ? (float)q[lane + 64 * i] * a.scale * kLog2e : 0.0f;
-    for (int64_t t = first + wave; t < n; t += 4) {
-        const int page = a.table[r * a.ld_table + t / a.page_size], slot = (int)(t % a.page_size);
-        if ((uint32_t)page >= (uint64_t)a.n_pages) continue;
-        const uint8_t* block = a.pages + page * a.page_stride + h * a.head_stride;
-        const int size = a.page_size * a.Dp * BITS / 8;
-        const float* scales = reinterpret_cast<const float*>(block + 2 * size);
-        float sum = 0.0f, v[4];
-        for (int i = 0; i < 4; ++i) {
-            const int d = lane + 64 * i;
-            v[i] = 0.0f;
-            if (d >= a.D) continue;
-            float k;
-            if constexpr (BITS == 16) {
-                k = (float)reinterpret_cast<const __bf16*>(block)[slot * a.Dp + d];
-                v[i] = (float)reinterpret_cast<const __bf16*>(block + size)[((slot >> 3) * a.Dp + d) * 8 + (slot & 7)];
-            } else if constexpr (BITS == 8) {
-                k = (float)(int8_t)block[slot * a.Dp + d];
-                v[i] = (float)(int8_t)block[size + ((slot >> 3) * a.Dp + d) * 8 + (slot & 7)];
-            } else {
-                k = (float)((int)((uint32_t)block[(slot * a.Dp + d) / 2] << (d & 1 ? 24 : 28)) >> 28);
-                v[i] = (float)((int)((uint32_t)block[size + ((slot >> 3) * (a.Dp / 2) + d / 2) * 8 + (slot & 7)] << (d & 1 ? 24 : 28)) >> 28);
-            }
-            sum += qv[i] * k;
-        }
-        for (int i = 32; i; i >>= 1) sum += __shfl_xor(sum, i);
-        float sv = 1.0f;
-        if constexpr (BITS < 16) {
-            sum *= scales[slot];
-            sv = scales[a.page_size + slot];
-        }
-        const float top = sum == sum ? fmaxf(m, sum) : sum;
-        const float base = top == -INFINITY ? 0.0f : top, keep = exp2f(m - base), p = exp2f(sum - base);
-        m = top;
-        l = l * keep + p;
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * keep + p * sv * v[i];
-    }
-    for (int i = 0; i < 4; ++i) part[wave][lane + 64 * i] = o[i];
-    if (lane == 0) part[wave][256] = m, part[wave][257] = l;
-    __syncthreads();
-    float top = -INFINITY, whole = 0.0f;
-    for (int w = 0; w < 4; ++w) top = part[w][256] == part[w][256] ? fmaxf(top, part[w][256]) : NAN;
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < 4; ++w) whole += part[w][257] * exp2f(part[w][256] - base);
-    if ((int)threadIdx.x < a.D) {
-        float sum = 0.0f;
-        for (int w = 0; w < 4; ++w) sum += part[w][threadIdx.x] * exp2f(part[w][256] - base);
-        static_cast<E*>(a.out)[r * a.o_rs + hq * a.o_hs + threadIdx.x] = (E)(whole == 0.0f ? 0.0f : sum / whole);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+constexpr int kWorkgroups = 1024;
+
+int rows_of(int64_t Hq, int64_t H) { return (int)std::min<int64_t>(Hq / H, kTileHeads); }
+
+void carve(Carver& c, AttentionKernelArgs& k, int Dp) {
+    k.records = c.take<AttentionRecord>(kWorkgroups);
+    k.partial_ml = c.take<float>((size_t)2 * kWorkgroups * k.rows * 2);
+    k.partial_o = c.take<float>((size_t)2 * kWorkgroups * k.rows * Dp);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D) { return kAlign; }
+size_t attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D) {
+    AttentionKernelArgs k{};
+    k.rows = rows_of(Hq, H);
+    Carver c(nullptr);
+    carve(c, k, stored_head_size(D));
+    return c.bytes();
+}
 
 hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t stream) {
-    AttentionKernelArgs k{a.q.p, a.out.p, a.q.ts, a.q.hs, a.out.ts, a.out.hs, a.R, a.Hq, a.H, a.D, stored_head_size(a.D),
-                          a.pages.p, a.pages.n, a.pages.page_stride, a.pages.head_stride, a.pages.page_size,
-                          a.table, a.ld_table, a.max_pages, a.lengths, a.scale, a.window, a.lse};
-    auto pick = [&](auto e) {
-        using E = decltype(e);
-        return a.pages.bits == 16 ? attention_kernel<E, 16> : a.pages.bits == 8 ? attention_kernel<E, 8> : attention_kernel<E, 4>;
-    };
-    (a.f32 ? pick(0.0f) : pick((__bf16)0.0f))<<<dim3((unsigned)a.Hq, (unsigned)a.R), 256, 0, stream>>>(k);
+    const int Dp = stored_head_size(a.D);
+    AttentionKernelArgs k{};
+    k.q = a.q.p, k.q_rs = a.q.ts, k.q_hs = a.q.hs;
+    k.out = a.out.p, k.o_rs = a.out.ts, k.o_hs = a.out.hs;
+    k.lse = a.lse;
+    k.pages = a.pages.p, k.page_stride = a.pages.page_stride, k.head_stride = a.pages.head_stride;
+    k.n_pages = (uint32_t)a.pages.n, k.page_size = a.pages.page_size;
+    while (((uint64_t)1 << k.page_shift) < (uint64_t)k.page_size) ++k.page_shift;
+    k.page_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << k.page_shift) - k.page_size)) / k.page_size + 1);
+    k.table = a.table, k.ld_table = a.ld_table;
+    k.max_tokens = (uint32_t)(a.max_pages * a.pages.page_size);
+    k.lengths = a.lengths;
+    k.scale_log2e = a.scale * kLog2e;
+    k.window = a.window;
+    k.R = a.R, k.Hq = a.Hq, k.H = a.H, k.D = a.D, k.group = a.Hq / a.H;
+    k.tiles = (int)ceil_div(k.group, kTileHeads), k.segments = a.H * k.tiles;
+    k.rows = rows_of(a.Hq, a.H);
+    Carver c(workspace);
+    carve(c, k, Dp);
+    const hipError_t e = a.pages.bits == 16  ? launch_attention<16>(k, Dp / 32, a.f32, kWorkgroups, stream)
+                         : a.pages.bits == 8 ? launch_attention<8>(k, Dp / 32, a.f32, kWorkgroups, stream)
+                                             : launch_attention<4>(k, Dp / 32, a.f32, kWorkgroups, stream);
+    if (e != hipSuccess) return e;
+    const dim3 grid(kWorkgroups, (unsigned)ceil_div(k.rows, 4));
+    if (a.f32) attention_join_kernel<float><<<grid, 256, 0, stream>>>(k, Dp);
+    else attention_join_kernel<__bf16><<<grid, 256, 0, stream>>>(k, Dp);
     return hipGetLastError();
 }
 

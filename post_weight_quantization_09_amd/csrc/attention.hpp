@@ -1,0 +1,46 @@
+// What the attention's host code (attention.hip) and its kernels (attention_kernel.hpp, one file per width of the cache)
+// share.
+#pragma once
+
+#include "context.hpp"
+
+namespace gptq {
+
+constexpr int kBlockTokens = 32;        // tokens of a wave's step: the K of the second product
+constexpr int kTileHeads = 16;          // query heads of a step: the N of both products
+
+// How a sum over a segment (a request and up to 16 query heads of one key head) goes on past a workgroup.
+struct AttentionRecord {
+    int32_t request, segment, last;     // request < 0: this workgroup leaves nothing to join
+    int32_t pad;
+};
+
+struct AttentionKernelArgs {
+    const void* q;
+    void* out;
+    int64_t q_rs, q_hs, o_rs, o_hs;
+    float* lse;
+    const uint8_t* pages;
+    int64_t page_stride, head_stride;
+    uint32_t n_pages;
+    int page_size;
+    uint32_t page_mul, page_shift;      // t / page_size = (umulhi(t, mul) + t) >> shift, t < 2^31
+    const int32_t* table;
+    int64_t ld_table;
+    uint32_t max_tokens;                // of the table's columns
+    const int32_t* lengths;
+    float scale_log2e;
+    int64_t window;
+    int R, Hq, H, D, group;             // group = Hq / H query heads share a key head
+    int tiles, segments;                // per key head and per request
+    float* partial_o;                   // two slots per workgroup, rows x Dp
+    float* partial_ml;                  // rows x 2
+    int rows;                           // of a slot: min(group, 16)
+    AttentionRecord* records;
+};
+
+// chunks: stored head size / 32.  Launches `workgroups` workgroups.
+template <int BITS>
+hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, int workgroups, hipStream_t stream);
+
+}  // namespace gptq

@@ -1,0 +1,10 @@
+// The attention's kernels for a cache of 16 bits.
+#include <type_traits>
+
+#include "attention_kernel.hpp"
+
+namespace gptq {
+
+template hipError_t launch_attention<16>(const AttentionKernelArgs&, int, bool, int, hipStream_t);
+
+}  // namespace gptq

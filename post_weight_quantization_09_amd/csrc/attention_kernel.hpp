@@ -1,0 +1,474 @@
+// Attention of new tokens over their pages, on the matrix cores.
+//
+// A wave takes 32 tokens at a time and 16 query heads of one key head, with two products of v_mfma_f32_16x16x32_bf16 whose
+// operands come straight from the pages, without LDS and without moving a value between lanes:
+//   scores   S^T (tokens x heads) = K Q^T.  Lane l gives, as row l % 16 of the A operand, eight dimensions of one token; which
+//            token is row m is free, and tile T of two takes token 8 (m / 4) + 4 T + m % 4.  The result's lane then holds for
+//            head l % 16 the tokens 8 (l / 16) .. + 7;
+//   output   O^T (dimensions x heads) += V^T P^T.  Those eight tokens are exactly the K octet that the B operand wants in this
+//            lane, so the probabilities go in where the scores came out; the A operand wants eight tokens of one dimension,
+//            which is how the pages store values.
+// Codes become bf16 exactly (8 bits: v_cvt_f32_i32 of a byte; 4 bits: v_cvt_off_f32_i4, which is code / 16); a token's key
+// scale multiplies its score, its value scale its probability.  With fp32 rows q and the probabilities are cut into three
+// bf16 parts each (exact), so that nothing is rounded but sums.  bf16 rows round probability times scale to bf16: an error
+// of 2^-9 in each of many terms, where the output's own rounding is 2^-9 of their sum.
+//
+// Softmax: scores are kept times log2 e.  A lane's maximum is raised (and what was summed rescaled) only where a score passes it
+// by 8: probabilities then reach 2^8, which fp32 sums and bf16 factors bear as well as 1, and few steps rescale.
+//
+// Work is shared out by blocks of 32 tokens: all blocks of all requests and heads lie on one line, and workgroup w takes the
+// w-th piece of it, whatever the lengths (an even share for 64 ragged requests as for one of 131072 tokens beside short
+// ones).  The line is found from a scan over the lengths, by every workgroup for itself.  A segment (request and heads) that
+// ends in another workgroup than it began leaves unnormalised sums, which the join adds in order.
+#pragma once
+
+#include "attention.hpp"
+
+namespace gptq {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRaise = 8.0f;
+
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+
+// the largest of lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float max_of_quarters(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float sum_of_quarters(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Eight bytes as bf16 (exact).
+__device__ __forceinline__ bf16x8 bytes_to_bf16(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    r[0] = high_halves((float)(int8_t)w0, (float)(int8_t)(w0 >> 8));
+    r[1] = high_halves((float)(int8_t)(w0 >> 16), (float)(int8_t)(w0 >> 24));
+    r[2] = high_halves((float)(int8_t)w1, (float)(int8_t)(w1 >> 8));
+    r[3] = high_halves((float)(int8_t)(w1 >> 16), (float)(int8_t)(w1 >> 24));
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// code / 16 of the low half of byte I
+template <int I>
+__device__ __forceinline__ float nibble(uint32_t w) { return __builtin_amdgcn_cvt_off_f32_i4((w >> 8 * I) & 0xFFu); }
+
+__device__ __forceinline__ uint32_t upper_nibbles(uint32_t w) {
+    uint32_t h = w >> 4;
+    asm("" : "+v"(h));                  // kept apart from the byte shifts, which the conversion then does by itself
+    return h;
+}
+
+// The low halves of eight bytes as bf16, code / 16 (exact).
+__device__ __forceinline__ bf16x8 nibbles_to_bf16(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    r[0] = high_halves(nibble<0>(w0), nibble<1>(w0));
+    r[1] = high_halves(nibble<2>(w0), nibble<3>(w0));
+    r[2] = high_halves(nibble<0>(w1), nibble<1>(w1));
+    r[3] = high_halves(nibble<2>(w1), nibble<3>(w1));
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// Four bytes' halves in order (low, high of byte 0, ...) as bf16, code / 16 (exact).
+__device__ __forceinline__ bf16x8 word_to_bf16(uint32_t w) {
+    const uint32_t h = upper_nibbles(w);
+    u32x4 r;
+    r[0] = high_halves(nibble<0>(w), nibble<0>(h));
+    r[1] = high_halves(nibble<1>(w), nibble<1>(h));
+    r[2] = high_halves(nibble<2>(w), nibble<2>(h));
+    r[3] = high_halves(nibble<3>(w), nibble<3>(h));
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// Eight fp32 values as PARTS bf16 operands: rounded (1), or cut into three parts of eight bits each, exactly.
+template <int PARTS>
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]) {
+    if constexpr (PARTS == 1) {
+        u32x4 r;
+        for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2_rne(x[2 * i], x[2 * i + 1]);
+        out[0] = __builtin_bit_cast(bf16x8, r);
+    } else {
+        float rest[8];
+        for (int i = 0; i < 8; ++i) rest[i] = x[i];
+        for (int p = 0; p < PARTS; ++p) {
+            u32x4 r;
+            for (int i = 0; i < 4; ++i) r[i] = high_halves(rest[2 * i], rest[2 * i + 1]);
+            out[p] = __builtin_bit_cast(bf16x8, r);
+            for (int i = 0; i < 8; ++i) rest[i] -= __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int WORDS>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* to) {
+    static_assert(WORDS == 1 || WORDS == 2 || WORDS == 4);
+    if constexpr (WORDS == 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+        for (int i = 0; i < 4; ++i) to[i] = v[i];
+    } else if constexpr (WORDS == 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+        to[0] = v[0], to[1] = v[1];
+    } else {
+        to[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// Visible tokens [first, n) of a request and the blocks that hold them (one at least, so that its output is written).
+struct Visible {
+    uint32_t first, n;
+    __device__ uint32_t block() const { return first / kBlockTokens; }
+    __device__ uint32_t blocks() const {
+        const uint32_t end = (n + kBlockTokens - 1) / kBlockTokens;
+        return end > block() ? end - block() : 1u;
+    }
+};
+
+__device__ __forceinline__ Visible visible(const AttentionKernelArgs& a, int r) {
+    const int32_t given = a.lengths[r];
+    Visible v;
+    v.n = given < 0 ? 0u : min((uint32_t)given, a.max_tokens);
+    v.first = a.window > 0 && (int64_t)v.n > a.window ? v.n - (uint32_t)a.window : 0u;
+    return v;
+}
+
+template <int NC, int BITS, int PARTS>
+struct AttentionTraits {
+    static constexpr int kDp = 32 * NC;
+    static constexpr int kRow = kDp * BITS / 8;                     // bytes of a key
+    static constexpr int kWordsPerChunk = BITS / 4;                 // of a lane's eight dimensions
+    // chunks whose dimensions lie side by side in a lane, for loads of 16 bytes
+    static constexpr int kSide = BITS == 16 ? 1 : BITS == 8 ? (NC % 2 ? 1 : 2) : NC % 4 == 0 ? 4 : NC % 2 == 0 ? 2 : 1;
+    static constexpr int kKeyLoads = NC / kSide;
+    static constexpr int kKeyLoadWords = kSide * kWordsPerChunk;
+    // neighbouring dimensions whose value octets a lane loads together
+    static constexpr int kDims = BITS == 16 ? 1 : BITS == 8 ? 2 : NC % 2 ? 2 : 4;
+    static constexpr int kValueLoads = 2 * NC / kDims;
+    static constexpr int kValueLoadWords = kDims * BITS / 4;
+    static constexpr int kRawWords = 2 * NC * kWordsPerChunk * 2;
+    static constexpr bool kAhead = kRawWords <= 64;                 // the next block's loads fit beside this one's
+};
+
+// What a lane holds of 32 tokens.
+template <int NC, int BITS, int PARTS>
+struct Block {
+    using Tr = AttentionTraits<NC, BITS, PARTS>;
+    uint32_t k[2][NC * Tr::kWordsPerChunk];
+    uint32_t v[2 * NC * Tr::kWordsPerChunk];
+    float ks[8], vs[8];
+    uint32_t seen;                                                  // of the tokens 8 (l / 16) + j: bit j
+    bool whole;                                                     // every token of the 32 is seen
+};
+
+template <int NC, int BITS, int PARTS>
+__device__ __forceinline__ void load_block(const AttentionKernelArgs& a, const int32_t* table, const Visible& vis,
+                                           uint32_t t0, const uint8_t* head, int lane, Block<NC, BITS, PARTS>& b) {
+    using Tr = AttentionTraits<NC, BITS, PARTS>;
+    const int m = lane & 15, quarter = lane >> 4;
+    const uint32_t t1 = t0 + 16;
+    const uint32_t j0 = (__umulhi(t0, a.page_mul) + t0) >> a.page_shift, j1 = (__umulhi(t1, a.page_mul) + t1) >> a.page_shift;
+    int32_t p0 = -1, p1 = -1;
+    if (t0 < vis.n) p0 = table[j0];
+    if (t1 < vis.n) p1 = table[j1];
+    const bool ok0 = (uint32_t)p0 < a.n_pages, ok1 = (uint32_t)p1 < a.n_pages;
+    // a half without a page reads page 0 and is masked
+    const uint32_t s0 = ok0 ? t0 - j0 * a.page_size : 0u, s1 = ok1 ? t1 - j1 * a.page_size : 0u;
+    const uint8_t* block0 = head + (ok0 ? p0 : 0) * a.page_stride;
+    const uint8_t* block1 = head + (ok1 ? p1 : 0) * a.page_stride;
+    const uint32_t part = (uint32_t)a.page_size * Tr::kRow;
+    b.whole = ok0 && ok1 && t0 >= vis.first && t0 + 32 <= vis.n;
+    const bool key_second = m >= 8, value_second = quarter >= 2;
+    {
+        const uint8_t* p = (key_second ? block1 : block0) + (key_second ? s1 : s0) * Tr::kRow +
+                           (8 * ((m >> 2) & 1) + (m & 3)) * Tr::kRow + quarter * Tr::kKeyLoadWords * 4;
+        for (int T = 0; T < 2; ++T)
+            for (int i = 0; i < Tr::kKeyLoads; ++i)
+                load_words<Tr::kKeyLoadWords>(p + 4 * T * Tr::kRow + i * Tr::kKeyLoadWords * 16, &b.k[T][i * Tr::kKeyLoadWords]);
+    }
+    const uint8_t* block = value_second ? block1 : block0;
+    const uint32_t slot = (value_second ? s1 : s0) + 8 * (quarter & 1);
+    if constexpr (BITS < 16) {
+        const uint8_t* p = block + 2 * part + 4 * slot;
+        for (int i = 0; i < 2; ++i) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p + 16 * i);
+            const f32x4 y = *reinterpret_cast<const f32x4*>(p + 16 * i + 4 * a.page_size);
+            for (int j = 0; j < 4; ++j) b.ks[4 * i + j] = x[j], b.vs[4 * i + j] = y[j];
+        }
+    }
+    {
+        const uint8_t* p = block + part + (slot / 8 * Tr::kDp + m * Tr::kDims) * BITS;
+        for (int i = 0; i < Tr::kValueLoads; ++i)
+            load_words<Tr::kValueLoadWords>(p + i * 16 * Tr::kDims * BITS, &b.v[i * Tr::kValueLoadWords]);
+    }
+    if (!b.whole) {
+        const uint32_t t = t0 + 8 * quarter;
+        uint32_t seen = 0;
+        for (uint32_t j = 0; j < 8; ++j) seen |= (uint32_t)(t + j >= vis.first && t + j < vis.n) << j;
+        b.seen = (value_second ? ok1 : ok0) ? seen : 0u;
+    }
+}
+
+template <int NC, int BITS, int PARTS>
+__device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q)[NC][PARTS], float to_log2, float& m, float& l,
+                                     f32x4 (&o)[2 * NC]) {
+    using Tr = AttentionTraits<NC, BITS, PARTS>;
+    f32x4 s[2];
+    for (int T = 0; T < 2; ++T) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t* w = &b.k[T][c * Tr::kWordsPerChunk];
+            bf16x8 k;
+            if constexpr (BITS == 16) k = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+            else if constexpr (BITS == 8) k = bytes_to_bf16(w[0], w[1]);
+            else k = word_to_bf16(w[0]);
+            for (int p = PARTS - 1; p >= 0; --p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[c][p], acc, 0, 0, 0);
+        }
+        s[T] = acc;
+    }
+    float x[8];
+    for (int j = 0; j < 8; ++j) {
+        x[j] = s[j / 4][j % 4];
+        if constexpr (BITS < 16) x[j] *= b.ks[j];
+        x[j] *= to_log2;
+    }
+    if (!b.whole) {
+        for (int j = 0; j < 8; ++j) x[j] = b.seen >> j & 1 ? x[j] : -INFINITY;
+        if constexpr (BITS == 16) {                                 // what an unseen slot holds may not be a number
+            u32x4 mask;
+            for (int i = 0; i < 4; ++i)
+                mask[i] = (b.seen >> 2 * i & 1 ? 0xFFFFu : 0u) | (b.seen >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+            for (int i = 0; i < 8 * NC; ++i) b.v[i] &= mask[i & 3];
+        }
+    }
+    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    top = max_of_quarters(top);
+    if (__any(top > m + kRaise)) {
+        const float now = fmaxf(m, top), base = now == -INFINITY ? 0.0f : now;
+        const float keep = __builtin_amdgcn_exp2f(m - base);
+        m = now;
+        l *= keep;
+        for (int i = 0; i < 2 * NC; ++i) o[i] *= keep;
+    }
+    const float base = m == -INFINITY ? 0.0f : m;
+    float p8[8];
+    for (int j = 0; j < 8; ++j) {
+        const float p = __builtin_amdgcn_exp2f(x[j] - base);
+        l += p;
+        p8[j] = p;
+        if constexpr (BITS < 16) p8[j] *= b.vs[j];
+    }
+    if constexpr (BITS < 16)
+        if (!b.whole)
+            for (int j = 0; j < 8; ++j) p8[j] = b.seen >> j & 1 ? p8[j] : 0.0f;
+    bf16x8 p[PARTS];
+    split8<PARTS>(p8, p);
+    for (int i = 0; i < Tr::kValueLoads; ++i) {
+        const uint32_t* w = &b.v[i * Tr::kValueLoadWords];
+        for (int e = 0; e < Tr::kDims; ++e) {
+            bf16x8 v;
+            if constexpr (BITS == 16) v = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+            else if constexpr (BITS == 8) v = bytes_to_bf16(w[2 * e], w[2 * e + 1]);
+            else if (e % 2 == 0) v = nibbles_to_bf16(w[e], w[e + 1]);
+            else v = nibbles_to_bf16(upper_nibbles(w[e - 1]), upper_nibbles(w[e]));
+            f32x4& acc = o[i * Tr::kDims + e];
+            for (int part = PARTS - 1; part >= 0; --part) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[part], acc, 0, 0, 0);
+        }
+    }
+}
+
+template <typename E, int NC, int BITS, int PARTS>
+__global__ __launch_bounds__(256, 2) void attention_kernel(AttentionKernelArgs a) {
+    using Tr = AttentionTraits<NC, BITS, PARTS>;
+    constexpr int kJoinDims = NC <= 4 ? Tr::kDp : NC == 6 ? 64 : 128;   // dimensions that the waves join at a time
+    constexpr int kPitch = kJoinDims + 4;
+    __shared__ __attribute__((aligned(16))) float joined[4][kTileHeads][kPitch];
+    __shared__ float ml[4][kTileHeads][2];
+    __shared__ int64_t sums[4], found_base;
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int quarter = lane >> 4;
+
+    // the line of all blocks: a scan over the requests' blocks, `share` requests a thread
+    const int share = (a.R + 255) / 256, r_first = tid * share, r_end = min(a.R, r_first + share);
+    int64_t mine = 0;
+    for (int r = r_first; r < r_end; ++r) mine += visible(a, r).blocks();
+    int64_t upto = mine;
+    for (int i = 1; i < 64; i *= 2) {
+        const int64_t y = __shfl_up(upto, i);
+        if (lane >= i) upto += y;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) upto += sums[w];
+        total += sums[w];
+    }
+    total *= a.segments;
+    const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t chunk = max((int64_t)4, (even + 3) / 4 * 4);      // a block for each wave
+    const int64_t begin = chunk * blockIdx.x, end = min(begin + chunk, total);
+    AttentionRecord record = {-1, 0, 0, 0};
+    if (begin >= end) {
+        if (tid == 0) a.records[blockIdx.x] = record;
+        return;
+    }
+    const int64_t at = begin / a.segments;
+    if (mine > 0 && upto - mine <= at && at < upto) {
+        int64_t base = upto - mine;
+        int r = r_first;
+        for (;; ++r) {
+            const uint32_t n = visible(a, r).blocks();
+            if (at < base + n) break;
+            base += n;
+        }
+        found = r;
+        found_base = base;
+    }
+    __syncthreads();
+    int r = __builtin_amdgcn_readfirstlane(found);
+    int64_t base = found_base, pos = begin;
+
+    for (; pos < end; ++r) {
+        const Visible vis = visible(a, r);
+        const int64_t blocks = vis.blocks(), inside = pos - a.segments * base;
+        int segment = (int)(inside / blocks);
+        int64_t off = inside - segment * blocks;
+        base += blocks;
+        for (; segment < a.segments && pos < end; ++segment, off = 0) {
+            const int count = (int)min(blocks - off, end - pos);
+            const int h = segment / a.tiles, tile = segment - h * a.tiles;
+            const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
+
+            // q of the tile's heads as B operands, times a power of two that keeps every sum in range
+            bf16x8 q[NC][PARTS];
+            float to_log2;
+            {
+                const int n = lane & 15;
+                const E* x = static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs;
+                float y[NC][8];
+                uint32_t most = 0;
+                for (int c = 0; c < NC; ++c) {
+                    const int d = 32 * Tr::kSide * (c / Tr::kSide) + 8 * Tr::kSide * quarter + 8 * (c % Tr::kSide);
+                    for (int i = 0; i < 8; ++i) {
+                        y[c][i] = n < heads && d < a.D ? (float)x[d + i] : 0.0f;
+                        most = max(most, __float_as_uint(y[c][i]) & 0x7FFFFFFFu);
+                    }
+                }
+                most = max(most, (uint32_t)__shfl_xor((int)most, 16));
+                most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+                const int e = most == 0 || most >= 0x7F800000u ? 0 : (int)(most >> 23) - 126;   // |q| 2^-e < 1
+                for (int c = 0; c < NC; ++c) {
+                    for (int i = 0; i < 8; ++i) y[c][i] = ldexpf(y[c][i], -e);
+                    split8<PARTS>(y[c], q[c]);
+                }
+                to_log2 = ldexpf(a.scale_log2e, e + (BITS == 4 ? 4 : 0));
+            }
+
+            f32x4 o[2 * NC];
+            for (int i = 0; i < 2 * NC; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            float m = -INFINITY, l = 0.0f;
+            if (vis.n > vis.first) {
+                const uint8_t* head = a.pages + h * a.head_stride;
+                const int32_t* table = a.table + r * a.ld_table;
+                const uint32_t first = (vis.block() + (uint32_t)off) * kBlockTokens;
+                if constexpr (Tr::kAhead) {
+                    Block<NC, BITS, PARTS> now, next;
+                    int i = wave;
+                    if (i < count) load_block(a, table, vis, first + i * kBlockTokens, head, lane, now);
+                    for (; i < count; i += 4) {
+                        if (i + 4 < count) load_block(a, table, vis, first + (i + 4) * kBlockTokens, head, lane, next);
+                        step<NC, BITS, PARTS>(now, q, to_log2, m, l, o);
+                        now = next;
+                    }
+                } else {
+                    Block<NC, BITS, PARTS> now;
+                    for (int i = wave; i < count; i += 4) {
+                        load_block(a, table, vis, first + i * kBlockTokens, head, lane, now);
+                        step<NC, BITS, PARTS>(now, q, to_log2, m, l, o);
+                    }
+                }
+            }
+
+            // the four waves' sums joined
+            l = sum_of_quarters(l);
+            const int n = lane & 15;
+            if (quarter == 0) ml[wave][n][0] = m, ml[wave][n][1] = l;
+            const bool starts = off == 0, ends = off + count == blocks;
+            const int64_t place = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+            constexpr int kRounds = Tr::kDp / kJoinDims, kPer = Tr::kValueLoads / kRounds;
+            static_assert(kPer * kRounds == Tr::kValueLoads && kPer * 16 * Tr::kDims == kJoinDims);
+            for (int round = 0; round < kRounds; ++round) {
+                for (int i = 0; i < kPer; ++i) {
+                    const f32x4* from = &o[(round * kPer + i) * Tr::kDims];
+                    float* to = &joined[wave][n][i * 16 * Tr::kDims + quarter * 4 * Tr::kDims];
+                    for (int j = 0; j < Tr::kDims; ++j) {           // dimension Tr::kDims * row + tile, four at a time
+                        f32x4 y;
+                        for (int z = 0; z < 4; ++z) y[z] = from[(4 * j + z) % Tr::kDims][(4 * j + z) / Tr::kDims];
+                        *reinterpret_cast<f32x4*>(to + 4 * j) = y;
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < heads * (kJoinDims / 4); i += 256) {
+                    const int row = i / (kJoinDims / 4), d4 = i % (kJoinDims / 4), d = round * kJoinDims + 4 * d4;
+                    float top = ml[0][row][0];
+                    for (int w = 1; w < 4; ++w) top = fmaxf(top, ml[w][row][0]);
+                    const float from = top == -INFINITY ? 0.0f : top;
+                    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float whole = 0.0f;
+                    for (int w = 0; w < 4; ++w) {
+                        const float keep = __builtin_amdgcn_exp2f(ml[w][row][0] - from);
+                        whole += keep * ml[w][row][1];
+                        sum += keep * *reinterpret_cast<const f32x4*>(&joined[w][row][4 * d4]);
+                    }
+                    if constexpr (BITS == 4) sum *= 16.0f;
+                    if (starts && ends) {
+                        E* to = static_cast<E*>(a.out) + r * a.o_rs + (hq + row) * a.o_hs + d;
+                        for (int z = 0; z < 4; ++z)
+                            if (d < a.D) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] / whole);
+                        if (a.lse && d == 0)
+                            a.lse[(int64_t)r * a.Hq + hq + row] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+                    } else {
+                        *reinterpret_cast<f32x4*>(a.partial_o + (place * a.rows + row) * Tr::kDp + d) = sum;
+                        if (d == 0) {
+                            a.partial_ml[(place * a.rows + row) * 2] = top;
+                            a.partial_ml[(place * a.rows + row) * 2 + 1] = whole;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            if (starts && !ends) record = {r, segment, (int32_t)((pos + blocks - 1) / chunk), 0};
+            pos += count;
+        }
+    }
+    if (tid == 0) a.records[blockIdx.x] = record;
+}
+
+template <int BITS>
+hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, int workgroups, hipStream_t stream) {
+    const auto pick = [&](auto e, auto parts) {
+        using E = decltype(e);
+        constexpr int P = decltype(parts)::value;
+        switch (chunks) {
+            case 2: return attention_kernel<E, 2, BITS, P>;
+            case 3: return attention_kernel<E, 3, BITS, P>;
+            case 4: return attention_kernel<E, 4, BITS, P>;
+            case 6: return attention_kernel<E, 6, BITS, P>;
+            default: return attention_kernel<E, 8, BITS, P>;
+        }
+    };
+    auto* kernel = f32 ? pick(0.0f, std::integral_constant<int, 3>{}) : pick((__bf16)0.0f, std::integral_constant<int, 1>{});
+    kernel<<<dim3((unsigned)workgroups), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace gptq
