@@ -10,43 +10,68 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// A wave joins one query head of the segment that begins in workgroup blockIdx.x and ends in a later one.
+// A workgroup joins one query head of the segment that begins in workgroup blockIdx.x and ends in a later one: the parts'
+// weights first, then their rows, Dp / 4 threads a row and as many rows at a time as there are threads for.
 template <typename E>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
+    __shared__ float weights[kMaxWorkgroups], most[4], wholes[4];
+    __shared__ f32x4 sums[256];
     const AttentionRecord rec = a.records[blockIdx.x];
     if (rec.request < 0) return;
-    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
+    const int tid = threadIdx.x, wave = tid >> 6, row = blockIdx.y;
     const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
     const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads + row;
     if (row >= heads) return;
     const int first = blockIdx.x, parts = rec.last - first + 1;
     const auto place = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
+    constexpr int kEach = kMaxWorkgroups / 256;
+    f32x2 ml[kEach];
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 64) top = fmaxf(top, a.partial_ml[place(i) * 2]);
-    for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
-    const float from = top == -INFINITY ? 0.0f : top;
-    float whole = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < parts; ++i) {
-        const int64_t p = place(i);
-        const float keep = __builtin_amdgcn_exp2f(a.partial_ml[p * 2] - from);
-        whole += keep * a.partial_ml[p * 2 + 1];
-        for (int z = 0; z < 4; ++z)
-            if (lane + 64 * z < Dp) o[z] += keep * a.partial_o[p * Dp + lane + 64 * z];
+    for (int i = 0; i < kEach; ++i) {
+        const int p = tid + 256 * i;
+        ml[i] = p < parts ? *reinterpret_cast<const f32x2*>(a.partial_ml + place(p) * 2) : f32x2{-INFINITY, 0.0f};
+        top = fmaxf(top, ml[i][0]);
     }
-    E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs;
-    for (int z = 0; z < 4; ++z)
-        if (lane + 64 * z < a.D) to[lane + 64 * z] = (E)(whole == 0.0f ? 0.0f : o[z] / whole);
-    if (a.lse && lane == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
-}
+    for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
+    if ((tid & 63) == 0) most[wave] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    const float from = top == -INFINITY ? 0.0f : top;
+    float whole = 0.0f;
+    for (int i = 0; i < kEach; ++i) {
+        const float keep = __builtin_amdgcn_exp2f(ml[i][0] - from);
+        whole += keep * ml[i][1];
+        if (tid + 256 * i < parts) weights[tid + 256 * i] = keep;
+    }
+    for (int i = 32; i; i >>= 1) whole += __shfl_xor(whole, i);
+    if ((tid & 63) == 0) wholes[wave] = whole;
+    __syncthreads();
+    whole = wholes[0] + wholes[1] + wholes[2] + wholes[3];
 
-constexpr int kWorkgroups = 1024;
+    const int quads = Dp / 4, at_once = 256 / quads, line = tid / quads, quad = tid - line * quads;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (line < at_once) {
+#pragma unroll 8
+        for (int p = line; p < parts; p += at_once)
+            sum += weights[p] * *reinterpret_cast<const f32x4*>(a.partial_o + place(p) * Dp + 4 * quad);
+    }
+    sums[tid] = sum;
+    __syncthreads();
+    const int d = 4 * tid;
+    if (d < a.D) {
+        for (int i = 1; i < at_once; ++i) sum += sums[tid + i * quads];
+        E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs + d;
+        for (int z = 0; z < 4; ++z) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] / whole);
+        if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+    }
+}
 
 int rows_of(int64_t Hq, int64_t H) { return (int)std::min<int64_t>(Hq / H, kTileHeads); }
 
 void carve(Carver& c, AttentionKernelArgs& k, int Dp) {
-    k.records = c.take<AttentionRecord>(kWorkgroups);
-    k.partial_ml = c.take<float>((size_t)2 * kWorkgroups * k.rows * 2);
-    k.partial_o = c.take<float>((size_t)2 * kWorkgroups * k.rows * Dp);
+    k.records = c.take<AttentionRecord>(kMaxWorkgroups);
+    k.partial_ml = c.take<float>((size_t)2 * kMaxWorkgroups * k.rows * 2);
+    k.partial_o = c.take<float>((size_t)2 * kMaxWorkgroups * k.rows * Dp);
 }
 
 }  // namespace
@@ -79,11 +104,11 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.rows = rows_of(a.Hq, a.H);
     Carver c(workspace);
     carve(c, k, Dp);
-    const hipError_t e = a.pages.bits == 16  ? launch_attention<16>(k, Dp / 32, a.f32, kWorkgroups, stream)
-                         : a.pages.bits == 8 ? launch_attention<8>(k, Dp / 32, a.f32, kWorkgroups, stream)
-                                             : launch_attention<4>(k, Dp / 32, a.f32, kWorkgroups, stream);
+    const hipError_t e = a.pages.bits == 16  ? launch_attention<16>(k, Dp / 32, a.f32, stream)
+                         : a.pages.bits == 8 ? launch_attention<8>(k, Dp / 32, a.f32, stream)
+                                             : launch_attention<4>(k, Dp / 32, a.f32, stream);
     if (e != hipSuccess) return e;
-    const dim3 grid(kWorkgroups, (unsigned)ceil_div(k.rows, 4));
+    const dim3 grid((unsigned)attention_workgroups(Dp / 32, a.pages.bits, a.f32 ? 3 : 1), (unsigned)k.rows);
     if (a.f32) attention_join_kernel<float><<<grid, 256, 0, stream>>>(k, Dp);
     else attention_join_kernel<__bf16><<<grid, 256, 0, stream>>>(k, Dp);
     return hipGetLastError();

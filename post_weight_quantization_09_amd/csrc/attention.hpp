@@ -39,8 +39,19 @@ struct AttentionKernelArgs {
     AttentionRecord* records;
 };
 
-// chunks: stored head size / 32.  Launches `workgroups` workgroups.
+// Waves of a SIMD that the registers are laid out for.
+constexpr int attention_waves(int chunks, int bits, int parts) {
+    if (parts == 1 && chunks <= 4) return bits == 16 && chunks == 4 ? 2 : 3;
+    return parts == 1 || chunks <= 4 ? 2 : 1;
+}
+
+// Workgroups of a launch: as many as are resident on 256 CUs, a wave of each on every SIMD.
+constexpr int attention_workgroups(int chunks, int bits, int parts) { return 256 * attention_waves(chunks, bits, parts); }
+
+constexpr int kMaxWorkgroups = 1024;
+
+// chunks: stored head size / 32.
 template <int BITS>
-hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, int workgroups, hipStream_t stream);
+hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, hipStream_t stream);
 
 }  // namespace gptq

@@ -5,6 +5,6 @@
 
 namespace gptq {
 
-template hipError_t launch_attention<8>(const AttentionKernelArgs&, int, bool, int, hipStream_t);
+template hipError_t launch_attention<8>(const AttentionKernelArgs&, int, bool, hipStream_t);
 
 }  // namespace gptq

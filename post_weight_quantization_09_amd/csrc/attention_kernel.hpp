@@ -108,6 +108,33 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
     }
 }
 
+// Eight elements of any alignment that their type has, as they are stored, and as fp32.
+template <typename E>
+struct Eight;
+template <>
+struct Eight<__bf16> {
+    typedef u32x4 __attribute__((aligned(2))) any;
+    u32x4 v;
+    __device__ void load(const __bf16* p) { v = *reinterpret_cast<const any*>(p); }
+    __device__ float get(int i) const { return i % 2 ? bf16hi_to_f32(v[i / 2]) : bf16lo_to_f32(v[i / 2]); }
+    __device__ void clear() { v = u32x4{0, 0, 0, 0}; }
+};
+template <>
+struct Eight<float> {
+    typedef f32x4 __attribute__((aligned(4))) any;
+    f32x4 v[2];
+    __device__ void load(const float* p) { v[0] = reinterpret_cast<const any*>(p)[0], v[1] = reinterpret_cast<const any*>(p)[1]; }
+    __device__ float get(int i) const { return v[i / 4][i % 4]; }
+    __device__ void clear() { v[0] = v[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+};
+
+// a / b where the quotient is below 2^20: from a reciprocal, put right by one where that was needed.
+__device__ __forceinline__ int small_quotient(int64_t a, int64_t b) {
+    int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b));
+    const int64_t rest = a - q * b;
+    return rest < 0 ? q - 1 : rest >= b ? q + 1 : q;
+}
+
 template <int WORDS>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* to) {
     static_assert(WORDS == 1 || WORDS == 2 || WORDS == 4);
@@ -132,6 +159,10 @@ struct Visible {
     }
 };
 
+// A segment's length on the line: its blocks, and what beginning with it costs beside them (places before its blocks, at
+// which nothing is done), so that workgroups with many short segments get fewer blocks.
+constexpr uint32_t kBeginCost = 4;
+
 __device__ __forceinline__ Visible visible(const AttentionKernelArgs& a, int r) {
     const int32_t given = a.lengths[r];
     Visible v;
@@ -153,8 +184,6 @@ struct AttentionTraits {
     static constexpr int kDims = BITS == 16 ? 1 : BITS == 8 ? 2 : NC % 2 ? 2 : 4;
     static constexpr int kValueLoads = 2 * NC / kDims;
     static constexpr int kValueLoadWords = kDims * BITS / 4;
-    static constexpr int kRawWords = 2 * NC * kWordsPerChunk * 2;
-    static constexpr bool kAhead = kRawWords <= 64;                 // the next block's loads fit beside this one's
 };
 
 // What a lane holds of 32 tokens.
@@ -285,48 +314,50 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
 }
 
 template <typename E, int NC, int BITS, int PARTS>
-__global__ __launch_bounds__(256, 2) void attention_kernel(AttentionKernelArgs a) {
+__global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attention_kernel(AttentionKernelArgs a) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     constexpr int kJoinDims = NC <= 4 ? Tr::kDp : NC == 6 ? 64 : 128;   // dimensions that the waves join at a time
     constexpr int kPitch = kJoinDims + 4;
     __shared__ __attribute__((aligned(16))) float joined[4][kTileHeads][kPitch];
     __shared__ float ml[4][kTileHeads][2];
-    __shared__ int64_t sums[4], found_base;
+    __shared__ uint32_t sums[4], found_base;
     __shared__ int found;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quarter = lane >> 4;
 
     // the line of all blocks: a scan over the requests' blocks, `share` requests a thread
     const int share = (a.R + 255) / 256, r_first = tid * share, r_end = min(a.R, r_first + share);
-    int64_t mine = 0;
-    for (int r = r_first; r < r_end; ++r) mine += visible(a, r).blocks();
-    int64_t upto = mine;
+    uint32_t mine = 0;
+    for (int r = r_first; r < r_end; ++r) mine += visible(a, r).blocks() + kBeginCost;
+    uint32_t upto = mine;
     for (int i = 1; i < 64; i *= 2) {
-        const int64_t y = __shfl_up(upto, i);
+        const uint32_t y = __shfl_up(upto, i);
         if (lane >= i) upto += y;
     }
     if (lane == 63) sums[wave] = upto;
     __syncthreads();
-    int64_t total = 0;
+    uint32_t all = 0;
     for (int w = 0; w < 4; ++w) {
         if (w < wave) upto += sums[w];
-        total += sums[w];
+        all += sums[w];
     }
-    total *= a.segments;
-    const int64_t even = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t chunk = max((int64_t)4, (even + 3) / 4 * 4);      // a block for each wave
+    const int64_t total = (int64_t)all * a.segments;
+    // a block at least for each wave (the double's quotient is off by one at most, which one more place makes up for)
+    const int64_t chunk = max((int64_t)(kBeginCost + 4), (int64_t)((double)total / gridDim.x) + 2);
     const int64_t begin = chunk * blockIdx.x, end = min(begin + chunk, total);
     AttentionRecord record = {-1, 0, 0, 0};
     if (begin >= end) {
         if (tid == 0) a.records[blockIdx.x] = record;
         return;
     }
-    const int64_t at = begin / a.segments;
-    if (mine > 0 && upto - mine <= at && at < upto) {
-        int64_t base = upto - mine;
+    uint32_t at = (uint32_t)((double)begin / a.segments);           // off by one at most, as begin < 2^42
+    if ((int64_t)at * a.segments > begin) --at;
+    else if ((int64_t)(at + 1) * a.segments <= begin) ++at;
+    if (upto - mine <= at && at < upto) {
+        uint32_t base = upto - mine;
         int r = r_first;
         for (;; ++r) {
-            const uint32_t n = visible(a, r).blocks();
+            const uint32_t n = visible(a, r).blocks() + kBeginCost;
             if (at < base + n) break;
             base += n;
         }
@@ -335,40 +366,53 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttentionKernelArgs a
     }
     __syncthreads();
     int r = __builtin_amdgcn_readfirstlane(found);
-    int64_t base = found_base, pos = begin;
+    int64_t base = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)found_base) * a.segments, pos = begin;
 
     for (; pos < end; ++r) {
         const Visible vis = visible(a, r);
-        const int64_t blocks = vis.blocks(), inside = pos - a.segments * base;
-        int segment = (int)(inside / blocks);
-        int64_t off = inside - segment * blocks;
-        base += blocks;
-        for (; segment < a.segments && pos < end; ++segment, off = 0) {
-            const int count = (int)min(blocks - off, end - pos);
+        const int64_t length = (int64_t)vis.blocks() + kBeginCost, inside = pos - base;
+        int segment = small_quotient(inside, length);
+        int64_t from = inside - segment * length;
+        base += a.segments * length;
+        for (; segment < a.segments && pos < end; ++segment, from = 0) {
+            // places [from, upto) of the segment's line; the first kBeginCost of it are no blocks
+            const int64_t upto = min(length, from + (end - pos));
+            const int off = (int)max(from - kBeginCost, (int64_t)0), count = (int)(upto - kBeginCost) - off;
+            const bool starts = off == 0, ends = upto == length;
+            pos += upto - from;
+            if (count <= 0) continue;
             const int h = segment / a.tiles, tile = segment - h * a.tiles;
             const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
 
-            // q of the tile's heads as B operands, times a power of two that keeps every sum in range
+            // the wave's first block, then q of the tile's heads as B operands, times a power of two that keeps every sum in range
+            const uint8_t* head = a.pages + h * a.head_stride;
+            const int32_t* table = a.table + r * a.ld_table;
+            const uint32_t first = (vis.block() + (uint32_t)off) * kBlockTokens;
+            const int todo = vis.n > vis.first ? count : 0;
+            Block<NC, BITS, PARTS> b;
+            if (wave < todo) load_block(a, table, vis, first + wave * kBlockTokens, head, lane, b);
             bf16x8 q[NC][PARTS];
             float to_log2;
             {
                 const int n = lane & 15;
                 const E* x = static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs;
-                float y[NC][8];
+                Eight<E> y[NC];
                 uint32_t most = 0;
                 for (int c = 0; c < NC; ++c) {
                     const int d = 32 * Tr::kSide * (c / Tr::kSide) + 8 * Tr::kSide * quarter + 8 * (c % Tr::kSide);
-                    for (int i = 0; i < 8; ++i) {
-                        y[c][i] = n < heads && d < a.D ? (float)x[d + i] : 0.0f;
-                        most = max(most, __float_as_uint(y[c][i]) & 0x7FFFFFFFu);
-                    }
+                    const bool in = n < heads && d < a.D;           // a row is read from its start where nothing of it is wanted
+                    y[c].load(x + (in ? d : 0));
+                    if (!in) y[c].clear();
                 }
+                for (int c = 0; c < NC; ++c)
+                    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[c].get(i)) & 0x7FFFFFFFu);
                 most = max(most, (uint32_t)__shfl_xor((int)most, 16));
                 most = max(most, (uint32_t)__shfl_xor((int)most, 32));
                 const int e = most == 0 || most >= 0x7F800000u ? 0 : (int)(most >> 23) - 126;   // |q| 2^-e < 1
                 for (int c = 0; c < NC; ++c) {
-                    for (int i = 0; i < 8; ++i) y[c][i] = ldexpf(y[c][i], -e);
-                    split8<PARTS>(y[c], q[c]);
+                    float z[8];
+                    for (int i = 0; i < 8; ++i) z[i] = ldexpf(y[c].get(i), -e);
+                    split8<PARTS>(z, q[c]);
                 }
                 to_log2 = ldexpf(a.scale_log2e, e + (BITS == 4 ? 4 : 0));
             }
@@ -376,33 +420,16 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttentionKernelArgs a
             f32x4 o[2 * NC];
             for (int i = 0; i < 2 * NC; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             float m = -INFINITY, l = 0.0f;
-            if (vis.n > vis.first) {
-                const uint8_t* head = a.pages + h * a.head_stride;
-                const int32_t* table = a.table + r * a.ld_table;
-                const uint32_t first = (vis.block() + (uint32_t)off) * kBlockTokens;
-                if constexpr (Tr::kAhead) {
-                    Block<NC, BITS, PARTS> now, next;
-                    int i = wave;
-                    if (i < count) load_block(a, table, vis, first + i * kBlockTokens, head, lane, now);
-                    for (; i < count; i += 4) {
-                        if (i + 4 < count) load_block(a, table, vis, first + (i + 4) * kBlockTokens, head, lane, next);
-                        step<NC, BITS, PARTS>(now, q, to_log2, m, l, o);
-                        now = next;
-                    }
-                } else {
-                    Block<NC, BITS, PARTS> now;
-                    for (int i = wave; i < count; i += 4) {
-                        load_block(a, table, vis, first + i * kBlockTokens, head, lane, now);
-                        step<NC, BITS, PARTS>(now, q, to_log2, m, l, o);
-                    }
-                }
+            for (int i = wave; i < todo;) {
+                step<NC, BITS, PARTS>(b, q, to_log2, m, l, o);
+                i += 4;
+                if (i < todo) load_block(a, table, vis, first + i * kBlockTokens, head, lane, b);
             }
 
             // the four waves' sums joined
             l = sum_of_quarters(l);
             const int n = lane & 15;
             if (quarter == 0) ml[wave][n][0] = m, ml[wave][n][1] = l;
-            const bool starts = off == 0, ends = off + count == blocks;
             const int64_t place = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
             constexpr int kRounds = Tr::kDp / kJoinDims, kPer = Tr::kValueLoads / kRounds;
             static_assert(kPer * kRounds == Tr::kValueLoads && kPer * 16 * Tr::kDims == kJoinDims);
@@ -446,28 +473,31 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttentionKernelArgs a
                 }
                 __syncthreads();
             }
-            if (starts && !ends) record = {r, segment, (int32_t)((pos + blocks - 1) / chunk), 0};
-            pos += count;
+            if (starts && !ends) record = {r, segment, small_quotient(pos - upto + length - 1, chunk), 0};
         }
     }
     if (tid == 0) a.records[blockIdx.x] = record;
 }
 
 template <int BITS>
-hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, int workgroups, hipStream_t stream) {
-    const auto pick = [&](auto e, auto parts) {
+hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, hipStream_t stream) {
+    const auto launch = [&](auto e, auto parts, auto nc) {
         using E = decltype(e);
-        constexpr int P = decltype(parts)::value;
+        constexpr int P = decltype(parts)::value, NC = decltype(nc)::value;
+        // as many workgroups as are resident: every one gets its share of the line at once
+        attention_kernel<E, NC, BITS, P><<<dim3((unsigned)attention_workgroups(NC, BITS, P)), 256, 0, stream>>>(a);
+    };
+    const auto pick = [&](auto e, auto parts) {
         switch (chunks) {
-            case 2: return attention_kernel<E, 2, BITS, P>;
-            case 3: return attention_kernel<E, 3, BITS, P>;
-            case 4: return attention_kernel<E, 4, BITS, P>;
-            case 6: return attention_kernel<E, 6, BITS, P>;
-            default: return attention_kernel<E, 8, BITS, P>;
+            case 2: return launch(e, parts, std::integral_constant<int, 2>{});
+            case 3: return launch(e, parts, std::integral_constant<int, 3>{});
+            case 4: return launch(e, parts, std::integral_constant<int, 4>{});
+            case 6: return launch(e, parts, std::integral_constant<int, 6>{});
+            default: return launch(e, parts, std::integral_constant<int, 8>{});
         }
     };
-    auto* kernel = f32 ? pick(0.0f, std::integral_constant<int, 3>{}) : pick((__bf16)0.0f, std::integral_constant<int, 1>{});
-    kernel<<<dim3((unsigned)workgroups), 256, 0, stream>>>(a);
+    if (f32) pick(0.0f, std::integral_constant<int, 3>{});
+    else pick((__bf16)0.0f, std::integral_constant<int, 1>{});
     return hipGetLastError();
 }
 
