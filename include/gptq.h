@@ -578,7 +578,7 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  *   Q          device, R x Hq x D, dtype.   R 0..65536.   Hq a multiple of H, at most 1024.   scale: finite.
  *   table      device int32, the page of tokens [j page_size, (j + 1) page_size) of request r at table[r * ld_table + j],
  *              j < max_pages; tokens of a page outside [0, n_pages) are left out.   max_pages * page_size < 2^31,
- *              R * max_pages * page_size <= 2^36.
+ *              R (max_pages page_size / 32 + 8) H ceil(Hq / H / 16) < 2^31.
  *   lengths    device int32[R], clamped to [0, max_pages * page_size].
  *   out        device, R x Hq x D, dtype; not Q.   lse: NULL, or device fp32[R * Hq]: ln sum_t exp(scale q . k_t).
  *   workspace  device scratch of gptq_attention_workspace_bytes(R, Hq, H, D).

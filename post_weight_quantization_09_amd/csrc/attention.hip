@@ -10,38 +10,35 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// A workgroup joins one query head of the segment that begins in workgroup blockIdx.x and ends in a later one: the parts'
-// weights first, then their rows, Dp / 4 threads a row and as many rows at a time as there are threads for.
+// A workgroup joins one query head of a segment: the parts' weights first, then their rows, Dp / 4 threads a row and as many
+// rows at a time as there are threads for.
 template <typename E>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
-    __shared__ float weights[kMaxWorkgroups], most[4], wholes[4];
+    constexpr int kEach = kMaxPieces / 256;
+    __shared__ float weights[kMaxPieces], most[4], wholes[4];
     __shared__ f32x4 sums[256];
     const AttentionRecord rec = a.records[blockIdx.x];
-    if (rec.request < 0) return;
     const int tid = threadIdx.x, wave = tid >> 6, row = blockIdx.y;
+    if (rec.parts == 0) return;
     const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
-    const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads + row;
-    if (row >= heads) return;
-    const int first = blockIdx.x, parts = rec.last - first + 1;
-    const auto place = [&](int i) { return (2 * (int64_t)(first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
-    constexpr int kEach = kMaxWorkgroups / 256;
-    f32x2 ml[kEach];
+    if (row >= min(kTileHeads, a.group - tile * kTileHeads)) return;
+    const auto place = [&](int i) { return (uint64_t)((2 * (rec.first + i) + (i == 0 ? 1 : 0)) * a.rows + row); };
     float top = -INFINITY;
-    for (int i = 0; i < kEach; ++i) {
-        const int p = tid + 256 * i;
-        ml[i] = p < parts ? *reinterpret_cast<const f32x2*>(a.partial_ml + place(p) * 2) : f32x2{-INFINITY, 0.0f};
-        top = fmaxf(top, ml[i][0]);
+    for (int p = tid; p < rec.parts; p += 256) {
+        const float m = a.partial_ml[place(p) * 2];
+        weights[p] = m;
+        top = fmaxf(top, m);
     }
     for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
     if ((tid & 63) == 0) most[wave] = top;
     __syncthreads();
     top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-    const float from = top == -INFINITY ? 0.0f : top;
+    const float ref = top == -INFINITY ? 0.0f : top;
     float whole = 0.0f;
-    for (int i = 0; i < kEach; ++i) {
-        const float keep = __builtin_amdgcn_exp2f(ml[i][0] - from);
-        whole += keep * ml[i][1];
-        if (tid + 256 * i < parts) weights[tid + 256 * i] = keep;
+    for (int p = tid; p < rec.parts; p += 256) {
+        const float keep = __builtin_amdgcn_exp2f(weights[p] - ref);
+        whole += keep * a.partial_ml[place(p) * 2 + 1];
+        weights[p] = keep;
     }
     for (int i = 32; i; i >>= 1) whole += __shfl_xor(whole, i);
     if ((tid & 63) == 0) wholes[wave] = whole;
@@ -52,16 +49,17 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (line < at_once) {
 #pragma unroll 8
-        for (int p = line; p < parts; p += at_once)
+        for (int p = line; p < rec.parts; p += at_once)
             sum += weights[p] * *reinterpret_cast<const f32x4*>(a.partial_o + place(p) * Dp + 4 * quad);
     }
     sums[tid] = sum;
     __syncthreads();
-    const int d = 4 * tid;
+    const int d = 4 * tid, hq = h * a.group + tile * kTileHeads + row;
     if (d < a.D) {
-        for (int i = 1; i < at_once; ++i) sum += sums[tid + i * quads];
+        for (int i = 1; i < min(at_once, rec.parts); ++i) sum += sums[tid + i * quads];
         E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs + d;
-        for (int z = 0; z < 4; ++z) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] / whole);
+        const float inverse = 1.0f / whole;
+        for (int z = 0; z < 4; ++z) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] * inverse);
         if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
     }
 }
@@ -69,12 +67,16 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
 int rows_of(int64_t Hq, int64_t H) { return (int)std::min<int64_t>(Hq / H, kTileHeads); }
 
 void carve(Carver& c, AttentionKernelArgs& k, int Dp) {
-    k.records = c.take<AttentionRecord>(kMaxWorkgroups);
-    k.partial_ml = c.take<float>((size_t)2 * kMaxWorkgroups * k.rows * 2);
-    k.partial_o = c.take<float>((size_t)2 * kMaxWorkgroups * k.rows * Dp);
+    k.records = c.take<AttentionRecord>(kMaxPieces);
+    k.partial_ml = c.take<float>((size_t)2 * kMaxPieces * k.rows * 2);
+    k.partial_o = c.take<float>((size_t)2 * kMaxPieces * k.rows * Dp);
 }
 
 }  // namespace
+
+bool attention_line_ok(int64_t R, int64_t Hq, int64_t H, int64_t max_tokens) {
+    return R * (max_tokens / kBlockTokens + 8) * H * ceil_div(Hq / H, kTileHeads) < kMaxLine;
+}
 
 size_t attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D) {
     AttentionKernelArgs k{};
@@ -92,8 +94,6 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.lse = a.lse;
     k.pages = a.pages.p, k.page_stride = a.pages.page_stride, k.head_stride = a.pages.head_stride;
     k.n_pages = (uint32_t)a.pages.n, k.page_size = a.pages.page_size;
-    while (((uint64_t)1 << k.page_shift) < (uint64_t)k.page_size) ++k.page_shift;
-    k.page_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << k.page_shift) - k.page_size)) / k.page_size + 1);
     k.table = a.table, k.ld_table = a.ld_table;
     k.max_tokens = (uint32_t)(a.max_pages * a.pages.page_size);
     k.lengths = a.lengths;
@@ -102,13 +102,17 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.R = a.R, k.Hq = a.Hq, k.H = a.H, k.D = a.D, k.group = a.Hq / a.H;
     k.tiles = (int)ceil_div(k.group, kTileHeads), k.segments = a.H * k.tiles;
     k.rows = rows_of(a.Hq, a.H);
+    const int workgroups = attention_workgroups(Dp / 32, a.pages.bits, a.f32 ? 3 : 1);
+    k.by_page = Divisor((uint32_t)k.page_size), k.by_segments = Divisor((uint32_t)k.segments);
+    k.by_pieces = Divisor(4u * workgroups);
     Carver c(workspace);
     carve(c, k, Dp);
     const hipError_t e = a.pages.bits == 16  ? launch_attention<16>(k, Dp / 32, a.f32, stream)
                          : a.pages.bits == 8 ? launch_attention<8>(k, Dp / 32, a.f32, stream)
                                              : launch_attention<4>(k, Dp / 32, a.f32, stream);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)attention_workgroups(Dp / 32, a.pages.bits, a.f32 ? 3 : 1), (unsigned)k.rows);
+    // one record per segment where that is not more than one per piece
+    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.R * k.segments, 4 * workgroups), (unsigned)k.rows);
     if (a.f32) attention_join_kernel<float><<<grid, 256, 0, stream>>>(k, Dp);
     else attention_join_kernel<__bf16><<<grid, 256, 0, stream>>>(k, Dp);
     return hipGetLastError();

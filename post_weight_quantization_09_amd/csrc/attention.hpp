@@ -9,10 +9,19 @@ namespace gptq {
 constexpr int kBlockTokens = 32;        // tokens of a wave's step: the K of the second product
 constexpr int kTileHeads = 16;          // query heads of a step: the N of both products
 
-// How a sum over a segment (a request and up to 16 query heads of one key head) goes on past a workgroup.
+// A segment (a request and up to 16 query heads of one key head) whose sums several pieces hold, from `first` on.
 struct AttentionRecord {
-    int32_t request, segment, last;     // request < 0: this workgroup leaves nothing to join
-    int32_t pad;
+    int32_t request, segment, first, parts;     // parts 0: nothing to join
+};
+
+// t / d = (umulhi(t, mul) + t) >> shift for t < 2^31
+struct Divisor {
+    uint32_t mul, shift;
+    Divisor(uint32_t d = 1) : shift(0) {
+        while (((uint64_t)1 << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ uint32_t quotient(uint32_t t) const { return (__umulhi(t, mul) + t) >> shift; }
 };
 
 struct AttentionKernelArgs {
@@ -24,7 +33,7 @@ struct AttentionKernelArgs {
     int64_t page_stride, head_stride;
     uint32_t n_pages;
     int page_size;
-    uint32_t page_mul, page_shift;      // t / page_size = (umulhi(t, mul) + t) >> shift, t < 2^31
+    Divisor by_page, by_segments, by_pieces;
     const int32_t* table;
     int64_t ld_table;
     uint32_t max_tokens;                // of the table's columns
@@ -33,22 +42,21 @@ struct AttentionKernelArgs {
     int64_t window;
     int R, Hq, H, D, group;             // group = Hq / H query heads share a key head
     int tiles, segments;                // per key head and per request
-    float* partial_o;                   // two slots per workgroup, rows x Dp
+    float* partial_o;                   // two slots per piece (ends and begins there), rows x Dp
     float* partial_ml;                  // rows x 2
     int rows;                           // of a slot: min(group, 16)
     AttentionRecord* records;
 };
 
-// Waves of a SIMD that the registers are laid out for.
+// Waves of a SIMD that the registers are laid out for: a launch has that many, and each its piece of the work.
 constexpr int attention_waves(int chunks, int bits, int parts) {
     if (parts == 1 && chunks <= 4) return bits == 16 && chunks == 4 ? 2 : 3;
     return parts == 1 || chunks <= 4 ? 2 : 1;
 }
-
-// Workgroups of a launch: as many as are resident on 256 CUs, a wave of each on every SIMD.
 constexpr int attention_workgroups(int chunks, int bits, int parts) { return 256 * attention_waves(chunks, bits, parts); }
 
-constexpr int kMaxWorkgroups = 1024;
+constexpr int kMaxPieces = 4 * 768;
+constexpr int64_t kMaxLine = (int64_t)1 << 31;  // places
 
 // chunks: stored head size / 32.
 template <int BITS>

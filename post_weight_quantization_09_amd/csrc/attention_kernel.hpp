@@ -16,10 +16,12 @@
 // Softmax: scores are kept times log2 e.  A lane's maximum is raised (and what was summed rescaled) only where a score passes it
 // by 8: probabilities then reach 2^8, which fp32 sums and bf16 factors bear as well as 1, and few steps rescale.
 //
-// Work is shared out by blocks of 32 tokens: all blocks of all requests and heads lie on one line, and workgroup w takes the
-// w-th piece of it, whatever the lengths (an even share for 64 ragged requests as for one of 131072 tokens beside short
-// ones).  The line is found from a scan over the lengths, by every workgroup for itself.  A segment (request and heads) that
-// ends in another workgroup than it began leaves unnormalised sums, which the join adds in order.
+// Work is shared out by blocks of 32 tokens: all blocks of all segments (a request and 16 query heads of a key head) lie on
+// one line, and wave w takes the w-th piece of it, whatever the lengths: an even share for 64 ragged requests as for one of
+// 131072 tokens beside short ones.  Every workgroup scans the lengths for itself.  A wave that has a whole segment writes its
+// output; one that has a part of it writes unnormalised sums, which the join adds in order.  Waves share nothing else: no LDS
+// and no barrier in the loop, and little code, which counts where a call is short (the instructions of a launch come from
+// memory once per CU).
 #pragma once
 
 #include "attention.hpp"
@@ -28,6 +30,7 @@ namespace gptq {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;
+constexpr uint32_t kLeastPiece = 2;     // places of a wave's piece
 
 __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
@@ -108,7 +111,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
     }
 }
 
-// Eight elements of any alignment that their type has, as they are stored, and as fp32.
+// Eight elements of any alignment that their type has.
 template <typename E>
 struct Eight;
 template <>
@@ -116,23 +119,56 @@ struct Eight<__bf16> {
     typedef u32x4 __attribute__((aligned(2))) any;
     u32x4 v;
     __device__ void load(const __bf16* p) { v = *reinterpret_cast<const any*>(p); }
-    __device__ float get(int i) const { return i % 2 ? bf16hi_to_f32(v[i / 2]) : bf16lo_to_f32(v[i / 2]); }
     __device__ void clear() { v = u32x4{0, 0, 0, 0}; }
+    __device__ float most() const {
+        float x = 0.0f;
+        for (int i = 0; i < 4; ++i) x = fmaxf(x, fmaxf(fabsf(bf16lo_to_f32(v[i])), fabsf(bf16hi_to_f32(v[i]))));
+        return x;
+    }
+    __device__ void scale(int e) {                                  // exact, but for what falls below the smallest values
+        for (int i = 0; i < 4; ++i) v[i] = high_halves(ldexpf(bf16lo_to_f32(v[i]), e), ldexpf(bf16hi_to_f32(v[i]), e));
+    }
+    __device__ void operand(bf16x8 (&q)[1]) const { q[0] = __builtin_bit_cast(bf16x8, v); }
 };
 template <>
 struct Eight<float> {
     typedef f32x4 __attribute__((aligned(4))) any;
-    f32x4 v[2];
-    __device__ void load(const float* p) { v[0] = reinterpret_cast<const any*>(p)[0], v[1] = reinterpret_cast<const any*>(p)[1]; }
-    __device__ float get(int i) const { return v[i / 4][i % 4]; }
-    __device__ void clear() { v[0] = v[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    float v[8];
+    __device__ void load(const float* p) {
+        for (int i = 0; i < 2; ++i) {
+            const f32x4 x = reinterpret_cast<const any*>(p)[i];
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = x[j];
+        }
+    }
+    __device__ void clear() {
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+    __device__ float most() const {
+        float x = 0.0f;
+        for (int i = 0; i < 8; ++i) x = fmaxf(x, fabsf(v[i]));
+        return x;
+    }
+    __device__ void scale(int e) {
+        for (int i = 0; i < 8; ++i) v[i] = ldexpf(v[i], e);
+    }
+    __device__ void operand(bf16x8 (&q)[3]) const { split8<3>(v, q); }
 };
 
-// a / b where the quotient is below 2^20: from a reciprocal, put right by one where that was needed.
-__device__ __forceinline__ int small_quotient(int64_t a, int64_t b) {
-    int q = (int)((float)a * __builtin_amdgcn_rcpf((float)b));
-    const int64_t rest = a - q * b;
-    return rest < 0 ? q - 1 : rest >= b ? q + 1 : q;
+// Four values rounded to rows of any alignment that their type has.
+__device__ __forceinline__ void store_four(__bf16* p, f32x4 x) {
+    typedef u32x2 __attribute__((aligned(2))) any;
+    *reinterpret_cast<any*>(p) = u32x2{pack_bf16x2_rne(x[0], x[1]), pack_bf16x2_rne(x[2], x[3])};
+}
+__device__ __forceinline__ void store_four(float* p, f32x4 x) {
+    typedef f32x4 __attribute__((aligned(4))) any;
+    *reinterpret_cast<any*>(p) = x;
+}
+
+// a / b where the quotient is below 2^20: from a reciprocal, put right by one where that was needed (a, b < 2^31).
+__device__ __forceinline__ uint32_t small_quotient(uint32_t a, uint32_t b) {
+    const uint32_t q = (uint32_t)((float)a * __builtin_amdgcn_rcpf((float)b));
+    const int rest = (int)(a - q * b);
+    return rest < 0 ? q - 1 : rest >= (int)b ? q + 1 : q;
 }
 
 template <int WORDS>
@@ -160,8 +196,8 @@ struct Visible {
 };
 
 // A segment's length on the line: its blocks, and what beginning with it costs beside them (places before its blocks, at
-// which nothing is done), so that workgroups with many short segments get fewer blocks.
-constexpr uint32_t kBeginCost = 4;
+// which nothing is done), so that waves with many segments get fewer blocks.
+constexpr uint32_t kBeginCost = 3;
 
 __device__ __forceinline__ Visible visible(const AttentionKernelArgs& a, int r) {
     const int32_t given = a.lengths[r];
@@ -197,21 +233,35 @@ struct Block {
     bool whole;                                                     // every token of the 32 is seen
 };
 
+// Page and place in it of the two halves of 32 tokens; -1 where there is none.  The same for all lanes of a wave.
+struct Halves {
+    uint32_t t0;
+    int32_t page[2];
+    uint32_t slot[2];
+};
+
+__device__ __forceinline__ Halves look_up(const AttentionKernelArgs& a, const int32_t* table, const Visible& vis, uint32_t t0) {
+    Halves h;
+    h.t0 = t0;
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = t0 + 16 * i, j = a.by_page.quotient(t);
+        h.page[i] = t < vis.n ? table[j] : -1;
+        h.slot[i] = t - j * a.page_size;
+    }
+    return h;
+}
+
 template <int NC, int BITS, int PARTS>
-__device__ __forceinline__ void load_block(const AttentionKernelArgs& a, const int32_t* table, const Visible& vis,
-                                           uint32_t t0, const uint8_t* head, int lane, Block<NC, BITS, PARTS>& b) {
+__device__ __forceinline__ void load_block(const AttentionKernelArgs& a, const Visible& vis, const Halves& at,
+                                           const uint8_t* head, int lane, Block<NC, BITS, PARTS>& b) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     const int m = lane & 15, quarter = lane >> 4;
-    const uint32_t t1 = t0 + 16;
-    const uint32_t j0 = (__umulhi(t0, a.page_mul) + t0) >> a.page_shift, j1 = (__umulhi(t1, a.page_mul) + t1) >> a.page_shift;
-    int32_t p0 = -1, p1 = -1;
-    if (t0 < vis.n) p0 = table[j0];
-    if (t1 < vis.n) p1 = table[j1];
-    const bool ok0 = (uint32_t)p0 < a.n_pages, ok1 = (uint32_t)p1 < a.n_pages;
+    const uint32_t t0 = at.t0;
+    const bool ok0 = (uint32_t)at.page[0] < a.n_pages, ok1 = (uint32_t)at.page[1] < a.n_pages;
     // a half without a page reads page 0 and is masked
-    const uint32_t s0 = ok0 ? t0 - j0 * a.page_size : 0u, s1 = ok1 ? t1 - j1 * a.page_size : 0u;
-    const uint8_t* block0 = head + (ok0 ? p0 : 0) * a.page_stride;
-    const uint8_t* block1 = head + (ok1 ? p1 : 0) * a.page_stride;
+    const uint32_t s0 = ok0 ? at.slot[0] : 0u, s1 = ok1 ? at.slot[1] : 0u;
+    const uint8_t* block0 = head + (ok0 ? at.page[0] : 0) * a.page_stride;
+    const uint8_t* block1 = head + (ok1 ? at.page[1] : 0) * a.page_stride;
     const uint32_t part = (uint32_t)a.page_size * Tr::kRow;
     b.whole = ok0 && ok1 && t0 >= vis.first && t0 + 32 <= vis.n;
     const bool key_second = m >= 8, value_second = quarter >= 2;
@@ -313,170 +363,151 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     }
 }
 
+// q of a lane's head as B operands.  Values of extreme size are brought near one by a power of two (which to_log2 takes back),
+// so that no sum on the way leaves the range of fp32.
+template <typename E, int NC, int BITS, int PARTS>
+__device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quarter, bf16x8 (&q)[NC][PARTS], float& to_log2) {
+    using Tr = AttentionTraits<NC, BITS, PARTS>;
+    Eight<E> y[NC];
+    for (int c = 0; c < NC; ++c) {
+        const int d = 32 * Tr::kSide * (c / Tr::kSide) + 8 * Tr::kSide * quarter + 8 * (c % Tr::kSide);
+        const bool in = wanted && d < D;                            // a row is read from its start where nothing of it is wanted
+        y[c].load(x + (in ? d : 0));
+        if (!in) y[c].clear();
+    }
+    float most = 0.0f;
+    for (int c = 0; c < NC; ++c) most = fmaxf(most, y[c].most());
+    most = max_of_quarters(most);
+    if (__any(most > 0x1p32f || (most < 0x1p-32f && most > 0.0f))) {
+        const int e = most == 0.0f || most > 3.4e38f ? 0 : ilogbf(most);
+        for (int c = 0; c < NC; ++c) y[c].scale(-e);
+        to_log2 = ldexpf(to_log2, e);
+    }
+    for (int c = 0; c < NC; ++c) y[c].operand(q[c]);
+}
+
 template <typename E, int NC, int BITS, int PARTS>
 __global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attention_kernel(AttentionKernelArgs a) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
-    constexpr int kJoinDims = NC <= 4 ? Tr::kDp : NC == 6 ? 64 : 128;   // dimensions that the waves join at a time
-    constexpr int kPitch = kJoinDims + 4;
-    __shared__ __attribute__((aligned(16))) float joined[4][kTileHeads][kPitch];
-    __shared__ float ml[4][kTileHeads][2];
-    __shared__ uint32_t sums[4], found_base;
-    __shared__ int found;
+    __shared__ uint32_t line[256], sums[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int quarter = lane >> 4;
+    const int quarter = lane >> 4, n = lane & 15;
 
-    // the line of all blocks: a scan over the requests' blocks, `share` requests a thread
-    const int share = (a.R + 255) / 256, r_first = tid * share, r_end = min(a.R, r_first + share);
-    uint32_t mine = 0;
-    for (int r = r_first; r < r_end; ++r) mine += visible(a, r).blocks() + kBeginCost;
-    uint32_t upto = mine;
-    for (int i = 1; i < 64; i *= 2) {
-        const uint32_t y = __shfl_up(upto, i);
-        if (lane >= i) upto += y;
-    }
-    if (lane == 63) sums[wave] = upto;
-    __syncthreads();
-    uint32_t all = 0;
-    for (int w = 0; w < 4; ++w) {
-        if (w < wave) upto += sums[w];
-        all += sums[w];
-    }
-    const int64_t total = (int64_t)all * a.segments;
-    // a block at least for each wave (the double's quotient is off by one at most, which one more place makes up for)
-    const int64_t chunk = max((int64_t)(kBeginCost + 4), (int64_t)((double)total / gridDim.x) + 2);
-    const int64_t begin = chunk * blockIdx.x, end = min(begin + chunk, total);
-    AttentionRecord record = {-1, 0, 0, 0};
-    if (begin >= end) {
-        if (tid == 0) a.records[blockIdx.x] = record;
-        return;
-    }
-    uint32_t at = (uint32_t)((double)begin / a.segments);           // off by one at most, as begin < 2^42
-    if ((int64_t)at * a.segments > begin) --at;
-    else if ((int64_t)(at + 1) * a.segments <= begin) ++at;
-    if (upto - mine <= at && at < upto) {
-        uint32_t base = upto - mine;
-        int r = r_first;
-        for (;; ++r) {
-            const uint32_t n = visible(a, r).blocks() + kBeginCost;
-            if (at < base + n) break;
-            base += n;
+    // the line of all blocks: a scan over the requests' lengths on it, `share` requests a thread
+    const int share = (a.R + 255) / 256;
+    {
+        uint32_t upto = 0;
+        for (int r = tid * share; r < min(a.R, (tid + 1) * share); ++r) upto += visible(a, r).blocks() + kBeginCost;
+        for (int i = 1; i < 64; i *= 2) {
+            const uint32_t y = __shfl_up(upto, i);
+            if (lane >= i) upto += y;
         }
-        found = r;
-        found_base = base;
+        line[tid] = upto;
+        if (lane == 63) sums[wave] = upto;
     }
     __syncthreads();
-    int r = __builtin_amdgcn_readfirstlane(found);
-    int64_t base = (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)found_base) * a.segments, pos = begin;
+    const uint32_t all = sums[0] + sums[1] + sums[2] + sums[3], total = all * a.segments;
+    const uint32_t chunk = max(kLeastPiece, a.by_pieces.quotient(total) + 1);
+    // neighbouring pieces are other workgroups': few pieces spread over the CUs
+    const uint32_t piece = wave * gridDim.x + blockIdx.x;
+    const bool by_piece = a.R * a.segments > (int)(4 * gridDim.x);  // how records are numbered
+    if (by_piece && lane == 0) a.records[piece].parts = 0;
+    if (piece * (uint64_t)chunk >= total) return;
+    const uint32_t begin = piece * chunk, end = min(begin + chunk, total);
 
+    // the request that the piece begins in: the thread whose requests' line holds it, then a walk over those
+    uint32_t base = 0;                                              // of request r, in places of one segment
+    int r;
+    {
+        const uint32_t at = a.by_segments.quotient(begin);
+        int before = 0;
+        uint32_t ahead = 0;
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t upto = line[w * 64 + lane] + ahead;
+            const uint64_t under = __ballot(upto <= at);
+            before += __popcll(under);
+            if (under) base = max(base, (uint32_t)__shfl(upto, 63 - __clzll(under)));
+            ahead += sums[w];
+        }
+        r = __builtin_amdgcn_readfirstlane(before) * share;
+        base = __builtin_amdgcn_readfirstlane(base);
+        for (;;) {
+            const uint32_t length = visible(a, r).blocks() + kBeginCost;
+            if (at < base + length) break;
+            base += length;
+            ++r;
+        }
+    }
+
+    uint32_t pos = begin, start = base * a.segments;                // of request r on the line
     for (; pos < end; ++r) {
-        const Visible vis = visible(a, r);
-        const int64_t length = (int64_t)vis.blocks() + kBeginCost, inside = pos - base;
-        int segment = small_quotient(inside, length);
-        int64_t from = inside - segment * length;
-        base += a.segments * length;
+        Visible vis = visible(a, r);
+        vis.n = (uint32_t)__builtin_amdgcn_readfirstlane((int)vis.n);
+        vis.first = (uint32_t)__builtin_amdgcn_readfirstlane((int)vis.first);
+        const uint32_t length = vis.blocks() + kBeginCost;
+        int segment = (int)small_quotient(pos - start, length);
+        uint32_t from = pos - start - segment * length;
+        start += a.segments * length;
         for (; segment < a.segments && pos < end; ++segment, from = 0) {
             // places [from, upto) of the segment's line; the first kBeginCost of it are no blocks
-            const int64_t upto = min(length, from + (end - pos));
-            const int off = (int)max(from - kBeginCost, (int64_t)0), count = (int)(upto - kBeginCost) - off;
+            const uint32_t upto = min(length, from + (end - pos));
+            const uint32_t off = max(from, kBeginCost) - kBeginCost;
+            const int count = (int)(upto - kBeginCost) - (int)off;
             const bool starts = off == 0, ends = upto == length;
             pos += upto - from;
             if (count <= 0) continue;
             const int h = segment / a.tiles, tile = segment - h * a.tiles;
             const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
+            if (starts) {
+                // the pieces that hold the rest; a segment in one piece leaves nothing to join
+                const uint32_t last = small_quotient(pos - upto + length - 1, chunk);
+                if (lane == 0 && (!ends || !by_piece))
+                    a.records[by_piece ? (int)piece : r * a.segments + segment] = {r, segment, (int32_t)piece, (int32_t)(ends ? 0 : last - piece + 1)};
+            }
 
-            // the wave's first block, then q of the tile's heads as B operands, times a power of two that keeps every sum in range
+            // the first block, then q of the tile's heads as B operands
             const uint8_t* head = a.pages + h * a.head_stride;
             const int32_t* table = a.table + r * a.ld_table;
-            const uint32_t first = (vis.block() + (uint32_t)off) * kBlockTokens;
-            const int todo = vis.n > vis.first ? count : 0;
+            uint32_t t = (vis.block() + off) * kBlockTokens;
+            int todo = vis.n > vis.first ? count : 0;
             Block<NC, BITS, PARTS> b;
-            if (wave < todo) load_block(a, table, vis, first + wave * kBlockTokens, head, lane, b);
+            if (todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
             bf16x8 q[NC][PARTS];
-            float to_log2;
-            {
-                const int n = lane & 15;
-                const E* x = static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs;
-                Eight<E> y[NC];
-                uint32_t most = 0;
-                for (int c = 0; c < NC; ++c) {
-                    const int d = 32 * Tr::kSide * (c / Tr::kSide) + 8 * Tr::kSide * quarter + 8 * (c % Tr::kSide);
-                    const bool in = n < heads && d < a.D;           // a row is read from its start where nothing of it is wanted
-                    y[c].load(x + (in ? d : 0));
-                    if (!in) y[c].clear();
-                }
-                for (int c = 0; c < NC; ++c)
-                    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[c].get(i)) & 0x7FFFFFFFu);
-                most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-                most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-                const int e = most == 0 || most >= 0x7F800000u ? 0 : (int)(most >> 23) - 126;   // |q| 2^-e < 1
-                for (int c = 0; c < NC; ++c) {
-                    float z[8];
-                    for (int i = 0; i < 8; ++i) z[i] = ldexpf(y[c].get(i), -e);
-                    split8<PARTS>(z, q[c]);
-                }
-                to_log2 = ldexpf(a.scale_log2e, e + (BITS == 4 ? 4 : 0));
-            }
+            float to_log2 = a.scale_log2e * (BITS == 4 ? 16.0f : 1.0f);
+            load_q<E, NC, BITS, PARTS>(static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs, n < heads, a.D,
+                                       quarter, q, to_log2);
 
             f32x4 o[2 * NC];
             for (int i = 0; i < 2 * NC; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             float m = -INFINITY, l = 0.0f;
-            for (int i = wave; i < todo;) {
+            while (todo > 0) {
                 step<NC, BITS, PARTS>(b, q, to_log2, m, l, o);
-                i += 4;
-                if (i < todo) load_block(a, table, vis, first + i * kBlockTokens, head, lane, b);
+                t += kBlockTokens;
+                if (--todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
             }
-
-            // the four waves' sums joined
             l = sum_of_quarters(l);
-            const int n = lane & 15;
-            if (quarter == 0) ml[wave][n][0] = m, ml[wave][n][1] = l;
-            const int64_t place = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-            constexpr int kRounds = Tr::kDp / kJoinDims, kPer = Tr::kValueLoads / kRounds;
-            static_assert(kPer * kRounds == Tr::kValueLoads && kPer * 16 * Tr::kDims == kJoinDims);
-            for (int round = 0; round < kRounds; ++round) {
-                for (int i = 0; i < kPer; ++i) {
-                    const f32x4* from = &o[(round * kPer + i) * Tr::kDims];
-                    float* to = &joined[wave][n][i * 16 * Tr::kDims + quarter * 4 * Tr::kDims];
-                    for (int j = 0; j < Tr::kDims; ++j) {           // dimension Tr::kDims * row + tile, four at a time
-                        f32x4 y;
-                        for (int z = 0; z < 4; ++z) y[z] = from[(4 * j + z) % Tr::kDims][(4 * j + z) / Tr::kDims];
-                        *reinterpret_cast<f32x4*>(to + 4 * j) = y;
-                    }
+            if (n >= heads) continue;
+
+            // four neighbouring dimensions at a time: j of value load i
+            const bool whole = starts && ends;
+            const uint32_t place = (2 * piece + (starts ? 1 : 0)) * a.rows + n;
+            const float inverse = (BITS == 4 ? 16.0f : 1.0f) * (whole ? l == 0.0f ? 0.0f : 1.0f / l : 1.0f);
+            E* to = static_cast<E*>(a.out) + r * a.o_rs + (hq + n) * a.o_hs;
+            float* part = a.partial_o + (uint64_t)place * Tr::kDp;
+            for (int i = 0; i < Tr::kValueLoads; ++i)
+                for (int j = 0; j < Tr::kDims; ++j) {
+                    const int d = (16 * i + 4 * quarter) * Tr::kDims + 4 * j;
+                    f32x4 y;
+                    for (int z = 0; z < 4; ++z) y[z] = o[i * Tr::kDims + (4 * j + z) % Tr::kDims][(4 * j + z) / Tr::kDims];
+                    if (!whole) *reinterpret_cast<f32x4*>(part + d) = y * inverse;
+                    else if (d < a.D) store_four(to + d, l == 0.0f ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : y * inverse);
                 }
-                __syncthreads();
-                for (int i = tid; i < heads * (kJoinDims / 4); i += 256) {
-                    const int row = i / (kJoinDims / 4), d4 = i % (kJoinDims / 4), d = round * kJoinDims + 4 * d4;
-                    float top = ml[0][row][0];
-                    for (int w = 1; w < 4; ++w) top = fmaxf(top, ml[w][row][0]);
-                    const float from = top == -INFINITY ? 0.0f : top;
-                    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                    float whole = 0.0f;
-                    for (int w = 0; w < 4; ++w) {
-                        const float keep = __builtin_amdgcn_exp2f(ml[w][row][0] - from);
-                        whole += keep * ml[w][row][1];
-                        sum += keep * *reinterpret_cast<const f32x4*>(&joined[w][row][4 * d4]);
-                    }
-                    if constexpr (BITS == 4) sum *= 16.0f;
-                    if (starts && ends) {
-                        E* to = static_cast<E*>(a.out) + r * a.o_rs + (hq + row) * a.o_hs + d;
-                        for (int z = 0; z < 4; ++z)
-                            if (d < a.D) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] / whole);
-                        if (a.lse && d == 0)
-                            a.lse[(int64_t)r * a.Hq + hq + row] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
-                    } else {
-                        *reinterpret_cast<f32x4*>(a.partial_o + (place * a.rows + row) * Tr::kDp + d) = sum;
-                        if (d == 0) {
-                            a.partial_ml[(place * a.rows + row) * 2] = top;
-                            a.partial_ml[(place * a.rows + row) * 2 + 1] = whole;
-                        }
-                    }
-                }
-                __syncthreads();
+            if (quarter == 0) {
+                if (!whole) *reinterpret_cast<f32x2*>(a.partial_ml + 2 * (uint64_t)place) = f32x2{m, l};
+                else if (a.lse) a.lse[(int64_t)r * a.Hq + hq + n] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
             }
-            if (starts && !ends) record = {r, segment, small_quotient(pos - upto + length - 1, chunk), 0};
         }
     }
-    if (tid == 0) a.records[blockIdx.x] = record;
 }
 
 template <int BITS>
@@ -484,7 +515,6 @@ hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, 
     const auto launch = [&](auto e, auto parts, auto nc) {
         using E = decltype(e);
         constexpr int P = decltype(parts)::value, NC = decltype(nc)::value;
-        // as many workgroups as are resident: every one gets its share of the line at once
         attention_kernel<E, NC, BITS, P><<<dim3((unsigned)attention_workgroups(NC, BITS, P)), 256, 0, stream>>>(a);
     };
     const auto pick = [&](auto e, auto parts) {

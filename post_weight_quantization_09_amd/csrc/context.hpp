@@ -53,6 +53,8 @@ struct AttentionArgs {
     float* lse;
 };
 
+// Whether the blocks of all requests and heads can be counted in 32 bits.
+bool attention_line_ok(int64_t R, int64_t Hq, int64_t H, int64_t max_tokens);
 size_t attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D);
 hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t stream);
 

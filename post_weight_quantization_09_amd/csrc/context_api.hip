@@ -12,7 +12,6 @@ namespace {
 bool dtype_ok(gptq_dtype_t d) { return d == GPTQ_DTYPE_F32 || d == GPTQ_DTYPE_BF16; }
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 22, kMaxHeads = 1024, kMaxRotaryHead = 1024;
-constexpr int64_t kMaxTableTokens = (int64_t)1 << 36;     // of all requests: the attention counts blocks of 32 in 32 bits
 constexpr int64_t kMaxRequests = 65536, kMaxPageSize = 65536, kMaxStride = (int64_t)1 << 40;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
@@ -147,7 +146,7 @@ gptq_status_t gptq_cache_attention(const void* Q, gptq_dtype_t dtype, int64_t R,
     if (!pages_ok(pages, n_pages, page_stride, head_stride, page_size, H, D, bits)) return GPTQ_ERR_ARG;
     if (!stride_ok(q_rs) || !stride_ok(q_hs) || !apart(R, Hq, D, o_rs, o_hs)) return GPTQ_ERR_ARG;
     if (max_pages < 0 || max_pages > (((int64_t)1 << 31) - 1) / page_size || ld_table < 0 || ld_table > kMaxStride) return GPTQ_ERR_ARG;
-    if (R * max_pages * page_size > kMaxTableTokens) return GPTQ_ERR_ARG;
+    if (!attention_line_ok(R, Hq, H, max_pages * page_size)) return GPTQ_ERR_ARG;
     if (!std::isfinite(scale) || window < 0) return GPTQ_ERR_ARG;
     if (R == 0) return GPTQ_OK;
     if (!Q || !out || Q == out || !lengths || (max_pages > 0 && !table)) return GPTQ_ERR_ARG;

@@ -827,7 +827,7 @@ def test_attention_refusals():
     for kw in (dict(dtype=2), dict(R=-1), dict(R=65537), dict(Hq=0), dict(Hq=1), dict(Hq=7), dict(Hq=1026), dict(H=0), dict(D=20), dict(D=512),
                dict(bits=6), dict(size=40), dict(n=0), dict(pages=None), dict(hs=block - 16), dict(ps=block), dict(Q=None), dict(out=None),
                dict(out=FAKE), dict(table=None), dict(lengths=None), dict(ld=-1), dict(max_pages=-1), dict(max_pages=1 << 26),
-               dict(R=65536, max_pages=(1 << 15) + 1, n=1 << 24, q_rs=512), dict(window=-1),
+               dict(R=65536, max_pages=1 << 14, n=1 << 24), dict(window=-1),
                dict(scale=math.inf), dict(scale=math.nan), dict(q_rs=-1), dict(o_rs=0), dict(o_hs=60)):
         assert change(call, base, ATTEND, **kw) == g.GPTQ_ERR_ARG, kw
     for kw in (dict(ws=None), dict(ws=ctypes.c_void_p(0x100010)), dict(ws_bytes=need - 1)):
