@@ -10,19 +10,51 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// A workgroup joins one query head of a segment: the parts' weights first, then their rows, Dp / 4 threads a row and as many
-// rows at a time as there are threads for.
+// Up to this many parts a workgroup joins all query heads of a segment, Dp / 4 threads each, which weigh the parts for
+// themselves; beyond it each of the workgroups along y has one head.
+constexpr int kFewParts = 4;
+
+template <typename E>
+__device__ __forceinline__ void write_joined(const AttentionKernelArgs& a, const AttentionRecord& rec, int hq, int d, f32x4 sum,
+                                             float top, float whole) {
+    if (d >= a.D) return;
+    E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs + d;
+    const float inverse = 1.0f / whole;
+    for (int z = 0; z < 4; ++z) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] * inverse);
+    if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+}
+
 template <typename E>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
-    constexpr int kEach = kMaxPieces / 256;
     __shared__ float weights[kMaxPieces], most[4], wholes[4];
     __shared__ f32x4 sums[256];
     const AttentionRecord rec = a.records[blockIdx.x];
-    const int tid = threadIdx.x, wave = tid >> 6, row = blockIdx.y;
-    if (rec.parts == 0) return;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    if (rec.parts == 0 || (rec.parts <= kFewParts && blockIdx.y > 0)) return;
     const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
-    if (row >= min(kTileHeads, a.group - tile * kTileHeads)) return;
-    const auto place = [&](int i) { return (uint64_t)((2 * (rec.first + i) + (i == 0 ? 1 : 0)) * a.rows + row); };
+    const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
+    const auto slot = [&](int i) { return (uint64_t)((2 * (rec.first + i) + (i == 0 ? 1 : 0)) * a.rows); };
+    const int quads = Dp / 4, at_once = 256 / quads, line = tid / quads, quad = tid - line * quads;
+    if (rec.parts <= kFewParts) {
+        for (int row = line; row < heads && line < at_once; row += at_once) {
+            float top = -INFINITY, whole = 0.0f;
+            for (int p = 0; p < rec.parts; ++p) top = fmaxf(top, a.partial_ml[(slot(p) + row) * 2]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int p = 0; p < rec.parts; ++p) {
+                const f32x2 ml = *reinterpret_cast<const f32x2*>(a.partial_ml + (slot(p) + row) * 2);
+                const float keep = __builtin_amdgcn_exp2f(ml[0] - ref);
+                whole += keep * ml[1];
+                sum += keep * *reinterpret_cast<const f32x4*>(a.partial_o + (slot(p) + row) * Dp + 4 * quad);
+            }
+            write_joined<E>(a, rec, hq + row, 4 * quad, sum, top, whole);
+        }
+        return;
+    }
+    const int row = blockIdx.y;
+    if (row >= heads) return;
+    const auto place = [&](int i) { return slot(i) + row; };
     float top = -INFINITY;
     for (int p = tid; p < rec.parts; p += 256) {
         const float m = a.partial_ml[place(p) * 2];
@@ -45,7 +77,6 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     __syncthreads();
     whole = wholes[0] + wholes[1] + wholes[2] + wholes[3];
 
-    const int quads = Dp / 4, at_once = 256 / quads, line = tid / quads, quad = tid - line * quads;
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (line < at_once) {
 #pragma unroll 8
@@ -54,13 +85,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     }
     sums[tid] = sum;
     __syncthreads();
-    const int d = 4 * tid, hq = h * a.group + tile * kTileHeads + row;
-    if (d < a.D) {
-        for (int i = 1; i < min(at_once, rec.parts); ++i) sum += sums[tid + i * quads];
-        E* to = static_cast<E*>(a.out) + rec.request * a.o_rs + hq * a.o_hs + d;
-        const float inverse = 1.0f / whole;
-        for (int z = 0; z < 4; ++z) to[z] = (E)(whole == 0.0f ? 0.0f : sum[z] * inverse);
-        if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
+    if (tid < quads) {
+        for (int i = 1; i < at_once; ++i) sum += sums[tid + i * quads];
+        write_joined<E>(a, rec, hq + row, 4 * tid, sum, top, whole);
     }
 }
 
