@@ -24,17 +24,17 @@ __device__ __forceinline__ void write_joined(const AttentionKernelArgs& a, const
     if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
 }
 
-template <typename E>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
-    __shared__ float weights[kMaxPieces], most[4], wholes[4];
-    __shared__ f32x4 sums[256];
+template <typename E, int THREADS>
+__global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
+    __shared__ float weights[kMaxPieces], most[THREADS / 64], wholes[THREADS / 64];
+    __shared__ f32x4 sums[THREADS];
     const AttentionRecord rec = a.records[blockIdx.x];
     const int tid = threadIdx.x, wave = tid >> 6;
     if (rec.parts == 0 || (rec.parts <= kFewParts && blockIdx.y > 0)) return;
     const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
     const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
     const auto slot = [&](int i) { return (uint64_t)((2 * (rec.first + i) + (i == 0 ? 1 : 0)) * a.rows); };
-    const int quads = Dp / 4, at_once = 256 / quads, line = tid / quads, quad = tid - line * quads;
+    const int quads = Dp / 4, at_once = THREADS / quads, line = tid / quads, quad = tid - line * quads;
     if (rec.parts <= kFewParts) {
         for (int row = line; row < heads && line < at_once; row += at_once) {
             float top = -INFINITY, whole = 0.0f;
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     if (row >= heads) return;
     const auto place = [&](int i) { return slot(i) + row; };
     float top = -INFINITY;
-    for (int p = tid; p < rec.parts; p += 256) {
+    for (int p = tid; p < rec.parts; p += THREADS) {
         const float m = a.partial_ml[place(p) * 2];
         weights[p] = m;
         top = fmaxf(top, m);
@@ -64,10 +64,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
     if ((tid & 63) == 0) most[wave] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    for (int w = 0; w < THREADS / 64; ++w) top = fmaxf(top, most[w]);
     const float ref = top == -INFINITY ? 0.0f : top;
     float whole = 0.0f;
-    for (int p = tid; p < rec.parts; p += 256) {
+    for (int p = tid; p < rec.parts; p += THREADS) {
         const float keep = __builtin_amdgcn_exp2f(weights[p] - ref);
         whole += keep * a.partial_ml[place(p) * 2 + 1];
         weights[p] = keep;
@@ -75,7 +75,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionKernelArgs
     for (int i = 32; i; i >>= 1) whole += __shfl_xor(whole, i);
     if ((tid & 63) == 0) wholes[wave] = whole;
     __syncthreads();
-    whole = wholes[0] + wholes[1] + wholes[2] + wholes[3];
+    whole = 0.0f;
+    for (int w = 0; w < THREADS / 64; ++w) whole += wholes[w];
 
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (line < at_once) {
@@ -129,9 +130,9 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.R = a.R, k.Hq = a.Hq, k.H = a.H, k.D = a.D, k.group = a.Hq / a.H;
     k.tiles = (int)ceil_div(k.group, kTileHeads), k.segments = a.H * k.tiles;
     k.rows = rows_of(a.Hq, a.H);
-    const int workgroups = attention_workgroups(Dp / 32, a.pages.bits, a.f32 ? 3 : 1);
+    const int pieces = attention_pieces(Dp / 32, a.pages.bits, a.f32 ? 3 : 1);
     k.by_page = Divisor((uint32_t)k.page_size), k.by_segments = Divisor((uint32_t)k.segments);
-    k.by_pieces = Divisor(4u * workgroups);
+    k.by_pieces = Divisor((uint32_t)pieces);
     Carver c(workspace);
     carve(c, k, Dp);
     const hipError_t e = a.pages.bits == 16  ? launch_attention<16>(k, Dp / 32, a.f32, stream)
@@ -139,9 +140,17 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
                                              : launch_attention<4>(k, Dp / 32, a.f32, stream);
     if (e != hipSuccess) return e;
     // one record per segment where that is not more than one per piece
-    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.R * k.segments, 4 * workgroups), (unsigned)k.rows);
-    if (a.f32) attention_join_kernel<float><<<grid, 256, 0, stream>>>(k, Dp);
-    else attention_join_kernel<__bf16><<<grid, 256, 0, stream>>>(k, Dp);
+    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.R * k.segments, pieces), (unsigned)k.rows);
+    // few segments may have many parts each: more threads for their rows
+    const auto join = [&](auto e) {
+        using E = decltype(e);
+        // few segments of long requests have hundreds of parts each (131072 tokens: 10.3 us with 256 threads, 8.6 with 1024;
+        // 777 tokens: 4.0 and 5.2)
+        if (grid.x * grid.y <= 512 && k.max_tokens >= 16384) attention_join_kernel<E, 1024><<<grid, 1024, 0, stream>>>(k, Dp);
+        else attention_join_kernel<E, 256><<<grid, 256, 0, stream>>>(k, Dp);
+    };
+    if (a.f32) join(0.0f);
+    else join((__bf16)0.0f);
     return hipGetLastError();
 }
 

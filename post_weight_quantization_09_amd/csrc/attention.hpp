@@ -48,14 +48,14 @@ struct AttentionKernelArgs {
     AttentionRecord* records;
 };
 
-// Waves of a SIMD that the registers are laid out for: a launch has that many, and each its piece of the work.
+// Waves of a SIMD that the registers are laid out for, and pieces of a launch: one for each of the 256 CUs' waves.
 constexpr int attention_waves(int chunks, int bits, int parts) {
     if (parts == 1 && chunks <= 4) return bits == 16 && chunks == 4 ? 2 : 3;
     return parts == 1 || chunks <= 4 ? 2 : 1;
 }
-constexpr int attention_workgroups(int chunks, int bits, int parts) { return 256 * attention_waves(chunks, bits, parts); }
+constexpr int attention_pieces(int chunks, int bits, int parts) { return 1024 * attention_waves(chunks, bits, parts); }
 
-constexpr int kMaxPieces = 4 * 768;
+constexpr int kMaxPieces = 1024 * 3;
 constexpr int64_t kMaxLine = (int64_t)1 << 31;  // places
 
 // chunks: stored head size / 32.

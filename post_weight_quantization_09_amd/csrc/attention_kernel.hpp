@@ -8,8 +8,12 @@
 //   output   O^T (dimensions x heads) += V^T P^T.  Those eight tokens are exactly the K octet that the B operand wants in this
 //            lane, so the probabilities go in where the scores came out; the A operand wants eight tokens of one dimension,
 //            which is how the pages store values.
-// Codes become bf16 exactly (8 bits: v_cvt_f32_i32 of a byte; 4 bits: v_cvt_off_f32_i4, which is code / 16); a token's key
-// scale multiplies its score, its value scale its probability.  With fp32 rows q and the probabilities are cut into three
+// Codes become bf16 exactly: 8 bits by v_cvt_f32_i32 of a byte, 4 bits for fp32 rows by v_cvt_off_f32_i4 (code / 16); for bf16
+// rows two 4-bit codes become bf16 by a shift and one and-xor that sets sign and exponent, code + 24 in the low half of a
+// register and code - 23 in the high half, and the excess 24 sum(low) - 23 sum(high) is taken off the sums in fp32: that of
+// the scores before they are begun, that of the output after them, from a product with (24, -23).  The signs alternate so that
+// the sums stay near the size of their result (an excess of one sign would reach 24 where the mean of many codes is near 0).
+// A token's key scale multiplies its score, its value scale its probability.  With fp32 rows q and the probabilities are cut into three
 // bf16 parts each (exact), so that nothing is rounded but sums.  bf16 rows round probability times scale to bf16: an error
 // of 2^-9 in each of many terms, where the output's own rounding is 2^-9 of their sum.
 //
@@ -92,6 +96,27 @@ __device__ __forceinline__ bf16x8 word_to_bf16(uint32_t w) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
+// Two 4-bit codes at bits 0 and 16 of w >> SHIFT as bf16 code + 24 and code - 23: in two's complement n ^ 8 is code + 8 and
+// n ^ 7 is 7 - code, which are the upper mantissa bits of 16 (1 + (code + 8) / 16) and -16 (1 + (7 - code) / 16).
+constexpr uint32_t kExcess = 0xC1B841C0u;      // (24, -23)
+template <int SHIFT>
+__device__ __forceinline__ uint32_t excess_pair(uint32_t w) {
+    uint32_t x;
+    if constexpr (SHIFT < 3) x = w << (3 - SHIFT);
+    else x = w >> (SHIFT - 3);
+    return (x & 0x00780078u) ^ kExcess;
+}
+
+// A word's eight codes: register i holds codes i and i + 4.
+__device__ __forceinline__ bf16x8 word_to_excess(uint32_t w) {
+    return __builtin_bit_cast(bf16x8, u32x4{excess_pair<0>(w), excess_pair<4>(w), excess_pair<8>(w), excess_pair<12>(w)});
+}
+// The low (0) or high (4) halves of eight bytes: registers (0, 2), (1, 3), (4, 6), (5, 7).
+template <int HALF>
+__device__ __forceinline__ bf16x8 nibbles_to_excess(uint32_t w0, uint32_t w1) {
+    return __builtin_bit_cast(bf16x8, u32x4{excess_pair<HALF>(w0), excess_pair<HALF + 8>(w0), excess_pair<HALF>(w1), excess_pair<HALF + 8>(w1)});
+}
+
 // Eight fp32 values as PARTS bf16 operands: rounded (1), or cut into three parts of eight bits each, exactly.
 template <int PARTS>
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]) {
@@ -129,6 +154,14 @@ struct Eight<__bf16> {
         for (int i = 0; i < 4; ++i) v[i] = high_halves(ldexpf(bf16lo_to_f32(v[i]), e), ldexpf(bf16hi_to_f32(v[i]), e));
     }
     __device__ void operand(bf16x8 (&q)[1]) const { q[0] = __builtin_bit_cast(bf16x8, v); }
+    // The order of word_to_excess; returns the negative of the excess that its sum will have.
+    __device__ float codes_order() {
+        v = u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                  __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+        float low = 0.0f, high = 0.0f;
+        for (int i = 0; i < 4; ++i) low += bf16lo_to_f32(v[i]), high += bf16hi_to_f32(v[i]);
+        return 23.0f * high - 24.0f * low;
+    }
 };
 template <>
 struct Eight<float> {
@@ -169,6 +202,15 @@ __device__ __forceinline__ uint32_t small_quotient(uint32_t a, uint32_t b) {
     const uint32_t q = (uint32_t)((float)a * __builtin_amdgcn_rcpf((float)b));
     const int rest = (int)(a - q * b);
     return rest < 0 ? q - 1 : rest >= (int)b ? q + 1 : q;
+}
+
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ uint32_t scan_of_wave(uint32_t x, int lane) {
+    for (int i = 1; i < 64; i *= 2) {
+        const uint32_t y = __shfl_up(x, i);
+        if (lane >= i) x += y;
+    }
+    return x;
 }
 
 template <int WORDS>
@@ -220,6 +262,9 @@ struct AttentionTraits {
     static constexpr int kDims = BITS == 16 ? 1 : BITS == 8 ? 2 : NC % 2 ? 2 : 4;
     static constexpr int kValueLoads = 2 * NC / kDims;
     static constexpr int kValueLoadWords = kDims * BITS / 4;
+    static constexpr bool kExcess = BITS == 4 && PARTS == 1;        // codes enter as code + 24 and code - 23
+    static constexpr float kUnit = BITS == 4 && !kExcess ? 16.0f : 1.0f;
+    static constexpr int kTiles = 2 * NC + (kExcess ? 1 : 0);       // of the output, and the sums of its excess
 };
 
 // What a lane holds of 32 tokens.
@@ -295,18 +340,20 @@ __device__ __forceinline__ void load_block(const AttentionKernelArgs& a, const V
     }
 }
 
+// less: what the scores begin with (the negative of their excess)
 template <int NC, int BITS, int PARTS>
-__device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q)[NC][PARTS], float to_log2, float& m, float& l,
-                                     f32x4 (&o)[2 * NC]) {
+__device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q)[NC][PARTS], float less, float to_log2, float& m,
+                                     float& l, f32x4 (&o)[AttentionTraits<NC, BITS, PARTS>::kTiles]) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     f32x4 s[2];
     for (int T = 0; T < 2; ++T) {
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 acc = {less, less, less, less};
         for (int c = 0; c < NC; ++c) {
             const uint32_t* w = &b.k[T][c * Tr::kWordsPerChunk];
             bf16x8 k;
             if constexpr (BITS == 16) k = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
             else if constexpr (BITS == 8) k = bytes_to_bf16(w[0], w[1]);
+            else if constexpr (Tr::kExcess) k = word_to_excess(w[0]);
             else k = word_to_bf16(w[0]);
             for (int p = PARTS - 1; p >= 0; --p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[c][p], acc, 0, 0, 0);
         }
@@ -334,7 +381,7 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
         const float keep = __builtin_amdgcn_exp2f(m - base);
         m = now;
         l *= keep;
-        for (int i = 0; i < 2 * NC; ++i) o[i] *= keep;
+        for (int i = 0; i < Tr::kTiles; ++i) o[i] *= keep;
     }
     const float base = m == -INFINITY ? 0.0f : m;
     float p8[8];
@@ -348,13 +395,21 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
         if (!b.whole)
             for (int j = 0; j < 8; ++j) p8[j] = b.seen >> j & 1 ? p8[j] : 0.0f;
     bf16x8 p[PARTS];
-    split8<PARTS>(p8, p);
+    if constexpr (Tr::kExcess) {
+        const float in_order[8] = {p8[0], p8[2], p8[1], p8[3], p8[4], p8[6], p8[5], p8[7]};
+        split8<PARTS>(in_order, p);
+        const bf16x8 excess = __builtin_bit_cast(bf16x8, u32x4{kExcess, kExcess, kExcess, kExcess});
+        o[2 * NC] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(excess, p[0], o[2 * NC], 0, 0, 0);
+    } else {
+        split8<PARTS>(p8, p);
+    }
     for (int i = 0; i < Tr::kValueLoads; ++i) {
         const uint32_t* w = &b.v[i * Tr::kValueLoadWords];
         for (int e = 0; e < Tr::kDims; ++e) {
             bf16x8 v;
             if constexpr (BITS == 16) v = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
             else if constexpr (BITS == 8) v = bytes_to_bf16(w[2 * e], w[2 * e + 1]);
+            else if constexpr (Tr::kExcess) v = e % 2 == 0 ? nibbles_to_excess<0>(w[e], w[e + 1]) : nibbles_to_excess<4>(w[e - 1], w[e]);
             else if (e % 2 == 0) v = nibbles_to_bf16(w[e], w[e + 1]);
             else v = nibbles_to_bf16(upper_nibbles(w[e - 1]), upper_nibbles(w[e]));
             f32x4& acc = o[i * Tr::kDims + e];
@@ -366,7 +421,8 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
 // q of a lane's head as B operands.  Values of extreme size are brought near one by a power of two (which to_log2 takes back),
 // so that no sum on the way leaves the range of fp32.
 template <typename E, int NC, int BITS, int PARTS>
-__device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quarter, bf16x8 (&q)[NC][PARTS], float& to_log2) {
+__device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quarter, bf16x8 (&q)[NC][PARTS], float& less,
+                                       float& to_log2) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     Eight<E> y[NC];
     for (int c = 0; c < NC; ++c) {
@@ -383,59 +439,45 @@ __device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quart
         for (int c = 0; c < NC; ++c) y[c].scale(-e);
         to_log2 = ldexpf(to_log2, e);
     }
-    for (int c = 0; c < NC; ++c) y[c].operand(q[c]);
+    less = 0.0f;
+    for (int c = 0; c < NC; ++c) {
+        if constexpr (Tr::kExcess) less += y[c].codes_order();
+        y[c].operand(q[c]);
+    }
+    if constexpr (Tr::kExcess) less = sum_of_quarters(less);
 }
 
 template <typename E, int NC, int BITS, int PARTS>
-__global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attention_kernel(AttentionKernelArgs a) {
+__global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attention_kernel(AttentionKernelArgs a) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
-    __shared__ uint32_t line[256], sums[4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int quarter = lane >> 4, n = lane & 15;
+    const int lane = threadIdx.x, quarter = lane >> 4, n = lane & 15;
+    const uint32_t piece = blockIdx.x;
 
-    // the line of all blocks: a scan over the requests' lengths on it, `share` requests a thread
-    const int share = (a.R + 255) / 256;
-    {
-        uint32_t upto = 0;
-        for (int r = tid * share; r < min(a.R, (tid + 1) * share); ++r) upto += visible(a, r).blocks() + kBeginCost;
-        for (int i = 1; i < 64; i *= 2) {
-            const uint32_t y = __shfl_up(upto, i);
-            if (lane >= i) upto += y;
-        }
-        line[tid] = upto;
-        if (lane == 63) sums[wave] = upto;
-    }
-    __syncthreads();
-    const uint32_t all = sums[0] + sums[1] + sums[2] + sums[3], total = all * a.segments;
+    // the line of all blocks: a scan over the requests' lengths on it, `share` requests a lane
+    const int share = (a.R + 63) / 64;
+    uint32_t mine = 0;
+#pragma unroll 8
+    for (int i = 0; i < share; ++i)
+        if (lane * share + i < a.R) mine += visible(a, lane * share + i).blocks() + kBeginCost;
+    const uint32_t line = scan_of_wave(mine, lane), total = (uint32_t)__builtin_amdgcn_readlane((int)line, 63) * a.segments;
     const uint32_t chunk = max(kLeastPiece, a.by_pieces.quotient(total) + 1);
-    // neighbouring pieces are other workgroups': few pieces spread over the CUs
-    const uint32_t piece = wave * gridDim.x + blockIdx.x;
-    const bool by_piece = a.R * a.segments > (int)(4 * gridDim.x);  // how records are numbered
+    const bool by_piece = a.R * a.segments > (int)gridDim.x;        // how records are numbered
     if (by_piece && lane == 0) a.records[piece].parts = 0;
-    if (piece * (uint64_t)chunk >= total) return;
+    if ((uint64_t)piece * chunk >= total) return;
     const uint32_t begin = piece * chunk, end = min(begin + chunk, total);
 
-    // the request that the piece begins in: the thread whose requests' line holds it, then a walk over those
-    uint32_t base = 0;                                              // of request r, in places of one segment
-    int r;
-    {
-        const uint32_t at = a.by_segments.quotient(begin);
-        int before = 0;
-        uint32_t ahead = 0;
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t upto = line[w * 64 + lane] + ahead;
-            const uint64_t under = __ballot(upto <= at);
-            before += __popcll(under);
-            if (under) base = max(base, (uint32_t)__shfl(upto, 63 - __clzll(under)));
-            ahead += sums[w];
-        }
-        r = __builtin_amdgcn_readfirstlane(before) * share;
-        base = __builtin_amdgcn_readfirstlane(base);
-        for (;;) {
-            const uint32_t length = visible(a, r).blocks() + kBeginCost;
-            if (at < base + length) break;
-            base += length;
-            ++r;
+    // the request that the piece begins in: the lane whose requests hold it, then the one among those
+    const uint32_t at = a.by_segments.quotient(begin);
+    const int before = __popcll(__ballot(line <= at));
+    int r = before * share;
+    uint32_t base = before ? (uint32_t)__builtin_amdgcn_readlane((int)line, before - 1) : 0u;   // of request r, in places of one segment
+    for (; share > 1; r += 64) {
+        const uint32_t inner = scan_of_wave(r + lane < a.R ? visible(a, r + lane).blocks() + kBeginCost : 0u, lane) + base;
+        const int under = __popcll(__ballot(inner <= at));
+        if (under) base = (uint32_t)__builtin_amdgcn_readlane((int)inner, under - 1);
+        if (under < 64) {
+            r += under;
+            break;
         }
     }
 
@@ -470,18 +512,19 @@ __global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attenti
             const int32_t* table = a.table + r * a.ld_table;
             uint32_t t = (vis.block() + off) * kBlockTokens;
             int todo = vis.n > vis.first ? count : 0;
+            asm("" : "+v"(todo));                                   // as a lane's own the loop leaves the block in its registers
             Block<NC, BITS, PARTS> b;
             if (todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
             bf16x8 q[NC][PARTS];
-            float to_log2 = a.scale_log2e * (BITS == 4 ? 16.0f : 1.0f);
+            float less, to_log2 = a.scale_log2e * Tr::kUnit;
             load_q<E, NC, BITS, PARTS>(static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs, n < heads, a.D,
-                                       quarter, q, to_log2);
+                                       quarter, q, less, to_log2);
 
-            f32x4 o[2 * NC];
-            for (int i = 0; i < 2 * NC; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 o[Tr::kTiles];
+            for (int i = 0; i < Tr::kTiles; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             float m = -INFINITY, l = 0.0f;
             while (todo > 0) {
-                step<NC, BITS, PARTS>(b, q, to_log2, m, l, o);
+                step<NC, BITS, PARTS>(b, q, less, to_log2, m, l, o);
                 t += kBlockTokens;
                 if (--todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
             }
@@ -491,7 +534,7 @@ __global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attenti
             // four neighbouring dimensions at a time: j of value load i
             const bool whole = starts && ends;
             const uint32_t place = (2 * piece + (starts ? 1 : 0)) * a.rows + n;
-            const float inverse = (BITS == 4 ? 16.0f : 1.0f) * (whole ? l == 0.0f ? 0.0f : 1.0f / l : 1.0f);
+            const float inverse = Tr::kUnit * (whole ? l == 0.0f ? 0.0f : 1.0f / l : 1.0f);
             E* to = static_cast<E*>(a.out) + r * a.o_rs + (hq + n) * a.o_hs;
             float* part = a.partial_o + (uint64_t)place * Tr::kDp;
             for (int i = 0; i < Tr::kValueLoads; ++i)
@@ -499,6 +542,7 @@ __global__ __launch_bounds__(256, attention_waves(NC, BITS, PARTS)) void attenti
                     const int d = (16 * i + 4 * quarter) * Tr::kDims + 4 * j;
                     f32x4 y;
                     for (int z = 0; z < 4; ++z) y[z] = o[i * Tr::kDims + (4 * j + z) % Tr::kDims][(4 * j + z) / Tr::kDims];
+                    if constexpr (Tr::kExcess) y -= o[2 * NC];
                     if (!whole) *reinterpret_cast<f32x4*>(part + d) = y * inverse;
                     else if (d < a.D) store_four(to + d, l == 0.0f ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : y * inverse);
                 }
@@ -515,7 +559,7 @@ hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, 
     const auto launch = [&](auto e, auto parts, auto nc) {
         using E = decltype(e);
         constexpr int P = decltype(parts)::value, NC = decltype(nc)::value;
-        attention_kernel<E, NC, BITS, P><<<dim3((unsigned)attention_workgroups(NC, BITS, P)), 256, 0, stream>>>(a);
+        attention_kernel<E, NC, BITS, P><<<dim3((unsigned)attention_pieces(NC, BITS, P)), 64, 0, stream>>>(a);
     };
     const auto pick = [&](auto e, auto parts) {
         switch (chunks) {
