@@ -14,16 +14,6 @@ struct AttentionRecord {
     int32_t request, segment, first, parts;     // parts 0: nothing to join
 };
 
-// t / d = (umulhi(t, mul) + t) >> shift for t < 2^31
-struct Divisor {
-    uint32_t mul, shift;
-    Divisor(uint32_t d = 1) : shift(0) {
-        while (((uint64_t)1 << shift) < d) ++shift;
-        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
-    }
-    __device__ uint32_t quotient(uint32_t t) const { return (__umulhi(t, mul) + t) >> shift; }
-};
-
 struct AttentionKernelArgs {
     const void* q;
     void* out;

@@ -2,6 +2,8 @@
 // cache.hip, attention.hip; the pages' layout in include/gptq.h).
 #pragma once
 
+#include <type_traits>
+
 #include "gptq_common.hpp"
 
 namespace gptq {
@@ -16,6 +18,16 @@ struct Pages {
     uint8_t* p;
     int64_t n, page_stride, head_stride;   // bytes from one page, one head to the next
     int page_size, bits;
+};
+
+// t / d = (umulhi(t, mul) + t) >> shift for t < 2^31
+struct Divisor {
+    uint32_t mul, shift;
+    Divisor(uint32_t d = 1) : shift(0) {
+        while (((uint64_t)1 << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ uint32_t quotient(uint32_t t) const { return (__umulhi(t, mul) + t) >> shift; }
 };
 
 constexpr int64_t kMaxHeadSize = 256;
