@@ -1,13 +1,15 @@
 // The paged cache of keys and values: rows quantised as they are written, and read back.
 //
 // A row of a token and head is kept on the symmetric grid of gptq_quantize_layer: s = absmax / (2^(b-1) - 1/2), codes
-// round-half-even(x / s).  The rounding is exact, not that of a rounded quotient: with q = rint(x * (1 / s)) the remainder
-// x - q s is representable (q has at most 8 bits, |x - q s| is not above s / 2 by more than a few of x's last places), so
-// one fused multiply-add gives it and comparing it with s / 2 moves q to the neighbour where that is nearer, or even.
+// round-half-even(x / s).  The rounding is exact, not that of a rounded quotient.  x times the reciprocal is off by less than
+// 2^-15 (8 bits; 2^-19 with 4), so q = rint(x * (1 / s)) is right where it is not that near to a border.  A wave with a value
+// that is (one in twenty or fewer) takes the remainder x - q s, which is representable (q has at most 8 bits, |x - q s| is not
+// above s / 2 by more than a few of x's last places), from one fused multiply-add, and comparing it with s / 2 moves q to the
+// neighbour where that is nearer, or even.
 //
 // Memory traffic is the bound.  A wave takes eight tokens of a head (two heads of 64): a lane holds two or four
 // dimensions of each, so that rows are read and written in whole lines, their largest values found by maxima across the
-// lanes, and eight tokens of a lane's dimensions are what the values' layout stores side by side.  Where eight
+// lanes (of eight rows together, so that every step halves the registers), and eight tokens of a lane's dimensions are what the values' layout stores side by side.  Where eight
 // tokens fill eight slots from a multiple of eight on, in order, they are stored with 8 or 16 bytes a lane; the wave that
 // holds the first of them takes all eight, so that runs of any beginning in the batch are written so.  Other tokens' values
 // go byte by byte into the octets that they share with tokens of other calls.
@@ -31,12 +33,14 @@ struct CacheArgs {
     Divisor by_page;
 };
 
-__device__ __forceinline__ int exact_code(float x, float s, float inv, float low, float high) {
-    float q = rintf(x * inv);
-    const float rem = fmaf(-q, s, x), twice = 2.0f * fabsf(rem);
-    const bool odd = ((int)q & 1) != 0;
-    if (twice > s || (twice == s && odd)) q += copysignf(1.0f, rem);
-    return (int)fminf(fmaxf(q, low), high);
+constexpr float kRound = 12582912.0f;           // 1.5 2^23: added to a small value, the sum's last bits are that value rounded
+
+// x / s rounded to nearest, ties to even, in the last bits of kRound + the result.
+__device__ __forceinline__ float exact_round(float x, float s, float inv) {
+    const float t = fmaf(x, inv, kRound), q = t - kRound, rem = fmaf(-q, s, x), twice = fabsf(rem) + fabsf(rem);
+    const bool odd = (__float_as_uint(t) & 1u) != 0;
+    const bool off = (twice > s) | ((twice == s) & odd);
+    return t + (off ? copysignf(1.0f, rem) : 0.0f);
 }
 
 template <int BITS>
@@ -50,18 +54,42 @@ __device__ __forceinline__ uint32_t max_dpp(uint32_t x) {
     return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true));
 }
 
-// The largest of a row's lanes: all 64, or each half's 32.
-__device__ __forceinline__ uint32_t max_of_lanes(uint32_t x, bool halves) {
+__device__ __forceinline__ uint32_t max_of_sixteen(uint32_t x) {
     x = max_dpp<0xB1>(x);                       // quad_perm 1, 0, 3, 2
     x = max_dpp<0x4E>(x);                       // quad_perm 2, 3, 0, 1
     x = max_dpp<0x141>(x);                      // row_half_mirror
-    x = max_dpp<0x140>(x);                      // row_mirror
-    auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    x = max(r[0], r[1]);
-    if (halves) return x;
-    r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return max_dpp<0x140>(x);                   // row_mirror
+}
+
+__device__ __forceinline__ uint32_t max_swap32(uint32_t x, uint32_t y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
     return max(r[0], r[1]);
 }
+__device__ __forceinline__ uint32_t max_swap16(uint32_t x, uint32_t y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    return max(r[0], r[1]);
+}
+
+// The largest of eight rows' values over all lanes, or (TWO) over each half's 32: a lane's result is that of row row_of(lane),
+// and row i's is in lane lane_of(i) (of each half).  A swap puts two rows where one was: each step has half the registers.
+template <bool TWO>
+__device__ __forceinline__ uint32_t max_of_rows(const uint32_t (&m)[kOctet], int lane) {
+    if constexpr (TWO) {
+        uint32_t c[4];
+        for (int i = 0; i < 4; ++i) c[i] = max_of_sixteen(max_swap16(m[i], m[i + 4]));      // 16 lanes: i, the next 16: i + 4
+        const uint32_t low = lane & 1 ? c[1] : c[0], high = lane & 1 ? c[3] : c[2];
+        return lane & 2 ? high : low;
+    } else {
+        uint32_t a[4], b[2];
+        for (int i = 0; i < 4; ++i) a[i] = max_swap32(m[i], m[i + 4]);                      // lower half: i, upper: i + 4
+        for (int i = 0; i < 2; ++i) b[i] = max_of_sixteen(max_swap16(a[i], a[i + 2]));      // 16 lanes each: i, i + 2, i + 4, i + 6
+        return lane & 1 ? b[1] : b[0];
+    }
+}
+template <bool TWO>
+__device__ __forceinline__ int lane_of(int i) { return TWO ? (i >> 2) * 16 + (i & 3) : (i >> 1) * 16 + (i & 1); }
+template <bool TWO>
+__device__ __forceinline__ int row_of(int lane) { return TWO ? (lane & 3) + 4 * (lane >> 4 & 1) : (lane & 1) + 2 * (lane >> 4); }
 
 // N elements of any alignment that their type has, as they are stored; N stored from fp32.
 template <typename E, int N>
@@ -106,8 +134,10 @@ struct Tokens {
     int octet;                                  // the first of eight tokens that fill eight slots, or -1
     int32_t octet_slot;
     uint32_t single;                            // tokens in no such eight
+    int32_t row_slot;                           // slot of token row_of(lane)
 };
 
+template <bool TWO>
 __device__ __forceinline__ Tokens tokens_of(const CacheArgs& a, int t0, int lane) {
     Tokens w;
     const int t = t0 - (kOctet - 1) + lane;
@@ -126,21 +156,22 @@ __device__ __forceinline__ Tokens tokens_of(const CacheArgs& a, int t0, int lane
     w.octet = own ? __ffs((int)own) - 1 : -1;
     w.octet_slot = __builtin_amdgcn_readlane(slot, own ? w.octet + kOctet - 1 : 0);
     for (int j = 0; j < kOctet; ++j) w.slot[j] = __builtin_amdgcn_readlane(slot, j + kOctet - 1);
+    w.row_slot = __shfl(slot, row_of<TWO>(lane) + kOctet - 1);
     w.single = (uint32_t)(~covered >> (kOctet - 1)) & 0xFFu & ((1u << min(a.T - t0, kOctet)) - 1u);
     return w;
 }
 
-// A wave's rows: its lanes' head and dimensions.
-template <int PD>
+// A wave's rows: its lanes' head and dimensions.  TWO: each half has a head (of 64 dimensions).
+template <int PD, bool TWO>
 struct Lanes {
-    int head, d;
-    bool on, halves;
+    int head, d, from;                          // from: where a lane reads; one that has no part of a row, its beginning
+    bool on, inside;                            // has part of a block's row, of the elements
     __device__ Lanes(const CacheArgs& a, int lane) {
-        halves = a.Dp == 64;                    // PD 2: two heads
-        const int in = halves ? lane & 31 : lane;
-        head = blockIdx.y * (halves ? 2 : 1) + (halves ? lane >> 5 : 0);
-        d = in * PD;
+        head = TWO ? 2 * blockIdx.y + (lane >> 5) : blockIdx.y;
+        d = (TWO ? lane & 31 : lane) * PD;
         on = d < a.Dp && head < a.H;
+        inside = on && d < a.D;
+        from = d < a.D ? d : 0;
     }
 };
 
@@ -161,55 +192,84 @@ struct Rows {
     }
 };
 
-template <int BITS, int PD>
+template <int BITS, int PD, bool TWO>
 struct Codes {
     uint32_t code[kOctet][PD];
-    float scale[kOctet];
+    float mine;                                 // scale of row row_of(lane)
     template <typename E>
-    __device__ void of(const Rows<E, PD>& r, bool inside, bool halves) {        // not inside: zeros
-        constexpr float kLow = -(float)(1 << (BITS < 16 ? BITS - 1 : 0)), kHigh = -kLow - 1.0f;
-        for (int i = 0; i < kOctet; ++i) {
-            float x[PD];
-            for (int j = 0; j < PD; ++j) x[j] = inside ? r.x[i].get(j) : 0.0f;
-            if constexpr (BITS == 16) {
-                for (int j = 0; j < PD; ++j) code[i][j] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[j]);
-            } else {
-                uint32_t m = 0;
-                for (int j = 0; j < PD; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-                const float s = grid_scale<BITS>(max_of_lanes(m, halves)), inv = __builtin_amdgcn_rcpf(s);
-                scale[i] = s;
-                const bool fine = s == s;
-                for (int j = 0; j < PD; ++j)
-                    code[i][j] = fine ? (uint32_t)exact_code(x[j], s, inv, kLow, kHigh) & ((1u << BITS) - 1u) : 0u;
+    __device__ void of(const Rows<E, PD>& r, bool inside, int lane) {                       // not inside: zeros
+        float x[kOctet][PD];
+        for (int i = 0; i < kOctet; ++i)
+            for (int j = 0; j < PD; ++j) x[i][j] = r.x[i].get(j);
+        constexpr uint32_t kMask = (1u << BITS) - 1u;
+        const uint32_t part = inside ? kMask : 0u;
+        if constexpr (BITS == 16) {
+            for (int i = 0; i < kOctet; ++i)
+                for (int j = 0; j < PD; ++j) code[i][j] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[i][j]) & part;
+        } else {
+            uint32_t m[kOctet];
+            for (int i = 0; i < kOctet; ++i) {
+                m[i] = 0;
+                for (int j = 0; j < PD; ++j) m[i] = max(m[i], __float_as_uint(x[i][j]) & 0x7FFFFFFFu);
+            }
+            mine = grid_scale<BITS>(max_of_rows<TWO>(m, lane));                             // a lane finds the scale of one row
+            float scale[kOctet], inv[kOctet], most = 0.0f;
+            for (int i = 0; i < kOctet; ++i) {
+                const int from = lane_of<TWO>(i);
+                scale[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from));
+                if (TWO) scale[i] = lane < 32 ? scale[i] : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from + 32));
+                inv[i] = __builtin_amdgcn_rcpf(scale[i]);
+            }
+            float t[kOctet][PD];
+            for (int i = 0; i < kOctet; ++i)
+                for (int j = 0; j < PD; ++j) {
+                    t[i][j] = fmaf(x[i][j], inv[i], kRound);
+                    most = fmaxf(most, fabsf(fmaf(x[i][j], inv[i], kRound - t[i][j])));
+                }
+            if (__any(most > 0.5f - (BITS == 8 ? 0x1p-15f : 0x1p-19f)))
+                for (int i = 0; i < kOctet; ++i)
+                    for (int j = 0; j < PD; ++j) t[i][j] = exact_round(x[i][j], scale[i], inv[i]);
+            const int top = __float_as_int(kRound) + (int)(kMask >> 1);
+            for (int i = 0; i < kOctet; ++i) {
+                const uint32_t mask = scale[i] == scale[i] ? part : 0u;                     // rows that are not finite: zeros
+                for (int j = 0; j < PD; ++j) code[i][j] = (uint32_t)min(__float_as_int(t[i][j]), top) & mask;
             }
         }
     }
 };
 
-template <typename E, int BITS, int PD>
+template <typename E, int BITS, int PD, bool TWO>
 __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
     const int lane = threadIdx.x & 63, t0 = (blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kOctet;
     if (t0 >= a.T) return;
-    const Lanes<PD> l(a, lane);
-    const Tokens w = tokens_of(a, t0, lane);
+    const Lanes<PD, TWO> l(a, lane);
+    const Tokens w = tokens_of<TWO>(a, t0, lane);
     uint32_t valid = 0;
     for (int i = 0; i < kOctet; ++i) valid |= (uint32_t)(w.slot[i] >= 0) << i;
     const uint32_t single = w.single & valid;
     if (!valid && w.octet < 0) return;
     const uint32_t part = (uint32_t)a.page_size * a.Dp * BITS / 8;
     uint8_t* head = a.pages + l.head * a.head_stride;
-    // lanes without an element of a row read the first of the first head
-    const bool inside = l.on && l.d < a.D, together = w.octet >= 0;
-    const E* k = static_cast<const E*>(a.k) + t0 * a.k_ts + (inside ? l.head * a.k_hs + l.d : 0);
-    const E* v = static_cast<const E*>(a.v) + t0 * a.v_ts + (inside ? l.head * a.v_hs + l.d : 0);
+    const bool together = w.octet >= 0;
+    const int source = min(l.head, a.H - 1);
+    const E* k = static_cast<const E*>(a.k) + t0 * a.k_ts + source * a.k_hs + l.from;
+    const E* v = static_cast<const E*>(a.v) + t0 * a.v_ts + source * a.v_hs + l.from;
+    // the scales' lanes: eight in a head, with a row each
+    const bool scaler = BITS < 16 && (lane & 15) < (TWO ? 4 : 2) && l.head < a.H;
+    const int row = row_of<TWO>(lane);
+    const auto write_scale = [&](float s, int32_t slot, bool values) {
+        const Place p(a, slot);
+        reinterpret_cast<float*>(head + (int64_t)p.page * a.page_stride + 2 * part)[(values ? a.page_size : 0) + p.at] = s;
+    };
 
     Rows<E, PD> x, z;
     if (valid) x.load(k, a.k_ts, 0, valid);
     if (together || single) z.load(v, a.v_ts, together ? w.octet : 0, together ? 0xFFu : single);
-    Codes<BITS, PD> c;
+    Codes<BITS, PD, TWO> c;
 
     // keys: a row per token
-    c.of(x, inside, l.halves);
+    c.of(x, l.inside, lane);
+    if (scaler && (valid >> row & 1)) write_scale(c.mine, w.row_slot, false);
     for (int i = 0; i < kOctet; ++i) {
         if (!(valid >> i & 1) || !l.on) continue;
         const Place p(a, w.slot[i]);
@@ -223,12 +283,12 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
             if constexpr (BITS * PD == 8) *to = (uint8_t)y;
             else if constexpr (BITS * PD == 16) *reinterpret_cast<uint16_t*>(to) = (uint16_t)y;
             else *reinterpret_cast<uint32_t*>(to) = y;
-            if (l.d == 0) reinterpret_cast<float*>(block + 2 * part)[p.at] = c.scale[i];
         }
     }
 
-    c.of(z, inside, l.halves);
+    c.of(z, l.inside, lane);
     if (together) {
+        if (scaler) write_scale(c.mine, w.octet_slot + row, true);
         const Place p(a, w.octet_slot);
         uint8_t* block = head + (int64_t)p.page * a.page_stride;
         if (l.on) {
@@ -254,17 +314,12 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
                 for (int i = 0; i < BITS * PD / 16; ++i)
                     reinterpret_cast<u32x4*>(to)[i] = u32x4{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
             }
-            if constexpr (BITS < 16)
-                if (l.d == 0) {
-                    f32x4* s = reinterpret_cast<f32x4*>(block + 2 * part + 4 * (a.page_size + p.at));
-                    s[0] = f32x4{c.scale[0], c.scale[1], c.scale[2], c.scale[3]};
-                    s[1] = f32x4{c.scale[4], c.scale[5], c.scale[6], c.scale[7]};
-                }
         }
         if (!single) return;
         z.load(v, a.v_ts, 0, single);               // beside an octet, at the end of a run
-        c.of(z, inside, l.halves);
+        c.of(z, l.inside, lane);
     }
+    if (scaler && (single >> row & 1)) write_scale(c.mine, w.row_slot, true);
     for (int i = 0; i < kOctet; ++i) {
         if (!(single >> i & 1) || !l.on) continue;
         const Place p(a, w.slot[i]);
@@ -277,8 +332,6 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
         } else {
             for (int j = 0; j < PD / 2; ++j) to[8 * j] = (uint8_t)(c.code[i][2 * j] | c.code[i][2 * j + 1] << 4);
         }
-        if constexpr (BITS < 16)
-            if (l.d == 0) reinterpret_cast<float*>(block + 2 * part)[a.page_size + p.at] = c.scale[i];
     }
 }
 
@@ -337,13 +390,13 @@ struct Kept {
     }
 };
 
-template <typename E, int BITS, int PD>
+template <typename E, int BITS, int PD, bool TWO>
 __global__ __launch_bounds__(256) void cache_read_kernel(CacheArgs a) {
     const int lane = threadIdx.x & 63, t0 = (blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kOctet;
     if (t0 >= a.T) return;
-    const Lanes<PD> l(a, lane);
-    const Tokens w = tokens_of(a, t0, lane);
-    if (!l.on || l.d >= a.D) return;
+    const Lanes<PD, TWO> l(a, lane);
+    const Tokens w = tokens_of<TWO>(a, t0, lane);
+    if (!l.inside) return;
     const uint32_t part = (uint32_t)a.page_size * a.Dp * BITS / 8, own = (1u << min(a.T - t0, kOctet)) - 1u;
     const uint8_t* head = a.pages + l.head * a.head_stride;
     E* k = (E*)a.k + t0 * a.k_ts + l.head * a.k_hs + l.d;
@@ -406,21 +459,33 @@ struct CacheGrid {
     }
 };
 
+// launch(element, dimensions of a lane, whether a wave has two heads)
+template <typename F>
+void for_lanes(const CacheArgs& a, bool f32, const F& launch) {
+    const auto with = [&](auto e) {
+        if (a.Dp == 64) launch(e, std::integral_constant<int, 2>{}, std::true_type{});
+        else if (a.Dp <= 128) launch(e, std::integral_constant<int, 2>{}, std::false_type{});
+        else launch(e, std::integral_constant<int, 4>{}, std::false_type{});
+    };
+    if (f32) with(0.0f);
+    else with((__bf16)0.0f);
+}
+
 }  // namespace
 
 hipError_t cache_write(HeadRows k, HeadRows v, bool f32, int64_t T, int H, int D, const int32_t* slots, Pages pages,
                        hipStream_t stream) {
     const CacheArgs a = cache_args(k, v, T, H, D, slots, pages);
     const CacheGrid g(a);
-    const auto pick = [&](auto e, auto pd) {
+    const auto launch = [&](auto e, auto pd, auto two) {
         using E = decltype(e);
         constexpr int PD = decltype(pd)::value;
-        return pages.bits == 16 ? cache_write_kernel<E, 16, PD> : pages.bits == 8 ? cache_write_kernel<E, 8, PD> : cache_write_kernel<E, 4, PD>;
+        constexpr bool TWO = decltype(two)::value;
+        if (pages.bits == 16) cache_write_kernel<E, 16, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
+        else if (pages.bits == 8) cache_write_kernel<E, 8, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
+        else cache_write_kernel<E, 4, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
     };
-    const auto two = std::integral_constant<int, 2>{};
-    const auto four = std::integral_constant<int, 4>{};
-    auto* kernel = a.Dp <= 128 ? (f32 ? pick(0.0f, two) : pick((__bf16)0.0f, two)) : (f32 ? pick(0.0f, four) : pick((__bf16)0.0f, four));
-    kernel<<<g.grid, g.threads, 0, stream>>>(a);
+    for_lanes(a, f32, launch);
     return hipGetLastError();
 }
 
@@ -428,15 +493,15 @@ hipError_t cache_read(Pages pages, const int32_t* slots, int64_t T, int H, int D
                       hipStream_t stream) {
     const CacheArgs a = cache_args(k, v, T, H, D, slots, pages);
     const CacheGrid g(a);
-    const auto pick = [&](auto e, auto pd) {
+    const auto launch = [&](auto e, auto pd, auto two) {
         using E = decltype(e);
         constexpr int PD = decltype(pd)::value;
-        return pages.bits == 16 ? cache_read_kernel<E, 16, PD> : pages.bits == 8 ? cache_read_kernel<E, 8, PD> : cache_read_kernel<E, 4, PD>;
+        constexpr bool TWO = decltype(two)::value;
+        if (pages.bits == 16) cache_read_kernel<E, 16, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
+        else if (pages.bits == 8) cache_read_kernel<E, 8, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
+        else cache_read_kernel<E, 4, PD, TWO><<<g.grid, g.threads, 0, stream>>>(a);
     };
-    const auto two = std::integral_constant<int, 2>{};
-    const auto four = std::integral_constant<int, 4>{};
-    auto* kernel = a.Dp <= 128 ? (f32 ? pick(0.0f, two) : pick((__bf16)0.0f, two)) : (f32 ? pick(0.0f, four) : pick((__bf16)0.0f, four));
-    kernel<<<g.grid, g.threads, 0, stream>>>(a);
+    for_lanes(a, f32, launch);
     return hipGetLastError();
 }
 
