@@ -784,11 +784,12 @@ _STORED = {D: next(n for n in (64, 96, 128, 192, 256) if n >= D) for D in range(
 
 def _heads(t: torch.Tensor, name: str, device) -> tuple:
     """Strides from token to token and head to head of a T x H x D tensor with unit element stride, on the GPU."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the GPU of the other tensors")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+    strides = t.stride()
+    if len(strides) != 3 or (strides[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name} must be tokens x heads x elements with unit element stride")
-    return t.stride(0), t.stride(1)
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU of the other tensors")
+    return strides[0], strides[1]
 
 
 def _row_type(t: torch.Tensor) -> int:
@@ -798,19 +799,25 @@ def _row_type(t: torch.Tensor) -> int:
     return dt
 
 
+@functools.lru_cache(maxsize=None)
+def _slot_bytes(D: int, bits: int) -> int:
+    if bits not in (4, 8, 16) or D not in _STORED:
+        raise ValueError("bits must be 4, 8 or 16, and the head size a multiple of 8 up to 256")
+    return 2 * (_STORED[D] * bits // 8) + (8 if bits < 16 else 0)
+
+
 def _pages(pages: torch.Tensor, H: int, D: int, bits: int, device) -> tuple:
     """Page count, strides and page size of a uint8 pages x heads x block tensor."""
     if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.device != device or not pages.is_cuda:
         raise ValueError("pages must be uint8 pages x heads x bytes on the GPU of the other tensors")
     n, heads, block = pages.shape
-    if heads != H or pages.stride(2) != 1:
+    page, head, byte = pages.stride()
+    if heads != H or byte != 1:
         raise ValueError(f"pages must hold {H} heads, each a contiguous block")
-    if bits not in (4, 8, 16) or D not in _STORED:
-        raise ValueError("bits must be 4, 8 or 16, and the head size a multiple of 8 up to 256")
-    slot = 2 * (_STORED[D] * bits // 8) + (8 if bits < 16 else 0)
-    if block < 1 or block % slot != 0:
-        raise ValueError(f"blocks of {block} bytes hold no whole number of slots of {slot} (gptq_cache_block_bytes)")
-    return n, pages.stride(0), pages.stride(1), block // slot
+    size, rest = divmod(block, _slot_bytes(D, bits))
+    if rest or size < 1:
+        raise ValueError(f"blocks of {block} bytes hold no whole number of slots of {_slot_bytes(D, bits)} (gptq_cache_block_bytes)")
+    return n, page, head, size
 
 
 def gptq_rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -849,7 +856,7 @@ def gptq_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, i
     if positions.numel() != T or freqs.dim() != 1:
         raise ValueError("positions must hold an entry per token, freqs be a vector")
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        out = x.new_empty((T, H, D))
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must match x")
     y_ts, y_hs = _heads(out, "out", dev)
@@ -899,7 +906,7 @@ def gptq_cache_read(pages: torch.Tensor, slots: torch.Tensor, D: int, bits: int,
     dev, H, T = pages.device, pages.shape[1], slots.numel()
     n, ps, hs, size = _pages(pages, H, D, bits, dev)
     sp = _device_tensor(slots, "slots", torch.int32, dev)
-    k, v = torch.empty((2, T, H, D), dtype=dtype, device=dev)
+    k, v = torch.empty((2, T, H, D), dtype=dtype, device=dev).unbind()
     _check(load().gptq_cache_read(pages.data_ptr(), n, ps, hs, size, bits, sp, T, H, D, k.data_ptr(), v.data_ptr(),
                                   _row_type(k), H * D, D, H * D, D, _handle(dev)), "gptq_cache_read")
     return k, v
@@ -931,14 +938,17 @@ def gptq_cache_attention(q: torch.Tensor, pages: torch.Tensor, table: torch.Tens
         raise ValueError("pages must be uint8 pages x heads x bytes")
     H = pages.shape[1]
     n, ps, hs, size = _pages(pages, H, D, bits, dev)
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or table.device != dev \
-            or (table.stride(1) != 1 and table.shape[1] > 1):
-        raise ValueError("table must be int32 requests x pages with unit column stride on the GPU of q")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.device != dev:
+        raise ValueError("table must be int32 requests x pages on the GPU of q")
+    rows, columns = table.shape
+    ld, unit = table.stride()
+    if rows != R or (unit != 1 and columns > 1):
+        raise ValueError("table must hold a row per request, with unit column stride")
     lp = _device_tensor(lengths, "lengths", torch.int32, dev)
     if lengths.numel() != R:
         raise ValueError("lengths must hold an entry per request")
     if out is None:
-        out = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
+        out = q.new_empty((R, Hq, D))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     o_rs, o_hs = _heads(out, "out", dev)
@@ -951,7 +961,7 @@ def gptq_cache_attention(q: torch.Tensor, pages: torch.Tensor, table: torch.Tens
     need = 0 if workspace is not None else lib.gptq_attention_workspace_bytes(R, Hq, H, D)
     workspace, wp, wb = _scratch(need, dev, workspace)
     _check(lib.gptq_cache_attention(q.data_ptr(), dt, R, Hq, H, D, q_rs, q_hs, pages.data_ptr(), n, ps, hs, size, bits,
-                                    table.data_ptr(), table.stride(0), table.shape[1], lp,
+                                    table.data_ptr(), ld, columns, lp,
                                     D ** -0.5 if scale is None else scale, window, out.data_ptr(), o_rs, o_hs, ep, wp, wb,
                                     _handle(dev)), "gptq_cache_attention")
     return out

@@ -1,12 +1,16 @@
 // Rotary positions: every pair of a head's elements turned by position * frequency.
 //
 // The angle is taken in turns and in 64 bits: position * f / 2 pi loses its whole turns there, so that what the sine and
-// cosine see is a fraction of a turn with 2^-32 or better at any 32-bit position; they are evaluated in fp32.
+// cosine see is a fraction of a turn with 2^-32 or better at any 32-bit position; they are evaluated in fp32, once for a
+// token's pair whatever the number of heads, and wait in LDS.  What is left is a copy: a workgroup takes some tokens' rows of
+// some heads, 16 bytes a load where the pairs allow it (units of V pairs), and is bound by memory traffic.
 #include "context.hpp"
 
 namespace gptq {
 
 namespace {
+
+constexpr int kThreads = 256, kMaxPairs = 1024;     // pairs of a workgroup's tokens, in LDS
 
 struct RotaryArgs {
     const void* x;
@@ -15,11 +19,11 @@ struct RotaryArgs {
     const int32_t* positions;
     const double* freqs;
     float factor;
-    int T, H, D, rot;
+    int T, H, D, half;
+    int tokens, heads;              // of a workgroup
+    int turned, units;              // units of a row that are turned, and all of them
+    Divisor by_units, by_heads;
 };
-
-template <typename E>
-__device__ __forceinline__ float as_float(E v) { return (float)v; }
 
 // cos and sin of position * f, times the factor
 __device__ __forceinline__ f32x2 turn(int position, double f, float factor) {
@@ -32,34 +36,156 @@ __device__ __forceinline__ f32x2 turn(int position, double f, float factor) {
     return cs;
 }
 
-template <typename E, bool INTERLEAVED>
-__global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
-    const int t = blockIdx.x, half = a.rot / 2;
-    const int position = a.positions[t];
-    for (int i = threadIdx.x; i < a.H * (a.D - half); i += 256) {
-        const int h = i / (a.D - half), j = i % (a.D - half);
-        const E* x = static_cast<const E*>(a.x) + t * a.x_ts + h * a.x_hs;
-        E* y = static_cast<E*>(a.y) + t * a.y_ts + h * a.y_hs;
-        if (j < half) {
-            const f32x2 cs = turn(position, a.freqs[j], a.factor);
-            const int d0 = INTERLEAVED ? 2 * j : j, d1 = INTERLEAVED ? 2 * j + 1 : j + half;
-            const float u = as_float(x[d0]), w = as_float(x[d1]);
-            y[d0] = (E)(u * cs[0] - w * cs[1]);
-            y[d1] = (E)(w * cs[0] + u * cs[1]);
+// N elements of any alignment that their type has.
+template <int N>
+__device__ __forceinline__ void load(const float* p, float (&x)[N]) {
+    typedef float __attribute__((ext_vector_type(N))) vec;
+    typedef vec __attribute__((aligned(4))) any;
+    if constexpr (N == 1) {
+        x[0] = *p;
+    } else {
+        const vec v = *reinterpret_cast<const any*>(p);
+        for (int i = 0; i < N; ++i) x[i] = v[i];
+    }
+}
+template <int N>
+__device__ __forceinline__ void load(const __bf16* p, float (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = (float)*p;
+    } else {
+        typedef uint32_t __attribute__((ext_vector_type(N / 2))) vec;
+        typedef vec __attribute__((aligned(2))) any;
+        const vec v = *reinterpret_cast<const any*>(p);
+        for (int i = 0; i < N; ++i) x[i] = i % 2 ? bf16hi_to_f32(v[i / 2]) : bf16lo_to_f32(v[i / 2]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store(float* p, const float (&x)[N]) {
+    typedef float __attribute__((ext_vector_type(N))) vec;
+    typedef vec __attribute__((aligned(4))) any;
+    if constexpr (N == 1) {
+        *p = x[0];
+    } else {
+        vec v;
+        for (int i = 0; i < N; ++i) v[i] = x[i];
+        *reinterpret_cast<any*>(p) = v;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store(__bf16* p, const float (&x)[N]) {
+    if constexpr (N == 1) {
+        *p = (__bf16)x[0];
+    } else {
+        typedef uint32_t __attribute__((ext_vector_type(N / 2))) vec;
+        typedef vec __attribute__((aligned(2))) any;
+        vec v;
+        for (int i = 0; i < N / 2; ++i) v[i] = pack_bf16x2_rne(x[2 * i], x[2 * i + 1]);
+        *reinterpret_cast<any*>(p) = v;
+    }
+}
+
+// N elements as they are (N even).
+template <int N, typename E>
+__device__ __forceinline__ void copy(const E* p, E* q) {
+    typedef uint32_t __attribute__((ext_vector_type(N * sizeof(E) / 4))) vec;
+    typedef vec __attribute__((aligned(sizeof(E)))) any;
+    *reinterpret_cast<any*>(q) = *reinterpret_cast<const any*>(p);
+}
+
+// A unit: V pairs to be turned, or up to 2 V elements to be copied.
+template <typename E, int V, bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
+    __shared__ f32x2 turns[kMaxPairs];
+    const int t0 = blockIdx.x * a.tokens, h0 = blockIdx.y * a.heads;
+    const int tokens = min(a.tokens, a.T - t0), heads = min(a.heads, a.H - h0);
+    for (int i = threadIdx.x; i < tokens * a.half; i += kThreads) {
+        const int t = i / a.half, j = i - t * a.half;
+        turns[i] = turn(a.positions[t0 + t], a.freqs[j], a.factor);
+    }
+    __syncthreads();
+    const int all = tokens * a.heads * a.units;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < all; i += kThreads) {
+        const int row = (int)a.by_units.quotient((uint32_t)i), u = i - row * a.units;
+        const int t = (int)a.by_heads.quotient((uint32_t)row), h = row - t * a.heads;
+        if (h >= heads) continue;
+        const E* x = static_cast<const E*>(a.x) + (t0 + t) * a.x_ts + (h0 + h) * a.x_hs;
+        E* y = static_cast<E*>(a.y) + (t0 + t) * a.y_ts + (h0 + h) * a.y_hs;
+        if (u < a.turned) {
+            const f32x2* cs = &turns[t * a.half + u * V];
+            float p[V], q[V];
+            if constexpr (INTERLEAVED) {
+                float w[2 * V];
+                load<2 * V>(x + 2 * V * u, w);
+                for (int k = 0; k < V; ++k) {
+                    p[k] = w[2 * k] * cs[k][0] - w[2 * k + 1] * cs[k][1];
+                    q[k] = w[2 * k + 1] * cs[k][0] + w[2 * k] * cs[k][1];
+                }
+                for (int k = 0; k < V; ++k) w[2 * k] = p[k], w[2 * k + 1] = q[k];
+                store<2 * V>(y + 2 * V * u, w);
+            } else {
+                load<V>(x + V * u, p);
+                load<V>(x + a.half + V * u, q);
+                for (int k = 0; k < V; ++k) {
+                    const float r = p[k] * cs[k][0] - q[k] * cs[k][1];
+                    q[k] = q[k] * cs[k][0] + p[k] * cs[k][1];
+                    p[k] = r;
+                }
+                store<V>(y + V * u, p);
+                store<V>(y + a.half + V * u, q);
+            }
         } else {
-            y[j + half] = x[j + half];
+            const int d = 2 * a.half + 2 * V * (u - a.turned);
+            if (d + 2 * V <= a.D) {
+                copy<2 * V>(x + d, y + d);
+            } else {
+                for (int k = d; k < a.D; ++k) y[k] = x[k];
+            }
         }
     }
+}
+
+template <typename E, int V>
+void launch(RotaryArgs a, bool interleaved, hipStream_t stream) {
+    const bool copies = a.x != a.y;
+    a.turned = a.half / V;
+    a.units = a.turned + (copies ? (int)ceil_div(a.D - 2 * a.half, 2 * V) : 0);
+    // Workgroups of up to 2048 units, or fewer where there would not be two for every CU: first some heads of a token (whose
+    // sines each of its workgroups then finds for itself), then more tokens.
+    const int64_t total = (int64_t)a.T * a.H * a.units;
+    const int64_t each = total / 512 < kThreads ? kThreads : total / 512 > 2048 ? 2048 : total / 512;
+    a.heads = (int)(ceil_div(each, a.units) < a.H ? ceil_div(each, a.units) : a.H);
+    a.tokens = 1;
+    if (a.heads == a.H) {
+        const int64_t by_units = each / ((int64_t)a.H * a.units), by_pairs = kMaxPairs / a.half;
+        a.tokens = (int)(by_units < by_pairs ? by_units : by_pairs);
+        if (a.tokens < 1) a.tokens = 1;
+    }
+    a.by_units = Divisor((uint32_t)a.units);
+    a.by_heads = Divisor((uint32_t)a.heads);
+    const dim3 grid((unsigned)ceil_div(a.T, a.tokens), (unsigned)ceil_div(a.H, a.heads));
+    if (interleaved) rotary_kernel<E, V, true><<<grid, kThreads, 0, stream>>>(a);
+    else rotary_kernel<E, V, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
 
 hipError_t rotary(HeadRows x, bool f32, int64_t T, int H, int D, const int32_t* positions, const double* freqs, int rot,
                   float factor, bool interleaved, HeadRows y, hipStream_t stream) {
-    RotaryArgs a{x.p, y.p, x.ts, x.hs, y.ts, y.hs, positions, freqs, factor, (int)T, H, D, rot};
-    auto* kernel = f32 ? (interleaved ? rotary_kernel<float, true> : rotary_kernel<float, false>)
-                       : (interleaved ? rotary_kernel<__bf16, true> : rotary_kernel<__bf16, false>);
-    kernel<<<dim3((unsigned)T), 256, 0, stream>>>(a);
+    RotaryArgs a{};
+    a.x = x.p, a.y = y.p, a.x_ts = x.ts, a.x_hs = x.hs, a.y_ts = y.ts, a.y_hs = y.hs;
+    a.positions = positions, a.freqs = freqs, a.factor = factor;
+    a.T = (int)T, a.H = H, a.D = D, a.half = rot / 2;
+    // 16 bytes a load in halves, 16 or 32 of neighbours; pairs that are no multiple of that go one by one
+    if (f32) {
+        if (a.half % 4 == 0) launch<float, 4>(a, interleaved, stream);
+        else if (a.half % 2 == 0) launch<float, 2>(a, interleaved, stream);
+        else launch<float, 1>(a, interleaved, stream);
+    } else {
+        if (a.half % 8 == 0) launch<__bf16, 8>(a, interleaved, stream);
+        else if (a.half % 2 == 0) launch<__bf16, 2>(a, interleaved, stream);
+        else launch<__bf16, 1>(a, interleaved, stream);
+    }
     return hipGetLastError();
 }
 

@@ -124,6 +124,18 @@ def test_rotary_keeps_what_is_not_finite_in_its_pair():
 
 
 @gpu
+@pytest.mark.parametrize("dtype,raw", [(BF16, torch.int16), (F32, torch.int32)])
+def test_rotary_copies_the_rest_as_it_is(dtype, raw):
+    """Whatever the bits: infinities, NaN of any payload, the smallest values."""
+    bits = torch.randint(-2 ** 15, 2 ** 15, (3, 2, 128), generator=torch.Generator().manual_seed(1)).to(torch.int16)
+    x = bits.view(BF16) if dtype == BF16 else (bits.int() * 65537).view(F32)
+    freqs = g.gptq_rotary_frequencies(32)[0].to(DEV)
+    for interleaved in (False, True):
+        y = g.gptq_rotary(x.to(DEV), ints([1, 2, 3]), freqs, interleaved).cpu()
+        assert torch.equal(y[..., 32:].contiguous().view(raw), x[..., 32:].contiguous().view(raw))
+
+
+@gpu
 def test_rotary_of_no_tokens():
     freqs, _ = g.gptq_rotary_frequencies(64)
     assert g.gptq_rotary(torch.empty(0, 3, 64, device=DEV), ints([]), freqs.to(DEV)).shape == (0, 3, 64)
