@@ -41,7 +41,7 @@ struct AttentionKernelArgs {
 // Waves of a SIMD that the registers are laid out for, and pieces of a launch: one for each of the 256 CUs' waves.
 constexpr int attention_waves(int chunks, int bits, int parts) {
     if (parts == 1 && chunks <= 4) return bits == 16 && chunks == 4 ? 2 : 3;
-    return parts == 1 || chunks <= 4 ? 2 : 1;
+    return (parts == 1 && !(bits == 16 && chunks == 8)) || (parts == 3 && chunks <= 4) ? 2 : 1;
 }
 constexpr int attention_pieces(int chunks, int bits, int parts) { return 1024 * attention_waves(chunks, bits, parts); }
 

@@ -14,8 +14,9 @@
 // the scores before they are begun, that of the output after them, from a product with (24, -23).  The signs alternate so that
 // the sums stay near the size of their result (an excess of one sign would reach 24 where the mean of many codes is near 0).
 // A token's key scale multiplies its score, its value scale its probability.  With fp32 rows q and the probabilities are cut into three
-// bf16 parts each (exact), so that nothing is rounded but sums.  bf16 rows round probability times scale to bf16: an error
-// of 2^-9 in each of many terms, where the output's own rounding is 2^-9 of their sum.
+// bf16 parts each (exact), so that nothing is rounded but sums.  bf16 rows have probability times scale in two bf16 parts, 16 of
+// its 24 bits: one part's error, 2^-9 of each of many terms of either sign, is as large in their sum as the output's own
+// rounding (against 64 bits 2.5e-3 where that alone is 1.7e-3).
 //
 // Softmax: scores are kept times log2 e.  A lane's maximum is raised (and what was summed rescaled) only where a score passes it
 // by 8: probabilities then reach 2^8, which fp32 sums and bf16 factors bear as well as 1, and few steps rescale.
@@ -117,22 +118,20 @@ __device__ __forceinline__ bf16x8 nibbles_to_excess(uint32_t w0, uint32_t w1) {
     return __builtin_bit_cast(bf16x8, u32x4{excess_pair<HALF>(w0), excess_pair<HALF + 8>(w0), excess_pair<HALF>(w1), excess_pair<HALF + 8>(w1)});
 }
 
-// Eight fp32 values as PARTS bf16 operands: rounded (1), or cut into three parts of eight bits each, exactly.
+// Eight fp32 values as PARTS bf16 operands, each but the last cut off after eight bits (exact with three), the last of two rounded.
 template <int PARTS>
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]) {
-    if constexpr (PARTS == 1) {
+    float rest[8];
+    for (int i = 0; i < 8; ++i) rest[i] = x[i];
+    for (int p = 0; p < PARTS; ++p) {
         u32x4 r;
-        for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2_rne(x[2 * i], x[2 * i + 1]);
-        out[0] = __builtin_bit_cast(bf16x8, r);
-    } else {
-        float rest[8];
-        for (int i = 0; i < 8; ++i) rest[i] = x[i];
-        for (int p = 0; p < PARTS; ++p) {
-            u32x4 r;
+        if (PARTS == 2 && p == 1) {
+            for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2_rne(rest[2 * i], rest[2 * i + 1]);
+        } else {
             for (int i = 0; i < 4; ++i) r[i] = high_halves(rest[2 * i], rest[2 * i + 1]);
-            out[p] = __builtin_bit_cast(bf16x8, r);
             for (int i = 0; i < 8; ++i) rest[i] -= __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u);
         }
+        out[p] = __builtin_bit_cast(bf16x8, r);
     }
 }
 
@@ -264,6 +263,7 @@ struct AttentionTraits {
     static constexpr int kValueLoadWords = kDims * BITS / 4;
     static constexpr bool kExcess = BITS == 4 && PARTS == 1;        // codes enter as code + 24 and code - 23
     static constexpr float kUnit = BITS == 4 && !kExcess ? 16.0f : 1.0f;
+    static constexpr int kProbabilityParts = PARTS == 1 ? 2 : 3;
     static constexpr int kTiles = 2 * NC + (kExcess ? 1 : 0);       // of the output, and the sums of its excess
 };
 
@@ -394,14 +394,16 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     if constexpr (BITS < 16)
         if (!b.whole)
             for (int j = 0; j < 8; ++j) p8[j] = b.seen >> j & 1 ? p8[j] : 0.0f;
-    bf16x8 p[PARTS];
+    constexpr int kParts = Tr::kProbabilityParts;
+    bf16x8 p[kParts];
     if constexpr (Tr::kExcess) {
         const float in_order[8] = {p8[0], p8[2], p8[1], p8[3], p8[4], p8[6], p8[5], p8[7]};
-        split8<PARTS>(in_order, p);
+        split8<kParts>(in_order, p);
         const bf16x8 excess = __builtin_bit_cast(bf16x8, u32x4{kExcess, kExcess, kExcess, kExcess});
-        o[2 * NC] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(excess, p[0], o[2 * NC], 0, 0, 0);
+        for (int part = kParts - 1; part >= 0; --part)
+            o[2 * NC] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(excess, p[part], o[2 * NC], 0, 0, 0);
     } else {
-        split8<PARTS>(p8, p);
+        split8<kParts>(p8, p);
     }
     for (int i = 0; i < Tr::kValueLoads; ++i) {
         const uint32_t* w = &b.v[i * Tr::kValueLoadWords];
@@ -413,7 +415,7 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
             else if (e % 2 == 0) v = nibbles_to_bf16(w[e], w[e + 1]);
             else v = nibbles_to_bf16(upper_nibbles(w[e - 1]), upper_nibbles(w[e]));
             f32x4& acc = o[i * Tr::kDims + e];
-            for (int part = PARTS - 1; part >= 0; --part) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[part], acc, 0, 0, 0);
+            for (int part = kParts - 1; part >= 0; --part) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[part], acc, 0, 0, 0);
         }
     }
 }

@@ -10,7 +10,9 @@ bf16):
     one, the scales' products and the multiplication by scale log2(e): es = 20 u scale sum |q k|, and u of the score
     itself when the largest is taken off (2 es + 4 u |score|).  A probability is then off by that relative part and 4 u of
     its exponential.  Sums over the tokens: one rounding per 32 tokens of a wave, then the joins: (n / 32 + 64) u.  bf16
-    rows round each probability times its value's scale to bf16 once: 2^-8.  All of it times sum p |v|.
+    rows have each probability times its value's scale with 16 bits: 2^-16.  All of it times sum p |v|.  With bf16 rows and 4
+    bits the products hold code + 24 or code - 23 in the code's place, at most 31 steps s, where the row's largest value is 7 s
+    at least: |k| and |v| are 31 / 7 of a row's largest there, and the excess that is taken off again is one more term.
 """
 import ctypes
 import math
@@ -435,7 +437,7 @@ def filled(lengths, H, D, ps, bits, seed, spare=2, stale=math.nan, extra=1):
     return pages, values64(k, bits).view(P, ps, H, D), values64(v, bits).view(P, ps, H, D), torch.from_numpy(table)
 
 
-def attend64(q, k, v, table, lengths, ps, scale, window, dtype):
+def attend64(q, k, v, table, lengths, ps, scale, window, dtype, bits):
     R, Hq, D = q.shape
     P, H = k.shape[0], k.shape[2]
     out, lse = torch.zeros(R, Hq, D, dtype=torch.float64), torch.full((R, Hq), -math.inf, dtype=torch.float64)
@@ -449,12 +451,15 @@ def attend64(q, k, v, table, lengths, ps, scale, window, dtype):
             continue
         kr, vr = (x[page, t % ps].repeat_interleave(Hq // H, 1) for x in (k, v))            # tokens x Hq x D
         s = torch.einsum("hd,thd->ht", q[r].double(), kr) * scale
-        size = torch.einsum("hd,thd->ht", q[r].double().abs(), kr.abs()) * abs(scale)
+        kr, held = kr.abs(), vr.abs()                                                       # what the sums hold, at most
+        if bits == 4 and dtype == BF16:
+            kr, held = (31 / 7 * z.amax(-1, keepdim=True).expand_as(z) for z in (kr, held))
+        size = torch.einsum("hd,thd->ht", q[r].double().abs(), kr) * abs(scale)
         p = torch.softmax(s, -1)
         out[r], lse[r] = torch.einsum("ht,thd->hd", p, vr), torch.logsumexp(s, -1)
         es = (40 * U * size + 4 * U * s.abs()).amax(-1, keepdim=True)                       # of a score and the largest one
-        rel = 2 * es + (8 + n / 32 + 64) * U + (2.0 ** -8 if dtype == BF16 else 0.0)
-        bound[r] = rel * torch.einsum("ht,thd->hd", p, vr.abs())
+        rel = 2 * es + (8 + n / 32 + 64) * U + (2.0 ** -16 if dtype == BF16 else 0.0)
+        bound[r] = rel * torch.einsum("ht,thd->hd", p, held)
         lse_bound[r] = (es + (8 + n / 32 + 64) * U).squeeze(-1) + 4 * U * lse[r].abs()
     return out, lse, bound, lse_bound
 
@@ -470,7 +475,7 @@ def check_attention(lengths, Hq, H, D, ps, bits, dtype, window=0, scale=None, se
     lse = torch.full((R, Hq), 7.0, device=DEV)
     out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints(lengths), bits, scale, window, lse=lse)
     used = D ** -0.5 if scale is None else scale
-    ref, ref_lse, bound, lse_bound = attend64(q, k, v, table, lengths, ps, used, window, dtype)
+    ref, ref_lse, bound, lse_bound = attend64(q, k, v, table, lengths, ps, used, window, dtype, bits)
     unit = 2.0 ** -8 if dtype == BF16 else U
     assert out.shape == q.shape and out.dtype == dtype
     off = (out.cpu().double() - ref).abs()
@@ -574,7 +579,7 @@ def test_attention_with_scores_far_apart(bits, dtype):
     pages, k, v, table = filled([200, 90], 2, 64, 16, bits, 3)
     q = k[table[:, 1].long(), 3].repeat_interleave(2, 1).to(dtype) * 40.0
     out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints([200, 90]), bits, 1.0)
-    ref, _, bound, _ = attend64(q, k, v, table, [200, 90], 16, 1.0, 0, dtype)
+    ref, _, bound, _ = attend64(q, k, v, table, [200, 90], 16, 1.0, 0, dtype, bits)
     unit = 2.0 ** -8 if dtype == BF16 else U
     assert ((out.cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound + 1e-30).all()
 
@@ -673,7 +678,7 @@ def test_prompts_then_tokens(bits, dtype):
             values[r].append(x[r, Hq + H:].cpu())
             kr, vr = (values64(torch.stack(z), bits).view(1, -1, H, D) for z in (keys[r], values[r]))
             n = lengths[r]
-            ref, _, bound, _ = attend64(x[r:r + 1, :Hq].cpu(), kr, vr, torch.zeros(1, 1, dtype=torch.int32), [n], n, D ** -0.5, 0, dtype)
+            ref, _, bound, _ = attend64(x[r:r + 1, :Hq].cpu(), kr, vr, torch.zeros(1, 1, dtype=torch.int32), [n], n, D ** -0.5, 0, dtype, bits)
             unit = 2.0 ** -8 if dtype == BF16 else U
             assert ((out[r:r + 1].cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound + 1e-30).all()
 
