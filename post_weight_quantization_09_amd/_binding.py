@@ -817,7 +817,7 @@ def _pages(pages: torch.Tensor, H: int, D: int, bits: int, device) -> tuple:
     size, rest = divmod(block, _slot_bytes(D, bits))
     if rest or size < 1:
         raise ValueError(f"blocks of {block} bytes hold no whole number of slots of {_slot_bytes(D, bits)} (gptq_cache_block_bytes)")
-    return n, page, head, size
+    return n, page if n > 1 else 0, head if H > 1 else 0, size     # a dimension of size one has any stride
 
 
 def gptq_rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,

@@ -95,9 +95,10 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernel
 int rows_of(int64_t Hq, int64_t H) { return (int)std::min<int64_t>(Hq / H, kTileHeads); }
 
 void carve(Carver& c, AttentionKernelArgs& k, int Dp) {
-    k.records = c.take<AttentionRecord>(kMaxPieces);
-    k.partial_ml = c.take<float>((size_t)2 * kMaxPieces * k.rows * 2);
-    k.partial_o = c.take<float>((size_t)2 * kMaxPieces * k.rows * Dp);
+    const size_t pieces = most_pieces(Dp / 32);
+    k.records = c.take<AttentionRecord>(pieces);
+    k.partial_ml = c.take<float>(2 * pieces * k.rows * 2);
+    k.partial_o = c.take<float>(2 * pieces * k.rows * Dp);
 }
 
 }  // namespace

@@ -38,14 +38,18 @@ struct AttentionKernelArgs {
     AttentionRecord* records;
 };
 
-// Waves of a SIMD that the registers are laid out for, and pieces of a launch: one for each of the 256 CUs' waves.
+// Waves of a SIMD that the registers are laid out for (512 among them; three waves have 168 each), and pieces of a launch: one
+// for each of the 256 CUs' waves.  More waves, where registers allowed them, were no faster: those that there are keep 100 to
+// 130 KB of a CU's loads under way, which is what the memory's latency takes at its rate.
 constexpr int attention_waves(int chunks, int bits, int parts) {
-    if (parts == 1 && chunks <= 4) return bits == 16 && chunks == 4 ? 2 : 3;
-    return (parts == 1 && !(bits == 16 && chunks == 8)) || (parts == 3 && chunks <= 4) ? 2 : 1;
+    if (parts == 1) return bits == 16 && chunks == 8 ? 1 : chunks <= (bits == 16 ? 3 : 4) ? 3 : 2;
+    return chunks <= 4 ? 2 : 1;
 }
 constexpr int attention_pieces(int chunks, int bits, int parts) { return 1024 * attention_waves(chunks, bits, parts); }
 
-constexpr int kMaxPieces = 1024 * 3;
+// The most pieces of any width of the cache and type of the rows.
+constexpr int most_pieces(int chunks) { return attention_pieces(chunks, 4, 1); }
+constexpr int kMaxPieces = most_pieces(4);
 constexpr int64_t kMaxLine = (int64_t)1 << 31;  // places
 
 // chunks: stored head size / 32.

@@ -355,6 +355,26 @@ def test_cache_of_extreme_rows(bits, dtype):
 
 @gpu
 @pytest.mark.parametrize("bits", [16, 8, 4])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_of_a_long_batch(bits, dtype):
+    """Runs of every length and beginning, next to one another in the batch, padding between and behind them."""
+    rng = np.random.default_rng(7)
+    slots, free = [], list(rng.permutation(40))
+    while len(slots) < 1900:
+        n, p = int(rng.integers(1, 70)), int(free.pop())
+        at = p * 64 + int(rng.integers(0, 64 - n + 1)) if n < 64 else p * 64
+        slots += list(range(at, at + min(n, 64)))
+        if rng.random() < 0.3:
+            slots += [-1] * int(rng.integers(1, 4))
+        if len(free) == 0:
+            break
+    slots = slots[:len(slots) - len(slots) % 8 - 3]
+    k, v = gen_rows((len(slots), 3, 64), dtype, 1), gen_rows((len(slots), 3, 64), dtype, 2)
+    check_cache(k, v, slots, new_pages(40, 3, 64, 64, bits), bits, 64)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 8, 4])
 def test_cache_of_views(bits):
     """Keys and values inside a fused projection's rows; pages of one layer among several, and heads before pages."""
     T, H, D, ps = 19, 3, 64, 16
@@ -529,6 +549,52 @@ def test_attention_over_long_and_uneven_lengths(lengths, bits, dtype):
 def test_attention_of_many_requests():
     rng = np.random.default_rng(0)
     check_attention([int(n) for n in rng.integers(0, 40, 1500)], 2, 1, 64, 16, 8, BF16)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,window", [(BF16, 0), (F32, 0), (BF16, 600)])
+def test_attention_of_more_segments_than_pieces_of_work(dtype, window):
+    """Requests times key heads above the number of waves, long ones among them that several waves share."""
+    lengths = [(37 * i) % 65 for i in range(900)]
+    lengths[5], lengths[640], lengths[899] = 9000, 3000, 5000
+    check_attention(lengths, 8, 4, 64, 16, 8, dtype, window=window)
+
+
+@gpu
+def test_attention_of_the_most_requests():
+    """Against the same requests in smaller calls; all of them read one page."""
+    R, H, D = 65536, 2, 64
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randn(R, 2 * H, D, device=DEV, generator=gen).to(BF16)
+    pages = torch.zeros(1, H, g.gptq_cache_block_bytes(32, D, 8), dtype=torch.uint8, device=DEV)
+    x = torch.randn(32, H, D, device=DEV, generator=gen)
+    g.gptq_cache_write(x, x.flip(0).contiguous(), pages, torch.arange(32, dtype=torch.int32, device=DEV), 8)
+    lengths = torch.randint(0, 33, (R,), device=DEV, generator=gen, dtype=torch.int32)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV).expand(R, 1)
+    lse, part = torch.empty(R, 2 * H, device=DEV), torch.empty(1000, 2 * H, device=DEV)
+    out = g.gptq_cache_attention(q, pages, table, lengths, 8, lse=lse)
+    for r in range(0, 65000, 13000):
+        at = slice(r, r + 1000)
+        assert torch.equal(g.gptq_cache_attention(q[at], pages, table[at], lengths[at], 8, lse=part), out[at]) and torch.equal(part, lse[at])
+    empty = lengths == 0
+    assert empty.any() and not out[empty].any() and (lse[empty] == -math.inf).all() and out[~empty].isfinite().all()
+
+
+@gpu
+def test_two_streams_at_once():
+    """Steps of two batches, each with its buffers, neither waiting for the other."""
+    made = []
+    for i, lengths in enumerate(([7000, 0, 33], [400] * 30)):
+        pages, _, _, table = filled(lengths, 2, 64, 16, 8, i)
+        q = torch.randn(len(lengths), 8, 64, device=DEV)
+        args = (q, pages, table.to(DEV), ints(lengths), 8)
+        made.append((torch.cuda.Stream(), args, g.gptq_cache_attention(*args)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [g.gptq_cache_attention(*args, stream=stream) for stream, args, _ in made]
+    torch.cuda.synchronize()
+    for y, (_, _, want) in zip(got, made):
+        assert torch.equal(y, want)
 
 
 @gpu
