@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
 
+// One instruction, without the canonicalisations that fmaxf asks for: a NaN is passed over, as by fmaxf.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+
 // the largest of lanes l, l ^ 16, l ^ 32, l ^ 48
 __device__ __forceinline__ float max_of_quarters(float x) {
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -126,7 +133,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
     for (int p = 0; p < PARTS; ++p) {
         u32x4 r;
         if (PARTS == 2 && p == 1) {
-            for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2_rne(rest[2 * i], rest[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
         } else {
             for (int i = 0; i < 4; ++i) r[i] = high_halves(rest[2 * i], rest[2 * i + 1]);
             for (int i = 0; i < 8; ++i) rest[i] -= __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u);
@@ -189,7 +196,7 @@ struct Eight<float> {
 // Four values rounded to rows of any alignment that their type has.
 __device__ __forceinline__ void store_four(__bf16* p, f32x4 x) {
     typedef u32x2 __attribute__((aligned(2))) any;
-    *reinterpret_cast<any*>(p) = u32x2{pack_bf16x2_rne(x[0], x[1]), pack_bf16x2_rne(x[2], x[3])};
+    *reinterpret_cast<any*>(p) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 }
 __device__ __forceinline__ void store_four(float* p, f32x4 x) {
     typedef f32x4 __attribute__((aligned(4))) any;
@@ -278,7 +285,8 @@ struct Block {
     bool whole;                                                     // every token of the 32 is seen
 };
 
-// Page and place in it of the two halves of 32 tokens; -1 where there is none.  The same for all lanes of a wave.
+// Page and place in it of the two halves of 32 tokens; -1 where there is none.  The same for all lanes of a wave, and read by
+// scalar loads (the table is not written while the kernel runs).
 struct Halves {
     uint32_t t0;
     int32_t page[2];
@@ -290,7 +298,7 @@ __device__ __forceinline__ Halves look_up(const AttentionKernelArgs& a, const in
     h.t0 = t0;
     for (int i = 0; i < 2; ++i) {
         const uint32_t t = t0 + 16 * i, j = a.by_page.quotient(t);
-        h.page[i] = t < vis.n ? table[j] : -1;
+        h.page[i] = t < vis.n ? (const int32_t)*(const __attribute__((address_space(4))) int32_t*)(table + j) : -1;
         h.slot[i] = t - j * a.page_size;
     }
     return h;
@@ -367,14 +375,17 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     }
     if (!b.whole) {
         for (int j = 0; j < 8; ++j) x[j] = b.seen >> j & 1 ? x[j] : -INFINITY;
-        if constexpr (BITS == 16) {                                 // what an unseen slot holds may not be a number
+        // what an unseen slot holds may not be a number
+        if constexpr (BITS < 16) {
+            for (int j = 0; j < 8; ++j) b.vs[j] = b.seen >> j & 1 ? b.vs[j] : 0.0f;
+        } else {
             u32x4 mask;
             for (int i = 0; i < 4; ++i)
                 mask[i] = (b.seen >> 2 * i & 1 ? 0xFFFFu : 0u) | (b.seen >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
             for (int i = 0; i < 8 * NC; ++i) b.v[i] &= mask[i & 3];
         }
     }
-    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
     top = max_of_quarters(top);
     if (__any(top > m + kRaise)) {
         const float now = fmaxf(m, top), base = now == -INFINITY ? 0.0f : now;
@@ -391,9 +402,6 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
         p8[j] = p;
         if constexpr (BITS < 16) p8[j] *= b.vs[j];
     }
-    if constexpr (BITS < 16)
-        if (!b.whole)
-            for (int j = 0; j < 8; ++j) p8[j] = b.seen >> j & 1 ? p8[j] : 0.0f;
     constexpr int kParts = Tr::kProbabilityParts;
     bf16x8 p[kParts];
     if constexpr (Tr::kExcess) {
@@ -512,11 +520,12 @@ __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attentio
             // the first block, then q of the tile's heads as B operands
             const uint8_t* head = a.pages + h * a.head_stride;
             const int32_t* table = a.table + r * a.ld_table;
-            uint32_t t = (vis.block() + off) * kBlockTokens;
+            uint32_t t = (uint32_t)__builtin_amdgcn_readfirstlane((int)((vis.block() + off) * kBlockTokens));
             int todo = vis.n > vis.first ? count : 0;
             asm("" : "+v"(todo));                                   // as a lane's own the loop leaves the block in its registers
             Block<NC, BITS, PARTS> b;
             if (todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
+            Halves next = look_up(a, table, vis, t += kBlockTokens);        // a block's pages are known when its turn comes
             bf16x8 q[NC][PARTS];
             float less, to_log2 = a.scale_log2e * Tr::kUnit;
             load_q<E, NC, BITS, PARTS>(static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs, n < heads, a.D,
@@ -527,8 +536,10 @@ __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attentio
             float m = -INFINITY, l = 0.0f;
             while (todo > 0) {
                 step<NC, BITS, PARTS>(b, q, less, to_log2, m, l, o);
-                t += kBlockTokens;
-                if (--todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
+                if (--todo > 0) {
+                    load_block(a, vis, next, head, lane, b);
+                    next = look_up(a, table, vis, t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(t + kBlockTokens)));
+                }
             }
             l = sum_of_quarters(l);
             if (n >= heads) continue;

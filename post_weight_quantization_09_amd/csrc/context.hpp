@@ -8,6 +8,12 @@
 
 namespace gptq {
 
+// Two values rounded to bf16 (lo | hi << 16), by one instruction.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // T x H rows of D elements; row (t, h) at t * ts + h * hs elements.
 struct HeadRows {
     void* p;

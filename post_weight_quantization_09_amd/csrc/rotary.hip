@@ -79,7 +79,7 @@ __device__ __forceinline__ void store(__bf16* p, const float (&x)[N]) {
         typedef uint32_t __attribute__((ext_vector_type(N / 2))) vec;
         typedef vec __attribute__((aligned(2))) any;
         vec v;
-        for (int i = 0; i < N / 2; ++i) v[i] = pack_bf16x2_rne(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < N / 2; ++i) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
         *reinterpret_cast<any*>(p) = v;
     }
 }
