@@ -131,7 +131,10 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.R = a.R, k.Hq = a.Hq, k.H = a.H, k.D = a.D, k.group = a.Hq / a.H;
     k.tiles = (int)ceil_div(k.group, kTileHeads), k.segments = a.H * k.tiles;
     k.rows = rows_of(a.Hq, a.H);
-    const int pieces = attention_pieces(Dp / 32, a.pages.bits, a.f32 ? 3 : 1);
+    // no more pieces than the table's pages could fill
+    const int64_t places = (int64_t)a.R * k.segments * (k.max_tokens / kBlockTokens + 2 + kBeginCost);
+    const int pieces = (int)std::min<int64_t>(attention_pieces(Dp / 32, a.pages.bits, a.f32 ? 3 : 1), ceil_div(places, kLeastPiece));
+    k.pieces = pieces;
     k.by_page = Divisor((uint32_t)k.page_size), k.by_segments = Divisor((uint32_t)k.segments);
     k.by_pieces = Divisor((uint32_t)pieces);
     Carver c(workspace);

@@ -9,6 +9,11 @@ namespace gptq {
 constexpr int kBlockTokens = 32;        // tokens of a wave's step: the K of the second product
 constexpr int kTileHeads = 16;          // query heads of a step: the N of both products
 
+// A segment's length on the line of all work: its blocks, and what beginning with it costs beside them (places before its blocks,
+// at which nothing is done), so that waves with many segments get fewer blocks.
+constexpr uint32_t kBeginCost = 1;      // 32 ragged requests of up to 1024: 17.8 us with 3, 16.8 with 1; 256 of 1900: 206 with 6, 204 with 1
+constexpr uint32_t kLeastPiece = 2;     // places of a wave's piece
+
 // A segment (a request and up to 16 query heads of one key head) whose sums several pieces hold, from `first` on.
 struct AttentionRecord {
     int32_t request, segment, first, parts;     // parts 0: nothing to join
@@ -32,6 +37,7 @@ struct AttentionKernelArgs {
     int64_t window;
     int R, Hq, H, D, group;             // group = Hq / H query heads share a key head
     int tiles, segments;                // per key head and per request
+    int pieces;                         // workgroups of the launch
     float* partial_o;                   // two slots per piece (ends and begins there), rows x Dp
     float* partial_ml;                  // rows x 2
     int rows;                           // of a slot: min(group, 16)

@@ -35,7 +35,6 @@ namespace gptq {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;
-constexpr uint32_t kLeastPiece = 2;     // places of a wave's piece
 
 __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
@@ -242,10 +241,6 @@ struct Visible {
         return end > block() ? end - block() : 1u;
     }
 };
-
-// A segment's length on the line: its blocks, and what beginning with it costs beside them (places before its blocks, at
-// which nothing is done), so that waves with many segments get fewer blocks.
-constexpr uint32_t kBeginCost = 1;      // 32 ragged requests of up to 1024: 17.8 us with 3, 16.8 with 1; 256 of 1900: 206 with 6, 204 with 1
 
 __device__ __forceinline__ Visible visible(const AttentionKernelArgs& a, int r) {
     const int32_t given = a.lengths[r];
@@ -461,7 +456,6 @@ template <typename E, int NC, int BITS, int PARTS>
 __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attention_kernel(AttentionKernelArgs a) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     const int lane = threadIdx.x, quarter = lane >> 4, n = lane & 15;
-    const uint32_t piece = blockIdx.x;
 
     // the line of all blocks: a scan over the requests' lengths on it, `share` requests a lane
     const int share = (a.R + 63) / 64;
@@ -471,8 +465,9 @@ __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attentio
         if (lane * share + i < a.R) mine += visible(a, lane * share + i).blocks() + kBeginCost;
     const uint32_t line = scan_of_wave(mine, lane), total = (uint32_t)__builtin_amdgcn_readlane((int)line, 63) * a.segments;
     const uint32_t chunk = max(kLeastPiece, a.by_pieces.quotient(total) + 1);
+    const uint32_t piece = blockIdx.x;
     const bool by_piece = a.R * a.segments > (int)gridDim.x;        // how records are numbered
-    if (by_piece && lane == 0) a.records[piece].parts = 0;
+    if (by_piece && lane == 0) a.records[piece].parts = 0;          // also where there is no such piece
     if ((uint64_t)piece * chunk >= total) return;
     const uint32_t begin = piece * chunk, end = min(begin + chunk, total);
 
@@ -572,7 +567,7 @@ hipError_t launch_attention(const AttentionKernelArgs& a, int chunks, bool f32, 
     const auto launch = [&](auto e, auto parts, auto nc) {
         using E = decltype(e);
         constexpr int P = decltype(parts)::value, NC = decltype(nc)::value;
-        attention_kernel<E, NC, BITS, P><<<dim3((unsigned)attention_pieces(NC, BITS, P)), 64, 0, stream>>>(a);
+        attention_kernel<E, NC, BITS, P><<<dim3((unsigned)a.pieces), 64, 0, stream>>>(a);
     };
     const auto pick = [&](auto e, auto parts) {
         switch (chunks) {
