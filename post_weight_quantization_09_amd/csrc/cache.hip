@@ -1,11 +1,11 @@
 // The paged cache of keys and values: rows quantised as they are written, and read back.
 //
 // A row of a token and head is kept on the symmetric grid of gptq_quantize_layer: s = absmax / (2^(b-1) - 1/2), codes
-// round-half-even(x / s).  The rounding is exact, not that of a rounded quotient.  x times the reciprocal is off by less than
-// 2^-15 (8 bits; 2^-19 with 4), so q = rint(x * (1 / s)) is right where it is not that near to a border.  A wave with a value
-// that is (one in twenty or fewer) takes the remainder x - q s, which is representable (q has at most 8 bits, |x - q s| is not
-// above s / 2 by more than a few of x's last places), from one fused multiply-add, and comparing it with s / 2 moves q to the
-// neighbour where that is nearer, or even.
+// round-half-even(x / s).  The rounding is exact, not that of a rounded quotient: x times the reciprocal is off by less than
+// 2^-15, so q = rint(x * (1 / s)) is right or, next to a border, the other neighbour's.  The remainder x - q s is representable
+// (q has at most 8 bits, |x - q s| is not above s / 2 by more than a few of x's last places): one fused multiply-add gives it,
+// and comparing it with s / 2 moves q where the other is nearer, or even.  Borders are no rare case to branch on: a row's largest
+// value lies on one, and bf16 values do often.
 //
 // Memory traffic is the bound.  A wave takes eight tokens of a head (two heads of 64): a lane holds two or four
 // dimensions of each, so that rows are read and written in whole lines, their largest values found by maxima across the
@@ -35,12 +35,13 @@ struct CacheArgs {
 
 constexpr float kRound = 12582912.0f;           // 1.5 2^23: added to a small value, the sum's last bits are that value rounded
 
-// x / s rounded to nearest, ties to even, in the last bits of kRound + the result.
-__device__ __forceinline__ float exact_round(float x, float s, float inv) {
-    const float t = fmaf(x, inv, kRound), q = t - kRound, rem = fmaf(-q, s, x), twice = fabsf(rem) + fabsf(rem);
-    const bool odd = (__float_as_uint(t) & 1u) != 0;
-    const bool off = (twice > s) | ((twice == s) & odd);
-    return t + (off ? copysignf(1.0f, rem) : 0.0f);
+// x / s rounded to nearest, ties to even, in the last bits of the result (kRound's added).
+__device__ __forceinline__ int exact_round(float x, float s, float inv) {
+    const float t = fmaf(x, inv, kRound), q = t - kRound, rem = fmaf(-q, s, x);
+    // twice the remainder against s as whole numbers, an odd q's with one more: a tie is not above s where q is even
+    const uint32_t twice = __float_as_uint(fabsf(rem) + fabsf(rem)) + (__float_as_uint(t) & 1u);
+    const int toward = (__float_as_int(rem) >> 31) | 1;
+    return __float_as_int(t) + (twice > __float_as_uint(s) ? toward : 0);
 }
 
 template <int BITS>
@@ -213,26 +214,14 @@ struct Codes {
                 for (int j = 0; j < PD; ++j) m[i] = max(m[i], __float_as_uint(x[i][j]) & 0x7FFFFFFFu);
             }
             mine = grid_scale<BITS>(max_of_rows<TWO>(m, lane));                             // a lane finds the scale of one row
-            float scale[kOctet], inv[kOctet], most = 0.0f;
-            for (int i = 0; i < kOctet; ++i) {
-                const int from = lane_of<TWO>(i);
-                scale[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from));
-                if (TWO) scale[i] = lane < 32 ? scale[i] : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from + 32));
-                inv[i] = __builtin_amdgcn_rcpf(scale[i]);
-            }
-            float t[kOctet][PD];
-            for (int i = 0; i < kOctet; ++i)
-                for (int j = 0; j < PD; ++j) {
-                    t[i][j] = fmaf(x[i][j], inv[i], kRound);
-                    most = fmaxf(most, fabsf(fmaf(x[i][j], inv[i], kRound - t[i][j])));
-                }
-            if (__any(most > 0.5f - (BITS == 8 ? 0x1p-15f : 0x1p-19f)))
-                for (int i = 0; i < kOctet; ++i)
-                    for (int j = 0; j < PD; ++j) t[i][j] = exact_round(x[i][j], scale[i], inv[i]);
             const int top = __float_as_int(kRound) + (int)(kMask >> 1);
             for (int i = 0; i < kOctet; ++i) {
-                const uint32_t mask = scale[i] == scale[i] ? part : 0u;                     // rows that are not finite: zeros
-                for (int j = 0; j < PD; ++j) code[i][j] = (uint32_t)min(__float_as_int(t[i][j]), top) & mask;
+                const int from = lane_of<TWO>(i);
+                float scale = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from));
+                if (TWO) scale = lane < 32 ? scale : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), from + 32));
+                const float inv = __builtin_amdgcn_rcpf(scale);
+                const uint32_t mask = scale == scale ? part : 0u;                           // rows that are not finite: zeros
+                for (int j = 0; j < PD; ++j) code[i][j] = (uint32_t)min(exact_round(x[i][j], scale, inv), top) & mask;
             }
         }
     }
