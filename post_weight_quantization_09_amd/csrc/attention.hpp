@@ -45,8 +45,9 @@ struct AttentionKernelArgs {
 };
 
 // Waves of a SIMD that the registers are laid out for (512 among them; three waves have 168 each), and pieces of a launch: one
-// for each of the 256 CUs' waves.  More waves, where registers allowed them, were no faster: those that there are keep 100 to
-// 130 KB of a CU's loads under way, which is what the memory's latency takes at its rate.
+// for each of the 256 CUs' waves.  Measured both ways: heads of 256 in 16 bits 59 us with one wave, 78 with two, which spill; heads
+// of 128 in 4 bits 48 with three, 57 with two; of 64 in 8 bits 66 with three, 76 with two, 65 with four (and a third more partial
+// sums to join); of 128 in 16 bits 203 with two, 208 with three.
 constexpr int attention_waves(int chunks, int bits, int parts) {
     if (parts == 1) return bits == 16 && chunks == 8 ? 1 : chunks <= (bits == 16 ? 3 : 4) ? 3 : 2;
     return chunks <= 4 ? 2 : 1;

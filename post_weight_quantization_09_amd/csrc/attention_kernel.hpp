@@ -26,7 +26,13 @@
 // 131072 tokens beside short ones.  Every workgroup scans the lengths for itself.  A wave that has a whole segment writes its
 // output; one that has a part of it writes unnormalised sums, which the join adds in order.  Waves share nothing else: no LDS
 // and no barrier in the loop, and little code, which counts where a call is short (the instructions of a launch come from
-// memory once per CU).
+// memory once per CU).  (Four waves of a workgroup on one segment, joined in LDS, with three times the code before the loop:
+// 111 us against 91 for 64 ragged requests, 15 against 12 for a short one.)
+//
+// Measured on MI355X, heads of 128: 256 requests of 1950 tokens in 16 bits, 1.02 GB, 195 us and 6 of the join (5.2 TB/s of
+// reads; a copy moves 4.9); 64 ragged requests in 8 bits, 415 MB, 83 and 6 us (5.0 TB/s); 131072 tokens in 4 bits, 64 query
+// heads, 145 MB, 36 and 8 us: there half the cycles issue vector instructions (356 a block: conversions, softmax, addresses).  A
+// call whose work is nothing takes 7 + 4 us: lengths, page table and pages are three latencies in a row, the join a launch.
 #pragma once
 
 #include "attention.hpp"

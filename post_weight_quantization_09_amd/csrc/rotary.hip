@@ -4,6 +4,9 @@
 // cosine see is a fraction of a turn with 2^-32 or better at any 32-bit position; they are evaluated in fp32, once for a
 // token's pair whatever the number of heads, and wait in LDS.  What is left is a copy: a workgroup takes some tokens' rows of
 // some heads, 16 bytes a load where the pairs allow it (units of V pairs), and is bound by memory traffic.
+//
+// Measured on MI355X: 8192 tokens x 40 heads x 128 in bf16, 168 MB, 38 us (4.4 TB/s; a copy moves 4.9); with an angle per head
+// and single elements 72 us.  One token 2.0 us (a launch).
 #include "context.hpp"
 
 namespace gptq {
