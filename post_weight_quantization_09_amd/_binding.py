@@ -782,14 +782,34 @@ _ROTARY_SCALINGS = {"plain": GPTQ_ROTARY_PLAIN, "linear": GPTQ_ROTARY_LINEAR, "b
 _STORED = {D: next(n for n in (64, 96, 128, 192, 256) if n >= D) for D in range(8, 257, 8)}
 
 
-def _heads(t: torch.Tensor, name: str, device) -> tuple:
-    """Strides from token to token and head to head of a T x H x D tensor with unit element stride, on the GPU."""
+# GPUs by their index here (-1: a tensor of the CPU), which is quicker to compare than a torch.device.
+
+def _gpu(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("device tensor expected")
+    return index
+
+
+def _heads(t: torch.Tensor, name: str, gpu: int) -> tuple:
+    """Strides from token to token and head to head of a T x H x D tensor with unit element stride, on this GPU."""
     strides = t.stride()
     if len(strides) != 3 or (strides[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name} must be tokens x heads x elements with unit element stride")
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != gpu:
         raise ValueError(f"{name} must be on the GPU of the other tensors")
     return strides[0], strides[1]
+
+
+def _list(t: torch.Tensor, name: str, dtype: torch.dtype, gpu: int) -> int:
+    """The address of a contiguous tensor of this dtype on this GPU."""
+    if t.dtype != dtype or not t.is_contiguous() or t.get_device() != gpu:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the GPU of the other tensors")
+    return t.data_ptr()
+
+
+def _handle_of(gpu: int) -> int:
+    return _current_handle(gpu) if _current_handle is not None else torch.cuda.current_stream(gpu).cuda_stream
 
 
 def _row_type(t: torch.Tensor) -> int:
@@ -806,9 +826,9 @@ def _slot_bytes(D: int, bits: int) -> int:
     return 2 * (_STORED[D] * bits // 8) + (8 if bits < 16 else 0)
 
 
-def _pages(pages: torch.Tensor, H: int, D: int, bits: int, device) -> tuple:
+def _pages(pages: torch.Tensor, H: int, D: int, bits: int, gpu: int) -> tuple:
     """Page count, strides and page size of a uint8 pages x heads x block tensor."""
-    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.device != device or not pages.is_cuda:
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.get_device() != gpu:
         raise ValueError("pages must be uint8 pages x heads x bytes on the GPU of the other tensors")
     n, heads, block = pages.shape
     page, head, byte = pages.stride()
@@ -844,24 +864,25 @@ def gptq_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, i
 
     Pairs (i, i + rot / 2), or neighbours with interleaved.  out=x turns in place.
     """
-    if stream is not None or _elsewhere(x):
+    gpu = _gpu(x)
+    if stream is not None or gpu != _device_now():
         with _current(stream, x):
             return gptq_rotary(x, positions, freqs, interleaved, factor, out)
     _no_gradient(x, freqs, out)
-    dt, dev = _row_type(x), x.device
-    x_ts, x_hs = _heads(x, "x", dev)
+    dt = _row_type(x)
+    x_ts, x_hs = _heads(x, "x", gpu)
     T, H, D = x.shape
-    pp = _device_tensor(positions, "positions", torch.int32, dev)
-    fp = _device_tensor(freqs, "freqs", torch.float64, dev)
+    pp = _list(positions, "positions", torch.int32, gpu)
+    fp = _list(freqs, "freqs", torch.float64, gpu)
     if positions.numel() != T or freqs.dim() != 1:
         raise ValueError("positions must hold an entry per token, freqs be a vector")
     if out is None:
         out = x.new_empty((T, H, D))
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must match x")
-    y_ts, y_hs = _heads(out, "out", dev)
+    y_ts, y_hs = _heads(out, "out", gpu)
     _check(load().gptq_rotary(x.data_ptr(), dt, T, H, D, x_ts, x_hs, pp, fp, 2 * freqs.numel(), factor,
-                              GPTQ_FLAG_INTERLEAVED if interleaved else 0, out.data_ptr(), y_ts, y_hs, _handle(dev)),
+                              GPTQ_FLAG_INTERLEAVED if interleaved else 0, out.data_ptr(), y_ts, y_hs, _handle_of(gpu)),
            "gptq_rotary")
     return out
 
@@ -877,38 +898,43 @@ def gptq_cache_write(k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor, slot
 
     pages: uint8 pages x H x gptq_cache_block_bytes(page_size, D, bits).
     """
-    if stream is not None or _elsewhere(k):
+    gpu = _gpu(k)
+    if stream is not None or gpu != _device_now():
         with _current(stream, k):
             return gptq_cache_write(k, v, pages, slots, bits)
     _no_gradient(k, v)
-    dt, dev = _row_type(k), k.device
-    k_ts, k_hs = _heads(k, "k", dev)
+    dt = _row_type(k)
+    k_ts, k_hs = _heads(k, "k", gpu)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("v must match k")
-    v_ts, v_hs = _heads(v, "v", dev)
+    v_ts, v_hs = _heads(v, "v", gpu)
     T, H, D = k.shape
-    n, ps, hs, size = _pages(pages, H, D, bits, dev)
-    sp = _device_tensor(slots, "slots", torch.int32, dev)
+    n, ps, hs, size = _pages(pages, H, D, bits, gpu)
+    sp = _list(slots, "slots", torch.int32, gpu)
     if slots.numel() != T:
         raise ValueError("slots must hold an entry per token")
     _check(load().gptq_cache_write(k.data_ptr(), v.data_ptr(), dt, T, H, D, k_ts, k_hs, v_ts, v_hs, sp, bits,
-                                   pages.data_ptr(), n, ps, hs, size, _handle(dev)), "gptq_cache_write")
+                                   pages.data_ptr(), n, ps, hs, size, _handle_of(gpu)), "gptq_cache_write")
 
 
 def gptq_cache_read(pages: torch.Tensor, slots: torch.Tensor, D: int, bits: int, dtype: torch.dtype = torch.bfloat16,
                     stream=None) -> tuple:
     """(k, v), T x H x D each: what the slots (int32[T]) hold; zeros for a slot outside the pages."""
-    if stream is not None or _elsewhere(pages):
+    gpu = _gpu(pages)
+    if stream is not None or gpu != _device_now():
         with _current(stream, pages):
             return gptq_cache_read(pages, slots, D, bits, dtype)
     if pages.dim() != 3:
         raise ValueError("pages must be uint8 pages x heads x bytes")
-    dev, H, T = pages.device, pages.shape[1], slots.numel()
-    n, ps, hs, size = _pages(pages, H, D, bits, dev)
-    sp = _device_tensor(slots, "slots", torch.int32, dev)
-    k, v = torch.empty((2, T, H, D), dtype=dtype, device=dev).unbind()
-    _check(load().gptq_cache_read(pages.data_ptr(), n, ps, hs, size, bits, sp, T, H, D, k.data_ptr(), v.data_ptr(),
-                                  _row_type(k), H * D, D, H * D, D, _handle(dev)), "gptq_cache_read")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    H, T = pages.shape[1], slots.numel()
+    n, ps, hs, size = _pages(pages, H, D, bits, gpu)
+    sp = _list(slots, "slots", torch.int32, gpu)
+    k, v = pages.new_empty((2, T, H, D), dtype=dtype).unbind()
+    _check(load().gptq_cache_read(pages.data_ptr(), n, ps, hs, size, bits, sp, T, H, D, k.data_ptr(), v.data_ptr(), dt,
+                                  H * D, D, H * D, D, _handle_of(gpu)), "gptq_cache_read")
     return k, v
 
 
@@ -927,41 +953,42 @@ def gptq_cache_attention(q: torch.Tensor, pages: torch.Tensor, table: torch.Tens
     pages per request.  lengths: int32[R].  scale: 1 / sqrt(D) unless given.  window: only the last `window` tokens.
     lse: fp32 R x Hq, written if given.
     """
-    if stream is not None or _elsewhere(q):
+    gpu = _gpu(q)
+    if stream is not None or gpu != _device_now():
         with _current(stream, q):
             return gptq_cache_attention(q, pages, table, lengths, bits, scale, window, out, lse, workspace)
     _no_gradient(q, out, lse)
-    dt, dev = _row_type(q), q.device
-    q_rs, q_hs = _heads(q, "q", dev)
+    dt = _row_type(q)
+    q_rs, q_hs = _heads(q, "q", gpu)
     R, Hq, D = q.shape
     if pages.dim() != 3:
         raise ValueError("pages must be uint8 pages x heads x bytes")
     H = pages.shape[1]
-    n, ps, hs, size = _pages(pages, H, D, bits, dev)
-    if table.dtype != torch.int32 or table.dim() != 2 or table.device != dev:
+    n, ps, hs, size = _pages(pages, H, D, bits, gpu)
+    if table.dtype != torch.int32 or table.dim() != 2 or table.get_device() != gpu:
         raise ValueError("table must be int32 requests x pages on the GPU of q")
     rows, columns = table.shape
     ld, unit = table.stride()
     if rows != R or (unit != 1 and columns > 1):
         raise ValueError("table must hold a row per request, with unit column stride")
-    lp = _device_tensor(lengths, "lengths", torch.int32, dev)
+    lp = _list(lengths, "lengths", torch.int32, gpu)
     if lengths.numel() != R:
         raise ValueError("lengths must hold an entry per request")
     if out is None:
         out = q.new_empty((R, Hq, D))
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
-    o_rs, o_hs = _heads(out, "out", dev)
+    o_rs, o_hs = _heads(out, "out", gpu)
     ep = None
     if lse is not None:
-        ep = _device_tensor(lse, "lse", torch.float32, dev)
+        ep = _list(lse, "lse", torch.float32, gpu)
         if lse.numel() != R * Hq:
             raise ValueError("lse must hold an entry per request and head")
     lib = load()
     need = 0 if workspace is not None else lib.gptq_attention_workspace_bytes(R, Hq, H, D)
-    workspace, wp, wb = _scratch(need, dev, workspace)
+    workspace, wp, wb = _scratch(need, q.device, workspace)
     _check(lib.gptq_cache_attention(q.data_ptr(), dt, R, Hq, H, D, q_rs, q_hs, pages.data_ptr(), n, ps, hs, size, bits,
                                     table.data_ptr(), ld, columns, lp,
                                     D ** -0.5 if scale is None else scale, window, out.data_ptr(), o_rs, o_hs, ep, wp, wb,
-                                    _handle(dev)), "gptq_cache_attention")
+                                    _handle_of(gpu)), "gptq_cache_attention")
     return out

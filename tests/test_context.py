@@ -831,6 +831,43 @@ def test_calls_on_another_stream():
 
 
 @gpu
+def test_calls_on_tensors_of_a_gpu_that_is_not_the_current_one(monkeypatch):
+    """Every call makes its tensors' GPU the current one first; another current GPU is only made believe here."""
+    from post_weight_quantization_09_amd import _binding
+    now, entered = [7], []
+
+    class Stream:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            entered.append(self.stream)
+            now.append(self.stream.device.index)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    lengths = [300, 10]
+    pages, _, _, table = filled(lengths, 2, 64, 16, 8, 2)
+    table, n, freqs, x = table.to(DEV), ints(lengths), g.gptq_rotary_frequencies(64)[0].to(DEV), torch.randn(2, 4, 64, device=DEV)
+    calls = [lambda: g.gptq_rotary(x, n, freqs), lambda: g.gptq_cache_attention(x, pages, table, n, 8),
+             lambda: g.gptq_cache_read(pages, ints([5, 700]), 64, 8, F32)[1].nan_to_num(0.5),
+             lambda: g.gptq_cache_write(x[:, :2], x[:, 2:], pages, ints([5, 9]), 8)]
+    want = [c() for c in calls]
+    monkeypatch.setattr(_binding, "_device_now", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    for call, before in zip(calls[:2] + calls[3:], want[:2] + want[3:]):
+        entered.clear()
+        after = call()
+        assert [st.device for st in entered] == [torch.device(DEV)] and now == [7]
+        if call is not calls[1]:                    # slot 5 may have been another request's
+            assert before is None or torch.equal(before, after)
+    entered.clear()
+    k, v = g.gptq_cache_read(pages, ints([5, 9]), 64, 8, F32)
+    assert len(entered) == 1 and torch.equal(k.cpu(), values64(x[:, :2].cpu(), 8).float()) and torch.equal(v.cpu(), values64(x[:, 2:].cpu(), 8).float())
+
+
+@gpu
 @pytest.mark.parametrize("bits", [16, 8, 4])
 def test_the_same_call_gives_the_same_bits(bits):
     lengths = [0, 9000, 1, 33, 700, 701]
