@@ -11,8 +11,8 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // Up to this many parts a workgroup joins all query heads of a segment, Dp / 4 threads each, which weigh the parts for
-// themselves; beyond it each of the workgroups along y has one head.
-constexpr int kFewParts = 4;
+// themselves; beyond it each of the workgroups along y has one head, and each along z a slice of its dimensions.
+constexpr int kFewParts = 4, kThreads = 256;
 
 template <typename E>
 __device__ __forceinline__ void write_joined(const AttentionKernelArgs& a, const AttentionRecord& rec, int hq, int d, f32x4 sum,
@@ -24,18 +24,20 @@ __device__ __forceinline__ void write_joined(const AttentionKernelArgs& a, const
     if (a.lse && d == 0) a.lse[(int64_t)rec.request * a.Hq + hq] = whole == 0.0f ? -INFINITY : top * kLn2 + logf(whole);
 }
 
-template <typename E, int THREADS>
-__global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
-    __shared__ float weights[kMaxPieces], most[THREADS / 64], wholes[THREADS / 64];
-    __shared__ f32x4 sums[THREADS];
+template <typename E>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionKernelArgs a, int Dp) {
+    __shared__ float weights[kMaxPieces], most[kThreads / 64], wholes[kThreads / 64];
+    __shared__ f32x4 sums[kThreads];
     const AttentionRecord rec = a.records[blockIdx.x];
     const int tid = threadIdx.x, wave = tid >> 6;
-    if (rec.parts == 0 || (rec.parts <= kFewParts && blockIdx.y > 0)) return;
+    const bool few = rec.parts <= kFewParts;
+    if (rec.parts == 0 || (few && blockIdx.y + blockIdx.z > 0)) return;
     const int h = rec.segment / a.tiles, tile = rec.segment - h * a.tiles;
     const int heads = min(kTileHeads, a.group - tile * kTileHeads), hq = h * a.group + tile * kTileHeads;
     const auto slot = [&](int i) { return (uint64_t)((2 * (rec.first + i) + (i == 0 ? 1 : 0)) * a.rows); };
-    const int quads = Dp / 4, at_once = THREADS / quads, line = tid / quads, quad = tid - line * quads;
-    if (rec.parts <= kFewParts) {
+    const int quads = Dp / 4 / (few ? 1 : (int)gridDim.z), at_once = kThreads / quads, line = tid / quads;
+    const int quad = tid - line * quads + (few ? 0 : (int)blockIdx.z * quads);
+    if (few) {
         for (int row = line; row < heads && line < at_once; row += at_once) {
             float top = -INFINITY, whole = 0.0f;
             for (int p = 0; p < rec.parts; ++p) top = fmaxf(top, a.partial_ml[(slot(p) + row) * 2]);
@@ -56,7 +58,7 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernel
     if (row >= heads) return;
     const auto place = [&](int i) { return slot(i) + row; };
     float top = -INFINITY;
-    for (int p = tid; p < rec.parts; p += THREADS) {
+    for (int p = tid; p < rec.parts; p += kThreads) {
         const float m = a.partial_ml[place(p) * 2];
         weights[p] = m;
         top = fmaxf(top, m);
@@ -64,10 +66,10 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernel
     for (int i = 32; i; i >>= 1) top = fmaxf(top, __shfl_xor(top, i));
     if ((tid & 63) == 0) most[wave] = top;
     __syncthreads();
-    for (int w = 0; w < THREADS / 64; ++w) top = fmaxf(top, most[w]);
+    for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, most[w]);
     const float ref = top == -INFINITY ? 0.0f : top;
     float whole = 0.0f;
-    for (int p = tid; p < rec.parts; p += THREADS) {
+    for (int p = tid; p < rec.parts; p += kThreads) {
         const float keep = __builtin_amdgcn_exp2f(weights[p] - ref);
         whole += keep * a.partial_ml[place(p) * 2 + 1];
         weights[p] = keep;
@@ -76,7 +78,7 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernel
     if ((tid & 63) == 0) wholes[wave] = whole;
     __syncthreads();
     whole = 0.0f;
-    for (int w = 0; w < THREADS / 64; ++w) whole += wholes[w];
+    for (int w = 0; w < kThreads / 64; ++w) whole += wholes[w];
 
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (line < at_once) {
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionKernel
     __syncthreads();
     if (tid < quads) {
         for (int i = 1; i < at_once; ++i) sum += sums[tid + i * quads];
-        write_joined<E>(a, rec, hq + row, 4 * tid, sum, top, whole);
+        write_joined<E>(a, rec, hq + row, 4 * quad, sum, top, whole);
     }
 }
 
@@ -144,17 +146,12 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
                                              : launch_attention<4>(k, Dp / 32, a.f32, stream);
     if (e != hipSuccess) return e;
     // one record per segment where that is not more than one per piece
-    const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.R * k.segments, pieces), (unsigned)k.rows);
-    // few segments may have many parts each: more threads for their rows
-    const auto join = [&](auto e) {
-        using E = decltype(e);
-        // few segments of long requests have hundreds of parts each (131072 tokens: 10.3 us with 256 threads, 8.6 with 1024;
-        // 777 tokens: 4.0 and 5.2)
-        if (grid.x * grid.y <= 512 && k.max_tokens >= 16384) attention_join_kernel<E, 1024><<<grid, 1024, 0, stream>>>(k, Dp);
-        else attention_join_kernel<E, 256><<<grid, 256, 0, stream>>>(k, Dp);
-    };
-    if (a.f32) join(0.0f);
-    else join((__bf16)0.0f);
+    // Few segments of long requests have hundreds of parts each: a row goes to four workgroups (131072 tokens: 10.3 us without,
+    // 7.9 with; one workgroup of 1024 threads for a row the same).
+    const unsigned segments = (unsigned)std::min<int64_t>((int64_t)a.R * k.segments, pieces);
+    const dim3 grid(segments, (unsigned)k.rows, segments * k.rows <= 512 && k.max_tokens >= 16384 ? 4 : 1);
+    if (a.f32) attention_join_kernel<float><<<grid, kThreads, 0, stream>>>(k, Dp);
+    else attention_join_kernel<__bf16><<<grid, kThreads, 0, stream>>>(k, Dp);
     return hipGetLastError();
 }
 
