@@ -445,7 +445,7 @@ __device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quart
     float most = 0.0f;
     for (int c = 0; c < NC; ++c) most = fmaxf(most, y[c].most());
     most = max_of_quarters(most);
-    if (__any(most > 0x1p32f || (most < 0x1p-32f && most > 0.0f))) {
+    if (__any(most > 0x1p20f || (most < 0x1p-20f && most > 0.0f))) {
         const int e = most == 0.0f || most > 3.4e38f ? 0 : ilogbf(most);
         for (int c = 0; c < NC; ++c) y[c].scale(-e);
         to_log2 = ldexpf(to_log2, e);

@@ -638,6 +638,22 @@ def test_attention_of_large_and_small_queries(bits, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("size", [2.0 ** 88, 2.0 ** -60])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_of_large_and_small_keys_and_values(bits, dtype, size):
+    n, H, D, ps = 75, 2, 64, 16
+    k, v = (gen_rows((80, H, D), BF16, i) * size for i in (1, 2))
+    pages = torch.zeros(5, H, g.gptq_cache_block_bytes(ps, D, bits), dtype=torch.uint8, device=DEV)
+    g.gptq_cache_write(k.to(DEV), v.to(DEV), pages, torch.arange(80, dtype=torch.int32, device=DEV), bits)
+    q, table = gen_rows((1, 4, D), dtype, 3), torch.arange(5, dtype=torch.int32)[None]
+    out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV), ints([n]), bits, 0.125 / size)
+    ref, _, bound, _ = attend64(q, values64(k, bits).view(5, ps, H, D), values64(v, bits).view(5, ps, H, D), table, [n], ps, 0.125 / size, 0, dtype, bits)
+    unit = 2.0 ** -8 if dtype == BF16 else U
+    assert ((out.cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound).all()
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("bits", [16, 8, 4])
 def test_attention_with_scores_far_apart(bits, dtype):
