@@ -586,8 +586,9 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  * no length reaches may hold anything.  A NaN or infinity in q, or in a key or value that is attended to, gives values that are
  * not finite in the rows that it enters and touches no others.  Scores, softmax and sums are fp32, over the exact codes;
  * scales multiply scores and probabilities.  For bf16 rows a probability (times its value's scale) enters the second product
- * with 16 of its bits (two bf16 parts); for fp32 rows q and the probabilities enter as three bf16 parts each, exactly.  Queries of
- * any size keep every sum in range; keys and values do up to 2^90 (the output's sums hold up to 2^8 times that of all |v|).
+ * with 16 of its bits (two bf16 parts); for fp32 rows q and the probabilities enter as three bf16 parts each, exactly.  Queries and
+ * scales of any size keep every sum in range, also where their product passes the largest number and the scores do not; keys
+ * and values do up to 2^90 (the output's sums hold up to 2^8 times that of all |v|).
  * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_cache_attention(const void* Q, gptq_dtype_t dtype, int64_t R, int64_t Hq, int64_t H, int64_t D,

@@ -1,6 +1,7 @@
 // Attention of new tokens over their pages: the launch, and the join of sums that several workgroups hold
 // (kernels in attention_kernel.hpp).
 #include <algorithm>
+#include <cmath>
 
 #include "attention.hpp"
 
@@ -128,7 +129,7 @@ hipError_t cache_attention(const AttentionArgs& a, void* workspace, hipStream_t 
     k.table = a.table, k.ld_table = a.ld_table;
     k.max_tokens = (uint32_t)(a.max_pages * a.pages.page_size);
     k.lengths = a.lengths;
-    k.scale_log2e = a.scale * kLog2e;
+    k.scale_log2e = std::frexp(a.scale, &k.scale_exponent) * kLog2e;
     k.window = a.window;
     k.R = a.R, k.Hq = a.Hq, k.H = a.H, k.D = a.D, k.group = a.Hq / a.H;
     k.tiles = (int)ceil_div(k.group, kTileHeads), k.segments = a.H * k.tiles;

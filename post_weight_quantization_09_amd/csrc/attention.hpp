@@ -33,7 +33,8 @@ struct AttentionKernelArgs {
     int64_t ld_table;
     uint32_t max_tokens;                // of the table's columns
     const int32_t* lengths;
-    float scale_log2e;
+    float scale_log2e;                  // scale log2 e is scale_log2e 2^scale_exponent, scale_log2e of size one
+    int scale_exponent;
     int64_t window;
     int R, Hq, H, D, group;             // group = Hq / H query heads share a key head
     int tiles, segments;                // per key head and per request

@@ -41,6 +41,7 @@ namespace gptq {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRaise = 8.0f;
+constexpr int kMostExponent = 120;              // of to_log2's power of two: what it multiplies is below 2^6
 
 __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
@@ -349,10 +350,11 @@ __device__ __forceinline__ void load_block(const AttentionKernelArgs& a, const V
     }
 }
 
-// less: what the scores begin with (the negative of their excess)
+// less: what the scores begin with (the negative of their excess); to_log2 2^more: what brings them to powers of two, far: whether
+// any lane's `more` is not 0
 template <int NC, int BITS, int PARTS>
-__device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q)[NC][PARTS], float less, float to_log2, float& m,
-                                     float& l, f32x4 (&o)[AttentionTraits<NC, BITS, PARTS>::kTiles]) {
+__device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q)[NC][PARTS], float less, float to_log2, bool far, int more,
+                                     float& m, float& l, f32x4 (&o)[AttentionTraits<NC, BITS, PARTS>::kTiles]) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     f32x4 s[2];
     for (int T = 0; T < 2; ++T) {
@@ -373,6 +375,9 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
         x[j] = s[j / 4][j % 4];
         if constexpr (BITS < 16) x[j] *= b.ks[j];
         x[j] *= to_log2;
+    }
+    if (far) {
+        for (int j = 0; j < 8; ++j) x[j] = ldexpf(x[j], more);
     }
     if (!b.whole) {
         for (int j = 0; j < 8; ++j) x[j] = b.seen >> j & 1 ? x[j] : -INFINITY;
@@ -429,11 +434,11 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     }
 }
 
-// q of a lane's head as B operands.  Values of extreme size are brought near one by a power of two (which to_log2 takes back),
-// so that no sum on the way leaves the range of fp32.
+// q of a lane's head as B operands.  Values of extreme size are brought near one by a power of two (which to_log2 and `more` take
+// back: their product may pass the largest number where the scores do not), so that no sum on the way leaves the range of fp32.
 template <typename E, int NC, int BITS, int PARTS>
-__device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quarter, bf16x8 (&q)[NC][PARTS], float& less,
-                                       float& to_log2) {
+__device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quarter, float scale, int exponent,
+                                       bf16x8 (&q)[NC][PARTS], float& less, float& to_log2, int& more) {
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     Eight<E> y[NC];
     for (int c = 0; c < NC; ++c) {
@@ -446,10 +451,12 @@ __device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quart
     for (int c = 0; c < NC; ++c) most = fmaxf(most, y[c].most());
     most = max_of_quarters(most);
     if (__any(most > 0x1p20f || (most < 0x1p-20f && most > 0.0f))) {
-        const int e = most == 0.0f || most > 3.4e38f ? 0 : ilogbf(most);
+        const int e = most == 0.0f || most == INFINITY ? 0 : ilogbf(most);
         for (int c = 0; c < NC; ++c) y[c].scale(-e);
-        to_log2 = ldexpf(to_log2, e);
+        exponent += e;
     }
+    more = max(exponent - kMostExponent, 0);
+    to_log2 = ldexpf(Tr::kUnit * scale, exponent - more);
     less = 0.0f;
     for (int c = 0; c < NC; ++c) {
         if constexpr (Tr::kExcess) less += y[c].codes_order();
@@ -528,15 +535,17 @@ __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attentio
             if (todo > 0) load_block(a, vis, look_up(a, table, vis, t), head, lane, b);
             Halves next = look_up(a, table, vis, t += kBlockTokens);        // a block's pages are known when its turn comes
             bf16x8 q[NC][PARTS];
-            float less, to_log2 = a.scale_log2e * Tr::kUnit;
+            float less, to_log2;
+            int more;
             load_q<E, NC, BITS, PARTS>(static_cast<const E*>(a.q) + r * a.q_rs + (hq + min(n, heads - 1)) * a.q_hs, n < heads, a.D,
-                                       quarter, q, less, to_log2);
+                                       quarter, a.scale_log2e, a.scale_exponent, q, less, to_log2, more);
+            const bool far = __any(more > 0);
 
             f32x4 o[Tr::kTiles];
             for (int i = 0; i < Tr::kTiles; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             float m = -INFINITY, l = 0.0f;
             while (todo > 0) {
-                step<NC, BITS, PARTS>(b, q, less, to_log2, m, l, o);
+                step<NC, BITS, PARTS>(b, q, less, to_log2, far, more, m, l, o);
                 if (--todo > 0) {
                     load_block(a, vis, next, head, lane, b);
                     next = look_up(a, table, vis, t = (uint32_t)__builtin_amdgcn_readfirstlane((int)(t + kBlockTokens)));
