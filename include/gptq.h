@@ -585,8 +585,9 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  * A request without a token to attend to gets zeros, and lse -infinity; so does one whose scores are all -infinity.  Slots that
  * no length reaches may hold anything.  A NaN or infinity in q, or in a key or value that is attended to, gives values that are
  * not finite in the rows that it enters and touches no others.  Scores, softmax and sums are fp32, over the exact codes;
- * scales multiply scores and probabilities.  For bf16 rows a probability (times its value's scale) enters the second product
- * with 16 of its bits (two bf16 parts); for fp32 rows q and the probabilities enter as three bf16 parts each, exactly.  Queries and
+ * scales multiply scores and probabilities.  Probabilities (times
+ * their value's scale), and q of fp32 rows, enter the products as three bf16 parts each, exactly.  With 4 bits under bf16 rows the
+ * sums hold code + 24 or code - 23 in the code's place, up to 31 steps s, and that excess is taken off them in fp32.  Queries and
  * scales of any size keep every sum in range, also where their product passes the largest number and the scores do not; keys
  * and values do up to 2^90 (the output's sums hold up to 2^8 times that of all |v|).
  * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.

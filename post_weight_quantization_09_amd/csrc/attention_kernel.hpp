@@ -13,10 +13,12 @@
 // register and code - 23 in the high half, and the excess 24 sum(low) - 23 sum(high) is taken off the sums in fp32: that of
 // the scores before they are begun, that of the output after them, from a product with (24, -23).  The signs alternate so that
 // the sums stay near the size of their result (an excess of one sign would reach 24 where the mean of many codes is near 0).
-// A token's key scale multiplies its score, its value scale its probability.  With fp32 rows q and the probabilities are cut into three
-// bf16 parts each (exact), so that nothing is rounded but sums.  bf16 rows have probability times scale in two bf16 parts, 16 of
-// its 24 bits: one part's error, 2^-9 of each of many terms of either sign, is as large in their sum as the output's own
-// rounding (against 64 bits 2.5e-3 where that alone is 1.7e-3).
+// A token's key scale multiplies its score, its value scale its probability.  Probabilities (times that scale), and q of fp32
+// rows, are cut into three bf16 parts each (exact), so that nothing is rounded but sums.  Fewer parts were measured for bf16
+// rows.  One: its error, 2^-9 of each of many terms of either sign, is as large in their sum as the output's own rounding
+// (against 64 bits 2.5e-3 where that alone is 1.7e-3).  Two, 16 bits: that rounding falls the other way in 0.4% of the outputs, with
+// three in 0.06% as between two orders of the sum (4 bits: 0.3%, by the sums of the excess); 131072 tokens in 4 bits 44.4 us with
+// two, 44.9 with three, heads of 64 45.0 and 47.3, no other case measured by more than 3%.
 //
 // Softmax: scores are kept times log2 e.  A lane's maximum is raised (and what was summed rescaled) only where a score passes it
 // by 8: probabilities then reach 2^8, which fp32 sums and bf16 factors bear as well as 1, and few steps rescale.
@@ -131,19 +133,14 @@ __device__ __forceinline__ bf16x8 nibbles_to_excess(uint32_t w0, uint32_t w1) {
     return __builtin_bit_cast(bf16x8, u32x4{excess_pair<HALF>(w0), excess_pair<HALF + 8>(w0), excess_pair<HALF>(w1), excess_pair<HALF + 8>(w1)});
 }
 
-// Eight fp32 values as PARTS bf16 operands, each but the last cut off after eight bits (exact with three), the last of two rounded.
-template <int PARTS>
-__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]) {
+// Eight fp32 values as three bf16 operands, each cut off after eight bits (exact).
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[3]) {
     float rest[8];
     for (int i = 0; i < 8; ++i) rest[i] = x[i];
-    for (int p = 0; p < PARTS; ++p) {
+    for (int p = 0; p < 3; ++p) {
         u32x4 r;
-        if (PARTS == 2 && p == 1) {
-            for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(rest[2 * i], rest[2 * i + 1]);
-        } else {
-            for (int i = 0; i < 4; ++i) r[i] = high_halves(rest[2 * i], rest[2 * i + 1]);
-            for (int i = 0; i < 8; ++i) rest[i] -= __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) r[i] = high_halves(rest[2 * i], rest[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) rest[i] -= __uint_as_float(__float_as_uint(rest[i]) & 0xFFFF0000u);
         out[p] = __builtin_bit_cast(bf16x8, r);
     }
 }
@@ -196,7 +193,7 @@ struct Eight<float> {
     __device__ void scale(int e) {
         for (int i = 0; i < 8; ++i) v[i] = ldexpf(v[i], e);
     }
-    __device__ void operand(bf16x8 (&q)[3]) const { split8<3>(v, q); }
+    __device__ void operand(bf16x8 (&q)[3]) const { split8(v, q); }
 };
 
 // Four values rounded to rows of any alignment that their type has.
@@ -272,7 +269,7 @@ struct AttentionTraits {
     static constexpr int kValueLoadWords = kDims * BITS / 4;
     static constexpr bool kExcess = BITS == 4 && PARTS == 1;        // codes enter as code + 24 and code - 23
     static constexpr float kUnit = BITS == 4 && !kExcess ? 16.0f : 1.0f;
-    static constexpr int kProbabilityParts = PARTS == 1 ? 2 : 3;
+    static constexpr int kProbabilityParts = 3;                     // bf16 operands of a probability times its value's scale
     static constexpr int kTiles = 2 * NC + (kExcess ? 1 : 0);       // of the output, and the sums of its excess
 };
 
@@ -412,12 +409,12 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     bf16x8 p[kParts];
     if constexpr (Tr::kExcess) {
         const float in_order[8] = {p8[0], p8[2], p8[1], p8[3], p8[4], p8[6], p8[5], p8[7]};
-        split8<kParts>(in_order, p);
+        split8(in_order, p);
         const bf16x8 excess = __builtin_bit_cast(bf16x8, u32x4{kExcess, kExcess, kExcess, kExcess});
         for (int part = kParts - 1; part >= 0; --part)
             o[2 * NC] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(excess, p[part], o[2 * NC], 0, 0, 0);
     } else {
-        split8<kParts>(p8, p);
+        split8(p8, p);
     }
     for (int i = 0; i < Tr::kValueLoads; ++i) {
         const uint32_t* w = &b.v[i * Tr::kValueLoadWords];

@@ -68,3 +68,46 @@ def test_attention_of_zero_keys_under_large_queries_and_scales(scale, bits, dtyp
         ref, _, bound, _ = attend64(torch.zeros_like(q), held(k, bits), held(v, bits), table.cpu(), [70], 16, 1.0, 0, dtype, bits)
         assert_near(out, ref, bound, dtype)
         assert (lse.cpu().double() - math.log(70)).abs().max() <= 80 * U
+
+
+# ------------------------------------------------------------------------------------------- probabilities in all bits
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_to_one_token_gives_its_value(bits, dtype):
+    """The probability is 1: the output is the value s c rounded once, whatever the scale's bits.  Its sum is at most three products
+    of eight-bit parts, each addition off by at most 2 u of what it holds: s c, or with 4 bits under bf16 rows s (c + 24), at most
+    31 s, and the excess 24 s, taken off at the end: 3 * 2 u (31 + 24) s + u 8 s < 344 u s."""
+    n, H, D = 64, 4, 128
+    k, v = gen_rows((n, H, D), BF16, 1), gen_rows((n, H, D), F32, 2)
+    pages, _ = written(k.to(F32), v, bits)
+    # a request for every token: its page, as many tokens as reach it, a window of one
+    at = torch.arange(n, dtype=torch.int32, device=DEV)
+    table, lengths = (at // 16)[:, None].contiguous(), at % 16 + 1
+    out = g.gptq_cache_attention(gen_rows((n, H, D), dtype, 3).to(DEV), pages, table, lengths, bits, window=1).cpu()
+    ref = values64(v, bits)
+    off = 8 * U * ref.abs()
+    if bits == 4 and dtype == BF16:
+        off = 344 * U * ref.abs().amax(-1, keepdim=True) / 7             # a row's largest code is 7, or -8 (then s is less)
+    low, high = (ref - off).float().to(dtype), (ref + off).float().to(dtype)
+    if dtype == F32:
+        low, high = ref - off, ref + off
+    assert ((out >= low) & (out <= high)).all(), int(((out < low) | (out > high)).sum())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_of_a_dimension_of_zeros_is_zero(dtype):
+    """4 bits under bf16 rows: what the codes are raised by is taken off again by the same sums, whatever the probabilities."""
+    lengths, H, D = [1, 40, 3000, 700], 2, 128
+    k, v = gen_rows((3776, H, D), BF16, 1), gen_rows((3776, H, D), BF16, 2)
+    v[..., [0, 5, 62, 127]] = 0.0
+    pages, table = written(k, v, 4)
+    tables = torch.zeros(4, 188, dtype=torch.int32, device=DEV)
+    first = 0
+    for r, n in enumerate(lengths):
+        tables[r, :-(-n // 16)] = table[0, first:first + -(-n // 16)]
+        first += -(-n // 16)
+    out = g.gptq_cache_attention(gen_rows((4, 8, D), dtype, 3).to(DEV), pages, tables, ints(lengths), 4)
+    assert not out[..., [0, 5, 62, 127]].any() and out.any(-1).all()
