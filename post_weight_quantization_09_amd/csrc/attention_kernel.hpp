@@ -453,7 +453,8 @@ __device__ __forceinline__ void load_q(const E* x, bool wanted, int D, int quart
         exponent += e;
     }
     more = max(exponent - kMostExponent, 0);
-    to_log2 = ldexpf(Tr::kUnit * scale, exponent - more);
+    // an infinity makes every score infinite or NaN: NaN for all of them, whatever the signs that it meets
+    to_log2 = most == INFINITY ? NAN : ldexpf(Tr::kUnit * scale, exponent - more);
     less = 0.0f;
     for (int c = 0; c < NC; ++c) {
         if constexpr (Tr::kExcess) less += y[c].codes_order();

@@ -111,3 +111,31 @@ def test_attention_of_a_dimension_of_zeros_is_zero(dtype):
         first += -(-n // 16)
     out = g.gptq_cache_attention(gen_rows((4, 8, D), dtype, 3).to(DEV), pages, tables, ints(lengths), 4)
     assert not out[..., [0, 5, 62, 127]].any() and out.any(-1).all()
+
+
+# ------------------------------------------------------------------------------------------------- what is not finite
+
+@gpu
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_of_a_query_that_is_not_finite(bits, dtype, value):
+    """NaN in its own row, also where every key meets the infinity with the sign that makes all scores -infinity; zeros where there
+    is nothing to attend to."""
+    lengths, H, D = [70, 0, 1, 3000], 2, 64
+    k, v = gen_rows((3168, H, D), BF16, 1), gen_rows((3168, H, D), BF16, 2)
+    k[..., 5] = -k[..., 5].abs() - 1.0                                # never a code of zero
+    k[..., 6] = k[..., 5].abs()
+    pages, table = written(k, v, bits)
+    tables = torch.stack([table[0, :188], table[0, :188], table[0, 2:190], table[0, 5:193]])
+    q = gen_rows((4, 4, D), dtype, 3)
+    call = lambda x, lse: g.gptq_cache_attention(x.to(DEV), pages, tables, ints(lengths), bits, lse=lse).cpu()  # noqa: E731
+    logs, clean_logs = torch.empty(4, 4, device=DEV), torch.empty(4, 4, device=DEV)
+    clean = call(q, clean_logs)
+    for d in (5, 6):
+        bad = q.clone()
+        bad[:, 1, d] = value
+        out = call(bad, logs)
+        assert out[[0, 2, 3], 1].isnan().all() and logs[[0, 2, 3], 1].isnan().all()
+        assert not out[1].any() and (logs[1] == -math.inf).all()
+        assert torch.equal(out[:, [0, 2, 3]], clean[:, [0, 2, 3]]) and torch.equal(logs[:, [0, 2, 3]], clean_logs[:, [0, 2, 3]])
