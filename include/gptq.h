@@ -584,8 +584,10 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  *   workspace  device scratch of gptq_attention_workspace_bytes(R, Hq, H, D).
  * A request without a token to attend to gets zeros, and lse -infinity; so does one whose scores are all -infinity.  Slots that
  * no length reaches may hold anything.  A NaN or infinity in q makes its row of out, and its lse, NaN (where it attends to a
- * token at all); one in a key or value that is attended to gives values that are not finite in the rows that it enters; neither
- * touches other rows.  Scores, softmax and sums are fp32, over the exact codes;
+ * token at all).  A key that is attended to and holds an infinity (16 bits; with 8 and 4 its row reads back as NaN) gives
+ * infinite scores: one of -infinity leaves its token out, one of +infinity makes the row NaN, as a NaN in a key does.  A NaN or
+ * infinity in a value that is attended to gives values that are not finite there (with 8 and 4 bits in the whole row).  Other rows
+ * are not touched.  Scores, softmax and sums are fp32, over the exact codes;
  * scales multiply scores and probabilities.  Probabilities (times
  * their value's scale), and q of fp32 rows, enter the products as three bf16 parts each, exactly.  With 4 bits under bf16 rows the
  * sums hold code + 24 or code - 23 in the code's place, up to 31 steps s, and that excess is taken off them in fp32.  Queries and

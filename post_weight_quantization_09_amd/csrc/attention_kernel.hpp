@@ -270,6 +270,9 @@ struct AttentionTraits {
     static constexpr bool kExcess = BITS == 4 && PARTS == 1;        // codes enter as code + 24 and code - 23
     static constexpr float kUnit = BITS == 4 && !kExcess ? 16.0f : 1.0f;
     static constexpr int kProbabilityParts = 3;                     // bf16 operands of a probability times its value's scale
+    // q's lower parts may be zeros: times an infinite key they are NaN where the product is an infinity, which the first part's sum
+    // has by itself (a NaN in a key, or a zero in q, makes that one NaN too)
+    static constexpr bool kLowApart = BITS == 16 && PARTS > 1;
     static constexpr int kTiles = 2 * NC + (kExcess ? 1 : 0);       // of the output, and the sums of its excess
 };
 
@@ -355,7 +358,7 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
     using Tr = AttentionTraits<NC, BITS, PARTS>;
     f32x4 s[2];
     for (int T = 0; T < 2; ++T) {
-        f32x4 acc = {less, less, less, less};
+        f32x4 acc = {less, less, less, less}, low = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int c = 0; c < NC; ++c) {
             const uint32_t* w = &b.k[T][c * Tr::kWordsPerChunk];
             bf16x8 k;
@@ -363,8 +366,13 @@ __device__ __forceinline__ void step(Block<NC, BITS, PARTS>& b, const bf16x8 (&q
             else if constexpr (BITS == 8) k = bytes_to_bf16(w[0], w[1]);
             else if constexpr (Tr::kExcess) k = word_to_excess(w[0]);
             else k = word_to_bf16(w[0]);
-            for (int p = PARTS - 1; p >= 0; --p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[c][p], acc, 0, 0, 0);
+            for (int p = PARTS - 1; p >= 0; --p) {
+                f32x4& sum = Tr::kLowApart && p > 0 ? low : acc;
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[c][p], sum, 0, 0, 0);
+            }
         }
+        if constexpr (Tr::kLowApart)
+            for (int i = 0; i < 4; ++i) acc[i] += low[i] == low[i] ? low[i] : 0.0f;
         s[T] = acc;
     }
     float x[8];

@@ -139,3 +139,29 @@ def test_attention_of_a_query_that_is_not_finite(bits, dtype, value):
         assert out[[0, 2, 3], 1].isnan().all() and logs[[0, 2, 3], 1].isnan().all()
         assert not out[1].any() and (logs[1] == -math.inf).all()
         assert torch.equal(out[:, [0, 2, 3]], clean[:, [0, 2, 3]]) and torch.equal(logs[:, [0, 2, 3]], clean_logs[:, [0, 2, 3]])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 2, 33, 70, 3000])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_attention_of_an_infinite_key(n, dtype, value):
+    """16 bits, the last token's key: a score of -infinity leaves its token out, as if the length were one less, and one of
+    +infinity makes the row NaN; also where q holds a number of few bits there (whose lower parts are zeros), or a zero."""
+    H, D, d = 1, 64, 9
+    k, v = gen_rows((n, H, D), BF16, 1), gen_rows((n, H, D), BF16, 2)
+    k[-1, 0, d] = value
+    pages, table = written(k, v, 16)
+    q = gen_rows((1, 9, D), dtype, 3)
+    sign = 1.0 if value > 0 else -1.0
+    q[0, :9, d] = torch.tensor([-1.0, -0.3333333, -1.0 - 2.0 ** -9, -2.0 ** -30, 1.0, 0.3333333, 1.0 + 2.0 ** -9, 2.0 ** 30, 0.0]).to(dtype) * sign
+    lse = torch.empty(1, 9, device=DEV)
+    out = g.gptq_cache_attention(q.to(DEV), pages, table, ints([n]), 16, lse=lse).cpu()
+    assert out[0, 4:].isnan().all() and lse[0, 4:].isnan().all()
+    fine = torch.nan_to_num(held(k, 16), nan=0.0, posinf=0.0, neginf=0.0)
+    ref, ref_lse, bound, lse_bound = attend64(q[:, :4], fine, held(v, 16), table.cpu(), [n - 1], 16, D ** -0.5, 0, dtype, 16)
+    assert_near(out[:, :4], ref, bound, dtype)
+    if n == 1:
+        assert (lse[0, :4] == -math.inf).all() and not out[:, :4].any()
+    else:
+        assert ((lse.cpu()[:, :4].double() - ref_lse).abs() <= lse_bound + U).all()
