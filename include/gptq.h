@@ -519,7 +519,8 @@ gptq_status_t gptq_rotary_frequencies(int64_t rot, double base, int scaling, dou
 /*
  * gptq_rotary - the first rot elements of every row turned by its token's position, the others copied:
  *   (a, b) -> factor (a cos - b sin, b cos + a sin) of the angle positions[t] * freqs[i],  i < rot / 2.
- * Angles are reduced in 64 bits; products and sums are fp32, with one rounding to bf16.
+ * Angles lose their whole turns in two 64-bit numbers, so that the fraction of a turn is right to fp32's last place (2^-25 of a
+ * turn) at every position; products and sums are fp32, with one rounding to bf16.
  *   X          device, T x H x D, dtype.   T 0..2^22, D 1..1024, rot even, 2..D.
  *   positions  device int32[T], any value.   freqs: device double[rot / 2], finite, of size at most 2^20.
  *   flags      GPTQ_FLAG_INTERLEAVED or 0.

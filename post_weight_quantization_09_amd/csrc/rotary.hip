@@ -1,7 +1,9 @@
 // Rotary positions: every pair of a head's elements turned by position * frequency.
 //
-// The angle is taken in turns and in 64 bits: position * f / 2 pi loses its whole turns there, so that what the sine and
-// cosine see is a fraction of a turn with 2^-32 or better at any 32-bit position; they are evaluated in fp32, once for a
+// The angle is taken in turns, position * f / 2 pi, in two 64-bit numbers (both products with what their rounding leaves off,
+// and 1 / 2 pi in two parts), and loses its whole turns there: what the sine and cosine see is a fraction of a turn within 2^-53
+// at any 32-bit position and any f up to 2^20, rounded to fp32.  (In one number it is off by 2^-24 of a turn at position 2^31 for f
+// near 1, by 2^-4 for f near 2^20.)  They are evaluated in fp32, once for a
 // token's pair whatever the number of heads, and wait in LDS.  What is left is a copy: a workgroup takes some tokens' rows of
 // some heads, 16 bytes a load where the pairs allow it (units of V pairs), and is bound by memory traffic.
 //
@@ -30,9 +32,10 @@ struct RotaryArgs {
 
 // cos and sin of position * f, times the factor
 __device__ __forceinline__ f32x2 turn(int position, double f, float factor) {
-    constexpr double kPerTurn = 0.15915494309189533577;   // 1 / 2 pi
-    const double turns = (double)position * f * kPerTurn;
-    const float part = (float)(turns - rint(turns));
+    constexpr double kPerTurn = 0.15915494309189533577, kPerTurnRest = -9.839338337591243e-18;      // 1 / 2 pi
+    const double angle = position * f, angle_rest = fma((double)position, f, -angle);
+    const double whole = rint(angle * kPerTurn);
+    const float part = (float)(fma(angle, kPerTurn, -whole) + (angle * kPerTurnRest + angle_rest * kPerTurn));
     f32x2 cs;
     cs[0] = factor * cospif(2.0f * part);
     cs[1] = factor * sinpif(2.0f * part);

@@ -165,3 +165,43 @@ def test_attention_of_an_infinite_key(n, dtype, value):
         assert (lse[0, :4] == -math.inf).all() and not out[:, :4].any()
     else:
         assert ((lse.cpu()[:, :4].double() - ref_lse).abs() <= lse_bound + U).all()
+
+
+# ---------------------------------------------------------------------------------------------------------- far angles
+
+def pi_times(scale):
+    """pi * scale as a whole number, off by a few units: 16 atan(1/5) - 4 atan(1/239)."""
+    def atan(n):
+        total, power, i = 0, scale // n, 1
+        while power:
+            total += power // i if i % 4 == 1 else -(power // i)
+            power //= n * n
+            i += 2
+        return total
+    return 16 * atan(5) - 4 * atan(239)
+
+
+TURN = Fraction(2 * pi_times(10 ** 60), 10 ** 60)       # of a double's product with a position, up to 2^51: wrong by 2^-140 of a turn
+
+
+def rotary_exactly(x, positions, freqs, factor):
+    """Halves turned by angles reduced in rationals, and the bound without any term of the angle's size."""
+    half = len(freqs)
+    angle = torch.tensor([[2 * math.pi * float(Fraction(p) * Fraction(f) / TURN % 1) for f in freqs.tolist()] for p in positions.tolist()],
+                         dtype=torch.float64)[:, None]
+    a, b = x.double()[..., :half], x.double()[..., half:]
+    c, s = factor * torch.cos(angle), factor * torch.sin(angle)
+    size = (11 * U * factor * (a.abs() + b.abs())).repeat(1, 1, 2)
+    return torch.cat([a * c - b * s, b * c + a * s], -1), size
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rotary_angles_are_exact_at_any_position(dtype):
+    """Every 32-bit position and frequencies up to 2^20: the fraction of a turn has fp32's last places."""
+    positions = torch.tensor([0, 1, -1, 2 ** 17 + 3, 2 ** 24 + 1, 2 ** 30 - 5, 2 ** 31 - 1, -(2 ** 31), -(2 ** 31) + 12345, 1999999973], dtype=torch.int32)
+    for freqs, factor in ((g.gptq_rotary_frequencies(64)[0], 1.0), (torch.tensor([2.0 ** 20, -(2.0 ** 20) / 3, 1.0, 0.7, 12345.678, 2.0 * math.pi, 0.0, -1e-9], dtype=torch.float64), 1.25)):
+        x = gen_rows((10, 3, 2 * len(freqs)), dtype, 1)
+        y = g.gptq_rotary(x.to(DEV), positions.to(DEV), freqs.to(DEV), factor=factor)
+        ref, bound = rotary_exactly(x, positions, freqs, factor)
+        assert_near(y, ref, bound, dtype)
