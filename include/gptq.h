@@ -498,7 +498,7 @@ gptq_status_t gptq_combine(const void* Y, gptq_dtype_t dtype, int64_t M, int64_t
 /* Scalings of gptq_rotary_frequencies. */
 #define GPTQ_ROTARY_PLAIN  0   /* f_i = base^(-2 i / rot) */
 #define GPTQ_ROTARY_LINEAR 1   /* f_i / factor: positions interpolated */
-#define GPTQ_ROTARY_BASE   2   /* base * factor^(rot / max(rot - 2, 1)) in base's place */
+#define GPTQ_ROTARY_BASE   2   /* base * factor^(rot / max(rot - 2, 1)), which must be finite, in base's place */
 #define GPTQ_ROTARY_RAMP   3   /* pairs of at least `high` turns over `original` positions as they are, of at most `low` f_i / factor,
                                   a ramp over the pairs between; magnitude 0.1 ln(factor) + 1 */
 #define GPTQ_ROTARY_BANDS  4   /* the same by frequency: share (original f_i / 2 pi - low) / (high - low), in [0, 1], as it is */

@@ -52,6 +52,7 @@ gptq_status_t gptq_rotary_frequencies(int64_t rot, double base, int scaling, dou
     if (banded && (!(original >= 1.0) || !std::isfinite(original) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
         return GPTQ_ERR_ARG;
     if (scaling == GPTQ_ROTARY_BASE) base *= std::pow(factor, (double)rot / (double)std::max<int64_t>(rot - 2, 1));
+    if (!std::isfinite(base)) return GPTQ_ERR_ARG;
     const double two_pi = 2.0 * M_PI;
     double first = 0.0, last = 0.0;
     if (scaling == GPTQ_ROTARY_RAMP) {

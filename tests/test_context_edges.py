@@ -205,3 +205,11 @@ def test_rotary_angles_are_exact_at_any_position(dtype):
         y = g.gptq_rotary(x.to(DEV), positions.to(DEV), freqs.to(DEV), factor=factor)
         ref, bound = rotary_exactly(x, positions, freqs, factor)
         assert_near(y, ref, bound, dtype)
+
+
+# -------------------------------------------------------------------------------------------------------- frequencies
+
+def test_frequencies_of_a_base_that_is_none_are_refused():
+    for rot, base, factor in ((2, 1e200, 1e60), (64, 1e300, 1e10), (4, 10.0, 1e155)):
+        with pytest.raises(g.GptqError):
+            g.gptq_rotary_frequencies(rot, base, "base", factor)
