@@ -66,7 +66,8 @@ gptq_status_t gptq_rotary_frequencies(int64_t rot, double base, int scaling, dou
         double keep = 1.0;                     // share of f that is not stretched
         if (scaling == GPTQ_ROTARY_LINEAR) keep = 0.0;
         if (scaling == GPTQ_ROTARY_RAMP)
-            keep = 1.0 - std::min(std::max(((double)i - first) / std::max(last - first, 0.001), 0.0), 1.0);
+            keep = last <= 0.0 ? 0.0             // no pair makes more than `low` turns
+                               : 1.0 - std::min(std::max(((double)i - first) / std::max(last - first, 0.001), 0.0), 1.0);
         if (scaling == GPTQ_ROTARY_BANDS)
             keep = std::min(std::max((original * f / two_pi - low) / (high - low), 0.0), 1.0);
         freqs[i] = keep == 1.0 ? f : f * keep + f / factor * (1.0 - keep);

@@ -209,6 +209,31 @@ def test_rotary_angles_are_exact_at_any_position(dtype):
 
 # -------------------------------------------------------------------------------------------------------- frequencies
 
+def test_frequencies_of_a_ramp_between_its_ends():
+    """Pair by pair: as they are up to the last of at least `high` turns, stretched from the first of at most `low` on, and between
+    them in even steps from one to the other."""
+    for rot, base, factor, original, low, high in ((128, 500000.0, 8.0, 8192.0, 1.0, 32.0), (64, 10000.0, 40.0, 4096.0, 1.0, 32.0),
+                                                   (96, 10000.0, 2.5, 1000.0, 2.0, 3.0), (18, 1e6, 4.0, 32768.0, 0.5, 100.0)):
+        plain = [base ** (-2 * i / rot) for i in range(rot // 2)]
+        turns = [original * f / (2 * math.pi) for f in plain]
+        first = max([i for i in range(rot // 2) if turns[i] >= high], default=0)
+        last = min([i for i in range(rot // 2) if turns[i] <= low], default=None)
+        assert last is not None
+        ramp, m = g.gptq_rotary_frequencies(rot, base, "ramp", factor, original, low, high)
+        for i, f in enumerate(plain):
+            share = min(max((i - first) / (last - first), 0.0), 1.0)
+            want = f * (1 - share) + f / factor * share
+            assert abs(ramp[i].item() / want - 1) < 1e-13, (rot, i)
+        assert abs(m - (0.1 * math.log(factor) + 1.0)) < 1e-7
+
+
+def test_frequencies_of_a_ramp_that_every_pair_is_behind():
+    """Even the fastest pair makes at most `low` turns: all of them are stretched."""
+    for original in (1.0, 4.0, 2 * math.pi * 0.999):
+        plain, ramp = g.gptq_rotary_frequencies(64)[0], g.gptq_rotary_frequencies(64, 10000.0, "ramp", 4.0, original)[0]
+        assert torch.allclose(ramp, plain / 4, rtol=1e-14, atol=0)
+
+
 def test_frequencies_of_a_base_that_is_none_are_refused():
     for rot, base, factor in ((2, 1e200, 1e60), (64, 1e300, 1e10), (4, 10.0, 1e155)):
         with pytest.raises(g.GptqError):
