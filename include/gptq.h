@@ -593,7 +593,7 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  * their value's scale), and q of fp32 rows, enter the products as three bf16 parts each, exactly.  With 4 bits under bf16 rows the
  * sums hold code + 24 or code - 23 in the code's place, up to 31 steps s, and that excess is taken off them in fp32.  Queries and
  * scales of any size keep every sum in range, also where their product passes the largest number and the scores do not; keys
- * and values do up to 2^90 (the output's sums hold up to 2^8 times that of all |v|).
+ * and values do up to 2^90 (the output's sums hold up to 2^8 times that of all |v|), and rows of size 2^-100 or more keep every bit.
  * Errors: GPTQ_ERR_ARG, GPTQ_ERR_WORKSPACE, GPTQ_ERR_HIP.
  */
 gptq_status_t gptq_cache_attention(const void* Q, gptq_dtype_t dtype, int64_t R, int64_t Hq, int64_t H, int64_t D,

@@ -3,7 +3,6 @@ the join's forms, packed projections around them.
 
 Bounds are those of test_context.py unless a test says otherwise.
 """
-import ctypes
 import math
 from fractions import Fraction
 
@@ -238,3 +237,92 @@ def test_frequencies_of_a_base_that_is_none_are_refused():
     for rot, base, factor in ((2, 1e200, 1e60), (64, 1e300, 1e10), (4, 10.0, 1e155)):
         with pytest.raises(g.GptqError):
             g.gptq_rotary_frequencies(rot, base, "base", factor)
+
+
+# ------------------------------------------------------------------------------------------------------------ the join
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,Hq,H", [(64, 3, 1), (80, 4, 2), (128, 17, 1), (160, 2, 1), (256, 5, 1)])
+def test_attention_join_of_few_rows_over_a_long_context(D, Hq, H, dtype):
+    """A row's parts joined by several workgroups, each a slice of the stored dimensions (which need not divide a workgroup)."""
+    check_attention([20000, 0, 33, 1500], Hq, H, D, 32, 8, dtype, seed=D)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 96, 256])
+def test_attention_of_short_requests_under_a_wide_table(D, dtype):
+    """Columns for 20000 tokens and lengths of a few: few parts, or none, where many were possible."""
+    check_attention([1, 100, 0, 700, 33], 4, 2, D, 16, 8, dtype, seed=D, extra=1250)
+    check_attention([300], 4, 1, D, 16, 16, dtype, window=40, seed=D, extra=1250)
+
+
+# ------------------------------------------------------------------------------------------------- the size of values
+
+@gpu
+@pytest.mark.parametrize("size", [2.0 ** 90, 2.0 ** -100])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_attention_of_the_largest_and_smallest_keys_and_values(bits, dtype, size):
+    k, v = ((gen_rows((75, 2, 64), F32, i) * size).to(BF16) for i in (1, 2))
+    pages, table = written(k, v, bits)
+    q = gen_rows((1, 4, 64), dtype, 3)
+    out = g.gptq_cache_attention(q.to(DEV), pages, table, ints([75]), bits, 0.125 / size)
+    ref, _, bound, _ = attend64(q, held(k, bits), held(v, bits), table.cpu(), [75], 16, 0.125 / size, 0, dtype, bits)
+    unit = 2.0 ** -8 if dtype == BF16 else U
+    assert ((out.cpu().double() - ref).abs() <= unit * ref.abs() + (1 + unit) * bound).all()
+
+
+# ------------------------------------------------------------------------------------------------------------ together
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_a_prompt_as_requests_of_one_table_row(bits, dtype):
+    """Every token of a prompt attends to what is before it: as a request of its own, all with the same row of the table."""
+    n, D = 75, 64
+    pages, k, v, table = filled([n], 2, D, 16, bits, 1)
+    q, lengths = gen_rows((n, 4, D), dtype, 2), list(range(1, n + 1))
+    out = g.gptq_cache_attention(q.to(DEV), pages, table.to(DEV).expand(n, -1), ints(lengths), bits)
+    ref, _, bound, _ = attend64(q, k, v, table.expand(n, -1), lengths, 16, D ** -0.5, 0, dtype, bits)
+    assert_near(out, ref, bound, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bits", [16, 8, 4])
+def test_between_packed_projections(bits, dtype):
+    """A layer's step from its input to the output of its last projection; every call against 64 bits of what it was given."""
+    from test_serve import close, layer, packed_on, rows_of, slack
+    R, K, Hq, H, D, ps = 9, 192, 6, 2, 64, 16
+    before = [33, 0, 5, 100, 16, 15, 31, 64, 1]
+    codes, scales, W, s = layer(K, (Hq + 2 * H) * D, 4, 64, 1)
+    codes_o, scales_o, W_o, s_o = layer(Hq * D, K, 4, 64, 2)
+    pages, keys, values, table = filled(before, H, D, ps, bits, 3, stale=0.0, spare=R)
+    free = [p for p in range(pages.shape[0]) if not (table == p).any()]
+    for r, n in enumerate(before):
+        if n % ps == 0:
+            table[r, n // ps] = free.pop()
+    slots = [int(table[r, n // ps]) * ps + n % ps for r, n in enumerate(before)]
+    lengths = [n + 1 for n in before]
+    freqs, factor = g.gptq_rotary_frequencies(D, 500000.0, "bands", 8.0)
+    x = rows_of(R, K, dtype, 4)
+
+    qkv = g.gptq_adapter_matmul(x.to(DEV), packed_on(codes, 4, DEV)[0], scales[0].to(DEV), 4, groupsize=64)
+    close(qkv, x.double() @ W[0], slack(x, s[0], 4, dtype, K), dtype)
+    heads = qkv.view(R, Hq + 2 * H, D)
+    given = heads.cpu()
+    turned = heads[:, :Hq + H]
+    g.gptq_rotary(turned, ints(before), freqs.to(DEV), factor=factor, out=turned)
+    assert_near(turned, *rotary_exactly(given[:, :Hq + H], torch.tensor(before), freqs, factor), dtype)
+    assert torch.equal(heads[:, Hq + H:].cpu(), given[:, Hq + H:])
+    g.gptq_cache_write(heads[:, Hq:Hq + H], heads[:, Hq + H:], pages, ints(slots), bits)
+    out = g.gptq_cache_attention(heads[:, :Hq], pages, table.to(DEV), ints(lengths), bits)
+    for where, rows in ((keys, heads[:, Hq:Hq + H]), (values, heads[:, Hq + H:])):
+        where.view(-1, H, D)[slots] = values64(rows.cpu(), bits)
+    ref, _, bound, _ = attend64(heads[:, :Hq].cpu(), keys, values, table, lengths, ps, D ** -0.5, 0, dtype, bits)
+    assert_near(out, ref, bound, dtype)
+    y = g.gptq_adapter_matmul(out.view(R, Hq * D), packed_on(codes_o, 4, DEV)[0], scales_o[0].to(DEV), 4, groupsize=64)
+    rows = out.view(R, Hq * D).cpu()
+    close(y, rows.double() @ W_o[0], slack(rows, s_o[0], 4, dtype, Hq * D), dtype)
