@@ -25,16 +25,22 @@
 //
 // Work is shared out by blocks of 32 tokens: all blocks of all segments (a request and 16 query heads of a key head) lie on
 // one line, and wave w takes the w-th piece of it, whatever the lengths: an even share for 64 ragged requests as for one of
-// 131072 tokens beside short ones.  Every workgroup scans the lengths for itself.  A wave that has a whole segment writes its
+// 131072 tokens beside short ones.  Every workgroup scans the lengths for itself, R / 64 of them a lane, one load after the other:
+// nothing beside the rest up to some hundred requests, most of the time of very many (below).  A wave that has a whole segment writes its
 // output; one that has a part of it writes unnormalised sums, which the join adds in order.  Waves share nothing else: no LDS
 // and no barrier in the loop, and little code, which counts where a call is short (the instructions of a launch come from
 // memory once per CU).  (Four waves of a workgroup on one segment, joined in LDS, with three times the code before the loop:
 // 111 us against 91 for 64 ragged requests, 15 against 12 for a short one.)
 //
-// Measured on MI355X, heads of 128: 256 requests of 1950 tokens in 16 bits, 1.02 GB, 195 us and 6 of the join (5.2 TB/s of
-// reads; a copy moves 4.9); 64 ragged requests in 8 bits, 415 MB, 83 and 6 us (5.0 TB/s); 131072 tokens in 4 bits, 64 query
-// heads, 145 MB, 36 and 8 us: there half the cycles issue vector instructions (356 a block: conversions, softmax, addresses).  A
-// call whose work is nothing takes 7 + 4 us: lengths, page table and pages are three latencies in a row, the join a launch.
+// Measured on MI355X, heads of 128: 256 requests of 1950 tokens in 16 bits, 1.02 GB, 190 to 195 us and 7 of the join (5.2 TB/s of
+// reads; a copy moves 4.9); 64 ragged requests in 8 bits, 415 MB, 83 to 86 and 7 us (4.9 TB/s); 131072 tokens in 4 bits, 64 query
+// heads, 145 MB, 37 to 39 and 8 us: there vector instructions take 48% of the cycles (some 380 a block: conversions, softmax,
+// addresses), and with three waves a SIMD most of the rest is their waiting for a block's loads, which are
+// issued when the block before is done.  A call whose work is nothing takes 7 + 4 us: lengths, page table and pages are three
+// latencies in a row, the join a launch.  Many requests, 4 query heads on one or two of 128, 8 bits: 2048 of 95 tokens 43 us, 16384
+// of 40 154, 65536 of 20 (heads of 64) 478.  Groups of more than 16 query heads are two segments, each of which reads the keys and
+// values: 16 requests of 4000 tokens, 4 key heads, 16 and 20 query heads each: 16 bits 32 and 47 us, 8 bits 26 and 34, 4 bits 25
+// and 29.
 #pragma once
 
 #include "attention.hpp"
@@ -479,7 +485,6 @@ __global__ __launch_bounds__(64, attention_waves(NC, BITS, PARTS)) void attentio
     // the line of all blocks: a scan over the requests' lengths on it, `share` requests a lane
     const int share = (a.R + 63) / 64;
     uint32_t mine = 0;
-#pragma unroll 8
     for (int i = 0; i < share; ++i)
         if (lane * share + i < a.R) mine += visible(a, lane * share + i).blocks() + kBeginCost;
     const uint32_t line = scan_of_wave(mine, lane), total = (uint32_t)__builtin_amdgcn_readlane((int)line, 63) * a.segments;

@@ -15,8 +15,10 @@
 // go byte by byte into the octets that they share with tokens of other calls.
 //
 // Measured on MI355X, 16384 tokens, 8 heads of 128, bf16 rows, 84 MB each way: 4 bits written in 27 us (3.1 TB/s; vector
-// instructions take 70% of the cycles, 13 a value for the exact rounding), read in 18 us (4.7 TB/s).  One row a workgroup, its
-// values stored byte by byte: 116 and 61 us.  64 tokens of a decode step: 5.3 and 4.6 us, latency.
+// instructions take 63% of the cycles, 24 a value: 13 round it exactly, the others take it from its word, mask it and pack its
+// code), read in 18 us (4.7 TB/s).  One row a workgroup, its values stored byte by byte: 116 and 61 us.  8 bits, 101 MB: 24.5 and
+// 18.1; 16 bits, 134 MB: 24.3 and 21.8; 65536 tokens in 4, 8 and 16 bits 85 and 84, 95 and 90, 110 and 108 (4 to 4.9 TB/s).
+// 64 tokens of a decode step: 5.3 and 4.7 us, latency.
 #include "context.hpp"
 
 namespace gptq {
@@ -440,7 +442,9 @@ CacheArgs cache_args(HeadRows k, HeadRows v, int64_t T, int H, int D, const int3
             (int)T, H, D, stored_head_size(D), p.page_size, Divisor((uint32_t)p.page_size)};
 }
 
-// A wave per eight tokens; as many waves a workgroup as leave a workgroup for every CU.
+// A wave per eight tokens; four waves a workgroup where that leaves one for every CU, else one.  With one and with four, 8 heads of
+// 128 in 8 bits: 64 tokens written 4.8 and 5.4 us, read 4.1 and 4.9; 1024 tokens 6.0 and 5.8, 5.0 and 4.6; 4096 tokens 11.9 and
+// 10.2, 8.8 and 7.5.
 struct CacheGrid {
     dim3 grid;
     unsigned threads;

@@ -7,7 +7,7 @@
 // token's pair whatever the number of heads, and wait in LDS.  What is left is a copy: a workgroup takes some tokens' rows of
 // some heads, 16 bytes a load where the pairs allow it (units of V pairs), and is bound by memory traffic.
 //
-// Measured on MI355X: 8192 tokens x 40 heads x 128 in bf16, 168 MB, 38 us (4.4 TB/s; a copy moves 4.9); with an angle per head
+// Measured on MI355X: 8192 tokens x 40 heads x 128 in bf16, 168 MB, 36 to 39 us (4.3 to 4.6 TB/s; a copy moves 4.9); with an angle per head
 // and single elements 72 us.  One token 2.0 us (a launch).
 #include "context.hpp"
 
@@ -110,7 +110,6 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     }
     __syncthreads();
     const int all = tokens * a.heads * a.units;
-#pragma unroll 4
     for (int i = threadIdx.x; i < all; i += kThreads) {
         const int row = (int)a.by_units.quotient((uint32_t)i), u = i - row * a.units;
         const int t = (int)a.by_heads.quotient((uint32_t)row), h = row - t * a.heads;
@@ -157,7 +156,9 @@ void launch(RotaryArgs a, bool interleaved, hipStream_t stream) {
     a.turned = a.half / V;
     a.units = a.turned + (copies ? (int)ceil_div(a.D - 2 * a.half, 2 * V) : 0);
     // Workgroups of up to 2048 units, or fewer where there would not be two for every CU: first some heads of a token (whose
-    // sines each of its workgroups then finds for itself), then more tokens.
+    // sines each of its workgroups then finds for itself), then more tokens.  With one, two and four for every CU: 512 tokens, 40
+    // heads of 128 3.7, 3.5 and 3.3 us; 2111 tokens, 11 heads of 80, 32 neighbours turned, fp32 6.7, 4.4 and 4.3.  With 1024, 2048,
+    // 4096 and 8192 units: 8192 tokens, 40 heads of 128 33, 37, 35 and 33 us, fp32 62, 70, 73 and 70 (in a graph; no order in them).
     const int64_t total = (int64_t)a.T * a.H * a.units;
     const int64_t each = total / 512 < kThreads ? kThreads : total / 512 > 2048 ? 2048 : total / 512;
     a.heads = (int)(ceil_div(each, a.units) < a.H ? ceil_div(each, a.units) : a.H);
@@ -182,7 +183,9 @@ hipError_t rotary(HeadRows x, bool f32, int64_t T, int H, int D, const int32_t* 
     a.x = x.p, a.y = y.p, a.x_ts = x.ts, a.x_hs = x.hs, a.y_ts = y.ts, a.y_hs = y.hs;
     a.positions = positions, a.freqs = freqs, a.factor = factor;
     a.T = (int)T, a.H = H, a.D = D, a.half = rot / 2;
-    // 16 bytes a load in halves, 16 or 32 of neighbours; pairs that are no multiple of that go one by one
+    // 16 bytes a load in halves, 16 or 32 of neighbours; pairs that are no multiple of that go by two or one.  8192 tokens, 40
+    // heads, bf16, by eights 128: 37 us (168 MB); by twos 72: 17.6 (94 MB), 104: 29.6 (136 MB), 80 with 40 turned: 20.6 (105 MB); by
+    // ones 96 with 18 turned: 37.9 (126 MB)
     if (f32) {
         if (a.half % 4 == 0) launch<float, 4>(a, interleaved, stream);
         else if (a.half % 2 == 0) launch<float, 2>(a, interleaved, stream);
