@@ -495,7 +495,8 @@ gptq_status_t gptq_combine(const void* Y, gptq_dtype_t dtype, int64_t M, int64_t
  * any >= 0 for what is read); rows that are written must not share elements.  At most 1024 heads.
  */
 
-/* Scalings of gptq_rotary_frequencies. */
+/* Scalings of gptq_rotary_frequencies: LINEAR is position interpolation, BASE the NTK-aware base, RAMP YaRN (low and high: its
+ * beta_slow and beta_fast), BANDS that of configurations' rope type "llama3" (low and high: its low_freq_factor and high_freq_factor). */
 #define GPTQ_ROTARY_PLAIN  0   /* f_i = base^(-2 i / rot) */
 #define GPTQ_ROTARY_LINEAR 1   /* f_i / factor: positions interpolated */
 #define GPTQ_ROTARY_BASE   2   /* base * factor^(rot / max(rot - 2, 1)), which must be finite, in base's place */
@@ -569,7 +570,7 @@ gptq_status_t gptq_cache_read(const void* pages, int64_t n_pages, int64_t page_s
                               void* V, gptq_dtype_t dtype, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
                               void* stream);
 
-/* Workspace of gptq_cache_attention, whatever the lengths; 0 for sizes that it refuses. */
+/* Workspace of gptq_cache_attention, whatever the lengths (at most 68 MB); 0 for sizes that it refuses. */
 size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t D);
 
 /*

@@ -844,7 +844,8 @@ def gptq_rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "pla
                             original: float = 8192.0, low: float = 1.0, high: Optional[float] = None, device=None):
     """(freqs float64[rot / 2], factor): radians per position of every pair, and gptq_rotary's factor on cos and sin.
 
-    scaling: "plain", "linear", "base", "ramp" (high 32 unless given) or "bands" (high 4); see include/gptq.h.
+    scaling: "plain", "linear" (position interpolation), "base" (NTK-aware), "ramp" (YaRN; high, its beta_fast, 32 unless
+    given) or "bands" (rope type "llama3"; high, its high_freq_factor, 4); see include/gptq.h.
     """
     if scaling not in _ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)}")
@@ -862,7 +863,7 @@ def gptq_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, i
                 factor: float = 1.0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The first 2 len(freqs) elements of every row of x (T x H x D) turned by positions (int32[T]), the others copied.
 
-    Pairs (i, i + rot / 2), or neighbours with interleaved.  out=x turns in place.
+    Pairs (i, i + rot / 2), or neighbours with interleaved.  out=x turns in place; another out must share no element with x.
     """
     gpu = _gpu(x)
     if stream is not None or gpu != _device_now():
@@ -951,7 +952,7 @@ def gptq_cache_attention(q: torch.Tensor, pages: torch.Tensor, table: torch.Tens
 
     q: R x Hq x D (fp32 or bf16).  pages: as gptq_cache_write left them, H heads with Hq a multiple of H.  table: int32 R x
     pages per request.  lengths: int32[R].  scale: 1 / sqrt(D) unless given.  window: only the last `window` tokens.
-    lse: fp32 R x Hq, written if given.
+    lse: fp32 R x Hq, written if given.  out shares no element with q.
     """
     gpu = _gpu(q)
     if stream is not None or gpu != _device_now():
