@@ -582,7 +582,7 @@ size_t gptq_attention_workspace_bytes(int64_t R, int64_t Hq, int64_t H, int64_t 
  *              j < max_pages; tokens of a page outside [0, n_pages) are left out.   max_pages * page_size < 2^31,
  *              R (max_pages page_size / 32 + 8) H ceil(Hq / H / 16) < 2^31.
  *   lengths    device int32[R], clamped to [0, max_pages * page_size].
- *   out        device, R x Hq x D, dtype; not Q.   lse: NULL, or device fp32[R * Hq]: ln sum_t exp(scale q . k_t).
+ *   out        device, R x Hq x D, dtype; no element of Q.   lse: NULL, or device fp32[R * Hq]: ln sum_t exp(scale q . k_t).
  *   workspace  device scratch of gptq_attention_workspace_bytes(R, Hq, H, D).
  * A request without a token to attend to gets zeros, and lse -infinity; so does one whose scores are all -infinity.  Slots that
  * no length reaches may hold anything.  A NaN or infinity in q makes its row of out, and its lse, NaN (where it attends to a
